@@ -388,6 +388,191 @@ mao_status dion_step(const mao_mat* X, const mao_mat* M, const mao_mat* G, const
                      size_t workspace_bytes, void* stream);
 
 /*
+ * ------------------------------------------------------------------ expert layers
+ *
+ * The calls below are the operators of an expert layer around the optimizer step (no
+ * counterpart on the pages, which name the layer's shapes only): routing tokens to experts,
+ * quantising to 8-bit floating point, the experts' products in both directions, and the
+ * combination of the experts' outputs. They take zero rows (nothing is written then, unless
+ * said otherwise), read no argument after they return and keep nothing between calls.
+ *
+ *   W8 <- fp8_quantize(W)                          after every optimizer step
+ *   weights, ids <- expert_route(logits)           T tokens, k experts each
+ *   offsets, row_of, slot_of <- expert_plan(ids)   the copies in the order of the experts
+ *   X8 <- fp8_quantize(X, slot_of / k)             the dispatch: gathered and quantised
+ *   H <- fp8_product(X8, W8, MAO_NT, offsets)      forward
+ *   y <- expert_combine(Z, row_of, weights)
+ *   dZ, dw <- expert_combine_backward(...)         and back
+ *   dX <- fp8_product(dH8, W8, MAO_NN, offsets);  dW <- fp8_product(dH8, X8, MAO_TN, offsets)
+ *   dlogits <- expert_route_backward(logits, ids, dw)
+ *   muon_step(W, M, dW)
+ */
+
+/* Which entries of a matrix share one scale. */
+enum {
+  MAO_BLOCKS_ROW = 1,   /* 128 consecutive columns of a row:   scales [rows][ceil(cols/128)] */
+  MAO_BLOCKS_COL = 2,   /* 128 consecutive rows of a column:   scales [ceil(rows/128)][cols] */
+  MAO_BLOCKS_TILE = 3   /* 128 x 128 tiles: scales [ceil(rows/128)][ceil(cols/128)] */
+};
+
+/*
+ * One matrix, or `count` stacked ones of equal shape, in 8-bit floating point: entry (i, j)
+ * of matrix b is e4m3(codes[b*rows*ld + i*ld + j]) * 2^(scale - 127), with the byte `scale` of
+ * its block at scales[(b*SR + r)*scale_ld + c], where SR is the number of scale rows above
+ * and (r, c) the block's place (i or i/128, j or j/128). e4m3 is the 8-bit format with four
+ * exponent and three mantissa bits, no infinities, largest value 448, NaN 0x7F.
+ */
+typedef struct mao_fp8 {
+  uint8_t* codes;    /* device, 16-byte aligned */
+  uint8_t* scales;   /* device */
+  int64_t rows;      /* R >= 0 (of one matrix) */
+  int64_t cols;      /* C >= 1 */
+  int64_t ld;        /* codes between row starts: >= cols, a multiple of 16 */
+  int64_t scale_ld;  /* bytes between rows of scales, >= their number of columns */
+  int32_t count;     /* stacked matrices, >= 1 */
+  int32_t blocks;    /* MAO_BLOCKS_* */
+} mao_fp8;
+
+/*
+ * Quantises matrices to 8-bit floating point with a power-of-two scale for each block of 128.
+ *
+ * A block whose largest finite magnitude is a gets the smallest exponent e >= -127 with
+ * a <= 448 * 2^e (scale byte e + 127; 0 for a block of zeros), and each entry x the code of
+ * x * 2^-e rounded to nearest even. Scaling by a power of two is exact, so x is rounded once.
+ * NaN and infinities get the code NaN: a product that reads them is NaN, not saturated.
+ *
+ *   X             batch_stride > 0: *X describes matrix 0 and matrix b lies b*batch_stride
+ *                 elements after it; 0: an array of `batch` descriptors of one shape and
+ *                 dtype. f32 or bf16. X->rows may be 0.
+ *   copies        0: the rows of X as they are (index and n_index are not looked at). >= 1
+ *                 (batch must be 1): row i of the result, i < n_index, is row index[i] /
+ *                 copies of X, or zeros where index[i] < 0 or that row does not exist; index
+ *                 is a device array of n_index int32 (the gather of an expert layer's
+ *                 dispatch: slot_of with copies = k). X is then [tokens][cols].
+ *   row, col, tile   the results, each NULL or a descriptor with blocks of that kind, count
+ *                 = batch, rows = X's (or n_index), cols = X's. Give row, col, both (one pass
+ *                 over X), or tile alone.
+ */
+mao_status fp8_quantize(const mao_mat* X, int32_t batch, int64_t batch_stride,
+                        const int32_t* index, int64_t n_index, int32_t copies,
+                        const mao_fp8* row, const mao_fp8* col, const mao_fp8* tile,
+                        void* stream);
+
+/* The three products of a layer y = x W^T and its gradients. */
+enum {
+  MAO_NT = 0,  /* D[t][n] = sum_k A[t][k] B[n][k]   A row blocks [R][K], B tiles [N][K] */
+  MAO_NN = 1,  /* D[t][k] = sum_n A[t][n] B[n][k]   A row blocks [R][N], B tiles [N][K] */
+  MAO_TN = 2   /* D[n][k] = sum_t A[t][n] B[t][k]   A, B column blocks [R][N], [R][K] */
+};
+
+/*
+ * Product of two 8-bit matrices on the tensor cores, fp32 sums, over groups of rows t.
+ *
+ *   offsets    NULL (groups must be 1): one group of all R rows. Otherwise a device array of
+ *              groups + 1 int32, rising from 0 to at most R: group g is rows offsets[g] ..
+ *              offsets[g+1] - 1 and, for MAO_NT and MAO_NN, multiplies matrix g of B
+ *              (B->count = groups); for MAO_TN it gives matrix g of D, and the offsets must
+ *              be multiples of 128 (expert_plan's are; blocks do not cross groups). Values
+ *              outside 0 .. R are cut to that range.
+ *   D          f32 or bf16. MAO_NT: R x N; MAO_NN: R x K; both: rows past the last group are
+ *              set to zero. MAO_TN: the groups' N x K matrices stacked, (groups*N) x K; an
+ *              empty group's matrix is zero.
+ *   accumulate nonzero: D <- D + product (in fp32, rounded to D's dtype once; rows past the
+ *              last group and empty groups' matrices keep their values).
+ *   Limits: groups <= 1024; A, B codes at most 2^31 rows in all. Products of e4m3 values are
+ *   exact in fp32; the order of the sums over K is fixed, so results are the same each time.
+ *   Codes that a NaN scale (255) covers are not supported: fp8_quantize never writes it.
+ */
+mao_status fp8_product(const mao_fp8* A, const mao_fp8* B, const mao_mat* D, int32_t form,
+                       const int32_t* offsets, int32_t groups, int32_t accumulate,
+                       void* stream);
+
+enum { MAO_SCORE_SOFTMAX = 0, MAO_SCORE_SIGMOID = 1 };
+enum { MAO_GROUP_MAX = 0, MAO_GROUP_TOP2 = 1 };
+
+/*
+ * Routing: the top_k experts of each token.
+ *
+ * Scores s = softmax(l) over the experts, or sigmoid(l), in fp32. Experts are chosen by a
+ * key: s + bias (bias: E floats that balance the load; they choose, but do not weigh), or l
+ * itself without bias and groups (the same order, with no rounding of s in it). With groups
+ * > 1 the experts form that many runs of E / groups; a run's score is its largest key
+ * (MAO_GROUP_MAX) or the sum of its two largest (MAO_GROUP_TOP2), and only experts of the
+ * keep_groups best runs are chosen. Ties go to the lower index, of runs and of experts.
+ * ids come in falling order of their keys, with weights
+ *   w = scale * s            or, with renorm,   w = scale * s / (sum of chosen s + 1e-20).
+ * A logit of -inf masks an expert: it is never chosen, and a token with fewer than top_k
+ * experts left gets ids -1 with weight 0 in the last places (all of them where every expert
+ * is masked). An expert whose key is NaN is not chosen either; a NaN or +inf logit makes
+ * the token's softmax, and so its weights, NaN.
+ *
+ *   logits   f32 or bf16, T x E, E <= 1024, T >= 0.
+ *   top_k    1..min(E, 32). groups divides E, <= 32. keep_groups 1..groups, enough of them
+ *            to hold top_k experts.
+ *   weights, ids   device, T x top_k floats and int32 (written).
+ */
+mao_status expert_route(const mao_mat* logits, const float* bias, int32_t top_k, int32_t score,
+                        int32_t groups, int32_t keep_groups, int32_t group_score,
+                        int32_t renorm, float scale, float* weights, int32_t* ids,
+                        void* stream);
+
+/*
+ * Gradient of expert_route's weights: dlogits (T x E, f32 or bf16) from dweights (T x top_k
+ * floats), the logits and the ids that the call gave; choosing has no gradient. With S =
+ * sum of chosen s, r = s / S, g = scale * dweights (0 where the id is -1):
+ *   ds_j = g_j, or with renorm (g_j - sum_i g_i r_i) / S
+ *   softmax: dl_i = s_i (ds_i - sum_j ds_j s_j)     sigmoid: dl_i = ds_i s_i (1 - s_i)
+ * where ds is 0 for experts that were not chosen (with softmax and renorm the sum is 0).
+ * A masked expert's gradient is 0.
+ */
+mao_status expert_route_backward(const mao_mat* logits, const int32_t* ids,
+                                 const float* dweights, int32_t top_k, int32_t score,
+                                 int32_t renorm, float scale, const mao_mat* dlogits,
+                                 void* stream);
+
+/*
+ * Where the tokens' copies go: each expert's copies, in the order of the tokens, in a run of
+ * rows that starts at a multiple of 128.
+ *
+ *   ids       device, n = tokens * top_k int32; entries outside 0 .. experts-1 are dropped.
+ *   counts    device, experts int32: copies of each expert.
+ *   offsets   device, experts + 1 int32: offsets[0] = 0, offsets[e+1] = offsets[e] +
+ *             counts[e] rounded up to a multiple of 128.
+ *   row_of    device, n int32: the row of copy i, -1 if dropped.
+ *   slot_of   device, n_slots int32: the copy in each row, -1 in padding rows; n_slots >=
+ *             expert_rows(n, experts).
+ *   Limits: n <= 2^27, experts <= 1024; n = 0 writes counts, offsets and slot_of.
+ *   workspace >= expert_plan_workspace_bytes(n, experts) bytes, 256-byte aligned.
+ */
+int64_t expert_rows(int64_t n, int32_t experts);
+size_t expert_plan_workspace_bytes(int64_t n, int32_t experts);
+mao_status expert_plan(const int32_t* ids, int64_t n, int32_t experts, int32_t* counts,
+                       int32_t* offsets, int32_t* row_of, int32_t* slot_of, int64_t n_slots,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Combination of the experts' outputs: y[t] = sum_j w[t][j] Z[row_of[t][j]] over j with
+ * row_of >= 0, in fp32 in the order of j, rounded once to Y's dtype.
+ *   Z        f32 or bf16, any number of rows; Y f32 or bf16, tokens x Z's columns.
+ *   row_of   device, tokens x top_k int32 (a row outside Z counts as dropped).
+ *   weights  device, tokens x top_k floats, or NULL: all 1 (the gradient of the dispatch).
+ *   top_k    1..32.
+ */
+mao_status expert_combine(const mao_mat* Z, const int32_t* row_of, const float* weights,
+                          int64_t tokens, int32_t top_k, const mao_mat* Y, void* stream);
+
+/*
+ * Gradients of expert_combine: for copy i = t*top_k + j in row r
+ *   dZ[r] = w[i] dY[t], rounded to dZ's dtype;   dweights[i] = <dY[t], Z[r]> in fp32,
+ * zero in dZ's rows that hold no copy, and dweights[i] = 0 where copy i was dropped.
+ *   slot_of  device, one int32 per row of Z (expert_plan's). dZ: f32 or bf16 of Z's shape.
+ *   weights  NULL: all 1; dweights may be NULL.
+ */
+mao_status expert_combine_backward(const mao_mat* dY, const mao_mat* Z, const int32_t* row_of,
+                                   const int32_t* slot_of, const float* weights, int32_t top_k,
+                                   const mao_mat* dZ, float* dweights, void* stream);
+
+/*
  * Bound of every device-side wait of the tensor-core kernels (default 4 s), used by launches
  * enqueued after the call; process-wide. A wait that runs past it makes the kernel stop
  * early (its outputs are then incomplete) and mao_sync_status() report MAO_ERR_TIMEOUT.

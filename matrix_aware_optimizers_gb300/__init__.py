@@ -18,6 +18,13 @@ Functions (same names as the C ABI):
   majority_vote_int8(s, n, sum, s_bar, vote)         int8 SUM over workers + threshold
   apply_update(W, lr, vote=..., U=...)               W <- W - lr*D
   dion_step(X, M, G, Q, mu, lr, ...)                 one Dion step (low-rank, error feedback)
+  fp8_quantize(X, blocks, ...)                       8-bit codes with a scale per block of 128
+  fp8_product(A, a_scales, B, b_scales, form, ...)   products of 8-bit matrices, grouped rows
+  expert_route(logits, top_k, ...)                   choice and weights of each token's experts
+  expert_route_backward(logits, ids, dweights, ...)  gradient of the logits
+  expert_plan(ids, experts)                          places of the copies among the experts' rows
+  expert_combine(Z, row_of, weights)                 weighted sum of a token's expert outputs
+  expert_combine_backward(dY, Z, row_of, ...)        its gradients
   sync_status()                                      stream sync + device error word
 """
 
@@ -394,6 +401,289 @@ def dion_step(X, M, G, Q, mu, lr, P_out=None, ws=None, stream=None, X_out=None):
                          float(mu), float(lr), _abi.MAO_BF16, ctypes.c_void_p(ws.data_ptr()),
                          ws.numel(), _stream(stream))
     _abi.check("dion_step", st)
+
+
+# ---------------------------------------------------------------- expert layers
+
+_BLOCKS = {"row": _abi.MAO_BLOCKS_ROW, "col": _abi.MAO_BLOCKS_COL, "tile": _abi.MAO_BLOCKS_TILE}
+_FORM = {"nt": _abi.MAO_NT, "nn": _abi.MAO_NN, "tn": _abi.MAO_TN}
+_SCORE = {"softmax": _abi.MAO_SCORE_SOFTMAX, "sigmoid": _abi.MAO_SCORE_SIGMOID}
+_GROUP_SCORE = {"max": _abi.MAO_GROUP_MAX, "top2": _abi.MAO_GROUP_TOP2}
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on `stream`: allocated there, so that its memory is reused
+    only after that stream's work."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _dense_ptr(t, dtype, shape, name):
+    """Device pointer of a contiguous tensor of the given type and shape (None: NULL)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s CUDA tensor of shape %s"
+                         % (name, dtype, tuple(shape)))
+    return t.data_ptr()
+
+
+def _scale_shape(rows, cols, blocks):
+    br = 1 if blocks == "row" else 128
+    bc = 1 if blocks == "col" else 128
+    return -(-rows // br), -(-cols // bc)
+
+
+def _fp8(codes, scales, blocks, name):
+    """MaoFp8 of a code tensor [R, C] or [B, R, C] and its scale bytes."""
+    if codes.dtype not in (torch.float8_e4m3fn, torch.uint8) or scales.dtype != torch.uint8:
+        raise ValueError("%s: codes are float8_e4m3fn and scales uint8 tensors" % name)
+    if not codes.is_cuda or not scales.is_cuda or codes.dim() not in (2, 3) or \
+            scales.dim() != codes.dim() or codes.stride(-1) != 1 or scales.stride(-1) != 1:
+        raise ValueError("%s: CUDA tensors of two or three dimensions, unit column stride" % name)
+    rows, cols = codes.shape[-2], codes.shape[-1]
+    count = codes.shape[0] if codes.dim() == 3 else 1
+    sr, sc = _scale_shape(rows, cols, blocks)
+    if tuple(scales.shape[-2:]) != (sr, sc) or (codes.dim() == 3 and scales.shape[0] != count):
+        raise ValueError("%s: scales of shape %s do not fit %s blocks of %s"
+                         % (name, tuple(scales.shape), blocks, tuple(codes.shape)))
+    # the row stride of a single row may be anything
+    ld = codes.stride(-2) if rows > 1 or (count > 1 and rows == 1) else -(-cols // 16) * 16
+    sld = scales.stride(-2) if sr > 1 else sc
+    if codes.dim() == 3 and count > 1:
+        ld = codes.stride(0) // max(rows, 1) if rows else ld
+        sld = scales.stride(0) // max(sr, 1) if sr else sld
+        if codes.stride(0) != rows * ld or (rows > 1 and codes.stride(1) != ld) or \
+                scales.stride(0) != sr * sld or (sr > 1 and scales.stride(1) != sld):
+            raise ValueError("%s: stacked matrices follow each other without gaps" % name)
+    return _abi.MaoFp8(codes.data_ptr(), scales.data_ptr(), rows, cols, ld, sld, count,
+                       _BLOCKS[blocks])
+
+
+def fp8_quantize(X, blocks, rows=None, copies=1, out=None, stream=None):
+    """Codes (float8_e4m3fn) and scale bytes of X in 8-bit floating point, with a
+    power-of-two scale 2^(byte - 127) for each block of 128.
+
+    X: a float32 or bfloat16 matrix [R, C], stacked matrices [B, R, C], or a list of B
+    matrices of one shape. blocks: "row" (128 columns of a row), "col" (128 rows of a column),
+    "tile" (128 x 128) or "both" (row and col, in one pass). Returns (codes, scales), or with
+    "both" (row codes, row scales, col codes, col scales), stacked as X is; code rows are 16-byte
+    aligned. rows: int32 tensor of source rows (one matrix X): row i of the result is row
+    rows[i] // copies of X, or zeros where rows[i] < 0. out: a tuple of tensors to fill.
+    """
+    many = isinstance(X, (list, tuple))
+    x0 = X[0] if many else X
+    stacked = many or x0.dim() == 3
+    if blocks not in ("row", "col", "tile", "both"):
+        raise ValueError("blocks must be row, col, tile or both")
+    if many:
+        mats, batch, stride = _mats(list(X)), len(X), 0
+        R, C = x0.shape
+    elif x0.dim() == 3:
+        batch, R, C = x0.shape
+        if batch == 0:
+            raise ValueError("no matrices")
+        if not x0.is_cuda or x0.dtype not in (torch.float32, torch.bfloat16) or x0.stride(2) != 1:
+            raise ValueError("expected a float32 or bfloat16 CUDA tensor with unit column stride")
+        stride = x0.stride(0) if batch > 1 else 0
+        if batch > 1 and stride < 1:
+            raise ValueError("stacked matrices need a positive stride")
+        ld = max(x0.stride(1), C) if R > 1 else C
+        mats = (_abi.MaoMat * 1)(_abi.MaoMat(x0.data_ptr(), R, C, ld, _DT[x0.dtype], 0))
+    else:
+        mats, batch, stride = _mats([x0]), 1, 0
+        R, C = x0.shape
+    index, n_index = None, 0
+    if rows is not None:
+        if batch != 1:
+            raise ValueError("rows go with a single matrix")
+        if copies < 1:
+            raise ValueError("copies must be at least 1")
+        n_index = R = rows.numel()
+        index = _dense_ptr(rows, torch.int32, rows.shape, "rows")
+    kinds = ("row", "col") if blocks == "both" else (blocks,)
+    if out is None:
+        out, wide = [], -(-C // 16) * 16
+        for k in kinds:
+            lead = (batch,) if stacked else ()
+            codes = _empty(lead + (R, wide), torch.float8_e4m3fn, x0.device, stream)
+            out += [codes if wide == C else codes[..., :C],
+                    _empty(lead + _scale_shape(R, C, k), torch.uint8, x0.device, stream)]
+    if len(out) != 2 * len(kinds):
+        raise ValueError("out needs codes and scales for each kind of blocks")
+    desc = {}
+    for i, k in enumerate(kinds):
+        desc[k] = ctypes.byref(_fp8(out[2 * i], out[2 * i + 1], k, k))
+    st = lib().fp8_quantize(mats, batch, stride, index, n_index,
+                            int(copies) if rows is not None else 0, desc.get("row"),
+                            desc.get("col"), desc.get("tile"), _stream(stream))
+    _abi.check("fp8_quantize", st)
+    return tuple(out)
+
+
+def fp8_product(A, a_scales, B, b_scales, form, offsets=None, out=None, out_dtype=torch.bfloat16,
+                accumulate=False, stream=None):
+    """Product of 8-bit matrices (fp8_quantize's codes and scales) with fp32 sums, over groups
+    of rows.
+
+    form "nt": out[t, n] = sum_k A[t, k] B[g, n, k]   A in row blocks, B in tiles
+         "nn": out[t, k] = sum_n A[t, n] B[g, n, k]   A in row blocks, B in tiles
+         "tn": out[g, n, k] = sum_t A[t, n] B[t, k]   A and B in column blocks
+    offsets: int32 tensor of groups + 1 row numbers (expert_plan's; for "tn" multiples of
+    128): g is the group of row t, and "tn" sums over the rows of group g. None: one group, and
+    B may then be [N, K]. out: a float32 or bfloat16 tensor to fill, or with accumulate to add
+    to; by default a new one of out_dtype. Rows past the last group become zero.
+    """
+    if form not in _FORM:
+        raise ValueError("form must be nt, nn or tn")
+    tn = form == "tn"
+    if A.dim() != 2 or (tn and B.dim() != 2):
+        raise ValueError("A (and for tn B) must be a matrix")
+    a = _fp8(A, a_scales, "col" if tn else "row", "A")
+    b = _fp8(B, b_scales, "col" if tn else "tile", "B")
+    if offsets is None:
+        groups, off = 1, None
+    else:
+        groups = offsets.numel() - 1
+        off = _dense_ptr(offsets, torch.int32, (groups + 1,), "offsets")
+    shape = (groups, a.cols, b.cols) if tn else (a.rows, b.rows if form == "nt" else b.cols)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = _empty(shape, out_dtype, A.device, stream)
+    if tuple(out.shape) != shape and not (tn and groups == 1 and tuple(out.shape) == shape[1:]):
+        raise ValueError("out must have shape %s" % (shape,))
+    d = out
+    if out.dim() == 3:
+        if groups > 1 and out.stride(0) != a.cols * out.stride(1):
+            raise ValueError("the groups' matrices follow each other without gaps")
+        d = out.as_strided((groups * a.cols, b.cols), (out.stride(1), out.stride(2)))
+    st = lib().fp8_product(ctypes.byref(a), ctypes.byref(b), ctypes.byref(_mat(d)), _FORM[form],
+                           off, groups, int(bool(accumulate)), _stream(stream))
+    _abi.check("fp8_product", st)
+    return out
+
+
+def expert_route(logits, top_k, score="softmax", bias=None, groups=1, keep_groups=None,
+                 group_score="top2", renorm=True, scale=1.0, weights=None, ids=None, stream=None):
+    """The top_k experts of each token: (weights float32 [T, top_k], ids int32 [T, top_k]).
+
+    score: "softmax" or "sigmoid" of the logits [T, E] (float32 or bfloat16). bias: float32 [E],
+    added to the scores for choosing only. groups, keep_groups, group_score ("max" or
+    "top2"): only experts of the best runs of E / groups are chosen. renorm: the chosen scores
+    are divided by their sum. Masked experts (logit -inf) are never chosen; ids -1 with
+    weight 0 fill the places that are left.
+    """
+    m = _mat(logits)
+    T, E = m.rows, m.cols
+    if weights is None:
+        weights = _empty((T, top_k), torch.float32, logits.device, stream)
+    if ids is None:
+        ids = _empty((T, top_k), torch.int32, logits.device, stream)
+    st = lib().expert_route(
+        ctypes.byref(m), _dense_ptr(bias, torch.float32, (E,), "bias"), int(top_k), _SCORE[score],
+        int(groups), int(groups if keep_groups is None else keep_groups),
+        _GROUP_SCORE[group_score], int(bool(renorm)), float(scale),
+        _dense_ptr(weights, torch.float32, (T, top_k), "weights"),
+        _dense_ptr(ids, torch.int32, (T, top_k), "ids"), _stream(stream))
+    _abi.check("expert_route", st)
+    return weights, ids
+
+
+def expert_route_backward(logits, ids, dweights, score="softmax", renorm=True, scale=1.0,
+                          dlogits=None, stream=None):
+    """Gradient of expert_route's weights with respect to the logits (dlogits: of the logits'
+    shape and dtype unless given)."""
+    m = _mat(logits)
+    if ids.dim() != 2 or ids.shape[0] != m.rows:
+        raise ValueError("ids must be [T, top_k]")
+    k = ids.shape[1]
+    if dlogits is None:
+        dlogits = _empty(tuple(logits.shape), logits.dtype, logits.device, stream)
+    st = lib().expert_route_backward(
+        ctypes.byref(m), _dense_ptr(ids, torch.int32, (m.rows, k), "ids"),
+        _dense_ptr(dweights, torch.float32, (m.rows, k), "dweights"), k, _SCORE[score],
+        int(bool(renorm)), float(scale), ctypes.byref(_mat(dlogits)), _stream(stream))
+    _abi.check("expert_route_backward", st)
+    return dlogits
+
+
+def expert_rows(n, experts):
+    """Rows that always hold n copies in the experts' padded runs."""
+    return int(lib().expert_rows(int(n), int(experts)))
+
+
+class ExpertPlan:
+    """Where the tokens' copies go (expert_plan): counts [E], offsets [E + 1], row_of [T, k]
+    (-1: dropped) and slot_of [rows] (the copy t * k + j in each row, -1 in padding rows)."""
+
+    __slots__ = ("counts", "offsets", "row_of", "slot_of")
+
+    def __init__(self, counts, offsets, row_of, slot_of):
+        self.counts, self.offsets, self.row_of, self.slot_of = counts, offsets, row_of, slot_of
+
+
+def expert_plan(ids, experts, ws=None, stream=None):
+    """Places of the copies ids [T, top_k] (int32; entries outside 0 .. experts - 1 are dropped):
+    each expert's copies, in the order of the tokens, in a run of rows that starts at a
+    multiple of 128. Returns an ExpertPlan."""
+    n = ids.numel()
+    p_ids = _dense_ptr(ids, torch.int32, ids.shape, "ids")
+    rows = expert_rows(n, experts)
+    nb = lib().expert_plan_workspace_bytes(n, int(experts))
+    if nb == 0:
+        raise ValueError("expert_plan takes up to 2^27 copies and 1 to 1024 experts")
+    # one allocation for the outputs and the workspace, each part 256-byte aligned
+    parts = [experts, experts + 1, n, rows, (nb + 3) // 4 if ws is None else 0]
+    at, total = [], 0
+    for c in parts:
+        at.append(total)
+        total += (c + 63) // 64 * 64
+    buf = _empty((total,), torch.int32, ids.device, stream)
+    counts, offsets, row_of, slot_of = (buf[a:a + c] for a, c in zip(at[:4], parts[:4]))
+    base = buf.data_ptr()
+    wptr, wbytes = (base + 4 * at[4], nb) if ws is None else (ws.data_ptr(), ws.numel())
+    st = lib().expert_plan(p_ids, n, int(experts), base, base + 4 * at[1], base + 4 * at[2],
+                           base + 4 * at[3], rows, wptr, wbytes, _stream(stream))
+    _abi.check("expert_plan", st)
+    return ExpertPlan(counts, offsets, row_of.view(ids.shape), slot_of)
+
+
+def expert_combine(Z, row_of, weights=None, out=None, stream=None):
+    """y[t] = sum_j weights[t, j] Z[row_of[t, j]] (entries below 0 are skipped; weights None:
+    all 1), summed in fp32; out: of Z's dtype unless given."""
+    T, k = row_of.shape
+    if out is None:
+        out = _empty((T, Z.shape[1]), Z.dtype, Z.device, stream)
+    st = lib().expert_combine(
+        ctypes.byref(_mat(Z)), _dense_ptr(row_of, torch.int32, (T, k), "row_of"),
+        _dense_ptr(weights, torch.float32, (T, k), "weights"), T, k, ctypes.byref(_mat(out)),
+        _stream(stream))
+    _abi.check("expert_combine", st)
+    return out
+
+
+def expert_combine_backward(dY, Z, row_of, slot_of, weights=None, dZ=None, dweights=None,
+                            stream=None):
+    """Gradients (dZ of Z's shape and dtype unless given, dweights float32 [T, k]) of
+    expert_combine."""
+    T, k = row_of.shape
+    if dY.dim() != 2 or dY.shape[0] != T:
+        raise ValueError("dY needs one row per token")
+    if dZ is None:
+        dZ = _empty(tuple(Z.shape), Z.dtype, Z.device, stream)
+    if dweights is None:
+        dweights = _empty((T, k), torch.float32, Z.device, stream)
+    st = lib().expert_combine_backward(
+        ctypes.byref(_mat(dY)), ctypes.byref(_mat(Z)),
+        _dense_ptr(row_of, torch.int32, (T, k), "row_of"),
+        _dense_ptr(slot_of, torch.int32, (Z.shape[0],), "slot_of"),
+        _dense_ptr(weights, torch.float32, (T, k), "weights"), k, ctypes.byref(_mat(dZ)),
+        _dense_ptr(dweights, torch.float32, (T, k), "dweights"), _stream(stream))
+    _abi.check("expert_combine_backward", st)
+    return dZ, dweights
 
 
 def set_wait_limit(ns):

@@ -19,6 +19,17 @@ MAO_BF16 = 1
 MAO_I8 = 2      # ns_orthogonalize input only
 MAO_SIGN1 = 3   # ns_orthogonalize input only (packed signs, ld == cols)
 
+MAO_BLOCKS_ROW = 1
+MAO_BLOCKS_COL = 2
+MAO_BLOCKS_TILE = 3
+MAO_NT = 0
+MAO_NN = 1
+MAO_TN = 2
+MAO_SCORE_SOFTMAX = 0
+MAO_SCORE_SIGMOID = 1
+MAO_GROUP_MAX = 0
+MAO_GROUP_TOP2 = 1
+
 # every symbol include/mao.h declares
 EXPORTS = (
     "mao_abi_version",
@@ -40,6 +51,15 @@ EXPORTS = (
     "apply_update",
     "dion_workspace_bytes",
     "dion_step",
+    "fp8_quantize",
+    "fp8_product",
+    "expert_route",
+    "expert_route_backward",
+    "expert_rows",
+    "expert_plan_workspace_bytes",
+    "expert_plan",
+    "expert_combine",
+    "expert_combine_backward",
     "mao_set_wait_limit",
     "mao_get_wait_limit",
     "mao_sync_status",
@@ -60,6 +80,19 @@ class MaoMat(ctypes.Structure):
         ("ld", ctypes.c_int64),
         ("dtype", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class MaoFp8(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("scale_ld", ctypes.c_int64),
+        ("count", ctypes.c_int32),
+        ("blocks", ctypes.c_int32),
     ]
 
 
@@ -149,6 +182,25 @@ def load():
                               P(ctypes.c_void_p),
                               ctypes.c_int32, ctypes.c_int32, ctypes.c_float, ctypes.c_float,
                               ctypes.c_int32, vp, ctypes.c_size_t, vp]
+    i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    for name, res, args in (
+            ("fp8_quantize", ctypes.c_int,
+             [P(MaoMat), i32, i64, vp, i64, i32, P(MaoFp8), P(MaoFp8), P(MaoFp8), vp]),
+            ("fp8_product", ctypes.c_int,
+             [P(MaoFp8), P(MaoFp8), P(MaoMat), i32, vp, i32, i32, vp]),
+            ("expert_route", ctypes.c_int,
+             [P(MaoMat), vp, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp]),
+            ("expert_route_backward", ctypes.c_int,
+             [P(MaoMat), vp, vp, i32, i32, i32, f32, P(MaoMat), vp]),
+            ("expert_rows", i64, [i64, i32]),
+            ("expert_plan_workspace_bytes", ctypes.c_size_t, [i64, i32]),
+            ("expert_plan", ctypes.c_int,
+             [vp, i64, i32, vp, vp, vp, vp, i64, vp, ctypes.c_size_t, vp]),
+            ("expert_combine", ctypes.c_int, [P(MaoMat), vp, vp, i64, i32, P(MaoMat), vp]),
+            ("expert_combine_backward", ctypes.c_int,
+             [P(MaoMat), P(MaoMat), vp, vp, vp, i32, P(MaoMat), vp, vp])):
+        getattr(lib, name).restype = res
+        getattr(lib, name).argtypes = args
     lib.mao_set_wait_limit.restype = None
     lib.mao_set_wait_limit.argtypes = [ctypes.c_uint64]
     lib.mao_get_wait_limit.restype = ctypes.c_uint64

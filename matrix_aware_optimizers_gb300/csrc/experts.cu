@@ -1,0 +1,536 @@
+// Routing of an expert layer: scores and choice of experts, the plan of the copies' places,
+// the combination of the experts' outputs, and the gradients.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "experts.h"
+#include "internal.h"
+
+namespace mao {
+namespace {
+
+constexpr uint32_t FULL = 0xFFFFFFFFu;
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
+  return v;
+}
+
+// Unsigned integers in the order of the floats; 0 for -inf and NaN, which are never chosen.
+__device__ __forceinline__ uint32_t order_of(float key) {
+  if (!(key > -INFINITY)) return 0u;
+  const uint32_t b = __float_as_uint(key + 0.0f);  // -0 counts as +0
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// ------------------------------------------------------------------ choice of experts
+//
+// One warp per token; lane l holds experts 32 i + l. The softmax is one maximum, one sum. The
+// top_k best are taken one by one: the lanes' best keys as ordered integers, one warp
+// maximum, and one warp minimum of the index among the lanes that hold it.
+
+constexpr int ROUTE_WARPS = 4;
+
+template <int VPL>
+__device__ __forceinline__ void load_logits(const void* base, int64_t row, int64_t ld, int dtype,
+                                            int experts, int lane, float (&x)[VPL]) {
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = 32 * i + lane;
+    x[i] = e < experts ? load_elem(base, row * ld + e, dtype) : -INFINITY;
+  }
+}
+
+// Scores of a token's experts from its logits (softmax over the warp, or sigmoid).
+template <int VPL>
+__device__ __forceinline__ void scores_of(const float (&x)[VPL], int score, float (&p)[VPL]) {
+  if (score == MAO_SCORE_SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) p[i] = 1.0f / (1.0f + expf(-x[i]));
+    return;
+  }
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
+  m = warp_max(m);
+  if (m == -INFINITY) m = 0.0f;  // every expert masked: all scores 0
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    p[i] = expf(x[i] - m);
+    sum += p[i];
+  }
+  sum = warp_sum(sum);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) p[i] *= inv;
+}
+
+template <int VPL>
+__global__ void __launch_bounds__(32 * ROUTE_WARPS) route_kernel(const RouteParams p) {
+  extern __shared__ float sm[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = int64_t(blockIdx.x) * ROUTE_WARPS + warp;
+  if (t >= p.tokens) return;
+  float* score_sm = sm + warp * 2 * 32 * VPL;
+  float* key_sm = score_sm + 32 * VPL;
+  float x[VPL], s[VPL];
+  load_logits<VPL>(p.logits, t, p.ld, p.dtype, p.experts, lane, x);
+  scores_of<VPL>(x, p.score, s);
+  uint32_t u[VPL];
+  const bool plain = !p.bias && p.groups == 1;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = 32 * i + lane;
+    float key = plain ? x[i] : s[i];
+    if (p.bias && e < p.experts) key += p.bias[e];
+    if (!(x[i] > -INFINITY)) key = -INFINITY;
+    score_sm[e] = s[i];
+    u[i] = order_of(key);
+    if (p.groups > 1) key_sm[e] = u[i] ? key : -INFINITY;
+  }
+  __syncwarp();
+  if (p.groups > 1) {
+    // lane g scores run g, starting at its own place so that the lanes' reads spread over
+    // the banks
+    const int size = p.experts / p.groups;
+    float first = -INFINITY, second = -INFINITY;
+    if (lane < p.groups) {
+      int at = lane % size;
+      for (int i = 0; i < size; ++i) {
+        const float k = key_sm[lane * size + at];
+        if (++at == size) at = 0;
+        second = fmaxf(second, fminf(first, k));
+        first = fmaxf(first, k);
+      }
+    }
+    float run = first;
+    if (p.group_score == MAO_GROUP_TOP2 && second > -INFINITY) run += second;
+    const uint32_t ru = order_of(run);
+    int better = 0;
+    for (int h = 0; h < p.groups; ++h) {
+      const uint32_t o = __shfl_sync(FULL, ru, h);
+      better += (o > ru || (o == ru && h < lane)) ? 1 : 0;
+    }
+    const uint32_t kept = __ballot_sync(FULL, lane < p.groups && better < p.keep);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = 32 * i + lane;
+      if (e >= p.experts || !((kept >> (e / size)) & 1u)) u[i] = 0u;
+    }
+  }
+  int id = -1;  // lane j ends with the j-th choice
+  for (int j = 0; j < p.top_k; ++j) {
+    uint32_t best = 0u;
+    int at = 0x7FFFFFFF;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (u[i] > best) {
+        best = u[i];
+        at = 32 * i + lane;
+      }
+    const uint32_t top = __reduce_max_sync(FULL, best);
+    if (top == 0u) break;
+    const int e = __reduce_min_sync(FULL, best == top ? at : 0x7FFFFFFF);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (32 * i + lane == e) u[i] = 0u;
+    if (lane == j) id = e;
+  }
+  float w = id >= 0 ? score_sm[id] : 0.0f;
+  if (p.renorm) w = w / (warp_sum(w) + 1e-20f);
+  if (lane < p.top_k) {
+    p.weights[t * p.top_k + lane] = id >= 0 ? p.scale * w : 0.0f;
+    p.ids[t * p.top_k + lane] = id;
+  }
+}
+
+// The logits' gradient of one token per warp; the chosen experts' ds go through shared
+// memory to the lanes that hold their logits.
+template <int VPL>
+__global__ void __launch_bounds__(32 * ROUTE_WARPS) route_back_kernel(const RouteBackParams p) {
+  extern __shared__ float sm[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = int64_t(blockIdx.x) * ROUTE_WARPS + warp;
+  if (t >= p.tokens) return;
+  float* score_sm = sm + warp * 2 * 32 * VPL;
+  float* ds_sm = score_sm + 32 * VPL;
+  float x[VPL], s[VPL];
+  load_logits<VPL>(p.logits, t, p.ld, p.dtype, p.experts, lane, x);
+  scores_of<VPL>(x, p.score, s);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    score_sm[32 * i + lane] = s[i];
+    ds_sm[32 * i + lane] = 0.0f;
+  }
+  __syncwarp();
+  int id = lane < p.top_k ? p.ids[t * p.top_k + lane] : -1;
+  if (id >= p.experts) id = -1;
+  const float sj = id >= 0 ? score_sm[id] : 0.0f;
+  float ds = id >= 0 ? p.scale * p.dweights[t * p.top_k + lane] : 0.0f;
+  if (p.renorm) {
+    const float inv = 1.0f / (warp_sum(sj) + 1e-20f);
+    const float mean = warp_sum(ds * (sj * inv));
+    ds = id >= 0 ? (ds - mean) * inv : 0.0f;
+  }
+  // with renorm the weights do not change when all chosen scores grow alike: the sum is 0
+  const float dot = p.score == MAO_SCORE_SOFTMAX && !p.renorm ? warp_sum(ds * sj) : 0.0f;
+  if (id >= 0) ds_sm[id] = ds;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = 32 * i + lane;
+    if (e >= p.experts) continue;
+    float d = ds_sm[e];
+    if (p.score == MAO_SCORE_SIGMOID) {
+      const float q = expf(-fabsf(x[i])), r = 1.0f / (1.0f + q);
+      d *= q * r * r;  // s (1 - s)
+    } else {
+      d = s[i] * (d - dot);
+    }
+    store_elem(p.dlogits, t * p.dld + e, p.ddtype, x[i] == -INFINITY ? 0.0f : d);
+  }
+}
+
+template <typename P>
+using RouteFn = void (*)(const P);
+
+// The instantiation whose lanes hold at least experts / 32 logits each.
+template <typename P, template <int> class Pick>
+mao_status route_run(const P& p, cudaStream_t stream) {
+  if (p.tokens == 0) return MAO_OK;
+  const int vpl = int(ceil_div(p.experts, 32));
+  RouteFn<P> k;
+  int v;
+  if (vpl <= 2) k = Pick<2>::fn(), v = 2;
+  else if (vpl <= 4) k = Pick<4>::fn(), v = 4;
+  else if (vpl <= 8) k = Pick<8>::fn(), v = 8;
+  else if (vpl <= 16) k = Pick<16>::fn(), v = 16;
+  else k = Pick<32>::fn(), v = 32;
+  const size_t smem = size_t(ROUTE_WARPS) * 2 * 32 * v * sizeof(float);
+  k<<<unsigned(ceil_div(p.tokens, ROUTE_WARPS)), 32 * ROUTE_WARPS, smem, stream>>>(p);
+  count_launch();
+  return cuda_status(cudaGetLastError());
+}
+template <int V>
+struct PickRoute {
+  static RouteFn<RouteParams> fn() { return route_kernel<V>; }
+};
+template <int V>
+struct PickBack {
+  static RouteFn<RouteBackParams> fn() { return route_back_kernel<V>; }
+};
+
+// ------------------------------------------------------------------ places of the copies
+//
+// A counting sort of the copies by expert that keeps their order. Each block takes
+// PLAN_CHUNK copies: its warps count theirs per expert, 32 at a time (equal experts in a
+// warp find each other by match), which also ranks every copy within its warp. A copy's row
+// is the expert's offset plus the counts of the blocks and warps before it plus its rank.
+// Integer sums only: the result does not depend on the order in which blocks run.
+
+constexpr int PLAN_WARPS = 8;
+constexpr int PLAN_ROUNDS = 4;
+constexpr int PLAN_CHUNK = PLAN_WARPS * 32 * PLAN_ROUNDS;
+constexpr int PLAN_THREADS = 32 * PLAN_WARPS;
+constexpr int PLAN_MAX_EXPERTS = 1024;
+
+// Counts of this block's copies per warp and expert into cnt[PLAN_WARPS][experts] (zeroed
+// here), with each copy's expert and rank among its warp's copies of that expert.
+__device__ __forceinline__ void plan_count(const int32_t* ids, int64_t n, int experts, int* cnt,
+                                           int (&ex)[PLAN_ROUNDS], int (&rank)[PLAN_ROUNDS]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < PLAN_WARPS * experts; i += PLAN_THREADS) cnt[i] = 0;
+  __syncthreads();
+  const int64_t first = int64_t(blockIdx.x) * PLAN_CHUNK + warp * 32 * PLAN_ROUNDS + lane;
+#pragma unroll
+  for (int r = 0; r < PLAN_ROUNDS; ++r) {
+    const int64_t i = first + 32 * r;
+    const int e = i < n ? ids[i] : -1;
+    ex[r] = e >= 0 && e < experts ? e : -1;
+  }
+#pragma unroll
+  for (int r = 0; r < PLAN_ROUNDS; ++r) {
+    const uint32_t same = __match_any_sync(FULL, ex[r]);
+    int* c = cnt + warp * experts + (ex[r] < 0 ? 0 : ex[r]);
+    const int before = ex[r] < 0 ? 0 : *c;
+    rank[r] = before + __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
+    if (ex[r] >= 0 && (__ffs(same) - 1) == lane) *c = before + __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(PLAN_THREADS)
+    plan_count_kernel(const int32_t* ids, int64_t n, int experts, int32_t* block_counts,
+                      int32_t* slot_of, int64_t n_slots) {
+  extern __shared__ int cnt[];
+  int ex[PLAN_ROUNDS], rank[PLAN_ROUNDS];
+  plan_count(ids, n, experts, cnt, ex, rank);
+  for (int e = threadIdx.x; e < experts; e += PLAN_THREADS) {
+    int c = 0;
+#pragma unroll
+    for (int w = 0; w < PLAN_WARPS; ++w) c += cnt[w * experts + e];
+    block_counts[int64_t(blockIdx.x) * experts + e] = c;
+  }
+  const int64_t step = int64_t(gridDim.x) * PLAN_THREADS;
+  for (int64_t i = int64_t(blockIdx.x) * PLAN_THREADS + threadIdx.x; i < n_slots; i += step)
+    slot_of[i] = -1;
+}
+
+// block_counts == nullptr: the grid is one block, which also clears slot_of.
+__global__ void __launch_bounds__(PLAN_THREADS)
+    plan_place_kernel(const int32_t* ids, int64_t n, int experts, const int32_t* block_counts,
+                      int blocks, int32_t* counts, int32_t* offsets, int32_t* row_of,
+                      int32_t* slot_of, int64_t n_slots) {
+  extern __shared__ int cnt[];
+  __shared__ int warp_total[PLAN_WARPS];
+  int ex[PLAN_ROUNDS], rank[PLAN_ROUNDS];
+  if (!block_counts)
+    for (int64_t i = threadIdx.x; i < n_slots; i += PLAN_THREADS) slot_of[i] = -1;
+  plan_count(ids, n, experts, cnt, ex, rank);
+  // thread i owns experts PER i .. PER i + PER - 1
+  constexpr int PER = PLAN_MAX_EXPERTS / PLAN_THREADS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (experts + PLAN_THREADS - 1) / PLAN_THREADS;
+  int total[PER], before[PER], own = 0;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int e = int(threadIdx.x) * per + q;
+    total[q] = before[q] = 0;
+    if (q >= per || e >= experts) continue;
+    if (block_counts) {
+#pragma unroll 8
+      for (int b = 0; b < blocks; ++b) {
+        const int c = block_counts[int64_t(b) * experts + e];
+        total[q] += c;
+        before[q] += b < int(blockIdx.x) ? c : 0;
+      }
+    } else {
+#pragma unroll
+      for (int w = 0; w < PLAN_WARPS; ++w) total[q] += cnt[w * experts + e];
+    }
+    own += (total[q] + 127) & ~127;
+  }
+  int scan = own;  // inclusive over the warp, then over the warps
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(FULL, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) warp_total[warp] = scan;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) scan += warp_total[w];
+  int off = scan - own;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int e = int(threadIdx.x) * per + q;
+    if (q >= per || e >= experts) continue;
+    if (blockIdx.x == 0) {
+      counts[e] = total[q];
+      offsets[e] = off;
+      if (e == experts - 1) offsets[experts] = off + ((total[q] + 127) & ~127);
+    }
+    // the counts become the first row of each warp's copies
+    int at = off + before[q];
+#pragma unroll
+    for (int w = 0; w < PLAN_WARPS; ++w) {
+      const int c = cnt[w * experts + e];
+      cnt[w * experts + e] = at;
+      at += c;
+    }
+    off += (total[q] + 127) & ~127;
+  }
+  __syncthreads();
+  const int64_t first = int64_t(blockIdx.x) * PLAN_CHUNK + warp * 32 * PLAN_ROUNDS + lane;
+#pragma unroll
+  for (int r = 0; r < PLAN_ROUNDS; ++r) {
+    const int64_t i = first + 32 * r;
+    if (i >= n) continue;
+    const int row = ex[r] < 0 ? -1 : cnt[warp * experts + ex[r]] + rank[r];
+    row_of[i] = row;
+    if (row >= 0) slot_of[row] = int32_t(i);
+  }
+}
+
+// ------------------------------------------------------------------ combination
+
+// Eight columns from c on (VEC: one 16-byte load for bf16, two for fp32); columns from `cols`
+// on read as 0.
+template <bool VEC>
+__device__ __forceinline__ void load_cols(const void* base, int64_t row, int64_t ld, int dtype,
+                                          int64_t c, int64_t cols, float (&v)[8]) {
+  if (VEC) {
+    load8(base, row * ld + c, dtype, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? load_elem(base, row * ld + c + i, dtype) : 0.0f;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_cols(void* base, int64_t row, int64_t ld, int dtype,
+                                           int64_t c, int64_t cols, const float (&v)[8]) {
+  if (VEC) {
+    store8(base, row * ld + c, dtype, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < cols) store_elem(base, row * ld + c + i, dtype, v[i]);
+  }
+}
+
+struct CombineParams {
+  const void* z;
+  void* y;
+  const int32_t* row_of;
+  const float* weights;
+  int64_t zrows, cols, zld, yld, tokens;
+  int32_t zdt, ydt, top_k;
+};
+
+// Threads of a row own eight columns each; a block holds as many tokens as fit.
+template <bool VEC>
+__global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
+  const int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+  const int64_t c = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * 8;
+  if (t >= p.tokens || c >= p.cols) return;
+  float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int j = 0; j < p.top_k; ++j) {
+    const int64_t i = t * p.top_k + j;
+    const int32_t row = p.row_of[i];
+    if (row < 0 || row >= p.zrows) continue;
+    const float w = p.weights ? p.weights[i] : 1.0f;
+    float v[8];
+    load_cols<VEC>(p.z, row, p.zld, p.zdt, c, p.cols, v);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] = fmaf(w, v[q], acc[q]);
+  }
+  store_cols<VEC>(p.y, t, p.yld, p.ydt, c, p.cols, acc);
+}
+
+struct CombineBackParams {
+  const void* dy;
+  const void* z;
+  void* dz;
+  const int32_t* row_of;
+  const int32_t* slot_of;
+  const float* weights;
+  float* dweights;
+  int64_t rows, cols, dyld, zld, dzld, copies;
+  int32_t dydt, zdt, dzdt, top_k;
+};
+
+// One warp per row of Z: its copy's token gives dZ's row, and the dot product of the two rows
+// the copy's weight's gradient.
+template <bool VEC>
+__global__ void __launch_bounds__(256) combine_back_kernel(const CombineBackParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  if (p.dweights) {  // dropped copies have no row
+    const int64_t step = int64_t(gridDim.x) * blockDim.x;
+    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < p.copies; i += step) {
+      const int32_t at = p.row_of[i];
+      if (at < 0 || at >= p.rows) p.dweights[i] = 0.0f;
+    }
+  }
+  if (r >= p.rows) return;
+  const int64_t slot = p.slot_of[r];
+  const bool used = slot >= 0 && slot < p.copies;
+  const int64_t t = used ? slot / p.top_k : 0;
+  const float w = used ? (p.weights ? p.weights[slot] : 1.0f) : 0.0f;
+  float dot = 0.0f;
+#pragma unroll 2
+  for (int64_t c = lane * 8; c < p.cols; c += 256) {
+    float g[8], v[8];
+    if (used) {
+      load_cols<VEC>(p.dy, t, p.dyld, p.dydt, c, p.cols, g);
+      if (p.dweights) {
+        load_cols<VEC>(p.z, r, p.zld, p.zdt, c, p.cols, v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) dot = fmaf(g[q], v[q], dot);
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) g[q] *= w;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) g[q] = 0.0f;
+    }
+    store_cols<VEC>(p.dz, r, p.dzld, p.dzdt, c, p.cols, g);
+  }
+  if (!p.dweights || !used) return;
+  dot = warp_sum(dot);
+  if (lane == 0) p.dweights[slot] = dot;
+}
+
+}  // namespace
+
+mao_status route_launch(const RouteParams& p, cudaStream_t stream) {
+  return route_run<RouteParams, PickRoute>(p, stream);
+}
+
+mao_status route_backward_launch(const RouteBackParams& p, cudaStream_t stream) {
+  return route_run<RouteBackParams, PickBack>(p, stream);
+}
+
+size_t plan_workspace_size(int64_t n, int32_t experts) {
+  const int64_t blocks = ceil_div(n, PLAN_CHUNK);
+  return size_t(round_up((blocks > 1 ? blocks : 1) * experts * 4, 256));
+}
+
+mao_status plan_launch(const int32_t* ids, int64_t n, int32_t experts, int32_t* counts,
+                       int32_t* offsets, int32_t* row_of, int32_t* slot_of, int64_t n_slots,
+                       void* workspace, cudaStream_t stream) {
+  const int blocks = int(ceil_div(n, PLAN_CHUNK));
+  const size_t smem = size_t(PLAN_WARPS) * experts * sizeof(int);
+  int32_t* bc = nullptr;
+  if (blocks > 1) {
+    bc = static_cast<int32_t*>(workspace);
+    plan_count_kernel<<<blocks, PLAN_THREADS, smem, stream>>>(ids, n, experts, bc, slot_of, n_slots);
+    count_launch();
+  }
+  plan_place_kernel<<<blocks > 1 ? blocks : 1, PLAN_THREADS, smem, stream>>>(
+      ids, n, experts, bc, blocks, counts, offsets, row_of, slot_of, n_slots);
+  count_launch();
+  return cuda_status(cudaGetLastError());
+}
+
+mao_status combine_launch(const mao_mat& Z, const int32_t* row_of, const float* weights,
+                          int64_t tokens, int32_t top_k, const mao_mat& Y, cudaStream_t stream) {
+  if (tokens == 0) return MAO_OK;
+  const CombineParams p{Z.data, Y.data, row_of, weights, Z.rows, Y.cols, Z.ld, Y.ld, tokens,
+                        Z.dtype, Y.dtype, top_k};
+  const bool vec = vec8_ok(Z) && vec8_ok(Y);
+  int tx = 1;
+  while (tx < 256 && tx * 8 < Y.cols) tx *= 2;
+  const dim3 block(tx, 256 / tx);
+  const dim3 grid(unsigned(ceil_div(tokens, block.y)), unsigned(ceil_div(Y.cols, tx * 8)));
+  if (vec) combine_kernel<true><<<grid, block, 0, stream>>>(p);
+  else combine_kernel<false><<<grid, block, 0, stream>>>(p);
+  count_launch();
+  return cuda_status(cudaGetLastError());
+}
+
+mao_status combine_backward_launch(const mao_mat& dY, const mao_mat& Z, const int32_t* row_of,
+                                   const int32_t* slot_of, const float* weights, int32_t top_k,
+                                   const mao_mat& dZ, float* dweights, cudaStream_t stream) {
+  const int64_t copies = dY.rows * top_k;
+  if (Z.rows == 0 && (copies == 0 || !dweights)) return MAO_OK;
+  const CombineBackParams p{dY.data, Z.data, dZ.data, row_of, slot_of, weights, dweights, Z.rows,
+                            Z.cols, dY.ld, Z.ld, dZ.ld, copies, dY.dtype, Z.dtype, dZ.dtype, top_k};
+  const bool vec = vec8_ok(dY) && vec8_ok(Z) && vec8_ok(dZ);
+  const unsigned grid = unsigned(ceil_div(Z.rows > 0 ? Z.rows : 1, 8));
+  if (vec) combine_back_kernel<true><<<grid, 256, 0, stream>>>(p);
+  else combine_back_kernel<false><<<grid, 256, 0, stream>>>(p);
+  count_launch();
+  return cuda_status(cudaGetLastError());
+}
+
+}  // namespace mao
