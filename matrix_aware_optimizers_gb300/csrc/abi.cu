@@ -6,6 +6,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "experts.h"
 #include "internal.h"
 #include "ns_small.h"
 
@@ -371,8 +372,10 @@ mao_status mao_sync_status(void* stream) {
   const mao_status a = tc_read_and_clear_error(static_cast<cudaStream_t>(stream));
   const mao_status b = dion_read_and_clear_error(static_cast<cudaStream_t>(stream));
   const mao_status c = small_read_and_clear_error(static_cast<cudaStream_t>(stream));
-  if (a == MAO_ERR_CUDA || b == MAO_ERR_CUDA || c == MAO_ERR_CUDA) return MAO_ERR_CUDA;
-  return a != MAO_OK ? a : b != MAO_OK ? b : c;
+  const mao_status d = product_read_and_clear_error(static_cast<cudaStream_t>(stream));
+  if (a == MAO_ERR_CUDA || b == MAO_ERR_CUDA || c == MAO_ERR_CUDA || d == MAO_ERR_CUDA)
+    return MAO_ERR_CUDA;
+  return a != MAO_OK ? a : b != MAO_OK ? b : c != MAO_OK ? c : d;
 }
 
 int64_t mao_launch_count(void) { return g_launches.load(); }

@@ -52,5 +52,7 @@ mao_status quantize_launch(const mao_mat* X, int32_t batch, int64_t batch_stride
 mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, int32_t form,
                           const int32_t* offsets, int32_t groups, int32_t accumulate,
                           cudaStream_t stream);
+// Reads and clears the device error word of the product kernel (after a stream sync).
+mao_status product_read_and_clear_error(cudaStream_t stream);
 
 }  // namespace mao

@@ -167,6 +167,10 @@ struct TcParams {
 // 64, at most ld; -1 for ld) limits the columns read, later ones load as zeros.
 mao_status tc_encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t ld,
                          int64_t count, int64_t cols = -1);
+// Operand map of [count][rows][ld] 8-bit codes (ld a multiple of 16, the first cols of each
+// row; what lies outside reads as zeros): boxes of 128 columns x box_rows rows.
+mao_status tc_encode_code_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
+                              int64_t ld, int64_t count, int32_t box_rows);
 // Bulk-store map of a workspace output buffer [count][rows][ld] bf16 (64 x 32 blocks).
 // fp32 [count][rows][ld] for bulk stores of 32 x 32 blocks (128-byte swizzle)
 mao_status tc_encode_store_map_f32(CUtensorMap* map, const void* base, int64_t rows, int64_t ld,

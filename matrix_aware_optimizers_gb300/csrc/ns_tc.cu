@@ -54,10 +54,9 @@
 
 #include "common.cuh"
 #include "ns_plan.h"
+#include "tc_ptx.cuh"
 
 namespace mao {
-
-__device__ unsigned int g_tc_error;  // bit 0: a barrier wait timed out
 
 #ifdef MAO_TC_TRACE
 // Debug builds only: cycles the even CTA's roles spend waiting, summed over CTAs.
@@ -73,202 +72,7 @@ __device__ unsigned long long g_tc_trace[16];
 namespace {
 
 using namespace tc;
-
-// ----------------------------------------------------------------- PTX wrappers
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ uint64_t globaltimer() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-
-// Address of the same shared-memory location in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-
-// Arrive on a barrier of the leader CTA. The signal it carries (this warp's TMEM reads are
-// done) is ordered by tcgen05.fence::before_thread_sync, not by the arrive's memory
-// semantics, so the arrive keeps the default CTA-scope release: a cluster-scope release
-// would also wait for this thread's earlier global stores.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// The same test with cluster-scope acquire (for barriers the peer CTA arrives on).
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Non-blocking test of the same phase (no suspension inside the instruction).
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// The same non-blocking test with cluster-scope acquire.
-__device__ __forceinline__ bool mbar_test_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Waits for the phase of `parity` to complete. Gives up after `limit_ns` or when another
-// role raised the CTA's abort flag; a timeout sets the abort flag and the error word. A
-// limit of 0 gives up at once unless a non-blocking test finds the phase complete (each
-// try_wait may suspend the thread for a while, so polling alone could always succeed).
-template <bool CLUSTER = false>
-__device__ __noinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                       uint64_t limit_ns) {
-  auto test = [&]() {
-    return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
-  };
-  if (limit_ns == 0) {
-    if (mbar_test_wait(bar, parity)) return true;
-    *abort_flag = 1;
-    atomicOr(&g_tc_error, 1u);
-    return false;
-  }
-  if (test()) return true;
-  const uint64_t t0 = globaltimer();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (test()) return true;
-    if (*abort_flag) return false;
-    if (globaltimer() - t0 > limit_ns) {
-      *abort_flag = 1;
-      atomicOr(&g_tc_error, 1u);
-      return false;
-    }
-  }
-}
-
-// mbar_wait with its common case inline: a phase that is already complete costs one
-// non-blocking test and no call.
-template <bool CLUSTER = false>
-__device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity,
-                                               volatile int* abort_flag, uint64_t limit_ns) {
-  const bool done = CLUSTER ? mbar_test_wait_cluster(bar, parity) : mbar_test_wait(bar, parity);
-  return done || mbar_wait<CLUSTER>(bar, parity, abort_flag, limit_ns);
-}
-
-// Bounded wait used only while draining after an abort (ignores the abort flag).
-__device__ __noinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer() - t0 > limit_ns) return;
-  }
-}
-
-// TMA load into this CTA's shared memory, completing its bytes on a barrier that may live
-// in the peer CTA (cta_group::2 form).
-__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map,
-                                                 uint32_t bar_cluster, int32_t x, int32_t y,
-                                                 int32_t z, int32_t w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar_cluster)
-      : "memory");
-}
-
-// Bulk tensor store of a staged block (shared -> global) and its group bookkeeping.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x,
-                                             int32_t y, int32_t z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(x), "r"(y), "r"(z), "r"(src)
-      : "memory");
-}
-// Asks L2 to fetch the line holding `src` (through the load/store path: bulk prefetches
-// would queue in the TMA unit behind, or ahead of, the operand loads).
-__device__ __forceinline__ void prefetch_l2(const void* src) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(src) : "memory");
-}
-
-__device__ __forceinline__ void bulk_commit() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// Waits until every committed bulk store of this thread has read its shared-memory source.
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-// Waits until every committed bulk store of this thread is complete.
-__device__ __forceinline__ void bulk_wait_all() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-// Orders this thread's shared-memory writes before later async-proxy reads of them.
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
+using namespace ptx;
 
 // Shared-memory matrix descriptor: 128-byte swizzle, fixed version field 0b001 at bit 46.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -289,16 +93,6 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t adesc, 
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Arrives on the barrier at this shared-memory offset in every CTA of `mask` once all
-// products issued so far by this thread are complete.
-__device__ __forceinline__ void umma_commit_pair(uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(bar),
-      "h"(mask)
       : "memory");
 }
 
@@ -1344,6 +1138,21 @@ mao_status tc_encode_map(CUtensorMap* map, const void* base, int64_t rows, int64
   return r == CUDA_SUCCESS ? MAO_OK : MAO_ERR_UNSUPPORTED;
 }
 
+mao_status tc_encode_code_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
+                              int64_t ld, int64_t count, int32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return MAO_ERR_UNSUPPORTED;
+  const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(count)};
+  const cuuint64_t strides[2] = {cuuint64_t(ld), cuuint64_t(rows) * cuuint64_t(ld)};
+  const cuuint32_t box[3] = {128, cuuint32_t(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MAO_OK : MAO_ERR_UNSUPPORTED;
+}
+
 mao_status tc_encode_store_map_f32(CUtensorMap* map, const void* base, int64_t rows, int64_t ld,
                                    int64_t count) {
   auto fn = encode_fn();
@@ -1449,21 +1258,6 @@ extern "C" int mao_debug_tc_trace(unsigned long long* out, int reset) {
 }
 #endif
 
-mao_status tc_read_and_clear_error(cudaStream_t stream) {
-  unsigned int v = 0;
-  if (cudaMemcpyFromSymbolAsync(&v, g_tc_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) !=
-      cudaSuccess)
-    return MAO_ERR_CUDA;
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return MAO_ERR_CUDA;
-  if (v) {
-    const unsigned int zero = 0;
-    if (cudaMemcpyToSymbolAsync(g_tc_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice,
-                                stream) != cudaSuccess)
-      return MAO_ERR_CUDA;
-    if (cudaStreamSynchronize(stream) != cudaSuccess) return MAO_ERR_CUDA;
-    return MAO_ERR_TIMEOUT;
-  }
-  return MAO_OK;
-}
+mao_status tc_read_and_clear_error(cudaStream_t stream) { return read_and_clear_error(stream); }
 
 }  // namespace mao
