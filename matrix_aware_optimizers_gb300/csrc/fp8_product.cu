@@ -15,14 +15,14 @@
 // So the sums over all of K stay in the fp32 accumulator in TMEM, and nothing is rescaled on
 // the way.
 //
-// Roles per CTA (448 threads):
+// Roles per CTA (416 threads):
 //   warp 0        TMA producer: a 128 x 128 box of each operand per 128-deep block, into a
 //                 ring of 32 KB stages
 //   warp 1        TMEM allocation; in the even CTA one thread copies the scale words into TMEM
 //                 (tcgen05.cp) and issues the products
 //   warps 2..9    epilogue: two warps per 32-lane quadrant of TMEM; lane = i, so a row of D is
 //                 written by consecutive lanes
-//   warps 10..13  scales: gather the scale bytes of four blocks, from whichever layout they
+//   warps 10..12  scales: gather the scale bytes of four blocks, from whichever layout they
 //                 have, into the words that tcgen05.cp expects
 // TMEM (512 columns) holds two accumulators of 256 columns that share 32 of them (columns
 // 0..255 and 224..479) and two sets of scale words (480..503). The shared columns are drained
@@ -51,22 +51,28 @@ constexpr int BK = 128;                    // depth per stage
 constexpr int OP_BYTES = HALF * BK;        // one operand of a stage
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
 constexpr int STAGES = 6;
-constexpr int SF_SLOTS = 2;                // scale words in flight (four blocks each)
+constexpr int SF_SLOTS = 3;                // scale words in shared memory (four blocks each)
+constexpr int SF_SETS = 2;                 // and in TMEM
 constexpr int SF_BYTES = 3 * 512;          // 128 words of P, 256 of Q
 constexpr int MAX_GROUPS = 1024;
 constexpr int EPI_WARPS = 8;
-constexpr int SF_WARPS = 4;
+constexpr int SF_WARPS = SF_SLOTS;         // each fills its own slot
 constexpr int THREADS = 64 + 32 * (EPI_WARPS + SF_WARPS);
 constexpr int ACC1 = 224;                  // first column of the second accumulator
 constexpr int SHARED = TILE - ACC1;        // columns that both accumulators use
-constexpr int SF_COL = ACC1 + TILE;        // scale words: 12 columns per slot
+constexpr int SF_COL = ACC1 + TILE;        // scale words: 12 columns per set
 constexpr int SF_COLS = 12;
 constexpr int TMEM_COLS = 512;
 constexpr int BAND = 8;                    // tiles of j that share a pass over i
 constexpr size_t TABLE_BYTES = size_t(2) * (MAX_GROUPS + 2) * 4;
-constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + SF_SLOTS * SF_BYTES + TABLE_BYTES + 256;
+// bf16 output is staged: sixteen rows of D at 128 columns, two buffers for each half of the
+// epilogue's warps; the rows' pitch puts neighbouring rows in different banks
+constexpr int PITCH = 2 * HALF + 64;
+constexpr int STAGED = 16 * PITCH;
+constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + SF_SLOTS * SF_BYTES + 4 * STAGED +
+                        TABLE_BYTES + 256;
 static_assert(SMEM <= 232448, "shared memory budget of one CTA");
-static_assert(SF_COL + SF_SLOTS * SF_COLS <= TMEM_COLS, "TMEM budget");
+static_assert(SF_COL + SF_SETS * SF_COLS <= TMEM_COLS, "TMEM budget");
 
 struct ProductParams {
   CUtensorMap map_p, map_q;
@@ -80,7 +86,7 @@ struct ProductParams {
   int32_t I, J;             // D's columns; D's rows (of a group, for MAO_TN)
   int32_t depth;            // K (MAO_TN: the group's rows)
   int32_t sp_rows;          // rows of scales of one matrix of P
-  int32_t tiles_i, groups, form, dtype, accumulate, paired;
+  int32_t tiles_i, groups, form, dtype, accumulate, wide;
   unsigned long long timeout_ns;
 };
 
@@ -106,15 +112,34 @@ __device__ __forceinline__ uint32_t instr_desc(int p_mn, int q_mn, int n, int by
          (uint32_t(byte) << 29);
 }
 
-__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t p, uint64_t q, uint32_t idesc,
-                                           uint32_t sp, uint32_t sq, uint32_t accumulate) {
+// The four 32-deep products of a block, issued by the elected lane of a converged warp: the
+// operands' descriptors advance by dp and dq (in 16-byte units) from one to the next.
+__device__ __forceinline__ void mma_block(uint32_t elected, uint32_t d, uint64_t p, uint64_t q,
+                                          uint32_t dp, uint32_t dq, uint32_t idesc, uint32_t sp,
+                                          uint32_t sq, uint32_t accumulate) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    asm volatile(
+        "{\n\t.reg .pred a, e;\n\t"
+        "setp.ne.b32 a, %6, 0;\n\t"
+        "setp.ne.b32 e, %7, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, "
+        "[%4], [%5], a;\n\t}\n" ::"r"(d),
+        "l"(p + uint64_t(k) * dp), "l"(q + uint64_t(k) * dq), "r"(idesc), "r"(sp), "r"(sq),
+        "r"(k ? 1u : accumulate), "r"(elected)
+        : "memory");
+  }
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
   asm volatile(
-      "{\n\t.reg .pred a;\n\t"
-      "setp.ne.b32 a, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
-      "[%5], a;\n\t}\n" ::"r"(d),
-      "l"(p), "l"(q), "r"(idesc), "r"(sp), "r"(sq), "r"(accumulate)
-      : "memory");
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(e));
+  return e;
 }
 
 // 128 scale words (512 bytes of each CTA's shared memory) into four TMEM columns of both.
@@ -152,6 +177,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// A wait of a whole warp: true once every lane has seen the phase complete.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          uint64_t limit) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_fast<CLUSTER>(smem_u32(bar), parity, abort_flag, limit));
 }
 
 // ------------------------------------------------------------------ tiles
@@ -246,6 +278,16 @@ __device__ __forceinline__ void decode(const ProductParams& p, const int* lo, co
   t.n = t.nkb ? (t.j_end - t.j0 + 31) & ~31 : 0;
 }
 
+// The first tile from `tile` on (in steps) that multiplies anything.
+__device__ __forceinline__ int next_tile(const ProductParams& p, const int* lo, const int* begin,
+                                         int tile, int step, int total, Tile& t) {
+  for (; tile < total; tile += step) {
+    decode(p, lo, begin, tile, t);
+    if (t.nkb) break;
+  }
+  return tile;
+}
+
 // ------------------------------------------------------------------ scales
 
 // Four scale bytes down a column (stride ld), from block kb on; 1.0 past the last block.
@@ -307,29 +349,47 @@ __device__ __forceinline__ void store16(const ProductParams& p, const Tile& t, i
     return;
   }
   __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + row * p.ld + i;
-  if (p.accumulate || !p.paired) {
 #pragma unroll
-    for (int c = 0; c < 16; ++c)
-      if (in && j + c < t.j_end)
-        d[c * p.ld] = __float2bfloat16_rn(p.accumulate ? __bfloat162float(d[c * p.ld]) + v[c] : v[c]);
-    return;
-  }
+  for (int c = 0; c < 16; ++c)
+    if (in && j + c < t.j_end)
+      d[c * p.ld] = __float2bfloat16_rn(p.accumulate ? __bfloat162float(d[c * p.ld]) + v[c] : v[c]);
+}
+
+// The same for bf16 rows that take 16-byte stores, by the four warps that hold 128 columns i
+// (i0 is the first): they transpose their sixteen rows in `buf` and write whole 256-byte
+// pieces of rows. Between two uses of a buffer lies the other buffer's barrier.
+__device__ __forceinline__ void store16_wide(const ProductParams& p, const Tile& t, int j, int i0,
+                                             const float (&v)[16], uint8_t* buf, int quad, int part,
+                                             int lane) {
   // rows c and c + 1 of lanes 2 l and 2 l + 1: the even lane writes both columns of row c, the
   // odd lane both of row c + 1
   const int odd = lane & 1;
-  d += odd ? p.ld - 1 : 0;
+  uint8_t* s = buf + odd * PITCH + 2 * (32 * quad + lane - odd);
 #pragma unroll
   for (int c = 0; c < 16; c += 2) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(v[c], v[c + 1]);
     const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
     const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
-    const uint32_t both = odd ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
-    const int left = i - odd;
-    if (left < p.I && j + c + odd < t.j_end) {
-      if (left + 1 < p.I) *reinterpret_cast<uint32_t*>(d) = both;
-      else *reinterpret_cast<uint16_t*>(d) = uint16_t(both);
+    *reinterpret_cast<uint32_t*>(s + c * PITCH) = odd ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+  }
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
+  const int i = i0 + 8 * (lane & 15);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = 4 * quad + 2 * h + (lane >> 4);
+    if (j + c >= t.j_end || i >= p.I) continue;
+    const uint4 x = *reinterpret_cast<const uint4*>(buf + c * PITCH + 16 * (lane & 15));
+    int64_t row = j + c;
+    if (p.form == MAO_TN) row += int64_t(t.g) * p.J;
+    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + row * p.ld + i;
+    if (i + 8 <= p.I) {
+      *reinterpret_cast<uint4*>(d) = x;
+    } else {
+      const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (i + q < p.I) d[q] = e[q];
     }
-    d += 2 * p.ld;
   }
 }
 
@@ -342,9 +402,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem;
   uint8_t* sf = ring + STAGES * STAGE_BYTES;
-  int* lo = reinterpret_cast<int*>(sf + SF_SLOTS * SF_BYTES);
+  uint8_t* staging = sf + SF_SLOTS * SF_BYTES;
+  int* lo = reinterpret_cast<int*>(staging + 4 * STAGED);
   int* begin = lo + MAX_GROUPS + 2;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sf + SF_SLOTS * SF_BYTES + TABLE_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 4 * STAGED + TABLE_BYTES);
   uint64_t* full_bar = bars;                    // [STAGES]    (used in the even CTA)
   uint64_t* empty_bar = full_bar + STAGES;      // [STAGES]
   uint64_t* sf_full_bar = empty_bar + STAGES;   // [SF_SLOTS]  (used in the even CTA)
@@ -371,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&empty_bar[s]), 1);
     }
     for (int s = 0; s < SF_SLOTS; ++s) {
-      mbar_init(smem_u32(&sf_full_bar[s]), 2 * SF_WARPS);
+      mbar_init(smem_u32(&sf_full_bar[s]), 2);
       mbar_init(smem_u32(&sf_empty_bar[s]), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -455,76 +516,106 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (leader && lane == 0) {
-      int stage = 0, slot = 0, local = 0;
-      uint32_t phase = 0, sf_phase = 0;
-      bool ok = true, issued = false;
-      for (int tile = pair; ok && tile < total; tile += npairs) {
-        Tile t;
-        decode(p, lo, begin, tile, t);
-        if (t.nkb == 0) continue;
+    // The whole warp runs the loop, converged, so that descriptors stay in uniform registers;
+    // one lane issues.
+    if (leader) {
+      const uint32_t elected = elect_one();
+      const uint64_t p_desc = desc_of(smem_u32(ring), 16, 1024, 2);
+      const uint64_t q_desc = desc_of(smem_u32(ring) + OP_BYTES, 16, 1024, 2);
+      const uint64_t sf_desc = desc_of(smem_u32(sf), 16, 128, 0);
+      // per 32-deep slice: 32 bytes along the swizzled rows (K-major), or four 1024-byte atoms
+      // of eight k rows (MN-major)
+      const uint32_t dp = p_mn ? 4096 >> 4 : 32 >> 4, dq = q_mn ? 4096 >> 4 : 32 >> 4;
+      int stage = 0, local = 0;
+      uint32_t phase = 0;
+      bool ok = true, issued = false, started = false;
+      // Scale words: the slot of the blocks being multiplied (every three groups of blocks the
+      // phase flips), the set of TMEM columns that holds them, and the slot copied next.
+      int slot = 0, set = 0, copied = 0;
+      uint32_t copied_phase = 0, before_phase = 1;
+      int before = SF_SLOTS - 2;  // slot of the group two before the one copied next
+      auto copy_next = [&]() {
+        // the set's columns were last used two groups ago
+        if (!wait_warp<false>(&sf_empty_bar[before], before_phase, abort_flag, limit) ||
+            !wait_warp<true>(&sf_full_bar[copied], copied_phase, abort_flag, limit))
+          return false;
+        tc_fence_after();
+        const uint32_t dst = tmem_base + uint32_t(SF_COL + SF_COLS * (set ^ (started ? 1 : 0)));
+        const uint64_t src = sf_desc + uint64_t(copied * (SF_BYTES >> 4));
+        if (elected) {
+          copy_scales(dst, src);
+          copy_scales(dst + 4, src + (512 >> 4));
+          copy_scales(dst + 8, src + (1024 >> 4));
+        }
+        started = issued = true;
+        if (++copied == SF_SLOTS) {
+          copied = 0;
+          copied_phase ^= 1u;
+        }
+        if (++before == SF_SLOTS) {
+          before = 0;
+          before_phase ^= 1u;
+        }
+        return true;
+      };
+      Tile t, next;
+      int tile = next_tile(p, lo, begin, pair, npairs, total, t);
+      if (tile < total) ok = copy_next();
+      while (ok && tile < total) {
+        const int after = next_tile(p, lo, begin, tile + npairs, npairs, total, next);
         const int acc = local & 1;
         // the accumulator's last tile has been read, and of the tile before this one the
         // columns that the two share
-        if (!mbar_wait_fast<true>(smem_u32(&tempty_bar[acc]), (uint32_t(local >> 1) & 1u) ^ 1u,
-                                  abort_flag, limit) ||
-            !mbar_wait_fast<true>(smem_u32(&tshared_bar[acc ^ 1]),
-                                  (uint32_t((local + 1) >> 1) & 1u) ^ 1u, abort_flag, limit)) {
+        if (!wait_warp<true>(&tempty_bar[acc], (uint32_t(local >> 1) & 1u) ^ 1u, abort_flag, limit) ||
+            !wait_warp<true>(&tshared_bar[acc ^ 1], (uint32_t((local + 1) >> 1) & 1u) ^ 1u, abort_flag,
+                             limit)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem_base + uint32_t(acc * ACC1);
-        uint32_t tsf = 0;
+        const uint32_t idesc0 = instr_desc(p_mn, q_mn, t.n, 0);
         for (int kb = 0; kb < t.nkb; ++kb) {
-          if ((kb & 3) == 0) {
-            if (!mbar_wait_fast<true>(smem_u32(&sf_full_bar[slot]), sf_phase, abort_flag, limit)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            tsf = tmem_base + uint32_t(SF_COL + SF_COLS * slot);
-            const uint32_t src = smem_u32(sf + slot * SF_BYTES);
-            copy_scales(tsf, desc_of(src, 16, 128, 0));
-            copy_scales(tsf + 4, desc_of(src + 512, 16, 128, 0));
-            if (t.n > HALF) copy_scales(tsf + 8, desc_of(src + 1024, 16, 128, 0));
-            issued = true;
-          }
-          if (!mbar_wait_fast(smem_u32(&full_bar[stage]), phase, abort_flag, limit)) {
+          if (!wait_warp<false>(&full_bar[stage], phase, abort_flag, limit)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t ps = smem_u32(ring + stage * STAGE_BYTES), qs = ps + OP_BYTES;
-          const uint32_t idesc = instr_desc(p_mn, q_mn, t.n, kb & 3);
-#pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk) {
-            // K-major: 32 bytes along the swizzled rows; MN-major: four 1024-byte atoms of
-            // eight k rows
-            const uint64_t pd = desc_of(ps + (p_mn ? kk * 4096 : kk * 32), 16, 1024, 2);
-            const uint64_t qd = desc_of(qs + (q_mn ? kk * 4096 : kk * 32), 16, 1024, 2);
-            mma_scaled(d, pd, qd, idesc, tsf, tsf + 4, (kb | kk) != 0 ? 1u : 0u);
-          }
+          const uint32_t tsf = tmem_base + uint32_t(SF_COL + SF_COLS * set);
+          const uint64_t at = uint64_t(stage * (STAGE_BYTES >> 4));
+          mma_block(elected, d, p_desc + at, q_desc + at, dp, dq,
+                    idesc0 | uint32_t(kb & 3) << 4 | uint32_t(kb & 3) << 29, tsf, tsf + 4,
+                    kb != 0 ? 1u : 0u);
           issued = true;
-          umma_commit_pair(smem_u32(&empty_bar[stage]), 3);
-          if ((kb & 3) == 3 || kb + 1 == t.nkb) {
-            umma_commit_pair(smem_u32(&sf_empty_bar[slot]), 3);
-            if (++slot == SF_SLOTS) {
-              slot = 0;
-              sf_phase ^= 1u;
-            }
-          }
+          if (elected) umma_commit_pair(smem_u32(&empty_bar[stage]), 3);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
+          const bool last = (kb & 3) == 3 || kb + 1 == t.nkb;
+          // the next scale words follow two or three blocks behind the current ones: by then
+          // the slot's last products are done, and the copy is done before it is needed
+          if (((kb & 3) == 2 || (last && (kb & 3) < 2)) && ((kb | 3) + 1 < t.nkb || after < total)) {
+            if (!copy_next()) {
+              ok = false;
+              break;
+            }
+          }
+          if (last) {
+            if (elected) umma_commit_pair(smem_u32(&sf_empty_bar[slot]), 3);
+            if (++slot == SF_SLOTS) slot = 0;
+            set ^= 1;
+          }
         }
         if (!ok) break;
-        umma_commit_pair(smem_u32(&tfull_bar[acc]), 3);
+        if (elected) umma_commit_pair(smem_u32(&tfull_bar[acc]), 3);
         ++local;
+        tile = after;
+        t = next;
       }
       if (!ok && issued) {  // wait for everything in flight before TMEM is freed
-        umma_commit_pair(smem_u32(drain_bar), 1);
+        if (elected) umma_commit_pair(smem_u32(drain_bar), 1);
+        __syncwarp();
         mbar_drain(smem_u32(drain_bar), 0u, 1000000000ull);
       }
     }
@@ -552,9 +643,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       const int acc = local & 1;
       // every lane waits; the warp goes on only if all of them saw the accumulator
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait_fast(smem_u32(&tfull_bar[acc]), uint32_t(local >> 1) & 1u,
-                                                  abort_flag, limit)))
-        break;
+      if (!wait_warp<false>(&tfull_bar[acc], uint32_t(local >> 1) & 1u, abort_flag, limit)) break;
       tc_fence_after();
       const uint32_t trow = tmem_base + (uint32_t(32 * quad) << 16) + uint32_t(acc * ACC1);
       // this warp's 128 columns in eight steps: its half of the shared ones, then the others
@@ -574,39 +663,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(tempty[acc]);
         }
-        if (any) store16(p, t, t.j0 + c, i, v, lane);
+        if (!any) continue;
+        if (p.wide) store16_wide(p, t, t.j0 + c, i - 32 * quad - lane, v, staging + (2 * part + (s & 1)) * STAGED, quad, part, lane);
+        else store16(p, t, t.j0 + c, i, v, lane);
       }
       ++local;
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ scales (both CTAs)
-    const int r = (warp - 2 - EPI_WARPS) * 32 + lane;
-    const uint32_t at = uint32_t((r & 31) * 16 + (r >> 5) * 4);
-    int slot = 0;
+    // The warps take the groups of four blocks in turn, each into its own slot, so that one
+    // group's loads and its hand-over (a release to the other CTA) have the time of three
+    // groups' products.
+    const int slot = warp - 2 - EPI_WARPS;
+    Tile t;
+    int tile = next_tile(p, lo, begin, pair, npairs, total, t);
+    int kb = 0, turn = 0;
     uint32_t phase = 0;
-    bool ok = true;
-    for (int tile = pair; ok && tile < total; tile += npairs) {
-      Tile t;
-      decode(p, lo, begin, tile, t);
-      for (int kb = 0; kb < t.nkb; kb += 4) {
-        uint32_t w[3];
-        load_scales(p, t, int(cta), kb, r, w);
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_fast(smem_u32(&sf_empty_bar[slot]), phase ^ 1u,
-                                                    abort_flag, limit))) {
-          ok = false;
-          break;
-        }
-        uint8_t* dst = sf + slot * SF_BYTES + at;
+    while (tile < total) {
+      if (turn == slot) {
+        uint32_t w[4][3];
 #pragma unroll
-        for (int q = 0; q < 3; ++q) *reinterpret_cast<uint32_t*>(dst + 512 * q) = w[q];
+        for (int q = 0; q < 4; ++q) load_scales(p, t, int(cta), kb, 32 * q + lane, w[q]);
+        if (!wait_warp<false>(&sf_empty_bar[slot], phase ^ 1u, abort_flag, limit)) break;
+        // word r of 128: row r % 32 of 16 bytes, column r / 32
+        uint8_t* dst = sf + slot * SF_BYTES + 16 * lane;
+#pragma unroll
+        for (int h = 0; h < 3; ++h)
+          *reinterpret_cast<uint4*>(dst + 512 * h) = make_uint4(w[0][h], w[1][h], w[2][h], w[3][h]);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_release(mapa_shared(smem_u32(&sf_full_bar[slot]), 0));
-        if (++slot == SF_SLOTS) {
-          slot = 0;
-          phase ^= 1u;
-        }
+      }
+      if (++turn == SF_WARPS) {
+        turn = 0;
+        phase ^= 1u;
+      }
+      kb += 4;
+      if (kb >= t.nkb) {
+        kb = 0;
+        tile = next_tile(p, lo, begin, tile + npairs, npairs, total, t);
       }
     }
     __syncwarp();
@@ -661,7 +757,7 @@ mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, 
   p.form = form;
   p.dtype = D.dtype;
   p.accumulate = accumulate != 0;
-  p.paired = D.dtype == MAO_BF16 && reinterpret_cast<uintptr_t>(D.data) % 4 == 0 && D.ld % 2 == 0;
+  p.wide = D.dtype == MAO_BF16 && !accumulate && reinterpret_cast<uintptr_t>(D.data) % 16 == 0 && D.ld % 8 == 0;
   p.timeout_ns = wait_limit_ns();
   // tiles at most: every group may end in a part of one
   const int64_t tiles = (tn ? ceil_div(p.J, TILE) * groups : ceil_div(A.rows, TILE) + groups + 1) * p.tiles_i;
