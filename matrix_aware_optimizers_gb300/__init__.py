@@ -29,6 +29,7 @@ Functions (same names as the C ABI):
 """
 
 import ctypes
+import functools
 
 import torch
 
@@ -420,11 +421,19 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _raw_stream(stream, t):
+    """The stream's handle, or that of the stream current on t's device (these calls may be
+    as short as a kernel launch, so the handle is fetched without a Stream object)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
 def _dense_ptr(t, dtype, shape, name):
     """Device pointer of a contiguous tensor of the given type and shape (None: NULL)."""
     if t is None:
         return None
-    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s CUDA tensor of shape %s"
                          % (name, dtype, tuple(shape)))
     return t.data_ptr()
@@ -436,27 +445,35 @@ def _scale_shape(rows, cols, blocks):
     return -(-rows // br), -(-cols // bc)
 
 
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
 def _fp8(codes, scales, blocks, name):
     """MaoFp8 of a code tensor [R, C] or [B, R, C] and its scale bytes."""
-    if codes.dtype not in (torch.float8_e4m3fn, torch.uint8) or scales.dtype != torch.uint8:
+    shape, sshape = codes.shape, scales.shape
+    if codes.dtype not in _CODES or scales.dtype != torch.uint8:
         raise ValueError("%s: codes are float8_e4m3fn and scales uint8 tensors" % name)
-    if not codes.is_cuda or not scales.is_cuda or codes.dim() not in (2, 3) or \
-            scales.dim() != codes.dim() or codes.stride(-1) != 1 or scales.stride(-1) != 1:
-        raise ValueError("%s: CUDA tensors of two or three dimensions, unit column stride" % name)
-    rows, cols = codes.shape[-2], codes.shape[-1]
-    count = codes.shape[0] if codes.dim() == 3 else 1
+    if not codes.is_cuda or not scales.is_cuda or len(shape) not in (2, 3) or \
+            len(sshape) != len(shape):
+        raise ValueError("%s: CUDA tensors of two or three dimensions" % name)
+    rows, cols = shape[-2], shape[-1]
+    count = shape[0] if len(shape) == 3 else 1
     sr, sc = _scale_shape(rows, cols, blocks)
-    if tuple(scales.shape[-2:]) != (sr, sc) or (codes.dim() == 3 and scales.shape[0] != count):
+    if sshape[-2] != sr or sshape[-1] != sc or (len(shape) == 3 and sshape[0] != count):
         raise ValueError("%s: scales of shape %s do not fit %s blocks of %s"
-                         % (name, tuple(scales.shape), blocks, tuple(codes.shape)))
+                         % (name, tuple(sshape), blocks, tuple(shape)))
+    st, sst = codes.stride(), scales.stride()
+    if (st[-1] != 1 and cols > 1) or (sst[-1] != 1 and sc > 1):
+        raise ValueError("%s: expected unit column stride" % name)
     # the row stride of a single row may be anything
-    ld = codes.stride(-2) if rows > 1 or (count > 1 and rows == 1) else -(-cols // 16) * 16
-    sld = scales.stride(-2) if sr > 1 else sc
-    if codes.dim() == 3 and count > 1:
-        ld = codes.stride(0) // max(rows, 1) if rows else ld
-        sld = scales.stride(0) // max(sr, 1) if sr else sld
-        if codes.stride(0) != rows * ld or (rows > 1 and codes.stride(1) != ld) or \
-                scales.stride(0) != sr * sld or (sr > 1 and scales.stride(1) != sld):
+    ld = st[-2] if rows > 1 else -(-cols // 16) * 16
+    sld = sst[-2] if sr > 1 else sc
+    if count > 1 and rows:
+        if rows == 1:
+            ld = st[0]
+        if sr == 1:
+            sld = sst[0]
+        if st[0] != rows * ld or sst[0] != sr * sld:
             raise ValueError("%s: stacked matrices follow each other without gaps" % name)
     return _abi.MaoFp8(codes.data_ptr(), scales.data_ptr(), rows, cols, ld, sld, count,
                        _BLOCKS[blocks])
@@ -504,21 +521,25 @@ def fp8_quantize(X, blocks, rows=None, copies=1, out=None, stream=None):
         n_index = R = rows.numel()
         index = _dense_ptr(rows, torch.int32, rows.shape, "rows")
     kinds = ("row", "col") if blocks == "both" else (blocks,)
+    desc = {"row": None, "col": None, "tile": None}
     if out is None:
-        out, wide = [], -(-C // 16) * 16
+        out, wide, dev = [], -(-C // 16) * 16, x0.device
+        lead = (batch,) if stacked else ()
         for k in kinds:
-            lead = (batch,) if stacked else ()
-            codes = _empty(lead + (R, wide), torch.float8_e4m3fn, x0.device, stream)
-            out += [codes if wide == C else codes[..., :C],
-                    _empty(lead + _scale_shape(R, C, k), torch.uint8, x0.device, stream)]
-    if len(out) != 2 * len(kinds):
-        raise ValueError("out needs codes and scales for each kind of blocks")
-    desc = {}
-    for i, k in enumerate(kinds):
-        desc[k] = ctypes.byref(_fp8(out[2 * i], out[2 * i + 1], k, k))
+            codes = _empty(lead + (R, wide), torch.float8_e4m3fn, dev, stream)
+            sshape = _scale_shape(R, C, k)
+            scales = _empty(lead + sshape, torch.uint8, dev, stream)
+            desc[k] = ctypes.byref(_abi.MaoFp8(codes.data_ptr(), scales.data_ptr(), R, C, wide,
+                                               sshape[1], batch, _BLOCKS[k]))
+            out += [codes if wide == C else codes[..., :C], scales]
+    else:
+        if len(out) != 2 * len(kinds):
+            raise ValueError("out needs codes and scales for each kind of blocks")
+        for i, k in enumerate(kinds):
+            desc[k] = ctypes.byref(_fp8(out[2 * i], out[2 * i + 1], k, k))
     st = lib().fp8_quantize(mats, batch, stride, index, n_index,
-                            int(copies) if rows is not None else 0, desc.get("row"),
-                            desc.get("col"), desc.get("tile"), _stream(stream))
+                            int(copies) if rows is not None else 0, desc["row"], desc["col"],
+                            desc["tile"], _raw_stream(stream, x0))
     _abi.check("fp8_quantize", st)
     return tuple(out)
 
@@ -561,7 +582,7 @@ def fp8_product(A, a_scales, B, b_scales, form, offsets=None, out=None, out_dtyp
             raise ValueError("the groups' matrices follow each other without gaps")
         d = out.as_strided((groups * a.cols, b.cols), (out.stride(1), out.stride(2)))
     st = lib().fp8_product(ctypes.byref(a), ctypes.byref(b), ctypes.byref(_mat(d)), _FORM[form],
-                           off, groups, int(bool(accumulate)), _stream(stream))
+                           off, groups, int(bool(accumulate)), _raw_stream(stream, A))
     _abi.check("fp8_product", st)
     return out
 
@@ -587,7 +608,7 @@ def expert_route(logits, top_k, score="softmax", bias=None, groups=1, keep_group
         int(groups), int(groups if keep_groups is None else keep_groups),
         _GROUP_SCORE[group_score], int(bool(renorm)), float(scale),
         _dense_ptr(weights, torch.float32, (T, top_k), "weights"),
-        _dense_ptr(ids, torch.int32, (T, top_k), "ids"), _stream(stream))
+        _dense_ptr(ids, torch.int32, (T, top_k), "ids"), _raw_stream(stream, logits))
     _abi.check("expert_route", st)
     return weights, ids
 
@@ -605,7 +626,7 @@ def expert_route_backward(logits, ids, dweights, score="softmax", renorm=True, s
     st = lib().expert_route_backward(
         ctypes.byref(m), _dense_ptr(ids, torch.int32, (m.rows, k), "ids"),
         _dense_ptr(dweights, torch.float32, (m.rows, k), "dweights"), k, _SCORE[score],
-        int(bool(renorm)), float(scale), ctypes.byref(_mat(dlogits)), _stream(stream))
+        int(bool(renorm)), float(scale), ctypes.byref(_mat(dlogits)), _raw_stream(stream, logits))
     _abi.check("expert_route_backward", st)
     return dlogits
 
@@ -625,30 +646,33 @@ class ExpertPlan:
         self.counts, self.offsets, self.row_of, self.slot_of = counts, offsets, row_of, slot_of
 
 
+@functools.lru_cache(maxsize=256)
+def _plan_sizes(n, experts):
+    """(rows, workspace bytes) of a plan."""
+    nb = lib().expert_plan_workspace_bytes(n, experts)
+    if nb == 0:
+        raise ValueError("expert_plan takes up to 2^27 copies and 1 to 1024 experts")
+    return expert_rows(n, experts), nb
+
+
 def expert_plan(ids, experts, ws=None, stream=None):
     """Places of the copies ids [T, top_k] (int32; entries outside 0 .. experts - 1 are dropped):
     each expert's copies, in the order of the tokens, in a run of rows that starts at a
     multiple of 128. Returns an ExpertPlan."""
-    n = ids.numel()
+    n, experts, dev = ids.numel(), int(experts), ids.device
     p_ids = _dense_ptr(ids, torch.int32, ids.shape, "ids")
-    rows = expert_rows(n, experts)
-    nb = lib().expert_plan_workspace_bytes(n, int(experts))
-    if nb == 0:
-        raise ValueError("expert_plan takes up to 2^27 copies and 1 to 1024 experts")
-    # one allocation for the outputs and the workspace, each part 256-byte aligned
-    parts = [experts, experts + 1, n, rows, (nb + 3) // 4 if ws is None else 0]
-    at, total = [], 0
-    for c in parts:
-        at.append(total)
-        total += (c + 63) // 64 * 64
-    buf = _empty((total,), torch.int32, ids.device, stream)
-    counts, offsets, row_of, slot_of = (buf[a:a + c] for a, c in zip(at[:4], parts[:4]))
-    base = buf.data_ptr()
-    wptr, wbytes = (base + 4 * at[4], nb) if ws is None else (ws.data_ptr(), ws.numel())
-    st = lib().expert_plan(p_ids, n, int(experts), base, base + 4 * at[1], base + 4 * at[2],
-                           base + 4 * at[3], rows, wptr, wbytes, _stream(stream))
+    rows, nb = _plan_sizes(n, experts)
+    counts = _empty((experts,), torch.int32, dev, stream)
+    offsets = _empty((experts + 1,), torch.int32, dev, stream)
+    row_of = _empty(ids.shape, torch.int32, dev, stream)
+    slot_of = _empty((rows,), torch.int32, dev, stream)
+    if ws is None:
+        ws = _empty((nb,), torch.uint8, dev, stream)
+    st = lib().expert_plan(p_ids, n, experts, counts.data_ptr(), offsets.data_ptr(),
+                           row_of.data_ptr(), slot_of.data_ptr(), rows, ws.data_ptr(),
+                           ws.numel() * ws.element_size(), _raw_stream(stream, ids))
     _abi.check("expert_plan", st)
-    return ExpertPlan(counts, offsets, row_of.view(ids.shape), slot_of)
+    return ExpertPlan(counts, offsets, row_of, slot_of)
 
 
 def expert_combine(Z, row_of, weights=None, out=None, stream=None):
@@ -660,7 +684,7 @@ def expert_combine(Z, row_of, weights=None, out=None, stream=None):
     st = lib().expert_combine(
         ctypes.byref(_mat(Z)), _dense_ptr(row_of, torch.int32, (T, k), "row_of"),
         _dense_ptr(weights, torch.float32, (T, k), "weights"), T, k, ctypes.byref(_mat(out)),
-        _stream(stream))
+        _raw_stream(stream, Z))
     _abi.check("expert_combine", st)
     return out
 
@@ -681,7 +705,7 @@ def expert_combine_backward(dY, Z, row_of, slot_of, weights=None, dZ=None, dweig
         _dense_ptr(row_of, torch.int32, (T, k), "row_of"),
         _dense_ptr(slot_of, torch.int32, (Z.shape[0],), "slot_of"),
         _dense_ptr(weights, torch.float32, (T, k), "weights"), k, ctypes.byref(_mat(dZ)),
-        _dense_ptr(dweights, torch.float32, (T, k), "dweights"), _stream(stream))
+        _dense_ptr(dweights, torch.float32, (T, k), "dweights"), _raw_stream(stream, Z))
     _abi.check("expert_combine_backward", st)
     return dZ, dweights
 

@@ -56,6 +56,13 @@ int device_cc();
 
 // -------------------------------------------------------------- device helpers
 
+// A kernel launched as a programmatic dependent waits here for the previous one's results,
+// and lets the next one start its set-up.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 struct alignas(16) bf16x8 { __nv_bfloat162 h[4]; };
 
 __device__ __forceinline__ float load_elem(const void* p, int64_t idx, int32_t dt) {

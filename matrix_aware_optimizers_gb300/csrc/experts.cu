@@ -75,6 +75,7 @@ __device__ __forceinline__ void scores_of(const float (&x)[VPL], int score, floa
 template <int VPL>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_kernel(const RouteParams p) {
   extern __shared__ float sm[];
+  wait_for_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = int64_t(blockIdx.x) * ROUTE_WARPS + warp;
   if (t >= p.tokens) return;
@@ -156,6 +157,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_kernel(const RoutePara
 template <int VPL>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_back_kernel(const RouteBackParams p) {
   extern __shared__ float sm[];
+  wait_for_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = int64_t(blockIdx.x) * ROUTE_WARPS + warp;
   if (t >= p.tokens) return;
@@ -214,9 +216,7 @@ mao_status route_run(const P& p, cudaStream_t stream) {
   else if (vpl <= 16) k = Pick<16>::fn(), v = 16;
   else k = Pick<32>::fn(), v = 32;
   const size_t smem = size_t(ROUTE_WARPS) * 2 * 32 * v * sizeof(float);
-  k<<<unsigned(ceil_div(p.tokens, ROUTE_WARPS)), 32 * ROUTE_WARPS, smem, stream>>>(p);
-  count_launch();
-  return cuda_status(cudaGetLastError());
+  return launch_dependent(k, unsigned(ceil_div(p.tokens, ROUTE_WARPS)), 32 * ROUTE_WARPS, smem, stream, p);
 }
 template <int V>
 struct PickRoute {
@@ -268,34 +268,48 @@ __device__ __forceinline__ void plan_count(const int32_t* ids, int64_t n, int ex
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(PLAN_THREADS)
-    plan_count_kernel(const int32_t* ids, int64_t n, int experts, int32_t* block_counts,
-                      int32_t* slot_of, int64_t n_slots) {
+struct PlanParams {
+  const int32_t* ids;
+  int64_t n, n_slots;
+  int32_t experts, blocks;
+  int32_t* block_counts;
+  int32_t* counts;
+  int32_t* offsets;
+  int32_t* row_of;
+  int32_t* slot_of;
+};
+
+__global__ void __launch_bounds__(PLAN_THREADS) plan_count_kernel(const PlanParams p) {
   extern __shared__ int cnt[];
+  wait_for_previous();
+  const int experts = p.experts;
+  const int64_t n_slots = p.n_slots;
   int ex[PLAN_ROUNDS], rank[PLAN_ROUNDS];
-  plan_count(ids, n, experts, cnt, ex, rank);
+  plan_count(p.ids, p.n, experts, cnt, ex, rank);
   for (int e = threadIdx.x; e < experts; e += PLAN_THREADS) {
     int c = 0;
 #pragma unroll
     for (int w = 0; w < PLAN_WARPS; ++w) c += cnt[w * experts + e];
-    block_counts[int64_t(blockIdx.x) * experts + e] = c;
+    p.block_counts[int64_t(blockIdx.x) * experts + e] = c;
   }
   const int64_t step = int64_t(gridDim.x) * PLAN_THREADS;
   for (int64_t i = int64_t(blockIdx.x) * PLAN_THREADS + threadIdx.x; i < n_slots; i += step)
-    slot_of[i] = -1;
+    p.slot_of[i] = -1;
 }
 
 // block_counts == nullptr: the grid is one block, which also clears slot_of.
-__global__ void __launch_bounds__(PLAN_THREADS)
-    plan_place_kernel(const int32_t* ids, int64_t n, int experts, const int32_t* block_counts,
-                      int blocks, int32_t* counts, int32_t* offsets, int32_t* row_of,
-                      int32_t* slot_of, int64_t n_slots) {
+__global__ void __launch_bounds__(PLAN_THREADS) plan_place_kernel(const PlanParams p) {
   extern __shared__ int cnt[];
+  wait_for_previous();
+  const int experts = p.experts, blocks = p.blocks;
+  const int64_t n = p.n, n_slots = p.n_slots;
+  const int32_t* block_counts = p.block_counts;
+  int32_t* slot_of = p.slot_of;
   __shared__ int warp_total[PLAN_WARPS];
   int ex[PLAN_ROUNDS], rank[PLAN_ROUNDS];
   if (!block_counts)
     for (int64_t i = threadIdx.x; i < n_slots; i += PLAN_THREADS) slot_of[i] = -1;
-  plan_count(ids, n, experts, cnt, ex, rank);
+  plan_count(p.ids, p.n, experts, cnt, ex, rank);
   // thread i owns experts PER i .. PER i + PER - 1
   constexpr int PER = PLAN_MAX_EXPERTS / PLAN_THREADS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -334,9 +348,9 @@ __global__ void __launch_bounds__(PLAN_THREADS)
     const int e = int(threadIdx.x) * per + q;
     if (q >= per || e >= experts) continue;
     if (blockIdx.x == 0) {
-      counts[e] = total[q];
-      offsets[e] = off;
-      if (e == experts - 1) offsets[experts] = off + ((total[q] + 127) & ~127);
+      p.counts[e] = total[q];
+      p.offsets[e] = off;
+      if (e == experts - 1) p.offsets[experts] = off + ((total[q] + 127) & ~127);
     }
     // the counts become the first row of each warp's copies
     int at = off + before[q];
@@ -355,7 +369,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
     const int64_t i = first + 32 * r;
     if (i >= n) continue;
     const int row = ex[r] < 0 ? -1 : cnt[warp * experts + ex[r]] + rank[r];
-    row_of[i] = row;
+    p.row_of[i] = row;
     if (row >= 0) slot_of[row] = int32_t(i);
   }
 }
@@ -398,6 +412,7 @@ struct CombineParams {
 // Threads of a row own eight columns each; a block holds as many tokens as fit.
 template <bool VEC>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
+  wait_for_previous();
   const int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
   const int64_t c = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * 8;
   if (t >= p.tokens || c >= p.cols) return;
@@ -432,6 +447,7 @@ struct CombineBackParams {
 // the copy's weight's gradient.
 template <bool VEC>
 __global__ void __launch_bounds__(256) combine_back_kernel(const CombineBackParams p) {
+  wait_for_previous();
   const int lane = threadIdx.x & 31;
   const int64_t r = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   if (p.dweights) {  // dropped copies have no row
@@ -490,16 +506,13 @@ mao_status plan_launch(const int32_t* ids, int64_t n, int32_t experts, int32_t* 
                        void* workspace, cudaStream_t stream) {
   const int blocks = int(ceil_div(n, PLAN_CHUNK));
   const size_t smem = size_t(PLAN_WARPS) * experts * sizeof(int);
-  int32_t* bc = nullptr;
+  PlanParams p{ids, n, n_slots, experts, blocks, nullptr, counts, offsets, row_of, slot_of};
   if (blocks > 1) {
-    bc = static_cast<int32_t*>(workspace);
-    plan_count_kernel<<<blocks, PLAN_THREADS, smem, stream>>>(ids, n, experts, bc, slot_of, n_slots);
-    count_launch();
+    p.block_counts = static_cast<int32_t*>(workspace);
+    const mao_status st = launch_dependent(plan_count_kernel, blocks, PLAN_THREADS, smem, stream, p);
+    if (st != MAO_OK) return st;
   }
-  plan_place_kernel<<<blocks > 1 ? blocks : 1, PLAN_THREADS, smem, stream>>>(
-      ids, n, experts, bc, blocks, counts, offsets, row_of, slot_of, n_slots);
-  count_launch();
-  return cuda_status(cudaGetLastError());
+  return launch_dependent(plan_place_kernel, blocks > 1 ? blocks : 1, PLAN_THREADS, smem, stream, p);
 }
 
 mao_status combine_launch(const mao_mat& Z, const int32_t* row_of, const float* weights,
@@ -512,10 +525,7 @@ mao_status combine_launch(const mao_mat& Z, const int32_t* row_of, const float* 
   while (tx < 256 && tx * 8 < Y.cols) tx *= 2;
   const dim3 block(tx, 256 / tx);
   const dim3 grid(unsigned(ceil_div(tokens, block.y)), unsigned(ceil_div(Y.cols, tx * 8)));
-  if (vec) combine_kernel<true><<<grid, block, 0, stream>>>(p);
-  else combine_kernel<false><<<grid, block, 0, stream>>>(p);
-  count_launch();
-  return cuda_status(cudaGetLastError());
+  return launch_dependent(vec ? combine_kernel<true> : combine_kernel<false>, grid, block, 0, stream, p);
 }
 
 mao_status combine_backward_launch(const mao_mat& dY, const mao_mat& Z, const int32_t* row_of,
@@ -527,10 +537,7 @@ mao_status combine_backward_launch(const mao_mat& dY, const mao_mat& Z, const in
                             Z.cols, dY.ld, Z.ld, dZ.ld, copies, dY.dtype, Z.dtype, dZ.dtype, top_k};
   const bool vec = vec8_ok(dY) && vec8_ok(Z) && vec8_ok(dZ);
   const unsigned grid = unsigned(ceil_div(Z.rows > 0 ? Z.rows : 1, 8));
-  if (vec) combine_back_kernel<true><<<grid, 256, 0, stream>>>(p);
-  else combine_back_kernel<false><<<grid, 256, 0, stream>>>(p);
-  count_launch();
-  return cuda_status(cudaGetLastError());
+  return launch_dependent(vec ? combine_back_kernel<true> : combine_back_kernel<false>, grid, 256, 0, stream, p);
 }
 
 }  // namespace mao

@@ -75,7 +75,8 @@ static_assert(SMEM <= 232448, "shared memory budget of one CTA");
 static_assert(SF_COL + SF_SETS * SF_COLS <= TMEM_COLS, "TMEM budget");
 
 struct ProductParams {
-  CUtensorMap map_p, map_q;
+  CUtensorMap map_p;
+  CUtensorMap map_q[3];     // boxes of 128, 64 and 16 rows (MAO_TN: the first only)
   const uint8_t* sp;        // scales of P and Q
   const uint8_t* sq;
   const int32_t* offsets;
@@ -86,12 +87,13 @@ struct ProductParams {
   int32_t I, J;             // D's columns; D's rows (of a group, for MAO_TN)
   int32_t depth;            // K (MAO_TN: the group's rows)
   int32_t sp_rows;          // rows of scales of one matrix of P
-  int32_t tiles_i, groups, form, dtype, accumulate, wide;
+  int32_t tiles_i, groups, dtype, accumulate, wide;
+  int32_t sp_words, sq_words;  // scales allow 4-byte loads
   unsigned long long timeout_ns;
 };
 
 struct Tile {
-  int g;        // group
+  int g = 0;    // group
   int i0, j0;   // first i; first j (a row of D, or of the group's matrix)
   int j_end;    // rows of D in the tile end here
   int n;        // j computed (a multiple of 32), 0: the rows are only cleared
@@ -164,19 +166,25 @@ __device__ __forceinline__ void mbar_arrive_release(uint32_t cluster_addr) {
                : "memory");
 }
 
+// Sixteen columns of this thread's TMEM lane: the load is issued, and its registers may be
+// used after tmem_wait.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
       : "r"(taddr)
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+                 "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
 }
 
 // A wait of a whole warp: true once every lane has seen the phase complete.
@@ -190,9 +198,9 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 //
 // lo[g] (g <= groups) is the first row of group g, cut to 0 .. rows and made rising; lo[groups]
 // is where the rows without a group begin. begin[g] counts the tiles of j before group g
-// (MAO_NT, MAO_NN: of 256 rows each; MAO_TN: the same number for every group), begin[groups]
-// those before the rest and begin[groups + 1] all of them.
+// (MAO_NT, MAO_NN: of its rows; MAO_TN: the same number for every group), begin[groups] all.
 
+template <int FORM>
 __device__ __forceinline__ void make_table(const ProductParams& p, int* lo, int* begin) {
   const int tid = threadIdx.x;
   const int n = p.groups;
@@ -223,12 +231,10 @@ __device__ __forceinline__ void make_table(const ProductParams& p, int* lo, int*
     for (int base = 0; base <= n; base += 32) {
       const int g = base + tid;
       int c = 0;
-      if (p.form == MAO_TN) {
+      if (FORM == MAO_TN) {
         c = g < n ? (p.J + TILE - 1) / TILE : 0;
       } else if (g < n) {
         c = (lo[g + 1] - lo[g] + TILE - 1) / TILE;
-      } else if (g == n && !p.accumulate) {
-        c = (p.rows - lo[n] + TILE - 1) / TILE;
       }
       int s = c;
 #pragma unroll
@@ -239,50 +245,62 @@ __device__ __forceinline__ void make_table(const ProductParams& p, int* lo, int*
       if (g <= n) begin[g] = sum + s - c;
       sum += __shfl_sync(0xFFFFFFFFu, s, 31);
     }
-    if (tid == 0) begin[n + 1] = sum;
   }
   __syncthreads();
 }
 
+// The whole warp decodes: t.g is a group at or before the tile's (tiles come in rising order).
+template <int FORM>
 __device__ __forceinline__ void decode(const ProductParams& p, const int* lo, const int* begin,
                                        int tile, Tile& t) {
-  // the group whose tiles hold this one: the last with begin * tiles_i <= tile
-  int a = 0, b = p.groups;
-  while (a < b) {
-    const int m = (a + b + 1) >> 1;
-    if (begin[m] * p.tiles_i <= tile) a = m;
-    else b = m - 1;
+  // the last group with begin * tiles_i <= tile: the one whose tiles hold this one
+  const int lane = threadIdx.x & 31;
+  int a = t.g;
+  while (true) {
+    const int g = a + 1 + lane;
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, g >= p.groups || begin[g] * p.tiles_i > tile);
+    if (past) {
+      a += __ffs(past) - 1;
+      break;
+    }
+    a += 32;
   }
   t.g = a;
   const int count = begin[a + 1] - begin[a];
   int local = tile - begin[a] * p.tiles_i;
-  // bands of BAND tiles of j: within a band j runs fastest, then i, so that the pairs at work
-  // at one time share operand rows in both directions
-  const int band = local / (BAND * p.tiles_i);
-  local -= band * BAND * p.tiles_i;
-  const int nb = min(BAND, count - band * BAND);
-  const int jt = band * BAND + local % nb;
-  t.i0 = (local / nb) * TILE;
-  t.k0 = 0;
-  if (p.form == MAO_TN) {
+  if (FORM == MAO_TN) {
+    // i runs fastest: the pairs at work at one time write whole rows of a matrix
+    const int jt = local / p.tiles_i;
+    t.i0 = (local - jt * p.tiles_i) * TILE;
     t.j0 = jt * TILE;
     t.j_end = min(t.j0 + TILE, p.J);
     t.k0 = lo[a];
     t.nkb = (lo[a + 1] - lo[a] + BK - 1) / BK;
-  } else {
-    const int end = a < p.groups ? lo[a + 1] : p.rows;
-    t.j0 = lo[a] + jt * TILE;
-    t.j_end = min(t.j0 + TILE, end);
-    t.nkb = a < p.groups ? (p.depth + BK - 1) / BK : 0;
+    t.n = t.nkb ? (t.j_end - t.j0 + 31) & ~31 : 0;
+    return;
   }
+  // bands of BAND tiles of j: within a band j runs fastest, then i, so that the pairs at work
+  // at one time share operand rows in both directions
+  const int band = count > BAND ? local / (BAND * p.tiles_i) : 0;
+  local -= band * BAND * p.tiles_i;
+  const int nb = min(BAND, count - band * BAND);
+  // local / nb by a float product: exact below 2^21 (half a unit is kept to either side)
+  const int it = int((float(local) + 0.5f) * (1.0f / float(nb)));
+  const int jt = band * BAND + local - it * nb;
+  t.i0 = it * TILE;
+  t.k0 = 0;
+  t.j0 = lo[a] + jt * TILE;
+  t.j_end = min(t.j0 + TILE, lo[a + 1]);
+  t.nkb = (p.depth + BK - 1) / BK;
   t.n = t.nkb ? (t.j_end - t.j0 + 31) & ~31 : 0;
 }
 
 // The first tile from `tile` on (in steps) that multiplies anything.
+template <int FORM>
 __device__ __forceinline__ int next_tile(const ProductParams& p, const int* lo, const int* begin,
                                          int tile, int step, int total, Tile& t) {
   for (; tile < total; tile += step) {
-    decode(p, lo, begin, tile, t);
+    decode<FORM>(p, lo, begin, tile, t);
     if (t.nkb) break;
   }
   return tile;
@@ -290,51 +308,129 @@ __device__ __forceinline__ int next_tile(const ProductParams& p, const int* lo, 
 
 // ------------------------------------------------------------------ scales
 
-// Four scale bytes down a column (stride ld), from block kb on; 1.0 past the last block.
-__device__ __forceinline__ uint32_t bytes_down(const uint8_t* s, int64_t ld, int kb, int nkb) {
-  uint32_t w = 0x7F7F7F7Fu;
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    if (kb + q < nkb) w = (w & ~(0xFFu << (8 * q))) | (uint32_t(s[(kb + q) * ld]) << (8 * q));
-  return w;
-}
-// Four consecutive scale bytes of a row.
-__device__ __forceinline__ uint32_t bytes_along(const uint8_t* s, int kb, int nkb) {
-  if (kb + 4 <= nkb && (reinterpret_cast<uintptr_t>(s + kb) & 3) == 0)
-    return *reinterpret_cast<const uint32_t*>(s + kb);
-  return bytes_down(s, 1, kb, nkb);
-}
+// The scale words of four blocks (from kb on) for 128 rows, row r as tcgen05.cp expects it: at
+// 16 (r % 32) + 4 (r / 32). Each lane of a warp gathers four words; the loads of a group are
+// all issued before the first is used. Blocks past the last and rows past `n` get 1.0 (they
+// meet zeros, or outputs that are not stored).
+constexpr uint32_t ONES = 0x7F7F7F7Fu;
 
-// Words of thread r: row r of this CTA's half of P, rows r and r + 128 of Q.
-__device__ __forceinline__ void load_scales(const ProductParams& p, const Tile& t, int cta, int kb,
-                                            int r, uint32_t (&w)[3]) {
-  const int i = t.i0 + HALF * cta + r;
-  const int row0 = t.k0 / BK;  // MAO_TN: the group's first row of scales
-  if (p.form == MAO_TN) {
-    w[0] = i < p.I ? bytes_down(p.sp + int64_t(row0) * p.sp_ld + i, p.sp_ld, kb, t.nkb) : 0x7F7F7F7Fu;
-  } else {
-    const uint8_t* s = p.sp + int64_t(t.g) * p.sp_group;
-    w[0] = i >= p.I ? 0x7F7F7F7Fu
-           : p.form == MAO_NT ? bytes_along(s + int64_t(i / BK) * p.sp_ld, kb, t.nkb)
-                              : bytes_down(s + i / BK, p.sp_ld, kb, t.nkb);
-  }
+// Scales that run along the rows (one row of scales per row): row r's at s + r * ld. Lane l
+// holds rows l + 32 q.
+struct Along {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const uint8_t* s, int64_t ld, int n, int kb, int nkb,
+                                       bool words, int lane) {
+    if (words && kb + 4 <= nkb) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int j = t.j0 + HALF * h + r;
-    w[1 + h] = j >= t.j_end ? 0x7F7F7F7Fu
-               : p.form == MAO_TN ? bytes_down(p.sq + int64_t(row0) * p.sq_ld + j, p.sq_ld, kb, t.nkb)
-                                  : bytes_along(p.sq + int64_t(j) * p.sq_ld, kb, t.nkb);
+      for (int q = 0; q < 4; ++q) {
+        const int r = lane + 32 * q;
+        w[q] = r < n ? *reinterpret_cast<const uint32_t*>(s + r * ld + kb) : ONES;
+      }
+    } else {
+      uint32_t b[4][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = lane + 32 * q;
+          b[q][k] = r < n && kb + k < nkb ? s[r * ld + kb + k] : 0x7Fu;
+        }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[q] = b[q][0] | b[q][1] << 8 | b[q][2] << 16 | b[q][3] << 24;
+    }
   }
-}
+  __device__ __forceinline__ void store(uint8_t* dst, int lane) const {
+    *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// Scales that run across them (one row of scales per block): block k's at s + k * ld. Lane l
+// holds rows 4 l .. 4 l + 3, loaded four bytes of one block at a time and transposed.
+struct Across {
+  uint32_t w[4];  // by block until store
+  __device__ __forceinline__ void load(const uint8_t* s, int64_t ld, int n, int kb, int nkb,
+                                       bool words, int lane) {
+    const int r = 4 * lane;
+    if (words && r + 4 <= n) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = kb + k < nkb ? *reinterpret_cast<const uint32_t*>(s + (kb + k) * ld + r) : ONES;
+    } else {
+      uint32_t b[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          b[k][q] = r + q < n && kb + k < nkb ? s[(kb + k) * ld + r + q] : 0x7Fu;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = b[k][0] | b[k][1] << 8 | b[k][2] << 16 | b[k][3] << 24;
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* dst, int lane) const {
+    const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
+    const uint32_t c = __byte_perm(w[0], w[1], 0x7362), d = __byte_perm(w[2], w[3], 0x7362);
+    const uint32_t o[4] = {__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632),
+                           __byte_perm(c, d, 0x5410), __byte_perm(c, d, 0x7632)};
+    // rows 4 l + q: 16-byte rows (4 l + q) % 32, column l / 8
+    uint8_t* at = dst + 64 * (lane & 7) + 4 * (lane >> 3);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint32_t*>(at + 16 * q) = o[q];
+  }
+};
+
+// Scales of 128 x 128 tiles: the same word for all rows; block k's byte at s + k * step.
+struct Same {
+  uint32_t w;
+  __device__ __forceinline__ void load(const uint8_t* s, int64_t step, int n, int kb, int nkb, int lane) {
+    uint32_t b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) b[k] = n > 0 && kb + k < nkb ? s[(kb + k) * step] : 0x7Fu;
+    w = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+  }
+  __device__ __forceinline__ void store(uint8_t* dst, int lane) const {
+    *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(w, w, w, w);
+  }
+};
+
+// Scale words of a group of blocks: 128 rows of this CTA's half of P, 256 of Q.
+template <int FORM>
+struct Scales;
+template <>
+struct Scales<MAO_TN> {
+  Across p0, q0, q1;
+  __device__ __forceinline__ void load(const ProductParams& p, const Tile& t, int cta, int kb, int lane) {
+    const int row0 = t.k0 / BK, i = t.i0 + HALF * cta;  // the group's first row of scales
+    const uint8_t* sp = p.sp + row0 * p.sp_ld + i;
+    const uint8_t* sq = p.sq + row0 * p.sq_ld + t.j0;
+    p0.load(sp, p.sp_ld, p.I - i, kb, t.nkb, p.sp_words, lane);
+    q0.load(sq, p.sq_ld, t.j_end - t.j0, kb, t.nkb, p.sq_words, lane);
+    q1.load(sq + HALF, p.sq_ld, t.j_end - t.j0 - HALF, kb, t.nkb, p.sq_words, lane);
+  }
+};
+template <int FORM>
+struct Scales {
+  Same p0;
+  Along q0, q1;
+  __device__ __forceinline__ void load(const ProductParams& p, const Tile& t, int cta, int kb, int lane) {
+    const int i = t.i0 + HALF * cta;
+    const uint8_t* sp = p.sp + int64_t(t.g) * p.sp_group;
+    if (FORM == MAO_NT) p0.load(sp + int64_t(i / BK) * p.sp_ld, 1, p.I - i, kb, t.nkb, lane);
+    else p0.load(sp + i / BK, p.sp_ld, p.I - i, kb, t.nkb, lane);
+    const uint8_t* sq = p.sq + int64_t(t.j0) * p.sq_ld;
+    q0.load(sq, p.sq_ld, t.j_end - t.j0, kb, t.nkb, p.sq_words, lane);
+    q1.load(sq + HALF * p.sq_ld, p.sq_ld, t.j_end - t.j0 - HALF, kb, t.nkb, p.sq_words, lane);
+  }
+};
 
 // ------------------------------------------------------------------ output
 
 // Sixteen rows of D (from row j on, those below j_end) at column i of this lane.
+template <int FORM>
 __device__ __forceinline__ void store16(const ProductParams& p, const Tile& t, int j, int i,
                                         const float (&v)[16], int lane) {
   const bool in = i < p.I;
   int64_t row = j;
-  if (p.form == MAO_TN) row += int64_t(t.g) * p.J;
+  if (FORM == MAO_TN) row += int64_t(t.g) * p.J;
   if (p.dtype == MAO_F32) {
     float* d = static_cast<float*>(p.d) + row * p.ld + i;
     if (p.accumulate) {
@@ -344,7 +440,8 @@ __device__ __forceinline__ void store16(const ProductParams& p, const Tile& t, i
     } else {
 #pragma unroll
       for (int c = 0; c < 16; ++c)
-        if (in && j + c < t.j_end) d[c * p.ld] = v[c];
+        if (in && j + c < t.j_end)
+          asm volatile("st.global.L1::no_allocate.f32 [%0], %1;" ::"l"(d + c * p.ld), "f"(v[c]) : "memory");
     }
     return;
   }
@@ -358,6 +455,7 @@ __device__ __forceinline__ void store16(const ProductParams& p, const Tile& t, i
 // The same for bf16 rows that take 16-byte stores, by the four warps that hold 128 columns i
 // (i0 is the first): they transpose their sixteen rows in `buf` and write whole 256-byte
 // pieces of rows. Between two uses of a buffer lies the other buffer's barrier.
+template <int FORM>
 __device__ __forceinline__ void store16_wide(const ProductParams& p, const Tile& t, int j, int i0,
                                              const float (&v)[16], uint8_t* buf, int quad, int part,
                                              int lane) {
@@ -380,10 +478,12 @@ __device__ __forceinline__ void store16_wide(const ProductParams& p, const Tile&
     if (j + c >= t.j_end || i >= p.I) continue;
     const uint4 x = *reinterpret_cast<const uint4*>(buf + c * PITCH + 16 * (lane & 15));
     int64_t row = j + c;
-    if (p.form == MAO_TN) row += int64_t(t.g) * p.J;
+    if (FORM == MAO_TN) row += int64_t(t.g) * p.J;
     __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + row * p.ld + i;
     if (i + 8 <= p.I) {
-      *reinterpret_cast<uint4*>(d) = x;
+      asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(d), "r"(x.x),
+                   "r"(x.y), "r"(x.z), "r"(x.w)
+                   : "memory");
     } else {
       const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&x);
 #pragma unroll
@@ -393,8 +493,27 @@ __device__ __forceinline__ void store16_wide(const ProductParams& p, const Tile&
   }
 }
 
+// Clears columns i0 .. i0 + ni of rows j0 .. j1 of D, one row per turn of a warp.
+__device__ __forceinline__ void clear_rows(const ProductParams& p, int64_t j0, int64_t j1, int64_t step,
+                                           int i0, int ni, int lane) {
+  const int es = p.dtype == MAO_F32 ? 4 : 2;
+  uint8_t* base = static_cast<uint8_t*>(p.d) + int64_t(i0) * es;
+  const int bytes = ni * es;
+  const bool vec = reinterpret_cast<uintptr_t>(base) % 16 == 0 && p.ld * es % 16 == 0;
+  for (int64_t j = j0; j < j1; j += step) {
+    uint8_t* d = base + j * p.ld * es;
+    int done = 0;
+    if (vec) {
+      for (int b = 16 * lane; b + 16 <= bytes; b += 512) *reinterpret_cast<uint4*>(d + b) = make_uint4(0u, 0u, 0u, 0u);
+      done = bytes & ~15;
+    }
+    for (int b = done + 2 * lane; b < bytes; b += 64) *reinterpret_cast<uint16_t*>(d + b) = 0;
+  }
+}
+
 // ------------------------------------------------------------------ the kernel
 
+template <int FORM>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     product_kernel(const __grid_constant__ ProductParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -424,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int pair = blockIdx.x >> 1;
   const int npairs = gridDim.x >> 1;
   const uint64_t limit = p.timeout_ns;
-  const int p_mn = p.form != MAO_NT, q_mn = p.form == MAO_TN;
+  constexpr int p_mn = FORM != MAO_NT, q_mn = FORM == MAO_TN;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -453,11 +572,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   if (warp == 0 && lane < 2) {
-    const CUtensorMap* map = lane ? &p.map_q : &p.map_p;
+    const CUtensorMap* map = lane ? &p.map_q[0] : &p.map_p;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }
-  make_table(p, lo, begin);
-  const int total = begin[p.groups + 1] * p.tiles_i;
+  // launched as a programmatic dependent: the set-up so far may overlap the previous kernel
+  wait_for_previous();
+  make_table<FORM>(p, lo, begin);
+  const int total = begin[p.groups] * p.tiles_i;
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA arrival
@@ -466,42 +587,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
-    // lane 0 loads this CTA's half of P, lane 1 its half of Q: P's rows i0 + 128 cta .., and
-    // Q's rows j0 + n/2 cta .. (each CTA supplies half of the tile's n values of j)
+    // P's rows i0 + 128 cta .. and Q's rows j0 + n/2 cta .. (each CTA supplies half of the
+    // tile's n values of j). The whole warp runs the loop, converged; one lane issues.
+    const uint32_t elected = elect_one();
+    const uint32_t full0 = mapa_shared(smem_u32(full_bar), 0);
+    const uint32_t ring0 = smem_u32(ring);
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
     uint32_t armed = 0, armed_phase = 0;
+    Tile t;
     for (int tile = pair; ok && tile < total; tile += npairs) {
-      Tile t;
-      decode(p, lo, begin, tile, t);
-      const int mn = lane == 0 ? t.i0 + HALF * int(cta) : t.j0 + (t.n >> 1) * int(cta);
-      const int z = lane == 0 && p.form != MAO_TN ? t.g : 0;
-      const bool mn_major = lane == 0 ? p_mn : q_mn;
-      const CUtensorMap* map = lane == 0 ? &p.map_p : &p.map_q;
+      decode<FORM>(p, lo, begin, tile, t);
+      const int i = t.i0 + HALF * int(cta), j = t.j0 + (t.n >> 1) * int(cta);
+      const int z = FORM != MAO_TN ? t.g : 0;
+      // the smallest box that holds this CTA's n / 2 rows of Q
+      const int small = q_mn || t.n > HALF ? 0 : t.n > 32 ? 1 : 2;
+      const uint32_t q_bytes = small == 0 ? OP_BYTES : small == 1 ? OP_BYTES / 2 : OP_BYTES / 8;
       for (int kb = 0; kb < t.nkb; ++kb) {
-        int okw = 1;
-        if (lane == 0) {
-          if (!mbar_wait_fast(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, limit)) {
-            okw = 0;
-          } else if (leader) {
-            mbar_expect_tx(smem_u32(&full_bar[stage]), 2 * STAGE_BYTES);
-            armed |= 1u << stage;
-            armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-          }
-        }
-        okw = __shfl_sync(0xFFFFFFFFu, okw, 0);
-        if (!okw) {
+        if (!wait_warp<false>(&empty_bar[stage], phase ^ 1u, abort_flag, limit)) {
           ok = false;
           break;
         }
-        if (lane < 2) {
-          const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
-          const uint32_t dst = smem_u32(ring + stage * STAGE_BYTES) + (lane ? OP_BYTES : 0);
-          const int k = t.k0 + kb * BK;
-          if (mn_major) tma_load_3d_pair(dst, map, fb, mn, k, z);
-          else tma_load_3d_pair(dst, map, fb, k, mn, z);
+        const uint32_t fb = full0 + 8 * stage, dst = ring0 + stage * STAGE_BYTES;
+        const int k = t.k0 + kb * BK;
+        if (elected) {
+          if (leader) mbar_expect_tx(smem_u32(&full_bar[stage]), 2 * (OP_BYTES + q_bytes));
+          if (p_mn) tma_load_3d_pair(dst, &p.map_p, fb, i, k, z);
+          else tma_load_3d_pair(dst, &p.map_p, fb, k, i, z);
+          if (q_mn) tma_load_3d_pair(dst + OP_BYTES, &p.map_q[0], fb, j, k, 0);
+          else tma_load_3d_pair(dst + OP_BYTES, &p.map_q[small], fb, k, j, 0);
         }
+        armed |= 1u << stage;
+        armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -559,10 +677,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         return true;
       };
       Tile t, next;
-      int tile = next_tile(p, lo, begin, pair, npairs, total, t);
+      int tile = next_tile<FORM>(p, lo, begin, pair, npairs, total, t);
       if (tile < total) ok = copy_next();
       while (ok && tile < total) {
-        const int after = next_tile(p, lo, begin, tile + npairs, npairs, total, next);
+        const int after = next_tile<FORM>(p, lo, begin, tile + npairs, npairs, total, next);
         const int acc = local & 1;
         // the accumulator's last tile has been read, and of the tile before this one the
         // columns that the two share
@@ -628,17 +746,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                 mapa_shared(smem_u32(&tempty_bar[1]), 0)};
     const uint32_t tshared[2] = {mapa_shared(smem_u32(&tshared_bar[0]), 0),
                                  mapa_shared(smem_u32(&tshared_bar[1]), 0)};
-    int local = 0;
+    // rows past the last group are cleared while the first tiles are multiplied
+    if (FORM != MAO_TN && !p.accumulate)
+      clear_rows(p, lo[p.groups] + int64_t(blockIdx.x) * EPI_WARPS + warp - 2, p.rows,
+                 int64_t(gridDim.x) * EPI_WARPS, 0, p.I, lane);
+    int local = 0, buffer = 0;
+    Tile t;
     for (int tile = pair; tile < total; tile += npairs) {
-      Tile t;
-      decode(p, lo, begin, tile, t);
+      decode<FORM>(p, lo, begin, tile, t);
       const int i = t.i0 + HALF * int(cta) + 32 * quad + lane;
-      float v[16];
-      if (t.nkb == 0) {  // nothing was multiplied: D is cleared (or stays, when added to)
-        if (p.accumulate) continue;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) v[c] = 0.0f;
-        for (int c = 16 * part; c < t.j_end - t.j0; c += 32) store16(p, t, t.j0 + c, i, v, lane);
+      if (t.nkb == 0) {  // MAO_TN: an empty group's matrix is cleared (or stays, when added to)
+        const int64_t row = int64_t(t.g) * p.J;
+        const int i0 = t.i0 + HALF * int(cta);
+        if (!p.accumulate)
+          clear_rows(p, row + t.j0 + warp - 2, row + t.j_end, EPI_WARPS, i0, min(HALF, p.I - i0), lane);
         continue;
       }
       const int acc = local & 1;
@@ -649,23 +770,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // this warp's 128 columns in eight steps: its half of the shared ones, then the others
       const int shared0 = (acc ? 0 : ACC1) + 16 * part;
       const int rest0 = (acc ? SHARED : 0) + (ACC1 / 2) * part;
+      const int n = t.j_end - t.j0;
+      auto column = [&](int s) { return s == 0 ? shared0 : rest0 + 16 * (s - 1); };
+      auto out = [&](int s, const float(&v)[16]) {
+        const int c = column(s);
+        if (c >= n) return;
+        if (p.wide) {
+          store16_wide<FORM>(p, t, t.j0 + c, i - 32 * quad - lane, v, staging + (2 * part + buffer) * STAGED,
+                             quad, part, lane);
+          buffer ^= 1;
+        } else {
+          store16<FORM>(p, t, t.j0 + c, i, v, lane);
+        }
+      };
+      // a step's columns are loaded while the step before is stored
+      float va[16], vb[16];
+      if (column(0) < n) tmem_ld16(trow + uint32_t(column(0)), va);
 #pragma unroll 1
-      for (int s = 0; s < 8; ++s) {
-        const int c = s == 0 ? shared0 : rest0 + 16 * (s - 1);
-        const bool any = c < t.j_end - t.j0;
-        if (any) tmem_ld16(trow + uint32_t(c), v);
+      for (int s = 0; s < 8; s += 2) {
+        tmem_wait(va);
         if (s == 0) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(tshared[acc]);
-        } else if (s == 7) {
+        }
+        if (column(s + 1) < n) tmem_ld16(trow + uint32_t(column(s + 1)), vb);
+        out(s, va);
+        tmem_wait(vb);
+        if (s == 6) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(tempty[acc]);
+        } else if (column(s + 2) < n) {
+          tmem_ld16(trow + uint32_t(column(s + 2)), va);
         }
-        if (!any) continue;
-        if (p.wide) store16_wide(p, t, t.j0 + c, i - 32 * quad - lane, v, staging + (2 * part + (s & 1)) * STAGED, quad, part, lane);
-        else store16(p, t, t.j0 + c, i, v, lane);
+        out(s + 1, vb);
       }
       ++local;
     }
@@ -677,20 +816,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // groups' products.
     const int slot = warp - 2 - EPI_WARPS;
     Tile t;
-    int tile = next_tile(p, lo, begin, pair, npairs, total, t);
+    int tile = next_tile<FORM>(p, lo, begin, pair, npairs, total, t);
     int kb = 0, turn = 0;
     uint32_t phase = 0;
     while (tile < total) {
       if (turn == slot) {
-        uint32_t w[4][3];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) load_scales(p, t, int(cta), kb, 32 * q + lane, w[q]);
+        Scales<FORM> w;
+        w.load(p, t, int(cta), kb, lane);
         if (!wait_warp<false>(&sf_empty_bar[slot], phase ^ 1u, abort_flag, limit)) break;
-        // word r of 128: row r % 32 of 16 bytes, column r / 32
-        uint8_t* dst = sf + slot * SF_BYTES + 16 * lane;
-#pragma unroll
-        for (int h = 0; h < 3; ++h)
-          *reinterpret_cast<uint4*>(dst + 512 * h) = make_uint4(w[0][h], w[1][h], w[2][h], w[3][h]);
+        uint8_t* dst = sf + slot * SF_BYTES;
+        w.p0.store(dst, lane);
+        w.q0.store(dst + 512, lane);
+        w.q1.store(dst + 1024, lane);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_release(mapa_shared(smem_u32(&sf_full_bar[slot]), 0));
@@ -702,7 +839,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       kb += 4;
       if (kb >= t.nkb) {
         kb = 0;
-        tile = next_tile(p, lo, begin, tile + npairs, npairs, total, t);
+        tile = next_tile<FORM>(p, lo, begin, tile + npairs, npairs, total, t);
       }
     }
     __syncwarp();
@@ -738,7 +875,8 @@ mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, 
   }
   ProductParams p = {};
   mao_status st = tc_encode_code_map(&p.map_p, B.codes, B.cols, B.rows, B.ld, B.count, HALF);
-  if (st == MAO_OK) st = tc_encode_code_map(&p.map_q, A.codes, A.cols, A.rows, A.ld, 1, HALF);
+  for (int b = 0; b < (tn ? 1 : 3) && st == MAO_OK; ++b)
+    st = tc_encode_code_map(&p.map_q[b], A.codes, A.cols, A.rows, A.ld, 1, b == 0 ? HALF : b == 1 ? 64 : 16);
   if (st != MAO_OK) return st;
   p.sp = B.scales;
   p.sq = A.scales;
@@ -754,26 +892,30 @@ mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, 
   p.depth = int32_t(A.cols);
   p.tiles_i = int32_t(ceil_div(D.cols, TILE));
   p.groups = groups;
-  p.form = form;
   p.dtype = D.dtype;
   p.accumulate = accumulate != 0;
-  p.wide = D.dtype == MAO_BF16 && !accumulate && reinterpret_cast<uintptr_t>(D.data) % 16 == 0 && D.ld % 8 == 0;
+  p.wide = D.dtype == MAO_BF16 && !accumulate && reinterpret_cast<uintptr_t>(D.data) % 16 == 0 && D.ld * es % 16 == 0;
+  p.sp_words = reinterpret_cast<uintptr_t>(B.scales) % 4 == 0 && B.scale_ld % 4 == 0;
+  p.sq_words = reinterpret_cast<uintptr_t>(A.scales) % 4 == 0 && A.scale_ld % 4 == 0;
   p.timeout_ns = wait_limit_ns();
   // tiles at most: every group may end in a part of one
-  const int64_t tiles = (tn ? ceil_div(p.J, TILE) * groups : ceil_div(A.rows, TILE) + groups + 1) * p.tiles_i;
-  if (tiles > 0x7FFFFFFF || A.cols > 0x7FFFFFFF || B.cols > 0x7FFFFFFF) return MAO_ERR_UNSUPPORTED;
+  const int64_t tiles = (tn ? ceil_div(p.J, TILE) * groups : ceil_div(A.rows, TILE) + groups) * p.tiles_i;
+  if (tiles > 0x7FFFFFFF || p.tiles_i > (1 << 17) || A.cols > 0x7FFFFFFF || B.cols > 0x7FFFFFFF) return MAO_ERR_UNSUPPORTED;
   static std::once_flag once[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MAO_ERR_CUDA;
   cudaError_t attr = cudaSuccess;
+  using Kernel = void (*)(const ProductParams);
+  const Kernel kernels[3] = {product_kernel<MAO_NT>, product_kernel<MAO_NN>, product_kernel<MAO_TN>};
   std::call_once(once[dev & 63], [&] {
-    attr = cudaFuncSetAttribute(product_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM));
+    for (const Kernel k : kernels) {
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM));
+      if (e != cudaSuccess) attr = e;
+    }
   });
   if (attr != cudaSuccess) return MAO_ERR_CUDA;
   const int64_t pairs = tiles < num_sms() / 2 ? tiles : num_sms() / 2;
-  product_kernel<<<unsigned(2 * pairs), THREADS, SMEM, stream>>>(p);
-  count_launch();
-  return cuda_status(cudaGetLastError());
+  return launch_dependent(kernels[form], unsigned(2 * pairs), THREADS, SMEM, stream, p);
 }
 
 mao_status product_read_and_clear_error(cudaStream_t stream) { return read_and_clear_error(stream); }

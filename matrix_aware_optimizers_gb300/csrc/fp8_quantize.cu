@@ -113,6 +113,7 @@ template <bool BF16, bool ROW, bool COL, bool TILE>
 __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ QuantParams p) {
   __shared__ uint32_t part[8][128];
   __shared__ __align__(8) uint8_t col_byte[128];
+  wait_for_previous();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cg = tid & 15, rr = tid >> 4;  // columns 8 cg .., rows rr + 16 it
   const int tiles = p.row_tiles * p.col_tiles;
@@ -315,10 +316,10 @@ mao_status quantize_launch(const mao_mat* X, int32_t batch, int64_t batch_stride
         p.lds[i] = X[b + i].ld;
       }
     }
-    k<<<unsigned(int64_t(n) * rt * ct), 256, 0, stream>>>(p);
-    count_launch();
+    const mao_status st = launch_dependent(k, unsigned(int64_t(n) * rt * ct), 256, 0, stream, p);
+    if (st != MAO_OK) return st;
   }
-  return cuda_status(cudaGetLastError());
+  return MAO_OK;
 }
 
 }  // namespace mao

@@ -46,6 +46,26 @@ unsigned long long wait_limit_ns();
 
 // Launch accounting (every kernel launch of the library calls this once).
 void count_launch();
+
+// Launches a kernel that may start before the previous one in the stream has finished: it
+// begins with griddepcontrol.wait, before which it touches no global memory.
+template <typename P>
+mao_status launch_dependent(void (*kernel)(const P), dim3 grid, dim3 block, size_t smem,
+                            cudaStream_t stream, const P& params) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, params);
+  count_launch();
+  return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? MAO_OK : MAO_ERR_CUDA;
+}
 // Optional timing of launches (see mao_profile_begin); tag 0 = tensor-core product kernel,
 // other tags name the Dion CUDA-core kernels (mao_profile_end_tagged).
 void profile_before_launch(cudaStream_t stream, int tag = 0);
