@@ -14,8 +14,12 @@
 namespace mao {
 namespace {
 
-constexpr uint32_t FULL = 0xFFFFFFFFu;
+constexpr uint32_t FULL_MASK = 0xFFFFFFFFu;
 constexpr uint32_t INF_BITS = 0x7F800000u;
+constexpr int THREADS = 256;
+constexpr int IT = 2048 / THREADS;    // rows of a thread
+constexpr int STEP = THREADS / 16;    // apart
+constexpr int WARPS = THREADS / 32;
 constexpr int TABLE = 64;  // matrices of a descriptor array per launch
 
 struct Out {
@@ -55,51 +59,45 @@ template <bool BF16>
 struct Raw;
 template <>
 struct Raw<true> {
-  uint4 q;
-  __device__ void zero() { q = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ void load(const void* base, int64_t at) {
-    q = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(base) + at);
+  uint32_t w[4];
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  __device__ __forceinline__ void load(const void* at) {
+    const uint4 q = *reinterpret_cast<const uint4*>(at);
+    w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
   }
-  __device__ void load_some(const void* base, int64_t at, int n) {
+  __device__ __forceinline__ void load_some(const void* at, int n) {
     zero();
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    const uint16_t* s = reinterpret_cast<const uint16_t*>(base) + at;
+    const uint16_t* s = reinterpret_cast<const uint16_t*>(at);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < n) w[i >> 1] |= uint32_t(s[i]) << (16 * (i & 1));
-    q = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ uint32_t word(int i) const { return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w; }
-  __device__ float value(int i) const {
-    const uint32_t w = word(i >> 1);
-    return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
+  __device__ __forceinline__ float value(int i) const {
+    return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
   }
 };
 template <>
 struct Raw<false> {
-  uint4 q[2];
-  __device__ void zero() { q[0] = q[1] = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ void load(const void* base, int64_t at) {
-    const uint4* s = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(base) + at);
-    q[0] = s[0];
-    q[1] = s[1];
+  uint32_t w[8];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0u;
   }
-  __device__ void load_some(const void* base, int64_t at, int n) {
-    uint32_t w[8];
-    const uint32_t* s = reinterpret_cast<const uint32_t*>(base) + at;
+  __device__ __forceinline__ void load(const void* at) {
+    const uint4 a = reinterpret_cast<const uint4*>(at)[0], b = reinterpret_cast<const uint4*>(at)[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+  __device__ __forceinline__ void load_some(const void* at, int n) {
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(at);
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = i < n ? s[i] : 0u;
-    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    q[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
-  __device__ float value(int i) const {
-    const uint4& u = q[i >> 2];
-    return __uint_as_float((i & 3) == 0 ? u.x : (i & 3) == 1 ? u.y : (i & 3) == 2 ? u.z : u.w);
-  }
+  __device__ __forceinline__ float value(int i) const { return __uint_as_float(w[i]); }
 };
 
-// Magnitudes as ordered integers: NaN and infinities are the largest, or count as 0 with
-// FINITE. bf16 works on two values per word.
+// Magnitudes: fp32 as ordered integers; bf16 two to a word. NaN is above infinity, and both
+// above all numbers; with `finite` they count as 0 instead.
 __device__ __forceinline__ uint32_t mag(uint32_t bits, bool finite) {
   const uint32_t a = bits & 0x7FFFFFFFu;
   return finite && a >= INF_BITS ? 0u : a;
@@ -108,163 +106,241 @@ __device__ __forceinline__ uint32_t mag2(uint32_t w, bool finite) {
   const uint32_t a = w & 0x7FFF7FFFu;
   return finite ? a & ~__vcmpgeu2(a, 0x7F807F80u) : a;
 }
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
 
-template <bool BF16, bool ROW, bool COL, bool TILE>
-__global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ QuantParams p) {
-  __shared__ uint32_t part[8][128];
-  __shared__ __align__(8) uint8_t col_byte[128];
-  wait_for_previous();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int cg = tid & 15, rr = tid >> 4;  // columns 8 cg .., rows rr + 16 it
-  const int tiles = p.row_tiles * p.col_tiles;
-  const int z = int(blockIdx.x / unsigned(tiles));
-  const int in = int(blockIdx.x - unsigned(z) * unsigned(tiles));
-  const int rb = in / p.col_tiles, cb = in - rb * p.col_tiles;
-  const int64_t es = BF16 ? 2 : 4;
-  const void* base = p.stride ? static_cast<const uint8_t*>(p.base) + int64_t(z) * p.stride * es : p.ptr[z];
-  const int64_t ld = p.stride ? p.ld : p.lds[z];
-  const int64_t c0 = int64_t(cb) * 128 + 8 * cg;
-  const int nc = int(min(int64_t(8), p.cols - c0));  // columns of this thread (may be <= 0)
-  const bool vec = nc == 8 && (reinterpret_cast<uintptr_t>(base) % 16 == 0) && (ld * es) % 16 == 0;
+// Two products at a time.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&r);
+}
 
-  Raw<BF16> x[8];
+// The codes of eight entries scaled by inv; `bad`: some may not be finite.
+template <bool BF16>
+__device__ __forceinline__ uint2 encode(const Raw<BF16>& x, const float2 (&inv)[4], bool bad) {
+  float2 v[4];
 #pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    int64_t r = int64_t(rb) * 128 + 16 * it + rr;
-    bool have = r < p.rows && nc > 0;
-    if (have && p.index) {
-      const int32_t i = p.index[r];
-      r = i < 0 ? -1 : i / p.copies;
-      have = r >= 0 && r < p.src_rows;
+  for (int i = 0; i < 4; ++i) v[i] = mul2(make_float2(x.value(2 * i), x.value(2 * i + 1)), inv[i]);
+  if (bad) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!(fabsf(x.value(2 * i)) < INFINITY)) v[i].x = __uint_as_float(0x7FC00000u);
+      if (!(fabsf(x.value(2 * i + 1)) < INFINITY)) v[i].y = __uint_as_float(0x7FC00000u);
+    }
+  }
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = __nv_cvt_float2_to_fp8x2(v[i], __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+}
+
+// FULL: the whole tile lies inside the matrix and its rows take 16-byte loads.
+template <bool BF16, bool ROW, bool COL, bool TILE, bool FULL>
+__device__ __forceinline__ void quantize_tile(const QuantParams& p, int64_t matrix, int rb, int cb,
+                                              const uint8_t* base, int64_t ld, bool vec,
+                                              uint32_t (*part)[128], uint8_t* col_byte,
+                                              const int32_t* src) {
+  constexpr int ES = BF16 ? 2 : 4;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cg = tid & 15, rr = tid >> 4;  // columns 8 cg .., rows rr + STEP it
+  const int64_t c0 = int64_t(cb) * 128 + 8 * cg;
+  const int nc = FULL ? 8 : int(min(int64_t(8), p.cols - c0));  // columns here (may be <= 0)
+  const int nr = FULL ? 128 : int(min(int64_t(128), p.rows - int64_t(rb) * 128));
+
+  Raw<BF16> x[IT];
+  const uint8_t* at = base + (int64_t(rb) * 128 * ld + c0) * ES;
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int r = STEP * it + rr;
+    const uint8_t* a;
+    bool have = FULL || (r < nr && nc > 0);
+    if (src) {
+      const int32_t i = src[r];
+      have = have && i >= 0;
+      a = base + (int64_t(i) * ld + c0) * ES;
+    } else {
+      a = at + r * ld * ES;
     }
     if (!have) x[it].zero();
-    else if (vec) x[it].load(base, r * ld + c0);
-    else x[it].load_some(base, r * ld + c0, nc);
+    else if (FULL || (vec && nc == 8)) x[it].load(a);
+    else x[it].load_some(a, nc);
   }
 
-  uint32_t rmax[8];             // the thread's share of each row
-  uint32_t cmax[BF16 ? 4 : 8];  // and of each column (bf16: two per word)
+  // the thread's share of each row's and column's largest magnitude (bf16: of two rows or
+  // columns per word)
+  constexpr int NR = BF16 ? IT / 2 : IT, NC = BF16 ? 4 : 8;
+  uint32_t rmax[NR], cmax[NC];
   auto largest = [&](bool finite) {
-#pragma unroll
-    for (int i = 0; i < (BF16 ? 4 : 8); ++i) cmax[i] = 0u;
     uint32_t all = 0u;
 #pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      if constexpr (BF16) {
-        uint32_t m = 0u;
+    for (int i = 0; i < NC; ++i) cmax[i] = 0u;
+    if constexpr (BF16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t a = mag2(x[it].word(i), finite);
-          m = __vmaxu2(m, a);
-          if (COL) cmax[i] = __vmaxu2(cmax[i], a);
+      for (int h = 0; h < NR; ++h) {
+        uint32_t m[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t a[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i] = mag2(x[2 * h + q].w[i], finite);
+            if (COL) cmax[i] = max2(cmax[i], a[i]);
+          }
+          m[q] = max2(max2(a[0], a[1]), max2(a[2], a[3]));
         }
-        rmax[it] = max(m & 0xFFFF0000u, m << 16);
-      } else {
+        rmax[h] = max2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+        all = max2(all, rmax[h]);
+      }
+      return max(all & 0xFFFF0000u, all << 16);
+    } else {
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
         uint32_t m = 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t a = mag(__float_as_uint(x[it].value(i)), finite);
+          const uint32_t a = mag(x[it].w[i], finite);
           m = max(m, a);
           if (COL) cmax[i] = max(cmax[i], a);
         }
         rmax[it] = m;
+        all = max(all, m);
       }
-      all = max(all, rmax[it]);
+      return all;
     }
-    return all;
   };
   uint32_t all = largest(false);
   const bool bad = __syncthreads_or(all >= INF_BITS) != 0;  // a NaN or infinity in the tile
   if (bad) all = largest(true);
 
-  auto write = [&](const Out& o, int it, const float (&inv)[8]) {
-    const int64_t r = int64_t(rb) * 128 + 16 * it + rr;
-    if (r >= p.rows || nc <= 0) return;
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = x[it].value(i) * inv[i];
-    if (bad) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (!(fabsf(x[it].value(i)) < INFINITY)) v[i] = __uint_as_float(0x7FC00000u);
-    }
-    uint32_t w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      w[h] = uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(v[4 * h], v[4 * h + 1]), __NV_SATFINITE, __NV_E4M3)) |
-             uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(v[4 * h + 2], v[4 * h + 3]), __NV_SATFINITE, __NV_E4M3)) << 16;
-    uint8_t* d = o.codes + ((p.first + z) * p.rows + r) * o.ld + c0;
-    if (nc == 8) {
-      *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
+  const int64_t row0 = matrix * p.rows + int64_t(rb) * 128 + rr;  // of the stacked results
+  auto put = [&](uint8_t* d, uint2 c) {
+    if (FULL || nc == 8) {
+      *reinterpret_cast<uint2*>(d) = c;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < nc) d[i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
+        if (i < nc) d[i] = uint8_t((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
     }
   };
 
-  if constexpr (ROW) {
-#pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      uint32_t m = rmax[it];
-#pragma unroll
-      for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(FULL, m, o));
-      const int byte = scale_byte(m);
-      const float s = scale_inverse(byte);
-      const float inv[8] = {s, s, s, s, s, s, s, s};
-      write(p.row, it, inv);
-      const int64_t r = int64_t(rb) * 128 + 16 * it + rr;
-      if (cg == 0 && r < p.rows)
-        p.row.scales[((p.first + z) * p.rows + r) * p.row.scale_ld + cb] = uint8_t(byte);
-    }
-  }
+  float2 col_inv[4];
   if constexpr (COL) {
 #pragma unroll
-    for (int i = 0; i < (BF16 ? 4 : 8); ++i) {
+    for (int i = 0; i < NC; ++i) {
+      const uint32_t other = __shfl_xor_sync(FULL_MASK, cmax[i], 16);
       if constexpr (BF16) {
-        const uint32_t m = __vmaxu2(cmax[i], __shfl_xor_sync(FULL, cmax[i], 16));
+        const uint32_t m = max2(cmax[i], other);
         if (lane < 16) {
           part[warp][8 * cg + 2 * i] = m << 16;
           part[warp][8 * cg + 2 * i + 1] = m & 0xFFFF0000u;
         }
       } else {
-        const uint32_t m = max(cmax[i], __shfl_xor_sync(FULL, cmax[i], 16));
-        if (lane < 16) part[warp][8 * cg + i] = m;
+        if (lane < 16) part[warp][8 * cg + i] = max(cmax[i], other);
       }
     }
     __syncthreads();
     if (tid < 128) {
       uint32_t m = 0u;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) m = max(m, part[w][tid]);
+      for (int w = 0; w < WARPS; ++w) m = max(m, part[w][tid]);
       const int byte = scale_byte(m);
       col_byte[tid] = uint8_t(byte);
       const int64_t c = int64_t(cb) * 128 + tid;
-      if (c < p.cols)
-        p.col.scales[((p.first + z) * p.row_tiles + rb) * p.col.scale_ld + c] = uint8_t(byte);
+      if (FULL || c < p.cols) p.col.scales[(matrix * p.row_tiles + rb) * p.col.scale_ld + c] = uint8_t(byte);
     }
     __syncthreads();
     const uint2 b = *reinterpret_cast<const uint2*>(&col_byte[8 * cg]);
-    float inv[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) inv[i] = scale_inverse(((i < 4 ? b.x : b.y) >> (8 * (i & 3))) & 255u);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = (i < 2 ? b.x : b.y) >> (16 * (i & 1));
+      col_inv[i] = make_float2(scale_inverse(h & 255u), scale_inverse((h >> 8) & 255u));
+    }
+  }
+  if constexpr (ROW) {
 #pragma unroll
-    for (int it = 0; it < 8; ++it) write(p.col, it, inv);
+    for (int h = 0; h < NR; ++h)
+#pragma unroll
+      for (int o = 8; o; o >>= 1) {
+        const uint32_t other = __shfl_xor_sync(FULL_MASK, rmax[h], o);
+        rmax[h] = BF16 ? max2(rmax[h], other) : max(rmax[h], other);
+      }
+  }
+  if constexpr (ROW || COL) {
+    uint8_t* dr = p.row.codes + row0 * p.row.ld + c0;
+    uint8_t* dc = p.col.codes + row0 * p.col.ld + c0;
+    uint8_t* sc = p.row.scales + row0 * p.row.scale_ld + cb;
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      if (FULL || (STEP * it + rr < nr && nc > 0)) {
+        if (ROW) {
+          const uint32_t m = !BF16 ? rmax[it % NR] : (it & 1) ? rmax[it / 2] & 0xFFFF0000u : rmax[it / 2] << 16;
+          const int byte = scale_byte(m);
+          const float s = scale_inverse(byte);
+          const float2 inv[4] = {{s, s}, {s, s}, {s, s}, {s, s}};
+          put(dr, encode<BF16>(x[it], inv, bad));
+          if (cg == 0) *sc = uint8_t(byte);
+        }
+        if (COL) put(dc, encode<BF16>(x[it], col_inv, bad));
+      }
+      dr += STEP * p.row.ld;
+      dc += STEP * p.col.ld;
+      sc += STEP * p.row.scale_ld;
+    }
   }
   if constexpr (TILE) {
-    const uint32_t m = __reduce_max_sync(FULL, all);
+    const uint32_t m = __reduce_max_sync(FULL_MASK, all);
     if (lane == 0) part[warp][0] = m;
     __syncthreads();
     uint32_t t = 0u;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t = max(t, part[w][0]);
+    for (int w = 0; w < WARPS; ++w) t = max(t, part[w][0]);
     const int byte = scale_byte(t);
     const float s = scale_inverse(byte);
-    const float inv[8] = {s, s, s, s, s, s, s, s};
+    const float2 inv[4] = {{s, s}, {s, s}, {s, s}, {s, s}};
+    uint8_t* d = p.tile.codes + row0 * p.tile.ld + c0;
 #pragma unroll
-    for (int it = 0; it < 8; ++it) write(p.tile, it, inv);
-    if (tid == 0) p.tile.scales[((p.first + z) * p.row_tiles + rb) * p.tile.scale_ld + cb] = uint8_t(byte);
+    for (int it = 0; it < IT; ++it) {
+      if (FULL || (STEP * it + rr < nr && nc > 0)) put(d, encode<BF16>(x[it], inv, bad));
+      d += STEP * p.tile.ld;
+    }
+    if (tid == 0) p.tile.scales[(matrix * p.row_tiles + rb) * p.tile.scale_ld + cb] = uint8_t(byte);
   }
+}
+
+template <bool BF16, bool ROW, bool COL, bool TILE>
+__global__ void __launch_bounds__(THREADS, BF16 ? 4 : 2) quantize_kernel(const __grid_constant__ QuantParams p) {
+  __shared__ uint32_t part[WARPS][128];
+  __shared__ __align__(8) uint8_t col_byte[128];
+  __shared__ int32_t src[128];  // source rows of the tile, -1: zeros
+  wait_for_previous();
+  const unsigned tiles = unsigned(p.row_tiles) * unsigned(p.col_tiles);
+  const unsigned z = blockIdx.x / tiles, in = blockIdx.x - z * tiles;
+  const int rb = int(in / unsigned(p.col_tiles)), cb = int(in - unsigned(rb) * unsigned(p.col_tiles));
+  constexpr int ES = BF16 ? 2 : 4;
+  const uint8_t* base = static_cast<const uint8_t*>(p.stride ? p.base : p.ptr[z]);
+  if (p.stride) base += int64_t(z) * p.stride * ES;
+  const int64_t ld = p.stride ? p.ld : p.lds[z];
+  const bool vec = reinterpret_cast<uintptr_t>(base) % 16 == 0 && (ld * ES) % 16 == 0;
+  bool full = vec && int64_t(rb + 1) * 128 <= p.rows && int64_t(cb + 1) * 128 <= p.cols;
+  if (p.index) {
+    const int64_t r = int64_t(rb) * 128 + threadIdx.x;
+    if (threadIdx.x < 128) {
+      int32_t i = r < p.rows ? p.index[r] : -1;
+      if (i >= 0 && p.copies > 1) i /= p.copies;
+      src[threadIdx.x] = i < p.src_rows ? i : -1;
+    }
+    __syncthreads();
+  }
+  const int64_t matrix = p.first + z;
+  const int32_t* rows = p.index ? src : nullptr;
+  if (full) quantize_tile<BF16, ROW, COL, TILE, true>(p, matrix, rb, cb, base, ld, vec, part, col_byte, rows);
+  else quantize_tile<BF16, ROW, COL, TILE, false>(p, matrix, rb, cb, base, ld, vec, part, col_byte, rows);
 }
 
 Out out_of(const mao_fp8* m) {
@@ -316,7 +392,7 @@ mao_status quantize_launch(const mao_mat* X, int32_t batch, int64_t batch_stride
         p.lds[i] = X[b + i].ld;
       }
     }
-    const mao_status st = launch_dependent(k, unsigned(int64_t(n) * rt * ct), 256, 0, stream, p);
+    const mao_status st = launch_dependent(k, unsigned(int64_t(n) * rt * ct), THREADS, 0, stream, p);
     if (st != MAO_OK) return st;
   }
   return MAO_OK;
