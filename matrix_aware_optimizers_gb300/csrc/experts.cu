@@ -2,6 +2,8 @@
 // the combination of the experts' outputs, and the gradients.
 #include <cuda_bf16.h>
 
+#include <mutex>
+
 #include "common.cuh"
 #include "experts.h"
 #include "internal.h"
@@ -31,9 +33,8 @@ __device__ __forceinline__ uint32_t order_of(float key) {
 
 // ------------------------------------------------------------------ choice of experts
 //
-// One warp per token; lane l holds experts 32 i + l. The softmax is one maximum, one sum. The
-// top_k best are taken one by one: the lanes' best keys as ordered integers, one warp
-// maximum, and one warp minimum of the index among the lanes that hold it.
+// One warp per token; lane l holds experts 32 i + l. The softmax is one maximum, one sum. Keys
+// are compared as ordered integers.
 
 constexpr int ROUTE_WARPS = 4;
 
@@ -52,7 +53,7 @@ template <int VPL>
 __device__ __forceinline__ void scores_of(const float (&x)[VPL], int score, float (&p)[VPL]) {
   if (score == MAO_SCORE_SIGMOID) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) p[i] = 1.0f / (1.0f + expf(-x[i]));
+    for (int i = 0; i < VPL; ++i) p[i] = __fdividef(1.0f, 1.0f + expf(-x[i]));  // within 2 ulp
     return;
   }
   float m = -INFINITY;
@@ -70,6 +71,75 @@ __device__ __forceinline__ void scores_of(const float (&x)[VPL], int score, floa
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) p[i] *= inv;
+}
+
+// Lane j's j-th best key of the warp (its index, or -1 where none is left). At least top_k
+// lanes hold a key that is no smaller than the top_k-th largest of the lanes' largest keys, so
+// only keys from there on can be chosen: usually about top_k of them, which are ranked against
+// one another, one to a lane. With more than 32 (many ties) the best are taken one by one.
+// `scratch`: 64 words of shared memory.
+template <int VPL>
+__device__ __forceinline__ int best_of(uint32_t (&u)[VPL], int top_k, int lane, float* scratch) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) m = max(m, u[i]);
+  uint32_t least = 0u;
+  for (int j = 0; j < top_k; ++j) {
+    const uint32_t top = __reduce_max_sync(FULL, m);
+    if (top == 0u) {  // fewer than top_k lanes hold anything: every key counts
+      least = 1u;
+      break;
+    }
+    least = top;
+    if (m == top) m = 0u;
+  }
+  __syncwarp();
+  uint2* list = reinterpret_cast<uint2*>(scratch);
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const uint32_t who = __ballot_sync(FULL, u[i] >= least);
+    if (u[i] >= least) {
+      const int at = n + __popc(who & ((1u << lane) - 1u));
+      if (at < 32) list[at] = make_uint2(u[i], uint32_t(32 * i + lane));
+    }
+    n += __popc(who);
+  }
+  __syncwarp();
+  int id = -1;
+  if (n <= 32) {
+    // listed by rising index, so of equal keys the one listed first is better
+    const uint2 mine = lane < n ? list[lane] : make_uint2(0u, 0u);
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t o = __shfl_sync(FULL, mine.x, j);
+      rank += (o > mine.x || (o == mine.x && j < lane)) ? 1 : 0;
+    }
+    __syncwarp();
+    int* place = reinterpret_cast<int*>(scratch);
+    if (lane < n) place[rank] = int(mine.y);
+    __syncwarp();
+    if (lane < n && lane < top_k) id = place[lane];
+    return id;
+  }
+  for (int j = 0; j < top_k; ++j) {
+    uint32_t best = 0u;
+    int at = 0x7FFFFFFF;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (u[i] > best) {
+        best = u[i];
+        at = 32 * i + lane;
+      }
+    const uint32_t top = __reduce_max_sync(FULL, best);
+    if (top == 0u) break;
+    const int e = __reduce_min_sync(FULL, best == top ? at : 0x7FFFFFFF);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (32 * i + lane == e) u[i] = 0u;
+    if (lane == j) id = e;
+  }
+  return id;
 }
 
 template <int VPL>
@@ -98,52 +168,48 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_kernel(const RoutePara
   }
   __syncwarp();
   if (p.groups > 1) {
-    // lane g scores run g, starting at its own place so that the lanes' reads spread over
-    // the banks
+    // `per` lanes score a run together, each every per-th key from a place of its own, so
+    // that the lanes' reads spread over the banks
     const int size = p.experts / p.groups;
+    const int shift = 31 - __clz(32 / p.groups), per = 1 << shift;
+    const int g = lane >> shift, sub = lane & (per - 1);
     float first = -INFINITY, second = -INFINITY;
-    if (lane < p.groups) {
-      int at = lane % size;
-      for (int i = 0; i < size; ++i) {
-        const float k = key_sm[lane * size + at];
-        if (++at == size) at = 0;
+    if (g < p.groups) {
+      const int mine = (size - sub + per - 1) >> shift;  // keys of this lane
+      const float* run = key_sm + g * size + sub;
+      int at = g < mine ? g : 0;
+      for (int i = 0; i < mine; ++i) {
+        const float k = run[at << shift];
+        at = at + 1 == mine ? 0 : at + 1;
         second = fmaxf(second, fminf(first, k));
         first = fmaxf(first, k);
       }
     }
+    for (int o = per >> 1; o; o >>= 1) {
+      const float f = __shfl_xor_sync(FULL, first, o), s2 = __shfl_xor_sync(FULL, second, o);
+      second = fmaxf(fmaxf(second, s2), fminf(first, f));
+      first = fmaxf(first, f);
+    }
     float run = first;
     if (p.group_score == MAO_GROUP_TOP2 && second > -INFINITY) run += second;
     const uint32_t ru = order_of(run);
-    int better = 0;
+    int better = 0;  // runs ahead of run `lane`
+    const uint32_t my = __shfl_sync(FULL, ru, (lane << shift) & 31);
     for (int h = 0; h < p.groups; ++h) {
-      const uint32_t o = __shfl_sync(FULL, ru, h);
-      better += (o > ru || (o == ru && h < lane)) ? 1 : 0;
+      const uint32_t o = __shfl_sync(FULL, ru, h << shift);
+      better += (o > my || (o == my && h < lane)) ? 1 : 0;
     }
     const uint32_t kept = __ballot_sync(FULL, lane < p.groups && better < p.keep);
+    // e / size by a float product: exact, half a unit is kept to either side
+    const float inv = 1.0f / float(size);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = 32 * i + lane;
-      if (e >= p.experts || !((kept >> (e / size)) & 1u)) u[i] = 0u;
+      const int run = int((float(e) + 0.5f) * inv);
+      if (!((kept >> (run & 31)) & 1u)) u[i] = 0u;  // keys past the last expert are 0 already
     }
   }
-  int id = -1;  // lane j ends with the j-th choice
-  for (int j = 0; j < p.top_k; ++j) {
-    uint32_t best = 0u;
-    int at = 0x7FFFFFFF;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (u[i] > best) {
-        best = u[i];
-        at = 32 * i + lane;
-      }
-    const uint32_t top = __reduce_max_sync(FULL, best);
-    if (top == 0u) break;
-    const int e = __reduce_min_sync(FULL, best == top ? at : 0x7FFFFFFF);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (32 * i + lane == e) u[i] = 0u;
-    if (lane == j) id = e;
-  }
+  const int id = best_of<VPL>(u, p.top_k, lane, key_sm);  // lane j: the j-th choice
   float w = id >= 0 ? score_sm[id] : 0.0f;
   if (p.renorm) w = w / (warp_sum(w) + 1e-20f);
   if (lane < p.top_k) {
@@ -163,18 +229,30 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_back_kernel(const Rout
   if (t >= p.tokens) return;
   float* score_sm = sm + warp * 2 * 32 * VPL;
   float* ds_sm = score_sm + 32 * VPL;
-  float x[VPL], s[VPL];
-  load_logits<VPL>(p.logits, t, p.ld, p.dtype, p.experts, lane, x);
-  scores_of<VPL>(x, p.score, s);
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    score_sm[32 * i + lane] = s[i];
-    ds_sm[32 * i + lane] = 0.0f;
-  }
-  __syncwarp();
   int id = lane < p.top_k ? p.ids[t * p.top_k + lane] : -1;
   if (id >= p.experts) id = -1;
-  const float sj = id >= 0 ? score_sm[id] : 0.0f;
+  const bool sigmoid = p.score == MAO_SCORE_SIGMOID;
+  float s[VPL];
+  float sj = 0.0f, slope = 0.0f;  // score of this lane's chosen expert; sigmoid: s (1 - s)
+  if (sigmoid) {  // only the chosen experts' logits matter
+    if (id >= 0) {
+      const float x = load_elem(p.logits, t * p.ld + id, p.dtype);
+      const float q = expf(-fabsf(x)), r = 1.0f / (1.0f + q);
+      sj = x >= 0.0f ? r : q * r;
+      slope = x == -INFINITY ? 0.0f : q * r * r;
+    }
+  } else {
+    float x[VPL];
+    load_logits<VPL>(p.logits, t, p.ld, p.dtype, p.experts, lane, x);
+    scores_of<VPL>(x, p.score, s);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) score_sm[32 * i + lane] = s[i];
+    __syncwarp();
+    if (id >= 0) sj = score_sm[id];
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) ds_sm[32 * i + lane] = 0.0f;
+  __syncwarp();
   float ds = id >= 0 ? p.scale * p.dweights[t * p.top_k + lane] : 0.0f;
   if (p.renorm) {
     const float inv = 1.0f / (warp_sum(sj) + 1e-20f);
@@ -182,21 +260,16 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_back_kernel(const Rout
     ds = id >= 0 ? (ds - mean) * inv : 0.0f;
   }
   // with renorm the weights do not change when all chosen scores grow alike: the sum is 0
-  const float dot = p.score == MAO_SCORE_SOFTMAX && !p.renorm ? warp_sum(ds * sj) : 0.0f;
-  if (id >= 0) ds_sm[id] = ds;
+  const float dot = !sigmoid && !p.renorm ? warp_sum(ds * sj) : 0.0f;
+  if (id >= 0) ds_sm[id] = sigmoid ? ds * slope : ds;
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = 32 * i + lane;
     if (e >= p.experts) continue;
     float d = ds_sm[e];
-    if (p.score == MAO_SCORE_SIGMOID) {
-      const float q = expf(-fabsf(x[i])), r = 1.0f / (1.0f + q);
-      d *= q * r * r;  // s (1 - s)
-    } else {
-      d = s[i] * (d - dot);
-    }
-    store_elem(p.dlogits, t * p.dld + e, p.ddtype, x[i] == -INFINITY ? 0.0f : d);
+    if (!sigmoid) d = s[i] == 0.0f ? 0.0f : s[i] * (d - dot);  // a masked expert's score is 0
+    store_elem(p.dlogits, t * p.dld + e, p.ddtype, d);
   }
 }
 
@@ -235,8 +308,8 @@ struct PickBack {
 // is the expert's offset plus the counts of the blocks and warps before it plus its rank.
 // Integer sums only: the result does not depend on the order in which blocks run.
 
-constexpr int PLAN_WARPS = 8;
-constexpr int PLAN_ROUNDS = 4;
+constexpr int PLAN_WARPS = 16;
+constexpr int PLAN_ROUNDS = 8;
 constexpr int PLAN_CHUNK = PLAN_WARPS * 32 * PLAN_ROUNDS;
 constexpr int PLAN_THREADS = 32 * PLAN_WARPS;
 constexpr int PLAN_MAX_EXPERTS = 1024;
@@ -311,7 +384,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_place_kernel(const PlanPara
     for (int64_t i = threadIdx.x; i < n_slots; i += PLAN_THREADS) slot_of[i] = -1;
   plan_count(p.ids, p.n, experts, cnt, ex, rank);
   // thread i owns experts PER i .. PER i + PER - 1
-  constexpr int PER = PLAN_MAX_EXPERTS / PLAN_THREADS;
+  constexpr int PER = (PLAN_MAX_EXPERTS + PLAN_THREADS - 1) / PLAN_THREADS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (experts + PLAN_THREADS - 1) / PLAN_THREADS;
   int total[PER], before[PER], own = 0;
@@ -504,6 +577,17 @@ size_t plan_workspace_size(int64_t n, int32_t experts) {
 mao_status plan_launch(const int32_t* ids, int64_t n, int32_t experts, int32_t* counts,
                        int32_t* offsets, int32_t* row_of, int32_t* slot_of, int64_t n_slots,
                        void* workspace, cudaStream_t stream) {
+  static std::once_flag once[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MAO_ERR_CUDA;
+  cudaError_t attr = cudaSuccess;
+  std::call_once(once[dev & 63], [&] {
+    const int most = PLAN_WARPS * PLAN_MAX_EXPERTS * int(sizeof(int));
+    attr = cudaFuncSetAttribute(plan_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (attr == cudaSuccess)
+      attr = cudaFuncSetAttribute(plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  });
+  if (attr != cudaSuccess) return MAO_ERR_CUDA;
   const int blocks = int(ceil_div(n, PLAN_CHUNK));
   const size_t smem = size_t(PLAN_WARPS) * experts * sizeof(int);
   PlanParams p{ids, n, n_slots, experts, blocks, nullptr, counts, offsets, row_of, slot_of};
