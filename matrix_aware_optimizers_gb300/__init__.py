@@ -439,6 +439,15 @@ def _dense_ptr(t, dtype, shape, name):
     return t.data_ptr()
 
 
+def _out(t, shape, dtype, name, like, stream):
+    """An output of a call: t, checked, or a new tensor; and its device pointer."""
+    if t is not None:
+        return t, _dense_ptr(t, dtype, shape, name)
+    t = torch.empty(shape, dtype=dtype, device=like.device) if stream is None else \
+        _empty(shape, dtype, like.device, stream)
+    return t, t.data_ptr()
+
+
 def _scale_shape(rows, cols, blocks):
     br = 1 if blocks == "row" else 128
     bc = 1 if blocks == "col" else 128
@@ -598,18 +607,15 @@ def expert_route(logits, top_k, score="softmax", bias=None, groups=1, keep_group
     weight 0 fill the places that are left.
     """
     m = _mat(logits)
-    T, E = m.rows, m.cols
-    if weights is None:
-        weights = _empty((T, top_k), torch.float32, logits.device, stream)
-    if ids is None:
-        ids = _empty((T, top_k), torch.int32, logits.device, stream)
+    shape = (m.rows, top_k)
+    weights, wp = _out(weights, shape, torch.float32, "weights", logits, stream)
+    ids, ip = _out(ids, shape, torch.int32, "ids", logits, stream)
     st = lib().expert_route(
-        ctypes.byref(m), _dense_ptr(bias, torch.float32, (E,), "bias"), int(top_k), _SCORE[score],
-        int(groups), int(groups if keep_groups is None else keep_groups),
-        _GROUP_SCORE[group_score], int(bool(renorm)), float(scale),
-        _dense_ptr(weights, torch.float32, (T, top_k), "weights"),
-        _dense_ptr(ids, torch.int32, (T, top_k), "ids"), _raw_stream(stream, logits))
-    _abi.check("expert_route", st)
+        ctypes.byref(m), _dense_ptr(bias, torch.float32, (m.cols,), "bias"), top_k, _SCORE[score],
+        groups, groups if keep_groups is None else keep_groups, _GROUP_SCORE[group_score],
+        bool(renorm), scale, wp, ip, _raw_stream(stream, logits))
+    if st:
+        _abi.check("expert_route", st)
     return weights, ids
 
 
@@ -648,44 +654,54 @@ class ExpertPlan:
 
 @functools.lru_cache(maxsize=256)
 def _plan_sizes(n, experts):
-    """(rows, workspace bytes) of a plan."""
+    """(rows, workspace bytes or 0 where none is needed) of a plan."""
     nb = lib().expert_plan_workspace_bytes(n, experts)
     if nb == 0:
         raise ValueError("expert_plan takes up to 2^27 copies and 1 to 1024 experts")
-    return expert_rows(n, experts), nb
+    return expert_rows(n, experts), nb if n > 4096 else 0
 
 
 def expert_plan(ids, experts, ws=None, stream=None):
     """Places of the copies ids [T, top_k] (int32; entries outside 0 .. experts - 1 are dropped):
     each expert's copies, in the order of the tokens, in a run of rows that starts at a
     multiple of 128. Returns an ExpertPlan."""
-    n, experts, dev = ids.numel(), int(experts), ids.device
+    n, experts = ids.numel(), int(experts)
     p_ids = _dense_ptr(ids, torch.int32, ids.shape, "ids")
     rows, nb = _plan_sizes(n, experts)
-    counts = _empty((experts,), torch.int32, dev, stream)
-    offsets = _empty((experts + 1,), torch.int32, dev, stream)
-    row_of = _empty(ids.shape, torch.int32, dev, stream)
-    slot_of = _empty((rows,), torch.int32, dev, stream)
-    if ws is None:
-        ws = _empty((nb,), torch.uint8, dev, stream)
-    st = lib().expert_plan(p_ids, n, experts, counts.data_ptr(), offsets.data_ptr(),
-                           row_of.data_ptr(), slot_of.data_ptr(), rows, ws.data_ptr(),
-                           ws.numel() * ws.element_size(), _raw_stream(stream, ids))
-    _abi.check("expert_plan", st)
+    i32 = torch.int32
+    counts, p_counts = _out(None, experts, i32, "", ids, stream)
+    offsets, p_off = _out(None, experts + 1, i32, "", ids, stream)
+    row_of, p_row = _out(None, ids.shape, i32, "", ids, stream)
+    slot_of, p_slot = _out(None, rows, i32, "", ids, stream)
+    wptr = None
+    if ws is not None:
+        wptr, nb = ws.data_ptr(), ws.numel() * ws.element_size()
+    elif nb:
+        ws, wptr = _out(None, nb, torch.uint8, "", ids, stream)
+    st = lib().expert_plan(p_ids, n, experts, p_counts, p_off, p_row, p_slot, rows, wptr, nb,
+                           _raw_stream(stream, ids))
+    if st:
+        _abi.check("expert_plan", st)
     return ExpertPlan(counts, offsets, row_of, slot_of)
 
 
 def expert_combine(Z, row_of, weights=None, out=None, stream=None):
     """y[t] = sum_j weights[t, j] Z[row_of[t, j]] (entries below 0 are skipped; weights None:
     all 1), summed in fp32; out: of Z's dtype unless given."""
-    T, k = row_of.shape
+    shape = row_of.shape
+    T, k = shape
+    z = _mat(Z)
     if out is None:
-        out = _empty((T, Z.shape[1]), Z.dtype, Z.device, stream)
+        out, yp = _out(None, (T, z.cols), Z.dtype, "", Z, stream)
+        y = _abi.MaoMat(yp, T, z.cols, z.cols, z.dtype, 0)
+    else:
+        y = _mat(out)
     st = lib().expert_combine(
-        ctypes.byref(_mat(Z)), _dense_ptr(row_of, torch.int32, (T, k), "row_of"),
-        _dense_ptr(weights, torch.float32, (T, k), "weights"), T, k, ctypes.byref(_mat(out)),
+        ctypes.byref(z), _dense_ptr(row_of, torch.int32, shape, "row_of"),
+        _dense_ptr(weights, torch.float32, shape, "weights"), T, k, ctypes.byref(y),
         _raw_stream(stream, Z))
-    _abi.check("expert_combine", st)
+    if st:
+        _abi.check("expert_combine", st)
     return out
 
 

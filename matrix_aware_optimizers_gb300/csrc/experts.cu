@@ -304,13 +304,14 @@ struct PickBack {
 //
 // A counting sort of the copies by expert that keeps their order. Each block takes
 // PLAN_CHUNK copies: its warps count theirs per expert, 32 at a time (equal experts in a
-// warp find each other by match), which also ranks every copy within its warp. A copy's row
+// warp find each other by ballots), which also ranks every copy within its warp. A copy's row
 // is the expert's offset plus the counts of the blocks and warps before it plus its rank.
 // Integer sums only: the result does not depend on the order in which blocks run.
 
 constexpr int PLAN_WARPS = 16;
 constexpr int PLAN_ROUNDS = 8;
 constexpr int PLAN_CHUNK = PLAN_WARPS * 32 * PLAN_ROUNDS;
+static_assert(PLAN_CHUNK == kPlanAlone, "copies of one block");
 constexpr int PLAN_THREADS = 32 * PLAN_WARPS;
 constexpr int PLAN_MAX_EXPERTS = 1024;
 
@@ -321,6 +322,7 @@ __device__ __forceinline__ void plan_count(const int32_t* ids, int64_t n, int ex
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < PLAN_WARPS * experts; i += PLAN_THREADS) cnt[i] = 0;
   __syncthreads();
+  const int bits = 32 - __clz(experts - 1);  // 0 for one expert
   const int64_t first = int64_t(blockIdx.x) * PLAN_CHUNK + warp * 32 * PLAN_ROUNDS + lane;
 #pragma unroll
   for (int r = 0; r < PLAN_ROUNDS; ++r) {
@@ -330,7 +332,15 @@ __device__ __forceinline__ void plan_count(const int32_t* ids, int64_t n, int ex
   }
 #pragma unroll
   for (int r = 0; r < PLAN_ROUNDS; ++r) {
-    const uint32_t same = __match_any_sync(FULL, ex[r]);
+    // lanes with this lane's expert: one ballot per bit of the number (dropped copies, -1, only
+    // ever meet each other)
+    uint32_t same = FULL;
+    for (int b = 0; b < bits; ++b) {
+      const uint32_t one = __ballot_sync(FULL, (ex[r] >> b) & 1);
+      same &= ((ex[r] >> b) & 1) ? one : ~one;
+    }
+    const uint32_t in = __ballot_sync(FULL, ex[r] >= 0);
+    same &= ex[r] >= 0 ? in : ~in;
     int* c = cnt + warp * experts + (ex[r] < 0 ? 0 : ex[r]);
     const int before = ex[r] < 0 ? 0 : *c;
     rank[r] = before + __popc(same & ((1u << lane) - 1u));

@@ -33,6 +33,7 @@ struct RouteBackParams {
 };
 mao_status route_backward_launch(const RouteBackParams& p, cudaStream_t stream);
 
+constexpr int64_t kPlanAlone = 4096;  // copies that one block places, without a workspace
 size_t plan_workspace_size(int64_t n, int32_t experts);
 mao_status plan_launch(const int32_t* ids, int64_t n, int32_t experts, int32_t* counts,
                        int32_t* offsets, int32_t* row_of, int32_t* slot_of, int64_t n_slots,

@@ -191,8 +191,9 @@ def test_route_plan_combine_refusals(lib):
         return lib.expert_plan(ids, n, e, FAKE, off, FAKE, FAKE, slots, ws, wsb, None)
 
     assert plan(n=-1) == bad and plan(e=0) == bad and plan(e=1025) == uns and plan(n=(1 << 27) + 1, slots=1 << 31) == uns
-    assert plan(slots=256) == bad and plan(ids=None) == bad and plan(ws=None) == bad and plan(off=None) == bad
-    assert plan(ws=FAKE + 16) == mis and plan(off=FAKE + 2) == mis and plan(wsb=0) == wsp
+    assert plan(slots=256) == bad and plan(ids=None) == bad and plan(off=None) == bad
+    assert plan(ws=FAKE + 16) == mis and plan(off=FAKE + 2) == mis
+    assert plan(n=5000, slots=8192, ws=None) == bad and plan(n=5000, slots=8192, wsb=0) == wsp
 
     comb = lambda z, y, t=4, k=2, r=FAKE, w=FAKE: lib.expert_combine(ref(z), r, w, t, k, ref(y), None)  # noqa: E731
     assert comb(x, mat(4, 31)) == bad and comb(x, x, t=5) == bad and comb(x, x, k=0) == bad
