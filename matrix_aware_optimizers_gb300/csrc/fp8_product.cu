@@ -63,6 +63,7 @@ constexpr int SHARED = TILE - ACC1;        // columns that both accumulators use
 constexpr int SF_COL = ACC1 + TILE;        // scale words: 12 columns per set
 constexpr int SF_COLS = 12;
 constexpr int TMEM_COLS = 512;
+constexpr int Q_BOXES = 8;                 // heights of boxes of Q: 16 (b + 1) rows
 constexpr int BAND = 8;                    // tiles of j that share a pass over i
 constexpr size_t TABLE_BYTES = size_t(2) * (MAX_GROUPS + 2) * 4;
 // bf16 output is staged: sixteen rows of D at 128 columns, two buffers for each half of the
@@ -76,7 +77,7 @@ static_assert(SF_COL + SF_SETS * SF_COLS <= TMEM_COLS, "TMEM budget");
 
 struct ProductParams {
   CUtensorMap map_p;
-  CUtensorMap map_q[3];     // boxes of 128, 64 and 16 rows (MAO_TN: the first only)
+  CUtensorMap map_q[Q_BOXES];  // boxes of 16, 32, .. 128 rows (MAO_TN: the last only)
   const uint8_t* sp;        // scales of P and Q
   const uint8_t* sq;
   const int32_t* offsets;
@@ -289,8 +290,11 @@ __device__ __forceinline__ void decode(const ProductParams& p, const int* lo, co
   const int jt = band * BAND + local - it * nb;
   t.i0 = it * TILE;
   t.k0 = 0;
-  t.j0 = lo[a] + jt * TILE;
-  t.j_end = min(t.j0 + TILE, lo[a + 1]);
+  // a group's tiles are of even height: those of up to 224 rows do not share TMEM columns
+  const int rows = lo[a + 1] - lo[a];
+  const int height = count > 1 ? ((rows + count - 1) / count + 31) & ~31 : TILE;
+  t.j0 = lo[a] + jt * height;
+  t.j_end = min(t.j0 + height, lo[a + 1]);
   t.nkb = (p.depth + BK - 1) / BK;
   t.n = t.nkb ? (t.j_end - t.j0 + 31) & ~31 : 0;
 }
@@ -572,7 +576,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   if (warp == 0 && lane < 2) {
-    const CUtensorMap* map = lane ? &p.map_q[0] : &p.map_p;
+    const CUtensorMap* map = lane ? &p.map_q[Q_BOXES - 1] : &p.map_p;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }
   // launched as a programmatic dependent: the set-up so far may overlap the previous kernel
@@ -601,9 +605,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       decode<FORM>(p, lo, begin, tile, t);
       const int i = t.i0 + HALF * int(cta), j = t.j0 + (t.n >> 1) * int(cta);
       const int z = FORM != MAO_TN ? t.g : 0;
-      // the smallest box that holds this CTA's n / 2 rows of Q
-      const int small = q_mn || t.n > HALF ? 0 : t.n > 32 ? 1 : 2;
-      const uint32_t q_bytes = small == 0 ? OP_BYTES : small == 1 ? OP_BYTES / 2 : OP_BYTES / 8;
+      // the box that holds this CTA's n / 2 rows of Q
+      const int box = q_mn ? Q_BOXES - 1 : (t.n >> 5) - 1;
+      const uint32_t q_bytes = uint32_t(box + 1) * (OP_BYTES / Q_BOXES);
       for (int kb = 0; kb < t.nkb; ++kb) {
         if (!wait_warp<false>(&empty_bar[stage], phase ^ 1u, abort_flag, limit)) {
           ok = false;
@@ -615,8 +619,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (leader) mbar_expect_tx(smem_u32(&full_bar[stage]), 2 * (OP_BYTES + q_bytes));
           if (p_mn) tma_load_3d_pair(dst, &p.map_p, fb, i, k, z);
           else tma_load_3d_pair(dst, &p.map_p, fb, k, i, z);
-          if (q_mn) tma_load_3d_pair(dst + OP_BYTES, &p.map_q[0], fb, j, k, 0);
-          else tma_load_3d_pair(dst + OP_BYTES, &p.map_q[small], fb, k, j, 0);
+          if (q_mn) tma_load_3d_pair(dst + OP_BYTES, &p.map_q[Q_BOXES - 1], fb, j, k, 0);
+          else tma_load_3d_pair(dst + OP_BYTES, &p.map_q[box], fb, k, j, 0);
         }
         armed |= 1u << stage;
         armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
@@ -644,7 +648,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // per 32-deep slice: 32 bytes along the swizzled rows (K-major), or four 1024-byte atoms
       // of eight k rows (MN-major)
       const uint32_t dp = p_mn ? 4096 >> 4 : 32 >> 4, dq = q_mn ? 4096 >> 4 : 32 >> 4;
-      int stage = 0, local = 0;
+      int stage = 0, local = 0, before_n = 0;
       uint32_t phase = 0;
       bool ok = true, issued = false, started = false;
       // Scale words: the slot of the blocks being multiplied (every three groups of blocks the
@@ -683,10 +687,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int after = next_tile<FORM>(p, lo, begin, tile + npairs, npairs, total, next);
         const int acc = local & 1;
         // the accumulator's last tile has been read, and of the tile before this one the
-        // columns that the two share
+        // columns that the two share (they do if the first accumulator's tile reaches there)
+        const bool meet = (acc ? before_n : t.n) > ACC1;
+        before_n = t.n;
         if (!wait_warp<true>(&tempty_bar[acc], (uint32_t(local >> 1) & 1u) ^ 1u, abort_flag, limit) ||
-            !wait_warp<true>(&tshared_bar[acc ^ 1], (uint32_t((local + 1) >> 1) & 1u) ^ 1u, abort_flag,
-                             limit)) {
+            (meet && !wait_warp<true>(&tshared_bar[acc ^ 1], (uint32_t((local + 1) >> 1) & 1u) ^ 1u,
+                                      abort_flag, limit))) {
           ok = false;
           break;
         }
@@ -875,8 +881,8 @@ mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, 
   }
   ProductParams p = {};
   mao_status st = tc_encode_code_map(&p.map_p, B.codes, B.cols, B.rows, B.ld, B.count, HALF);
-  for (int b = 0; b < (tn ? 1 : 3) && st == MAO_OK; ++b)
-    st = tc_encode_code_map(&p.map_q[b], A.codes, A.cols, A.rows, A.ld, 1, b == 0 ? HALF : b == 1 ? 64 : 16);
+  for (int b = tn ? Q_BOXES - 1 : 0; b < Q_BOXES && st == MAO_OK; ++b)
+    st = tc_encode_code_map(&p.map_q[b], A.codes, A.cols, A.rows, A.ld, 1, 16 * (b + 1));
   if (st != MAO_OK) return st;
   p.sp = B.scales;
   p.sq = A.scales;
