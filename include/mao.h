@@ -479,13 +479,18 @@ enum {
  *              empty group's matrix is zero.
  *   accumulate nonzero: D <- D + product (in fp32, rounded to D's dtype once; rows past the
  *              last group and empty groups' matrices keep their values).
+ *   workspace  NULL, or a device buffer, 256-byte aligned: without groups a product with few
+ *              outputs and a long sum is then split over the sum, if the buffer has
+ *              fp8_product_workspace_bytes(A, B, form) bytes (0 where a split would not pay),
+ *              and its parts added up in a fixed order by a second kernel. Clobbered.
  *   Limits: groups <= 1024; A, B codes at most 2^31 rows in all. Products of e4m3 values are
- *   exact in fp32; the order of the sums over K is fixed, so results are the same each time.
+ *   exact in fp32; the order of the sums is fixed, so results are the same each time.
  *   Codes that a NaN scale (255) covers are not supported: fp8_quantize never writes it.
  */
 mao_status fp8_product(const mao_fp8* A, const mao_fp8* B, const mao_mat* D, int32_t form,
                        const int32_t* offsets, int32_t groups, int32_t accumulate,
-                       void* stream);
+                       void* workspace, size_t workspace_bytes, void* stream);
+size_t fp8_product_workspace_bytes(const mao_fp8* A, const mao_fp8* B, int32_t form);
 
 enum { MAO_SCORE_SOFTMAX = 0, MAO_SCORE_SIGMOID = 1 };
 enum { MAO_GROUP_MAX = 0, MAO_GROUP_TOP2 = 1 };

@@ -554,7 +554,7 @@ def fp8_quantize(X, blocks, rows=None, copies=1, out=None, stream=None):
 
 
 def fp8_product(A, a_scales, B, b_scales, form, offsets=None, out=None, out_dtype=torch.bfloat16,
-                accumulate=False, stream=None):
+                accumulate=False, ws=None, stream=None):
     """Product of 8-bit matrices (fp8_quantize's codes and scales) with fp32 sums, over groups
     of rows.
 
@@ -564,7 +564,9 @@ def fp8_product(A, a_scales, B, b_scales, form, offsets=None, out=None, out_dtyp
     offsets: int32 tensor of groups + 1 row numbers (expert_plan's; for "tn" multiples of
     128): g is the group of row t, and "tn" sums over the rows of group g. None: one group, and
     B may then be [N, K]. out: a float32 or bfloat16 tensor to fill, or with accumulate to add
-    to; by default a new one of out_dtype. Rows past the last group become zero.
+    to; by default a new one of out_dtype. Rows past the last group become zero. ws: a uint8
+    buffer for products without groups whose sum is split (fp8_product_workspace_bytes);
+    allocated when needed.
     """
     if form not in _FORM:
         raise ValueError("form must be nt, nn or tn")
@@ -590,9 +592,18 @@ def fp8_product(A, a_scales, B, b_scales, form, offsets=None, out=None, out_dtyp
         if groups > 1 and out.stride(0) != a.cols * out.stride(1):
             raise ValueError("the groups' matrices follow each other without gaps")
         d = out.as_strided((groups * a.cols, b.cols), (out.stride(1), out.stride(2)))
-    st = lib().fp8_product(ctypes.byref(a), ctypes.byref(b), ctypes.byref(_mat(d)), _FORM[form],
-                           off, groups, int(bool(accumulate)), _raw_stream(stream, A))
-    _abi.check("fp8_product", st)
+    ra, rb = ctypes.byref(a), ctypes.byref(b)
+    wptr, wbytes = None, 0
+    if ws is not None:
+        wptr, wbytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    elif off is None:
+        wbytes = lib().fp8_product_workspace_bytes(ra, rb, _FORM[form])
+        if wbytes:
+            ws, wptr = _out(None, wbytes, torch.uint8, "", A, stream)
+    st = lib().fp8_product(ra, rb, ctypes.byref(_mat(d)), _FORM[form], off, groups,
+                           bool(accumulate), wptr, wbytes, _raw_stream(stream, A))
+    if st:
+        _abi.check("fp8_product", st)
     return out
 
 

@@ -53,6 +53,7 @@ EXPORTS = (
     "dion_step",
     "fp8_quantize",
     "fp8_product",
+    "fp8_product_workspace_bytes",
     "expert_route",
     "expert_route_backward",
     "expert_rows",
@@ -187,7 +188,8 @@ def load():
             ("fp8_quantize", ctypes.c_int,
              [P(MaoMat), i32, i64, vp, i64, i32, P(MaoFp8), P(MaoFp8), P(MaoFp8), vp]),
             ("fp8_product", ctypes.c_int,
-             [P(MaoFp8), P(MaoFp8), P(MaoMat), i32, vp, i32, i32, vp]),
+             [P(MaoFp8), P(MaoFp8), P(MaoMat), i32, vp, i32, i32, vp, ctypes.c_size_t, vp]),
+            ("fp8_product_workspace_bytes", ctypes.c_size_t, [P(MaoFp8), P(MaoFp8), i32]),
             ("expert_route", ctypes.c_int,
              [P(MaoMat), vp, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp]),
             ("expert_route_backward", ctypes.c_int,

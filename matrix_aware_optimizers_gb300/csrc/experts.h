@@ -52,7 +52,8 @@ mao_status quantize_launch(const mao_mat* X, int32_t batch, int64_t batch_stride
 
 mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, int32_t form,
                           const int32_t* offsets, int32_t groups, int32_t accumulate,
-                          cudaStream_t stream);
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t product_workspace_size(const mao_fp8& A, const mao_fp8& B, int32_t form);
 // Reads and clears the device error word of the product kernel (after a stream sync).
 mao_status product_read_and_clear_error(cudaStream_t stream);
 

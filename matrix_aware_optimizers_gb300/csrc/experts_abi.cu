@@ -71,11 +71,12 @@ mao_status fp8_quantize(const mao_mat* X, int32_t batch, int64_t batch_stride,
 
 mao_status fp8_product(const mao_fp8* A, const mao_fp8* B, const mao_mat* D, int32_t form,
                        const int32_t* offsets, int32_t groups, int32_t accumulate,
-                       void* stream) {
+                       void* workspace, size_t workspace_bytes, void* stream) {
   if (form < MAO_NT || form > MAO_TN || groups < 1) return MAO_ERR_INVALID_ARG;
   if (groups > 1024) return MAO_ERR_UNSUPPORTED;
   if (!offsets && groups != 1) return MAO_ERR_INVALID_ARG;
   if (offsets && !aligned(offsets, 4)) return MAO_ERR_MISALIGNED;
+  if (!aligned(workspace, 256)) return MAO_ERR_MISALIGNED;
   const bool tn = form == MAO_TN;
   mao_status st = check_fp8(A, tn ? MAO_BLOCKS_COL : MAO_BLOCKS_ROW);
   if (st == MAO_OK) st = check_fp8(B, tn ? MAO_BLOCKS_COL : MAO_BLOCKS_TILE);
@@ -89,8 +90,15 @@ mao_status fp8_product(const mao_fp8* A, const mao_fp8* B, const mao_mat* D, int
                                            D->rows == A->cols * groups;
   if (!fits) return MAO_ERR_INVALID_ARG;
   if (device_cc() / 10 != 10) return MAO_ERR_UNSUPPORTED;
-  return product_launch(*A, *B, *D, form, offsets, groups, accumulate,
+  return product_launch(*A, *B, *D, form, offsets, groups, accumulate, workspace, workspace_bytes,
                         static_cast<cudaStream_t>(stream));
+}
+
+size_t fp8_product_workspace_bytes(const mao_fp8* A, const mao_fp8* B, int32_t form) {
+  if (!A || !B || form < MAO_NT || form > MAO_TN || A->rows < 0 || A->cols < 1 || B->rows < 0 ||
+      B->cols < 1)
+    return 0;
+  return product_workspace_size(*A, *B, form);
 }
 
 mao_status expert_route(const mao_mat* logits, const float* bias, int32_t top_k, int32_t score,

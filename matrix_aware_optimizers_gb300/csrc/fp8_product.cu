@@ -90,6 +90,7 @@ struct ProductParams {
   int32_t sp_rows;          // rows of scales of one matrix of P
   int32_t tiles_i, groups, dtype, accumulate, wide;
   int32_t sp_words, sq_words;  // scales allow 4-byte loads
+  int32_t splits, split_kb;    // parts of the depth (one group), blocks of each
   unsigned long long timeout_ns;
 };
 
@@ -99,7 +100,9 @@ struct Tile {
   int j_end;    // rows of D in the tile end here
   int n;        // j computed (a multiple of 32), 0: the rows are only cleared
   int k0;       // first row of the depth (MAO_TN)
+  int kb0;      // first block of the depth (of a split)
   int nkb;      // blocks of the depth
+  int64_t row0; // row of the output that j counts from
 };
 
 __device__ __forceinline__ uint64_t desc_of(uint32_t saddr, uint32_t lbo, uint32_t sbo,
@@ -145,10 +148,28 @@ __device__ __forceinline__ uint32_t elect_one() {
   return e;
 }
 
-// 128 scale words (512 bytes of each CTA's shared memory) into four TMEM columns of both.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-               : "memory");
+// 128 scale words (512 bytes of each CTA's shared memory) into four TMEM columns of both, for
+// the three sets of words of a slot.
+__device__ __forceinline__ void copy_scales(uint32_t elected, uint32_t taddr, uint64_t desc) {
+#pragma unroll
+  for (int h = 0; h < 3; ++h)
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %2, 0;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(taddr + 4 * h),
+        "l"(desc + uint64_t(h * (512 >> 4))), "r"(elected)
+        : "memory");
+}
+
+// umma_commit_pair to both CTAs by the elected lane of a converged warp.
+__device__ __forceinline__ void commit_both(uint32_t elected, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %2, 0;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n\t}\n" ::"r"(bar),
+      "h"(uint16_t(3)), "r"(elected)
+      : "memory");
 }
 
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map,
@@ -202,8 +223,8 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 // (MAO_NT, MAO_NN: of its rows; MAO_TN: the same number for every group), begin[groups] all.
 
 template <int FORM>
-__device__ __forceinline__ void make_table(const ProductParams& p, int* lo, int* begin) {
-  const int tid = threadIdx.x;
+__device__ __forceinline__ void make_table(const ProductParams& p, int* lo, int* begin, int* sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = p.groups;
   if (!p.offsets) {
     if (tid == 0) {
@@ -214,46 +235,59 @@ __device__ __forceinline__ void make_table(const ProductParams& p, int* lo, int*
     for (int g = tid; g <= n; g += THREADS) lo[g] = max(0, min(p.offsets[g], p.rows));
   }
   __syncthreads();
-  if (tid < 32) {
-    int high = 0, sum = 0;  // the largest offset and the tiles so far
-    for (int base = 0; base <= n; base += 32) {
-      const int g = base + tid;
-      int v = g <= n ? lo[g] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-        if (tid >= o) v = max(v, u);
-      }
-      v = max(v, high);
-      if (g <= n) lo[g] = v;
-      high = __shfl_sync(0xFFFFFFFFu, v, 31);
-    }
-    __syncwarp();
-    for (int base = 0; base <= n; base += 32) {
-      const int g = base + tid;
-      int c = 0;
-      if (FORM == MAO_TN) {
-        c = g < n ? (p.J + TILE - 1) / TILE : 0;
-      } else if (g < n) {
-        c = (lo[g + 1] - lo[g] + TILE - 1) / TILE;
-      }
-      int s = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (tid >= o) s += u;
-      }
-      if (g <= n) begin[g] = sum + s - c;
-      sum += __shfl_sync(0xFFFFFFFFu, s, 31);
-    }
+  bool falls = false;
+  for (int g = tid; g < n; g += THREADS) falls = falls || lo[g + 1] < lo[g];
+  if (__syncthreads_or(falls)) {  // offsets that fall are raised to the largest before them
+    if (tid == 0)
+      for (int g = 0; g < n; ++g) lo[g + 1] = max(lo[g + 1], lo[g]);
+    __syncthreads();
   }
+  // thread i (of 256) sums the tiles of groups 4 i .. 4 i + 3
+  int c[4], own = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int g = 4 * tid + q;
+    c[q] = g >= n ? 0 : FORM == MAO_TN ? (p.J + TILE - 1) / TILE : (lo[g + 1] - lo[g] + TILE - 1) / TILE;
+    own += c[q];
+  }
+  int s = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+    if (lane >= o) s += u;
+  }
+  if (lane == 31) sums[warp] = s;
   __syncthreads();
+  for (int w = 0; w < warp; ++w) s += sums[w];
+  s -= own;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int g = 4 * tid + q;
+    if (g <= n) begin[g] = s;
+    s += c[q];
+  }
+}
+
+// A split's share of the depth, and its rows of the partial sums.
+__device__ __forceinline__ void take_split(const ProductParams& p, int split, Tile& t) {
+  t.kb0 = 0;
+  if (p.splits > 1) {
+    t.kb0 = split * p.split_kb;
+    t.nkb = min(p.split_kb, t.nkb - t.kb0);
+    t.row0 = int64_t(split) * p.J;
+  }
 }
 
 // The whole warp decodes: t.g is a group at or before the tile's (tiles come in rising order).
 template <int FORM>
 __device__ __forceinline__ void decode(const ProductParams& p, const int* lo, const int* begin,
                                        int tile, Tile& t) {
+  int split = 0;
+  if (p.splits > 1) {
+    const int tiles = begin[1] * p.tiles_i;
+    split = tile / tiles;
+    tile -= split * tiles;
+  }
   // the last group with begin * tiles_i <= tile: the one whose tiles hold this one
   const int lane = threadIdx.x & 31;
   int a = t.g;
@@ -277,6 +311,8 @@ __device__ __forceinline__ void decode(const ProductParams& p, const int* lo, co
     t.j_end = min(t.j0 + TILE, p.J);
     t.k0 = lo[a];
     t.nkb = (lo[a + 1] - lo[a] + BK - 1) / BK;
+    t.row0 = int64_t(a) * p.J;
+    take_split(p, split, t);
     t.n = t.nkb ? (t.j_end - t.j0 + 31) & ~31 : 0;
     return;
   }
@@ -296,6 +332,8 @@ __device__ __forceinline__ void decode(const ProductParams& p, const int* lo, co
   t.j0 = lo[a] + jt * height;
   t.j_end = min(t.j0 + height, lo[a + 1]);
   t.nkb = (p.depth + BK - 1) / BK;
+  t.row0 = 0;
+  take_split(p, split, t);
   t.n = t.nkb ? (t.j_end - t.j0 + 31) & ~31 : 0;
 }
 
@@ -403,12 +441,13 @@ template <>
 struct Scales<MAO_TN> {
   Across p0, q0, q1;
   __device__ __forceinline__ void load(const ProductParams& p, const Tile& t, int cta, int kb, int lane) {
+    const int end = t.kb0 + t.nkb;
     const int row0 = t.k0 / BK, i = t.i0 + HALF * cta;  // the group's first row of scales
     const uint8_t* sp = p.sp + row0 * p.sp_ld + i;
     const uint8_t* sq = p.sq + row0 * p.sq_ld + t.j0;
-    p0.load(sp, p.sp_ld, p.I - i, kb, t.nkb, p.sp_words, lane);
-    q0.load(sq, p.sq_ld, t.j_end - t.j0, kb, t.nkb, p.sq_words, lane);
-    q1.load(sq + HALF, p.sq_ld, t.j_end - t.j0 - HALF, kb, t.nkb, p.sq_words, lane);
+    p0.load(sp, p.sp_ld, p.I - i, kb, end, p.sp_words, lane);
+    q0.load(sq, p.sq_ld, t.j_end - t.j0, kb, end, p.sq_words, lane);
+    q1.load(sq + HALF, p.sq_ld, t.j_end - t.j0 - HALF, kb, end, p.sq_words, lane);
   }
 };
 template <int FORM>
@@ -416,13 +455,14 @@ struct Scales {
   Same p0;
   Along q0, q1;
   __device__ __forceinline__ void load(const ProductParams& p, const Tile& t, int cta, int kb, int lane) {
+    const int end = t.kb0 + t.nkb;
     const int i = t.i0 + HALF * cta;
     const uint8_t* sp = p.sp + int64_t(t.g) * p.sp_group;
-    if (FORM == MAO_NT) p0.load(sp + int64_t(i / BK) * p.sp_ld, 1, p.I - i, kb, t.nkb, lane);
-    else p0.load(sp + i / BK, p.sp_ld, p.I - i, kb, t.nkb, lane);
+    if (FORM == MAO_NT) p0.load(sp + int64_t(i / BK) * p.sp_ld, 1, p.I - i, kb, end, lane);
+    else p0.load(sp + i / BK, p.sp_ld, p.I - i, kb, end, lane);
     const uint8_t* sq = p.sq + int64_t(t.j0) * p.sq_ld;
-    q0.load(sq, p.sq_ld, t.j_end - t.j0, kb, t.nkb, p.sq_words, lane);
-    q1.load(sq + HALF * p.sq_ld, p.sq_ld, t.j_end - t.j0 - HALF, kb, t.nkb, p.sq_words, lane);
+    q0.load(sq, p.sq_ld, t.j_end - t.j0, kb, end, p.sq_words, lane);
+    q1.load(sq + HALF * p.sq_ld, p.sq_ld, t.j_end - t.j0 - HALF, kb, end, p.sq_words, lane);
   }
 };
 
@@ -433,8 +473,7 @@ template <int FORM>
 __device__ __forceinline__ void store16(const ProductParams& p, const Tile& t, int j, int i,
                                         const float (&v)[16], int lane) {
   const bool in = i < p.I;
-  int64_t row = j;
-  if (FORM == MAO_TN) row += int64_t(t.g) * p.J;
+  const int64_t row = t.row0 + j;
   if (p.dtype == MAO_F32) {
     float* d = static_cast<float*>(p.d) + row * p.ld + i;
     if (p.accumulate) {
@@ -481,8 +520,7 @@ __device__ __forceinline__ void store16_wide(const ProductParams& p, const Tile&
     const int c = 4 * quad + 2 * h + (lane >> 4);
     if (j + c >= t.j_end || i >= p.I) continue;
     const uint4 x = *reinterpret_cast<const uint4*>(buf + c * PITCH + 16 * (lane & 15));
-    int64_t row = j + c;
-    if (FORM == MAO_TN) row += int64_t(t.g) * p.J;
+    const int64_t row = t.row0 + j + c;
     __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + row * p.ld + i;
     if (i + 8 <= p.I) {
       asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(d), "r"(x.x),
@@ -581,10 +619,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   // launched as a programmatic dependent: the set-up so far may overlap the previous kernel
   wait_for_previous();
-  make_table<FORM>(p, lo, begin);
-  const int total = begin[p.groups] * p.tiles_i;
+  make_table<FORM>(p, lo, begin, reinterpret_cast<int*>(staging));
   tc_fence_before();
   __syncthreads();
+  const int total = begin[p.groups] * p.tiles_i * p.splits;
   cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
@@ -614,7 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           break;
         }
         const uint32_t fb = full0 + 8 * stage, dst = ring0 + stage * STAGE_BYTES;
-        const int k = t.k0 + kb * BK;
+        const int k = t.k0 + (t.kb0 + kb) * BK;
         if (elected) {
           if (leader) mbar_expect_tx(smem_u32(&full_bar[stage]), 2 * (OP_BYTES + q_bytes));
           if (p_mn) tma_load_3d_pair(dst, &p.map_p, fb, i, k, z);
@@ -650,7 +688,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const uint32_t dp = p_mn ? 4096 >> 4 : 32 >> 4, dq = q_mn ? 4096 >> 4 : 32 >> 4;
       int stage = 0, local = 0, before_n = 0;
       uint32_t phase = 0;
-      bool ok = true, issued = false, started = false;
+      bool ok = true, issued = false, started = false, ready = false;
       // Scale words: the slot of the blocks being multiplied (every three groups of blocks the
       // phase flips), the set of TMEM columns that holds them, and the slot copied next.
       int slot = 0, set = 0, copied = 0;
@@ -661,14 +699,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!wait_warp<false>(&sf_empty_bar[before], before_phase, abort_flag, limit) ||
             !wait_warp<true>(&sf_full_bar[copied], copied_phase, abort_flag, limit))
           return false;
-        tc_fence_after();
-        const uint32_t dst = tmem_base + uint32_t(SF_COL + SF_COLS * (set ^ (started ? 1 : 0)));
-        const uint64_t src = sf_desc + uint64_t(copied * (SF_BYTES >> 4));
-        if (elected) {
-          copy_scales(dst, src);
-          copy_scales(dst + 4, src + (512 >> 4));
-          copy_scales(dst + 8, src + (1024 >> 4));
-        }
+        copy_scales(elected, tmem_base + uint32_t(SF_COL + SF_COLS * (set ^ (started ? 1 : 0))),
+                    sf_desc + uint64_t(copied * (SF_BYTES >> 4)));
         started = issued = true;
         if (++copied == SF_SLOTS) {
           copied = 0;
@@ -700,22 +732,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint32_t d = tmem_base + uint32_t(acc * ACC1);
         const uint32_t idesc0 = instr_desc(p_mn, q_mn, t.n, 0);
         for (int kb = 0; kb < t.nkb; ++kb) {
-          if (!wait_warp<false>(&full_bar[stage], phase, abort_flag, limit)) {
+          // the stage was looked at while the products before were issued
+          if (!__all_sync(0xFFFFFFFFu, ready) && !wait_warp<false>(&full_bar[stage], phase, abort_flag, limit)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t tsf = tmem_base + uint32_t(SF_COL + SF_COLS * set);
+          const uint32_t empty = smem_u32(&empty_bar[stage]);
           const uint64_t at = uint64_t(stage * (STAGE_BYTES >> 4));
-          mma_block(elected, d, p_desc + at, q_desc + at, dp, dq,
-                    idesc0 | uint32_t(kb & 3) << 4 | uint32_t(kb & 3) << 29, tsf, tsf + 4,
-                    kb != 0 ? 1u : 0u);
-          issued = true;
-          if (elected) umma_commit_pair(smem_u32(&empty_bar[stage]), 3);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
+          ready = limit != 0 && mbar_test_wait(smem_u32(&full_bar[stage]), phase);
+          const uint32_t tsf = tmem_base + uint32_t(SF_COL + SF_COLS * set);
+          mma_block(elected, d, p_desc + at, q_desc + at, dp, dq,
+                    idesc0 | uint32_t(kb & 3) << 4 | uint32_t(kb & 3) << 29, tsf, tsf + 4,
+                    kb != 0 ? 1u : 0u);
+          issued = true;
+          commit_both(elected, empty);
           const bool last = (kb & 3) == 3 || kb + 1 == t.nkb;
           // the next scale words follow two or three blocks behind the current ones: by then
           // the slot's last products are done, and the copy is done before it is needed
@@ -726,13 +760,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
           }
           if (last) {
-            if (elected) umma_commit_pair(smem_u32(&sf_empty_bar[slot]), 3);
+            commit_both(elected, smem_u32(&sf_empty_bar[slot]));
             if (++slot == SF_SLOTS) slot = 0;
             set ^= 1;
           }
         }
         if (!ok) break;
-        if (elected) umma_commit_pair(smem_u32(&tfull_bar[acc]), 3);
+        commit_both(elected, smem_u32(&tfull_bar[acc]));
         ++local;
         tile = after;
         t = next;
@@ -762,10 +796,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       decode<FORM>(p, lo, begin, tile, t);
       const int i = t.i0 + HALF * int(cta) + 32 * quad + lane;
       if (t.nkb == 0) {  // MAO_TN: an empty group's matrix is cleared (or stays, when added to)
-        const int64_t row = int64_t(t.g) * p.J;
         const int i0 = t.i0 + HALF * int(cta);
         if (!p.accumulate)
-          clear_rows(p, row + t.j0 + warp - 2, row + t.j_end, EPI_WARPS, i0, min(HALF, p.I - i0), lane);
+          clear_rows(p, t.row0 + t.j0 + warp - 2, t.row0 + t.j_end, EPI_WARPS, i0, min(HALF, p.I - i0), lane);
         continue;
       }
       const int acc = local & 1;
@@ -821,32 +854,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // group's loads and its hand-over (a release to the other CTA) have the time of three
     // groups' products.
     const int slot = warp - 2 - EPI_WARPS;
+    uint8_t* dst = sf + slot * SF_BYTES;
+    const uint32_t full = mapa_shared(smem_u32(&sf_full_bar[slot]), 0);
     Tile t;
     int tile = next_tile<FORM>(p, lo, begin, pair, npairs, total, t);
-    int kb = 0, turn = 0;
+    int kb = 0;
+    auto skip = [&](int groups) {
+      for (int q = 0; q < groups && tile < total; ++q) {
+        kb += 4;
+        if (kb >= t.nkb) {
+          kb = 0;
+          tile = next_tile<FORM>(p, lo, begin, tile + npairs, npairs, total, t);
+        }
+      }
+    };
+    skip(slot);
+    Scales<FORM> w;
+    if (tile < total) w.load(p, t, int(cta), t.kb0 + kb, lane);
     uint32_t phase = 0;
     while (tile < total) {
-      if (turn == slot) {
-        Scales<FORM> w;
-        w.load(p, t, int(cta), kb, lane);
-        if (!wait_warp<false>(&sf_empty_bar[slot], phase ^ 1u, abort_flag, limit)) break;
-        uint8_t* dst = sf + slot * SF_BYTES;
-        w.p0.store(dst, lane);
-        w.q0.store(dst + 512, lane);
-        w.q1.store(dst + 1024, lane);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_release(mapa_shared(smem_u32(&sf_full_bar[slot]), 0));
-      }
-      if (++turn == SF_WARPS) {
-        turn = 0;
-        phase ^= 1u;
-      }
-      kb += 4;
-      if (kb >= t.nkb) {
-        kb = 0;
-        tile = next_tile<FORM>(p, lo, begin, tile + npairs, npairs, total, t);
-      }
+      if (!wait_warp<false>(&sf_empty_bar[slot], phase ^ 1u, abort_flag, limit)) break;
+      w.p0.store(dst, lane);
+      w.q0.store(dst + 512, lane);
+      w.q1.store(dst + 1024, lane);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_release(full);
+      phase ^= 1u;
+      skip(SF_WARPS);
+      if (tile < total) w.load(p, t, int(cta), t.kb0 + kb, lane);
     }
     __syncwarp();
   }
@@ -867,11 +903,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
+// D = (D +) the sum of the splits' partial sums, in their order; four columns per thread.
+struct SumParams {
+  const float* parts;
+  void* d;
+  int64_t rows, cols, pld, ld;
+  int32_t splits, dtype, accumulate, vec;
+};
+
+__global__ void __launch_bounds__(256) split_sum_kernel(const SumParams p) {
+  wait_for_previous();
+  const int64_t quads = p.pld / 4, all = p.rows * quads;
+  for (int64_t q = int64_t(blockIdx.x) * 256 + threadIdx.x; q < all; q += int64_t(gridDim.x) * 256) {
+    const int64_t j = q / quads, i = 4 * (q - j * quads);
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+      const float4 x = *reinterpret_cast<const float4*>(p.parts + (s * p.rows + j) * p.pld + i);
+      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+    }
+    const int64_t at = j * p.ld + i;
+    if (p.accumulate) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (i + c < p.cols) v[c] += load_elem(p.d, at + c, p.dtype);
+    }
+    if (p.vec && i + 4 <= p.cols) {
+      if (p.dtype == MAO_F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.d) + at) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.d) + at) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (i + c < p.cols) store_elem(p.d, at + c, p.dtype, v[c]);
+    }
+  }
+}
+
+// How many parts the depth of a product without groups is split into when its tiles leave
+// pairs of SMs idle: the number with the least time by a model of the two kernels (about
+// 0.25 us per block of the depth; 2.5 us for the second kernel and 3 TB/s for the partial
+// sums, which stay in L2), parts of whole scale words.
+struct Split {
+  int splits, kb;
+};
+Split choose_split(int64_t tiles, int64_t nkb, int64_t outputs) {
+  Split best{1, int(nkb)};
+  const int64_t pairs = num_sms() / 2;
+  double least = 0.25 * double(nkb);
+  for (int64_t s = 2; s <= 32 && s * tiles <= pairs && 4 * s <= nkb; ++s) {
+    const int64_t kb = round_up(ceil_div(nkb, s), 4), parts = ceil_div(nkb, kb);
+    const double t = 0.25 * double(kb) + 2.5 + double(parts) * double(outputs) * 8.0 / 3e6;
+    if (parts > 1 && t < least) {
+      least = t;
+      best = Split{int(parts), int(kb)};
+    }
+  }
+  return best;
+}
+
+struct Shape {
+  int64_t rows, cols, depth;  // of D (one group) and the product
+};
+Shape shape_of(const mao_fp8& A, const mao_fp8& B, int32_t form) {
+  return form == MAO_NT   ? Shape{A.rows, B.rows, A.cols}
+         : form == MAO_NN ? Shape{A.rows, B.cols, A.cols}
+                          : Shape{A.cols, B.cols, A.rows};
+}
+Split split_of(const Shape& d) {
+  return choose_split(ceil_div(d.rows, TILE) * ceil_div(d.cols, TILE), ceil_div(d.depth, BK), d.rows * d.cols);
+}
+size_t parts_bytes(const Shape& d, const Split& s) {
+  return s.splits > 1 ? size_t(round_up(int64_t(s.splits) * d.rows * round_up(d.cols, 4) * 4, 256)) : 0;
+}
+
 }  // namespace
+
+size_t product_workspace_size(const mao_fp8& A, const mao_fp8& B, int32_t form) {
+  const Shape d = shape_of(A, B, form);
+  return A.rows == 0 ? 0 : parts_bytes(d, split_of(d));
+}
 
 mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, int32_t form,
                           const int32_t* offsets, int32_t groups, int32_t accumulate,
-                          cudaStream_t stream) {
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   const bool tn = form == MAO_TN;
   const int es = elem_size(D.dtype);
   if (A.rows == 0) {  // no rows of D, or sums over nothing
@@ -920,8 +1039,32 @@ mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, 
     }
   });
   if (attr != cudaSuccess) return MAO_ERR_CUDA;
-  const int64_t pairs = tiles < num_sms() / 2 ? tiles : num_sms() / 2;
-  return launch_dependent(kernels[form], unsigned(2 * pairs), THREADS, SMEM, stream, p);
+  p.splits = 1;
+  const Shape shape = shape_of(A, B, form);
+  Split split{1, 0};
+  if (!offsets && workspace) {
+    split = split_of(shape);
+    if (workspace_bytes < parts_bytes(shape, split)) split = Split{1, 0};
+  }
+  if (split.splits > 1) {  // fp32 partial sums in the workspace, then their sum
+    p.splits = split.splits;
+    p.split_kb = split.kb;
+    p.J = int32_t(shape.rows);
+    p.d = workspace;
+    p.ld = round_up(D.cols, 4);
+    p.dtype = MAO_F32;
+    p.accumulate = p.wide = 0;
+  }
+  const int64_t units = tiles * p.splits;
+  const int64_t pairs = units < num_sms() / 2 ? units : num_sms() / 2;
+  st = launch_dependent(kernels[form], unsigned(2 * pairs), THREADS, SMEM, stream, p);
+  if (st != MAO_OK || split.splits == 1) return st;
+  const SumParams sum{static_cast<const float*>(workspace), D.data, shape.rows, D.cols, p.ld, D.ld,
+                      split.splits, D.dtype, accumulate,
+                      reinterpret_cast<uintptr_t>(D.data) % 16 == 0 && D.ld % 4 == 0};
+  const int64_t blocks = ceil_div(shape.rows * (p.ld / 4), 256);
+  return launch_dependent(split_sum_kernel, unsigned(blocks < 4 * num_sms() ? blocks : 4 * num_sms()),
+                          256, 0, stream, sum);
 }
 
 mao_status product_read_and_clear_error(cudaStream_t stream) { return read_and_clear_error(stream); }

@@ -140,8 +140,8 @@ def test_quantize_refusals(lib):
 def test_product_refusals(lib):
     ROW, COL, TILE = 1, 2, 3
 
-    def call(a, b, d, form=0, off=None, groups=1):
-        return lib.fp8_product(ref(a), ref(b), ref(d), form, off, groups, 0, None)
+    def call(a, b, d, form=0, off=None, groups=1, ws=None):
+        return lib.fp8_product(ref(a), ref(b), ref(d), form, off, groups, 0, ws, 0, None)
 
     a, b, d = fp8(8, 32, ROW), fp8(16, 32, TILE), mat(8, 16)
     bad, uns, mis = 1, 2, 3
@@ -150,7 +150,9 @@ def test_product_refusals(lib):
     assert call(a, b, d, groups=0) == bad
     assert call(a, b, d, groups=2) == bad                              # groups need offsets
     assert call(a, b, d, off=FAKE, groups=1025) == uns
-    assert call(a, b, d, off=FAKE + 1) == mis
+    assert call(a, b, d, off=FAKE + 1) == mis and call(a, b, d, ws=FAKE + 16) == mis
+    assert lib.fp8_product_workspace_bytes(None, ref(b), 0) == 0
+    assert lib.fp8_product_workspace_bytes(ref(a), ref(b), 3) == 0
     assert call(a, b, d, off=FAKE, groups=2) == bad                    # one matrix, two groups
     assert call(fp8(8, 32, COL), b, d) == bad and call(a, fp8(16, 32, ROW), d) == bad
     assert call(a, fp8(16, 33, TILE), d) == bad and call(a, b, mat(8, 17)) == bad

@@ -167,6 +167,30 @@ def test_product_dense(cuda, form, out, shape):
     check_product(y, av, bv, form, None)
 
 
+@pytest.mark.parametrize("form", ["nt", "nn", "tn"])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_product_long_sum_is_split(cuda, form, out, accumulate):
+    """Few outputs and a long sum: parts of it, of unlike sizes, added up in their order."""
+    deep = 7001
+    R, N, K = {"nt": (37, 130, deep), "nn": (37, deep, 130), "tn": (deep, 37, 130)}[form]
+    A, As, B, Bs, av, bv = operands(form, R, N, K, 1, 31, cuda)
+    shape = ox.product(av, bv, form, None).shape
+    base = randn(3, *shape).to(dt(out)).to(cuda)
+    y = base.clone()
+    assert mao.lib().fp8_product_workspace_bytes(
+        mao.ctypes.byref(mao._fp8(A, As, "col" if form == "tn" else "row", "A")),
+        mao.ctypes.byref(mao._fp8(B, Bs, "col" if form == "tn" else "tile", "B")),
+        {"nt": 0, "nn": 1, "tn": 2}[form]) > 0
+    mao.fp8_product(A, As, B, Bs, form, out=y, accumulate=accumulate)
+    mao.sync_status()
+    check_product(y, av, bv, form, None, np64(base).reshape(shape) if accumulate else None)
+    z = base.clone()  # too small a workspace: in one part
+    mao.fp8_product(A, As, B, Bs, form, out=z, accumulate=accumulate,
+                    ws=torch.empty(256, dtype=torch.uint8, device=cuda))
+    check_product(z, av, bv, form, None, np64(base).reshape(shape) if accumulate else None)
+
+
 SIZES = [[0, 128, 0, 256, 384, 0], [128], [0, 0], [640, 128, 0, 0, 128], [128] * 9]
 
 
