@@ -255,9 +255,11 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_back_kernel(const Rout
   __syncwarp();
   float ds = id >= 0 ? p.scale * p.dweights[t * p.top_k + lane] : 0.0f;
   if (p.renorm) {
-    const float inv = 1.0f / (warp_sum(sj) + 1e-20f);
-    const float mean = warp_sum(ds * (sj * inv));
-    ds = id >= 0 ? (ds - mean) * inv : 0.0f;
+    // divided, not multiplied by a reciprocal: a lone expert's share is then exactly 1, and
+    // its gradient exactly 0
+    const float total = warp_sum(sj) + 1e-20f;
+    const float mean = warp_sum(ds * (sj / total));
+    ds = id >= 0 ? (ds - mean) / total : 0.0f;
   }
   // with renorm the weights do not change when all chosen scores grow alike: the sum is 0
   const float dot = !sigmoid && !p.renorm ? warp_sum(ds * sj) : 0.0f;

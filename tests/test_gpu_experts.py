@@ -387,6 +387,15 @@ def test_route_one_and_no_token(cuda):
     assert mao.expert_route(x, 4)[1].tolist() == [[0, 3, 1, 2]]
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_lone_expert_has_no_gradient(cuda, score):
+    """With renorm a single expert's weight is 1 whatever its score."""
+    x = randn(5, 300, 60).to(cuda)
+    w, ids = mao.expert_route(x, 1, score=score, scale=2.5)
+    assert (w == 2.5).all()
+    assert (mao.expert_route_backward(x, ids, randn(6, 300, 1).to(cuda), score=score, scale=2.5) == 0).all()
+
+
 def test_route_nan_and_infinity(cuda):
     x = torch.tensor([[1.0, float("nan"), 2.0, 0.0], [1.0, float("inf"), 2.0, 0.0]], device=cuda)
     w, ids = mao.expert_route(x, 2)
