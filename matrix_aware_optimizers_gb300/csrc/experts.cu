@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(256) combine_back_kernel(const CombineBackPara
   const int64_t t = used ? slot / p.top_k : 0;
   const float w = used ? (p.weights ? p.weights[slot] : 1.0f) : 0.0f;
   float dot = 0.0f;
-#pragma unroll 2
+#pragma unroll 1
   for (int64_t c = lane * 8; c < p.cols; c += 256) {
     float g[8], v[8];
     if (used) {
