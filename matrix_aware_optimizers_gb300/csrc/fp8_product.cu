@@ -496,8 +496,8 @@ __device__ __forceinline__ void store16(const ProductParams& p, const Tile& t, i
 }
 
 // The same for bf16 rows that take 16-byte stores, by the four warps that hold 128 columns i
-// (i0 is the first): they transpose their sixteen rows in `buf`, and bulk copies take them out,
-// one 256-byte piece of a row each. Between two uses of a buffer lies the other's barrier.
+// (i0 is the first): they transpose their sixteen rows in `buf` and write whole 256-byte
+// pieces of rows. Between two uses of a buffer lies the other buffer's barrier.
 template <int FORM>
 __device__ __forceinline__ void store16_wide(const ProductParams& p, const Tile& t, int j, int i0,
                                              const float (&v)[16], uint8_t* buf, int quad, int part,
@@ -513,19 +513,25 @@ __device__ __forceinline__ void store16_wide(const ProductParams& p, const Tile&
     const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
     *reinterpret_cast<uint32_t*>(s + c * PITCH) = odd ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
   }
-  // the copies out of the other buffer have been read before its next use, which follows the
-  // barrier
-  fence_async_smem();
-  if (lane < 4) bulk_wait_read();
   asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
-  const int c = 4 * quad + lane;
-  if (lane < 4 && j + c < t.j_end && i0 < p.I) {
-    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + (t.row0 + j + c) * p.ld + i0;
-    const uint32_t bytes = 2u * uint32_t(min(HALF, p.I - i0));
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(d),
-                 "r"(smem_u32(buf + c * PITCH)), "r"(bytes)
-                 : "memory");
-    bulk_commit();
+  const int i = i0 + 8 * (lane & 15);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = 4 * quad + 2 * h + (lane >> 4);
+    if (j + c >= t.j_end || i >= p.I) continue;
+    const uint4 x = *reinterpret_cast<const uint4*>(buf + c * PITCH + 16 * (lane & 15));
+    const int64_t row = t.row0 + j + c;
+    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + row * p.ld + i;
+    if (i + 8 <= p.I) {
+      asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(d), "r"(x.x),
+                   "r"(x.y), "r"(x.z), "r"(x.w)
+                   : "memory");
+    } else {
+      const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (i + q < p.I) d[q] = e[q];
+    }
   }
 }
 
@@ -841,7 +847,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       ++local;
     }
-    bulk_wait_all();  // copies complete before the CTA leaves
     __syncwarp();
   } else {
     // ------------------------------------------------------------ scales (both CTAs)
@@ -1014,7 +1019,7 @@ mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, 
   p.groups = groups;
   p.dtype = D.dtype;
   p.accumulate = accumulate != 0;
-  p.wide = D.dtype == MAO_BF16 && !accumulate && D.cols % 8 == 0 && reinterpret_cast<uintptr_t>(D.data) % 16 == 0 && D.ld * es % 16 == 0;
+  p.wide = D.dtype == MAO_BF16 && !accumulate && reinterpret_cast<uintptr_t>(D.data) % 16 == 0 && D.ld * es % 16 == 0;
   p.sp_words = reinterpret_cast<uintptr_t>(B.scales) % 4 == 0 && B.scale_ld % 4 == 0;
   p.sq_words = reinterpret_cast<uintptr_t>(A.scales) % 4 == 0 && A.scale_ld % 4 == 0;
   p.timeout_ns = wait_limit_ns();
