@@ -483,7 +483,7 @@ enum {
  *              outputs and a long sum is then split over the sum, if the buffer has
  *              fp8_product_workspace_bytes(A, B, form) bytes (0 where a split would not pay),
  *              and its parts added up in a fixed order by a second kernel. Clobbered.
- *   Limits: groups <= 1024; A, B codes at most 2^31 rows in all. Products of e4m3 values are
+ *   Limits: groups <= 1024; A, B at most 2^31 - 1024 rows in all and columns, D 2^25 columns. Products of e4m3 values are
  *   exact in fp32; the order of the sums is fixed, so results are the same each time.
  *   Codes that a NaN scale (255) covers are not supported: fp8_quantize never writes it.
  */

@@ -11,6 +11,7 @@ using namespace mao;
 namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 31;
+constexpr int64_t kMaxCodes = kMaxRows - 1024;  // rows or columns of codes: tile ends fit 32 bits
 
 bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 
@@ -29,7 +30,7 @@ mao_status check_fp8(const mao_fp8* m, int32_t blocks) {
     return MAO_ERR_INVALID_ARG;
   if (m->scale_ld < (blocks == MAO_BLOCKS_COL ? m->cols : ceil_div(m->cols, 128)))
     return MAO_ERR_INVALID_ARG;
-  if (m->rows > kMaxRows || m->cols > kMaxRows || m->rows * m->count >= kMaxRows)
+  if (m->rows > kMaxCodes || m->cols > kMaxCodes || m->rows * m->count > kMaxCodes)
     return MAO_ERR_UNSUPPORTED;
   if (m->rows == 0) return MAO_OK;
   if (!m->codes || !m->scales) return MAO_ERR_INVALID_ARG;

@@ -1025,7 +1025,7 @@ mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, 
   p.timeout_ns = wait_limit_ns();
   // tiles at most: every group may end in a part of one
   const int64_t tiles = (tn ? ceil_div(p.J, TILE) * groups : ceil_div(A.rows, TILE) + groups) * p.tiles_i;
-  if (tiles > 0x7FFFFFFF || p.tiles_i > (1 << 17) || A.cols > 0x7FFFFFFF || B.cols > 0x7FFFFFFF) return MAO_ERR_UNSUPPORTED;
+  if (tiles > 0x7FFF0000 || p.tiles_i > (1 << 17)) return MAO_ERR_UNSUPPORTED;
   static std::once_flag once[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MAO_ERR_CUDA;

@@ -134,6 +134,7 @@ def test_quantize_refusals(lib):
     assert call(x, row=fp8(9, 40, ROW), index=FAKE + 2, n=9, copies=1) == mis
     assert call(x, row=fp8(9, 40, ROW, count=2), batch=2, stride=160, index=FAKE, n=9, copies=1) == bad
     assert call(x, row=fp8(1 << 31, 40, ROW), index=FAKE, n=1 << 31, copies=1) == uns
+    assert call(x, row=fp8((1 << 31) - 1000, 40, ROW), index=FAKE, n=(1 << 31) - 1000, copies=1) == uns
     assert call(mat(0, 40, data=None), row=fp8(0, 40, ROW)) == 0       # no rows: nothing to do
 
 

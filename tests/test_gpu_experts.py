@@ -325,6 +325,25 @@ def test_product_in_a_graph(cuda):
         check_product(y, av, bv, "nt", off)
 
 
+def test_product_wait_limit(cuda):
+    """With a limit of 0 every wait that is not over at once gives up: the error is reported,
+    and the next product is whole again."""
+    A, As, B, Bs, av, bv = operands("nt", 600, 300, 4000, 1, 8, cuda)
+    torch.cuda.synchronize()
+    limit = mao.get_wait_limit()
+    mao.set_wait_limit(0)
+    try:
+        mao.fp8_product(A, As, B, Bs, "nt", out_dtype=torch.float32)
+        with pytest.raises(mao.MaoError) as e:
+            mao.sync_status()
+        assert "TIMEOUT" in str(e.value)
+    finally:
+        mao.set_wait_limit(limit)
+    y = mao.fp8_product(A, As, B, Bs, "nt", out_dtype=torch.float32)
+    mao.sync_status()
+    check_product(y, av, bv, "nt", None)
+
+
 # ------------------------------------------------------------------------------ routing
 
 
