@@ -35,6 +35,11 @@ __device__ __forceinline__ uint32_t order_of(float key) {
 //
 // One warp per token; lane l holds experts 32 i + l. The softmax is one maximum, one sum. Keys
 // are compared as ordered integers.
+//
+// The instructions bound it (about 1070 per token of 256 experts in 8 runs with sigmoid scores,
+// 70% of the issue slots), not its 17 MB: 16,384 tokens take 20 us, and the gradient, which for
+// sigmoid scores reads only the chosen logits, 8.5 us. Choosing the best one by one over all
+// keys took 35 us.
 
 constexpr int ROUTE_WARPS = 4;
 
@@ -308,7 +313,9 @@ struct PickBack {
 // PLAN_CHUNK copies: its warps count theirs per expert, 32 at a time (equal experts in a
 // warp find each other by ballots), which also ranks every copy within its warp. A copy's row
 // is the expert's offset plus the counts of the blocks and warps before it plus its rank.
-// Integer sums only: the result does not depend on the order in which blocks run.
+// Integer sums only: the result does not depend on the order in which blocks run. Latency
+// bounds it: 131,072 copies among 256 experts take 6.5 us to count and 11 to place; up to
+// 4096 copies one block does both.
 
 constexpr int PLAN_WARPS = 16;
 constexpr int PLAN_ROUNDS = 8;
@@ -494,7 +501,8 @@ struct CombineParams {
   int32_t zdt, ydt, top_k;
 };
 
-// Threads of a row own eight columns each; a block holds as many tokens as fit.
+// Threads of a row own eight columns each; a block holds as many tokens as fit. HBM bounds it:
+// 8192 tokens of 8 x 2048 bf16 take 55 us (5.5 TB/s).
 template <bool VEC>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
   wait_for_previous();
@@ -529,7 +537,9 @@ struct CombineBackParams {
 };
 
 // One warp per row of Z: its copy's token gives dZ's row, and the dot product of the two rows
-// the copy's weight's gradient.
+// the copy's weight's gradient; no sums across warps, and none over copies. HBM bounds it: the
+// gradient of the case above takes 119 us (5.4 TB/s; 126 and 163 with the column loop unrolled
+// twice and four times, which costs resident warps).
 template <bool VEC>
 __global__ void __launch_bounds__(256) combine_back_kernel(const CombineBackParams p) {
   wait_for_previous();

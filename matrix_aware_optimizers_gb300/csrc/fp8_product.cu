@@ -16,18 +16,34 @@
 // the way.
 //
 // Roles per CTA (416 threads):
-//   warp 0        TMA producer: a 128 x 128 box of each operand per 128-deep block, into a
-//                 ring of 32 KB stages
-//   warp 1        TMEM allocation; in the even CTA one thread copies the scale words into TMEM
-//                 (tcgen05.cp) and issues the products
-//   warps 2..9    epilogue: two warps per 32-lane quadrant of TMEM; lane = i, so a row of D is
-//                 written by consecutive lanes
+//   warp 0        TMA producer: a 128 x 128 box of P and the tile's rows of Q per 128-deep
+//                 block, into a ring of six 32 KB stages
+//   warp 1        TMEM allocation; in the even CTA the whole warp runs the loop, converged, and
+//                 one lane copies the scale words into TMEM (tcgen05.cp) and issues the products
+//                 (issued from a divergent lane, the descriptors' arithmetic cost more than the
+//                 products: 387 us against 338 on the dense forward below)
+//   warps 2..9    epilogue: two warps per 32-lane quadrant of TMEM; lane = i. bf16 rows are
+//                 transposed through shared memory and stored 16 bytes per lane; fp32 rows are
+//                 stored as they come, 128 bytes per warp. Both go past L1 (no_allocate: the
+//                 fp32 gradient below went from 358 to 326 us by that alone)
 //   warps 10..12  scales: gather the scale bytes of four blocks, from whichever layout they
 //                 have, into the words that tcgen05.cp expects
 // TMEM (512 columns) holds two accumulators of 256 columns that share 32 of them (columns
 // 0..255 and 224..479) and two sets of scale words (480..503). The shared columns are drained
 // first: the next tile's products wait for them only, so the rest of a tile's epilogue runs
-// under the next tile's products.
+// under the next tile's products. Without sharing, tiles of 224 columns fit twice; they were
+// slower (320 against 301 us dense), as every block of P then serves fewer columns.
+//
+// What bounds it: a pair's block of 256 x 256 x 128 takes 512 cycles of the tensor cores and
+// brings 32 KB into each SM, which near 55 bytes per cycle and SM takes as long; products
+// that run back to back also meet the power limit. Measured alone (CUDA events) and in a run
+// of 0.15 s, on experts 128 x [1536 x 2048], 65,536 rows:
+//   dense 8192 x 14336 x 4096, bf16 out     290 us (3.3 PFLOP/s), 343 us in a run
+//   forward (nt), bf16 out                  177 us (2.3 PFLOP/s), 206 us in a run
+//   input gradient (nn, 128 x [2048 x 768]) 94 us, 103 us in a run
+//   weight gradient (tn), fp32 out          325 us (5.7 TB/s, the outputs' 1.6 GB bound it)
+// Parts of the work taken out, to see what they cost (forward, 174 us): no stores 156, no loads
+// of Q 165, all loads from the same L2 lines 154. The tensor pipe is active 58% of the time.
 // Barriers and their bounded waits are as in the Newton–Schulz product kernel.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -350,6 +366,11 @@ __device__ __forceinline__ int next_tile(const ProductParams& p, const int* lo, 
 
 // ------------------------------------------------------------------ scales
 
+// Where the scales come from takes a path of their own, since their bytes lie in the order of
+// the quantised tensor: a byte per row and block, or per block and column, or per tile. A lane
+// issues all of a group's loads before it uses one (done byte by byte, each waiting for the one
+// before, the weight gradient took 394 us instead of 369).
+//
 // The scale words of four blocks (from kb on) for 128 rows, row r as tcgen05.cp expects it: at
 // 16 (r % 32) + 4 (r / 32). Each lane of a warp gathers four words; the loads of a group are
 // all issued before the first is used. Blocks past the last and rows past `n` get 1.0 (they
@@ -944,6 +965,7 @@ __global__ void __launch_bounds__(256) split_sum_kernel(const SumParams p) {
   }
 }
 
+// 768 x 768 over 32,768 rows: 26 us in eight parts, 76 whole; 1 x 4096 over 14,336: 15 and 32.
 // How many parts the depth of a product without groups is split into when its tiles leave
 // pairs of SMs idle: the number with the least time by a model of the two kernels (about
 // 0.25 us per block of the depth; 2.5 us for the second kernel and 3 TB/s for the partial

@@ -4,6 +4,18 @@
 // rows of eight columns each, 16-byte loads), finds the largest magnitudes of the tile's row
 // blocks, column blocks or of the whole tile, and writes the codes: one pass over the input
 // whatever the blocks, both directions included.
+//
+// With y = x 2^-e exact, the only rounding is that of the code, and the code and scale do not
+// depend on how or where they are computed.
+//
+// HBM bounds it, except for both directions of gathered bf16 rows, which the instructions
+// bound (fifteen per entry, 67% of the issue slots). So bf16 maxima are taken two to a
+// register and products two to an instruction, and registers are kept to 64 for four blocks per
+// SM (bf16; two for fp32): with 121 registers the gathered both-direction pass took 133 us
+// instead of 94. Blocks of 512 and 1024 threads were slower everywhere (80 and 150 us against 61
+// for bf16 rows). Measured, 65,536 x 2048: bf16 row 61 us (6.6 TB/s), column 60, tile 59, both
+// 80 (6.7 TB/s); fp32 row 101 us (6.7 TB/s), both 130; 65,536 + padding rows gathered from
+// 8192, bf16, both: 94 us; 128 matrices of 1536 x 2048, bf16, tile: 166 us (7.3 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
