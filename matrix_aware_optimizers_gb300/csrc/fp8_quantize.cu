@@ -8,14 +8,16 @@
 // With y = x 2^-e exact, the only rounding is that of the code, and the code and scale do not
 // depend on how or where they are computed.
 //
-// HBM bounds it, except for both directions of gathered bf16 rows, which the instructions
-// bound (fifteen per entry, 67% of the issue slots). So bf16 maxima are taken two to a
-// register and products two to an instruction, and registers are kept to 64 for four blocks per
-// SM (bf16; two for fp32): with 121 registers the gathered both-direction pass took 133 us
-// instead of 94. Blocks of 512 and 1024 threads were slower everywhere (80 and 150 us against 61
-// for bf16 rows). Measured, 65,536 x 2048: bf16 row 61 us (6.6 TB/s), column 60, tile 59, both
-// 80 (6.7 TB/s); fp32 row 101 us (6.7 TB/s), both 130; 65,536 + padding rows gathered from
-// 8192, bf16, both: 94 us; 128 matrices of 1536 x 2048, bf16, tile: 166 us (7.3 TB/s).
+// HBM bounds it, except for both directions of gathered bf16 rows, which instructions and
+// their latency bound (twelve per entry, 60% of the issue slots). So bf16 maxima are taken two
+// to a register and products two to an instruction, an entry is unpacked once for both
+// directions, tiles that reach over an edge or hold NaN or infinities take a path out of line, and
+// registers are kept to 64 for four blocks per SM (bf16; two for fp32): with 121 registers the
+// gathered both-direction pass took 133 us instead of 87. Blocks of 512 and 1024 threads were
+// slower everywhere (80 and 150 us against 61 for bf16 rows). Measured, 65,536 x 2048: bf16 row 60
+// us (6.8 TB/s), column 59, tile 59, both 80 (6.8 TB/s); fp32 row 100 us (6.7 TB/s), both 125;
+// 81,792 rows gathered from 8192, bf16, both: 87 us; 128 matrices of 1536 x 2048, bf16, tile: 168
+// us (7.2 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -152,9 +154,10 @@ __device__ __forceinline__ uint2 encode(const Raw<BF16>& x, const float2 (&inv)[
   return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
-// FULL: the whole tile lies inside the matrix and its rows take 16-byte loads.
-template <bool BF16, bool ROW, bool COL, bool TILE, bool FULL>
-__device__ __forceinline__ void quantize_tile(const QuantParams& p, int64_t matrix, int rb, int cb,
+// A tile wherever it lies and whatever it holds; out of line, so that the common path keeps
+// its registers.
+template <bool BF16, bool ROW, bool COL, bool TILE>
+__device__ __noinline__ void quantize_tile(const QuantParams& p, int64_t matrix, int rb, int cb,
                                               const uint8_t* base, int64_t ld, bool vec,
                                               uint32_t (*part)[128], uint8_t* col_byte,
                                               const int32_t* src) {
@@ -162,8 +165,8 @@ __device__ __forceinline__ void quantize_tile(const QuantParams& p, int64_t matr
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cg = tid & 15, rr = tid >> 4;  // columns 8 cg .., rows rr + STEP it
   const int64_t c0 = int64_t(cb) * 128 + 8 * cg;
-  const int nc = FULL ? 8 : int(min(int64_t(8), p.cols - c0));  // columns here (may be <= 0)
-  const int nr = FULL ? 128 : int(min(int64_t(128), p.rows - int64_t(rb) * 128));
+  const int nc = int(min(int64_t(8), p.cols - c0));  // columns here (may be <= 0)
+  const int nr = int(min(int64_t(128), p.rows - int64_t(rb) * 128));
 
   Raw<BF16> x[IT];
   const uint8_t* at = base + (int64_t(rb) * 128 * ld + c0) * ES;
@@ -171,7 +174,7 @@ __device__ __forceinline__ void quantize_tile(const QuantParams& p, int64_t matr
   for (int it = 0; it < IT; ++it) {
     const int r = STEP * it + rr;
     const uint8_t* a;
-    bool have = FULL || (r < nr && nc > 0);
+    bool have = r < nr && nc > 0;
     if (src) {
       const int32_t i = src[r];
       have = have && i >= 0;
@@ -180,7 +183,7 @@ __device__ __forceinline__ void quantize_tile(const QuantParams& p, int64_t matr
       a = at + r * ld * ES;
     }
     if (!have) x[it].zero();
-    else if (FULL || (vec && nc == 8)) x[it].load(a);
+    else if (vec && nc == 8) x[it].load(a);
     else x[it].load_some(a, nc);
   }
 
@@ -232,7 +235,7 @@ __device__ __forceinline__ void quantize_tile(const QuantParams& p, int64_t matr
 
   const int64_t row0 = matrix * p.rows + int64_t(rb) * 128 + rr;  // of the stacked results
   auto put = [&](uint8_t* d, uint2 c) {
-    if (FULL || nc == 8) {
+    if (nc == 8) {
       *reinterpret_cast<uint2*>(d) = c;
     } else {
 #pragma unroll
@@ -264,7 +267,7 @@ __device__ __forceinline__ void quantize_tile(const QuantParams& p, int64_t matr
       const int byte = scale_byte(m);
       col_byte[tid] = uint8_t(byte);
       const int64_t c = int64_t(cb) * 128 + tid;
-      if (FULL || c < p.cols) p.col.scales[(matrix * p.row_tiles + rb) * p.col.scale_ld + c] = uint8_t(byte);
+      if (c < p.cols) p.col.scales[(matrix * p.row_tiles + rb) * p.col.scale_ld + c] = uint8_t(byte);
     }
     __syncthreads();
     const uint2 b = *reinterpret_cast<const uint2*>(&col_byte[8 * cg]);
@@ -289,7 +292,7 @@ __device__ __forceinline__ void quantize_tile(const QuantParams& p, int64_t matr
     uint8_t* sc = p.row.scales + row0 * p.row.scale_ld + cb;
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
-      if (FULL || (STEP * it + rr < nr && nc > 0)) {
+      if (STEP * it + rr < nr && nc > 0) {
         if (ROW) {
           const uint32_t m = !BF16 ? rmax[it % NR] : (it & 1) ? rmax[it / 2] & 0xFFFF0000u : rmax[it / 2] << 16;
           const int byte = scale_byte(m);
@@ -318,17 +321,166 @@ __device__ __forceinline__ void quantize_tile(const QuantParams& p, int64_t matr
     uint8_t* d = p.tile.codes + row0 * p.tile.ld + c0;
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
-      if (FULL || (STEP * it + rr < nr && nc > 0)) put(d, encode<BF16>(x[it], inv, bad));
+      if (STEP * it + rr < nr && nc > 0) put(d, encode<BF16>(x[it], inv, bad));
       d += STEP * p.tile.ld;
     }
     if (tid == 0) p.tile.scales[(matrix * p.row_tiles + rb) * p.tile.scale_ld + cb] = uint8_t(byte);
   }
 }
 
+// The codes of four entries, the first in the lowest byte.
+__device__ __forceinline__ uint32_t codes4(float2 a, float2 b) {
+  uint32_t c;
+  asm("{\n\t.reg .b16 x, y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\t"
+      "mov.b32 %0, {x, y};\n\t}"
+      : "=r"(c)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return c;
+}
+
+// A tile inside the matrix whose rows take 16-byte loads and that holds finite numbers only:
+// returns false, with nothing written, if there are others.
+template <bool BF16, bool ROW, bool COL, bool TILE>
+__device__ __forceinline__ bool quantize_full(const QuantParams& p, int64_t matrix, int rb, int cb,
+                                              const uint8_t* base, int64_t ld, uint32_t (*part)[128],
+                                              uint8_t* byte_of, const int32_t* src) {
+  constexpr int ES = BF16 ? 2 : 4;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cg = tid & 15, rr = tid >> 4;  // columns 8 cg .., rows rr + STEP it
+  Raw<BF16> x[IT];
+  const uint8_t* at = base + (int64_t(cb) * 128 + 8 * cg) * ES;
+  if (src) {
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int32_t i = src[STEP * it + rr];
+      x[it].zero();
+      if (i >= 0) x[it].load(at + int64_t(i) * ld * ES);
+    }
+  } else {
+    at += (int64_t(rb) * 128 + rr) * ld * ES;
+#pragma unroll
+    for (int it = 0; it < IT; ++it) x[it].load(at + int64_t(STEP * it) * ld * ES);
+  }
+  // largest magnitudes of the thread's share of rows and columns (bf16: two to a word)
+  constexpr int NR = BF16 ? IT / 2 : IT, NC = BF16 ? 4 : 8;
+  uint32_t rmax[NR], cmax[NC], all = 0u;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) cmax[i] = 0u;
+#pragma unroll
+  for (int h = 0; h < NR; ++h) {
+    if constexpr (BF16) {
+      uint32_t m[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = x[2 * h + q].w[i] & 0x7FFF7FFFu;
+          if (COL) cmax[i] = max2(cmax[i], a[i]);
+        }
+        m[q] = max2(max2(a[0], a[1]), max2(a[2], a[3]));
+      }
+      rmax[h] = max2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+      all = max2(all, rmax[h]);
+    } else {
+      uint32_t m = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t a = x[h].w[i] & 0x7FFFFFFFu;
+        m = max(m, a);
+        if (COL) cmax[i] = max(cmax[i], a);
+      }
+      rmax[h] = m;
+      all = max(all, m);
+    }
+  }
+  if (BF16) all = max(all & 0xFFFF0000u, all << 16);
+  if constexpr (COL) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const uint32_t other = __shfl_xor_sync(FULL_MASK, cmax[i], 16);
+      if constexpr (BF16) {
+        const uint32_t m = max2(cmax[i], other);
+        if (lane < 16) *reinterpret_cast<uint2*>(&part[warp][8 * cg + 2 * i]) = make_uint2(m << 16, m & 0xFFFF0000u);
+      } else {
+        if (lane < 16) part[warp][8 * cg + i] = max(cmax[i], other);
+      }
+    }
+  }
+  if constexpr (TILE) {
+    const uint32_t m = __reduce_max_sync(FULL_MASK, all);
+    if (lane == 0) part[warp][0] = m;
+  }
+  if (__syncthreads_or(all >= INF_BITS)) return false;
+  const int64_t row0 = matrix * p.rows + int64_t(rb) * 128;  // of the stacked results
+  if (COL && tid < 128) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) m = max(m, part[w][tid]);
+    byte_of[tid] = uint8_t(scale_byte(m));
+    p.col.scales[(matrix * p.row_tiles + rb) * p.col.scale_ld + int64_t(cb) * 128 + tid] = byte_of[tid];
+  }
+  if constexpr (ROW) {
+#pragma unroll
+    for (int h = 0; h < NR; ++h)
+#pragma unroll
+      for (int o = 8; o; o >>= 1) {
+        const uint32_t other = __shfl_xor_sync(FULL_MASK, rmax[h], o);
+        rmax[h] = BF16 ? max2(rmax[h], other) : max(rmax[h], other);
+      }
+  }
+  float2 inv[4];  // of the columns, or of the tile
+  if constexpr (COL) {
+    __syncthreads();
+    const uint2 b = *reinterpret_cast<const uint2*>(&byte_of[8 * cg]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = (i < 2 ? b.x : b.y) >> (16 * (i & 1));
+      inv[i] = make_float2(scale_inverse(h & 255u), scale_inverse((h >> 8) & 255u));
+    }
+  }
+  if constexpr (TILE) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) m = max(m, part[w][0]);
+    const int byte = scale_byte(m);
+    inv[0] = inv[1] = inv[2] = inv[3] = make_float2(scale_inverse(byte), scale_inverse(byte));
+    if (tid == 0) p.tile.scales[(matrix * p.row_tiles + rb) * p.tile.scale_ld + cb] = uint8_t(byte);
+  }
+  const Out& o = TILE ? p.tile : p.col;
+  uint8_t* dr = p.row.codes + (row0 + rr) * p.row.ld + int64_t(cb) * 128 + 8 * cg;
+  uint8_t* d = o.codes + (row0 + rr) * o.ld + int64_t(cb) * 128 + 8 * cg;
+  uint8_t* row_byte = byte_of + 128;
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    float2 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(x[it].value(2 * i), x[it].value(2 * i + 1));
+    if constexpr (ROW) {
+      const uint32_t m = !BF16 ? rmax[it % NR] : (it & 1) ? rmax[it / 2] & 0xFFFF0000u : rmax[it / 2] << 16;
+      const int byte = scale_byte(m);
+      const float2 s = make_float2(scale_inverse(byte), scale_inverse(byte));
+      *reinterpret_cast<uint2*>(dr + int64_t(STEP * it) * p.row.ld) =
+          make_uint2(codes4(mul2(v[0], s), mul2(v[1], s)), codes4(mul2(v[2], s), mul2(v[3], s)));
+      if (cg == 0) row_byte[STEP * it + rr] = uint8_t(byte);
+    }
+    if constexpr (COL || TILE)
+      *reinterpret_cast<uint2*>(d + int64_t(STEP * it) * o.ld) =
+          make_uint2(codes4(mul2(v[0], inv[0]), mul2(v[1], inv[1])), codes4(mul2(v[2], inv[2]), mul2(v[3], inv[3])));
+  }
+  if constexpr (ROW) {
+    __syncthreads();
+    if (tid < 128) p.row.scales[(row0 + tid) * p.row.scale_ld + cb] = row_byte[tid];
+  }
+  return true;
+}
+
 template <bool BF16, bool ROW, bool COL, bool TILE>
 __global__ void __launch_bounds__(THREADS, BF16 ? 4 : 2) quantize_kernel(const __grid_constant__ QuantParams p) {
   __shared__ uint32_t part[WARPS][128];
-  __shared__ __align__(8) uint8_t col_byte[128];
+  __shared__ __align__(8) uint8_t byte_of[256];  // scale bytes of the columns, of the rows
   __shared__ int32_t src[128];  // source rows of the tile, -1: zeros
   wait_for_previous();
   const unsigned tiles = unsigned(p.row_tiles) * unsigned(p.col_tiles);
@@ -339,7 +491,7 @@ __global__ void __launch_bounds__(THREADS, BF16 ? 4 : 2) quantize_kernel(const _
   if (p.stride) base += int64_t(z) * p.stride * ES;
   const int64_t ld = p.stride ? p.ld : p.lds[z];
   const bool vec = reinterpret_cast<uintptr_t>(base) % 16 == 0 && (ld * ES) % 16 == 0;
-  bool full = vec && int64_t(rb + 1) * 128 <= p.rows && int64_t(cb + 1) * 128 <= p.cols;
+  const bool full = vec && int64_t(rb + 1) * 128 <= p.rows && int64_t(cb + 1) * 128 <= p.cols;
   if (p.index) {
     const int64_t r = int64_t(rb) * 128 + threadIdx.x;
     if (threadIdx.x < 128) {
@@ -351,8 +503,9 @@ __global__ void __launch_bounds__(THREADS, BF16 ? 4 : 2) quantize_kernel(const _
   }
   const int64_t matrix = p.first + z;
   const int32_t* rows = p.index ? src : nullptr;
-  if (full) quantize_tile<BF16, ROW, COL, TILE, true>(p, matrix, rb, cb, base, ld, vec, part, col_byte, rows);
-  else quantize_tile<BF16, ROW, COL, TILE, false>(p, matrix, rb, cb, base, ld, vec, part, col_byte, rows);
+  if (full && quantize_full<BF16, ROW, COL, TILE>(p, matrix, rb, cb, base, ld, part, byte_of, rows)) return;
+  __syncthreads();  // the shared memory is used again
+  quantize_tile<BF16, ROW, COL, TILE>(p, matrix, rb, cb, base, ld, vec, part, byte_of, rows);
 }
 
 Out out_of(const mao_fp8* m) {
