@@ -22,10 +22,12 @@
 //                 one lane copies the scale words into TMEM (tcgen05.cp) and issues the products
 //                 (issued from a divergent lane, the descriptors' arithmetic cost more than the
 //                 products: 387 us against 338 on the dense forward below)
-//   warps 2..9    epilogue: two warps per 32-lane quadrant of TMEM; lane = i. bf16 rows are
-//                 transposed through shared memory and stored 16 bytes per lane; fp32 rows are
-//                 stored as they come, 128 bytes per warp. Both go past L1 (no_allocate: the
-//                 fp32 gradient below went from 358 to 326 us by that alone)
+//   warps 2..9    epilogue: two warps per 32-lane quadrant of TMEM; lane = i, so a warp
+//                 stores rows as they come: 128 bytes of an fp32 row, or, by pairs of lanes
+//                 that swap halves, 64 bytes of two bf16 rows; past L1 (no_allocate: the fp32
+//                 gradient below went from 358 to 326 us by that alone). Transposing bf16 rows in
+//                 shared memory for wider stores or bulk copies made no difference (335, 334
+//                 and 333 us dense, each in a run); fp32 rows got slower (423 and 468 us)
 //   warps 10..12  scales: gather the scale bytes of four blocks, from whichever layout they
 //                 have, into the words that tcgen05.cp expects
 // TMEM (512 columns) holds two accumulators of 256 columns that share 32 of them (columns
@@ -82,12 +84,7 @@ constexpr int TMEM_COLS = 512;
 constexpr int Q_BOXES = 8;                 // heights of boxes of Q: 16 (b + 1) rows
 constexpr int BAND = 8;                    // tiles of j that share a pass over i
 constexpr size_t TABLE_BYTES = size_t(2) * (MAX_GROUPS + 2) * 4;
-// bf16 output is staged: sixteen rows of D at 128 columns, two buffers for each half of the
-// epilogue's warps; the rows' pitch puts neighbouring rows in different banks
-constexpr int PITCH = 2 * HALF + 64;
-constexpr int STAGED = 16 * PITCH;
-constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + SF_SLOTS * SF_BYTES + 4 * STAGED +
-                        TABLE_BYTES + 256;
+constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + SF_SLOTS * SF_BYTES + TABLE_BYTES + 256;
 static_assert(SMEM <= 232448, "shared memory budget of one CTA");
 static_assert(SF_COL + SF_SETS * SF_COLS <= TMEM_COLS, "TMEM budget");
 
@@ -104,7 +101,7 @@ struct ProductParams {
   int32_t I, J;             // D's columns; D's rows (of a group, for MAO_TN)
   int32_t depth;            // K (MAO_TN: the group's rows)
   int32_t sp_rows;          // rows of scales of one matrix of P
-  int32_t tiles_i, groups, dtype, accumulate, wide;
+  int32_t tiles_i, groups, dtype, accumulate, paired;
   int32_t sp_words, sq_words;  // scales allow 4-byte loads
   int32_t splits, split_kb;    // parts of the depth (one group), blocks of each
   unsigned long long timeout_ns;
@@ -490,7 +487,6 @@ struct Scales {
 // ------------------------------------------------------------------ output
 
 // Sixteen rows of D (from row j on, those below j_end) at column i of this lane.
-template <int FORM>
 __device__ __forceinline__ void store16(const ProductParams& p, const Tile& t, int j, int i,
                                         const float (&v)[16], int lane) {
   const bool in = i < p.I;
@@ -510,50 +506,27 @@ __device__ __forceinline__ void store16(const ProductParams& p, const Tile& t, i
     return;
   }
   __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + row * p.ld + i;
+  if (p.paired) {
+    // rows c and c + 1 of lanes 2 l and 2 l + 1: the even lane writes both columns of row c, the
+    // odd lane both of row c + 1
+    const int odd = lane & 1;
+    d += odd ? p.ld - 1 : 0;
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[c], v[c + 1]);
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
+      const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
+      const uint32_t both = odd ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+      if (in && j + c + odd < t.j_end)  // an even number of columns: both or none are there
+        asm volatile("st.global.L1::no_allocate.u32 [%0], %1;" ::"l"(d), "r"(both) : "memory");
+      d += 2 * p.ld;
+    }
+    return;
+  }
 #pragma unroll
   for (int c = 0; c < 16; ++c)
     if (in && j + c < t.j_end)
       d[c * p.ld] = __float2bfloat16_rn(p.accumulate ? __bfloat162float(d[c * p.ld]) + v[c] : v[c]);
-}
-
-// The same for bf16 rows that take 16-byte stores, by the four warps that hold 128 columns i
-// (i0 is the first): they transpose their sixteen rows in `buf` and write whole 256-byte
-// pieces of rows. Between two uses of a buffer lies the other buffer's barrier.
-template <int FORM>
-__device__ __forceinline__ void store16_wide(const ProductParams& p, const Tile& t, int j, int i0,
-                                             const float (&v)[16], uint8_t* buf, int quad, int part,
-                                             int lane) {
-  // rows c and c + 1 of lanes 2 l and 2 l + 1: the even lane writes both columns of row c, the
-  // odd lane both of row c + 1
-  const int odd = lane & 1;
-  uint8_t* s = buf + odd * PITCH + 2 * (32 * quad + lane - odd);
-#pragma unroll
-  for (int c = 0; c < 16; c += 2) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[c], v[c + 1]);
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
-    const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
-    *reinterpret_cast<uint32_t*>(s + c * PITCH) = odd ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
-  }
-  asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
-  const int i = i0 + 8 * (lane & 15);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int c = 4 * quad + 2 * h + (lane >> 4);
-    if (j + c >= t.j_end || i >= p.I) continue;
-    const uint4 x = *reinterpret_cast<const uint4*>(buf + c * PITCH + 16 * (lane & 15));
-    const int64_t row = t.row0 + j + c;
-    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + row * p.ld + i;
-    if (i + 8 <= p.I) {
-      asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(d), "r"(x.x),
-                   "r"(x.y), "r"(x.z), "r"(x.w)
-                   : "memory");
-    } else {
-      const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&x);
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (i + q < p.I) d[q] = e[q];
-    }
-  }
 }
 
 // Clears columns i0 .. i0 + ni of rows j0 .. j1 of D, one row per turn of a warp.
@@ -584,10 +557,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem;
   uint8_t* sf = ring + STAGES * STAGE_BYTES;
-  uint8_t* staging = sf + SF_SLOTS * SF_BYTES;
-  int* lo = reinterpret_cast<int*>(staging + 4 * STAGED);
+  int* lo = reinterpret_cast<int*>(sf + SF_SLOTS * SF_BYTES);
   int* begin = lo + MAX_GROUPS + 2;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 4 * STAGED + TABLE_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sf + SF_SLOTS * SF_BYTES + TABLE_BYTES);
   uint64_t* full_bar = bars;                    // [STAGES]    (used in the even CTA)
   uint64_t* empty_bar = full_bar + STAGES;      // [STAGES]
   uint64_t* sf_full_bar = empty_bar + STAGES;   // [SF_SLOTS]  (used in the even CTA)
@@ -640,7 +612,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   // launched as a programmatic dependent: the set-up so far may overlap the previous kernel
   wait_for_previous();
-  make_table<FORM>(p, lo, begin, reinterpret_cast<int*>(staging));
+  make_table<FORM>(p, lo, begin, reinterpret_cast<int*>(sf));
   tc_fence_before();
   __syncthreads();
   const int total = begin[p.groups] * p.tiles_i * p.splits;
@@ -811,7 +783,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (FORM != MAO_TN && !p.accumulate)
       clear_rows(p, lo[p.groups] + int64_t(blockIdx.x) * EPI_WARPS + warp - 2, p.rows,
                  int64_t(gridDim.x) * EPI_WARPS, 0, p.I, lane);
-    int local = 0, buffer = 0;
+    int local = 0;
     Tile t;
     for (int tile = pair; tile < total; tile += npairs) {
       decode<FORM>(p, lo, begin, tile, t);
@@ -827,21 +799,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!wait_warp<false>(&tfull_bar[acc], uint32_t(local >> 1) & 1u, abort_flag, limit)) break;
       tc_fence_after();
       const uint32_t trow = tmem_base + (uint32_t(32 * quad) << 16) + uint32_t(acc * ACC1);
-      // this warp's 128 columns in eight steps: its half of the shared ones, then the others
+      // this warp's 128 columns in eight steps: its half of the shared ones, then of the others
+      // (every second sixteen, so that both warps have work in small tiles)
       const int shared0 = (acc ? 0 : ACC1) + 16 * part;
-      const int rest0 = (acc ? SHARED : 0) + (ACC1 / 2) * part;
+      const int rest0 = (acc ? SHARED : 0) + 16 * part;
       const int n = t.j_end - t.j0;
-      auto column = [&](int s) { return s == 0 ? shared0 : rest0 + 16 * (s - 1); };
+      auto column = [&](int s) { return s == 0 ? shared0 : rest0 + 32 * (s - 1); };
       auto out = [&](int s, const float(&v)[16]) {
         const int c = column(s);
         if (c >= n) return;
-        if (p.wide) {
-          store16_wide<FORM>(p, t, t.j0 + c, i - 32 * quad - lane, v, staging + (2 * part + buffer) * STAGED,
-                             quad, part, lane);
-          buffer ^= 1;
-        } else {
-          store16<FORM>(p, t, t.j0 + c, i, v, lane);
-        }
+        store16(p, t, t.j0 + c, i, v, lane);
       };
       // a step's columns are loaded while the step before is stored
       float va[16], vb[16];
@@ -1041,7 +1008,7 @@ mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, 
   p.groups = groups;
   p.dtype = D.dtype;
   p.accumulate = accumulate != 0;
-  p.wide = D.dtype == MAO_BF16 && !accumulate && reinterpret_cast<uintptr_t>(D.data) % 16 == 0 && D.ld * es % 16 == 0;
+  p.paired = D.dtype == MAO_BF16 && !accumulate && D.cols % 2 == 0 && reinterpret_cast<uintptr_t>(D.data) % 4 == 0 && D.ld % 2 == 0;
   p.sp_words = reinterpret_cast<uintptr_t>(B.scales) % 4 == 0 && B.scale_ld % 4 == 0;
   p.sq_words = reinterpret_cast<uintptr_t>(A.scales) % 4 == 0 && A.scale_ld % 4 == 0;
   p.timeout_ns = wait_limit_ns();
@@ -1075,7 +1042,7 @@ mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, 
     p.d = workspace;
     p.ld = round_up(D.cols, 4);
     p.dtype = MAO_F32;
-    p.accumulate = p.wide = 0;
+    p.accumulate = p.paired = 0;
   }
   const int64_t units = tiles * p.splits;
   const int64_t pairs = units < num_sms() / 2 ? units : num_sms() / 2;
