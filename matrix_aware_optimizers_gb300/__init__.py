@@ -79,6 +79,8 @@ def _mat(t, allow_none=False, like=None):
         raise ValueError("expected a CUDA tensor")
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError("expected a 2-D tensor with unit column stride")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError("expected a tensor whose rows do not overlap")
     if t.dtype not in _DT:
         raise ValueError("dtype must be float32, bfloat16 or int8")
     return _abi.MaoMat(t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]),

@@ -493,6 +493,25 @@ def test_combine_dropped_tokens_and_slices(cuda):
 # ------------------------------------------------------------------------------ refusals
 
 
+def test_overlapping_rows_are_refused(cuda):
+    """A row repeated by a stride of 0 is not a matrix in memory."""
+    row = torch.zeros(1, 32, device=cuda).expand(8, 32)
+    slots = torch.zeros(8, dtype=torch.int32, device=cuda)
+    places = torch.zeros(8, 1, dtype=torch.int32, device=cuda)
+    with pytest.raises(ValueError):
+        mao.fp8_quantize(row, "row")
+    with pytest.raises(ValueError):
+        mao.fp8_quantize(row[None].expand(2, 8, 32), "row")
+    with pytest.raises(ValueError):
+        mao.fp8_quantize(torch.zeros(2, 1, 32, device=cuda).expand(2, 8, 32), "row")
+    with pytest.raises(ValueError):
+        mao.expert_route(row, 2)
+    with pytest.raises(ValueError):
+        mao.expert_combine_backward(row, torch.zeros(8, 32, device=cuda), places, slots)
+    with pytest.raises(ValueError):
+        mao.apply_update(torch.zeros(8, 32, device=cuda), 0.1, U=row)
+
+
 def test_refusals(cuda):
     x = torch.zeros(4, 32, device=cuda)
     codes, scales = mao.fp8_quantize(x, "row")
