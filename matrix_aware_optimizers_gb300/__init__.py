@@ -409,6 +409,7 @@ def dion_step(X, M, G, Q, mu, lr, P_out=None, ws=None, stream=None, X_out=None):
 # ---------------------------------------------------------------- expert layers
 
 _BLOCKS = {"row": _abi.MAO_BLOCKS_ROW, "col": _abi.MAO_BLOCKS_COL, "tile": _abi.MAO_BLOCKS_TILE}
+_KINDS = {"row": ("row",), "col": ("col",), "tile": ("tile",), "both": ("row", "col")}
 _FORM = {"nt": _abi.MAO_NT, "nn": _abi.MAO_NN, "tn": _abi.MAO_TN}
 _SCORE = {"softmax": _abi.MAO_SCORE_SOFTMAX, "sigmoid": _abi.MAO_SCORE_SIGMOID}
 _GROUP_SCORE = {"max": _abi.MAO_GROUP_MAX, "top2": _abi.MAO_GROUP_TOP2}
@@ -421,6 +422,33 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty_strided(shape, strides, dtype, device, stream):
+    if stream is None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+
+
+_FLOATS = {torch.float32: _abi.MAO_F32, torch.bfloat16: _abi.MAO_BF16}
+
+
+def _desc(t):
+    """_mat of a float32 or bfloat16 matrix, with as few calls as it takes."""
+    shape, st = t.shape, t.stride()
+    if len(shape) != 2 or (st[1] != 1 and shape[1] > 1) or not t.is_cuda:
+        raise ValueError("expected a 2-D CUDA tensor with unit column stride")
+    rows, cols = shape
+    ld = st[0]
+    if ld < cols:
+        if rows > 1:
+            raise ValueError("expected a tensor whose rows do not overlap")
+        ld = cols
+    dt = _FLOATS.get(t.dtype)
+    if dt is None:
+        raise ValueError("dtype must be float32 or bfloat16")
+    return _abi.MaoMat(t.data_ptr(), rows, cols, ld, dt, 0)
 
 
 def _raw_stream(stream, t):
@@ -504,54 +532,60 @@ def fp8_quantize(X, blocks, rows=None, copies=1, out=None, stream=None):
     many = isinstance(X, (list, tuple))
     x0 = X[0] if many else X
     stacked = many or x0.dim() == 3
-    if blocks not in ("row", "col", "tile", "both"):
-        raise ValueError("blocks must be row, col, tile or both")
     if many:
         mats, batch, stride = _mats(list(X)), len(X), 0
         R, C = x0.shape
-    elif x0.dim() == 3:
+    elif stacked:
         batch, R, C = x0.shape
         if batch == 0:
             raise ValueError("no matrices")
-        if not x0.is_cuda or x0.dtype not in (torch.float32, torch.bfloat16) or x0.stride(2) != 1:
-            raise ValueError("expected a float32 or bfloat16 CUDA tensor with unit column stride")
+        m = _desc(x0[0])
         stride = x0.stride(0) if batch > 1 else 0
         if batch > 1 and stride < 1:
             raise ValueError("stacked matrices need a positive stride")
-        ld = max(x0.stride(1), C) if R > 1 else C
-        mats = (_abi.MaoMat * 1)(_abi.MaoMat(x0.data_ptr(), R, C, ld, _DT[x0.dtype], 0))
+        mats = ctypes.byref(m)
     else:
-        mats, batch, stride = _mats([x0]), 1, 0
-        R, C = x0.shape
+        m = _desc(x0)
+        mats, batch, stride = ctypes.byref(m), 1, 0
+        R, C = m.rows, m.cols
     index, n_index = None, 0
-    if rows is not None:
+    if rows is None:
+        copies = 0
+    else:
         if batch != 1:
             raise ValueError("rows go with a single matrix")
         if copies < 1:
             raise ValueError("copies must be at least 1")
         n_index = R = rows.numel()
         index = _dense_ptr(rows, torch.int32, rows.shape, "rows")
-    kinds = ("row", "col") if blocks == "both" else (blocks,)
-    desc = {"row": None, "col": None, "tile": None}
+    kinds = _KINDS.get(blocks)
+    if kinds is None:
+        raise ValueError("blocks must be row, col, tile or both")
+    desc = {}
     if out is None:
-        out, wide, dev = [], -(-C // 16) * 16, x0.device
-        lead = (batch,) if stacked else ()
+        out, wide = [], (C + 15) // 16 * 16
         for k in kinds:
-            codes = _empty(lead + (R, wide), torch.float8_e4m3fn, dev, stream)
-            sshape = _scale_shape(R, C, k)
-            scales = _empty(lead + sshape, torch.uint8, dev, stream)
-            desc[k] = ctypes.byref(_abi.MaoFp8(codes.data_ptr(), scales.data_ptr(), R, C, wide,
-                                               sshape[1], batch, _BLOCKS[k]))
-            out += [codes if wide == C else codes[..., :C], scales]
+            sr, sc = _scale_shape(R, C, k)
+            size, ssize, strides = (R, C), (sr, sc), (wide, 1)
+            if stacked:
+                size, ssize, strides = (batch, R, C), (batch, sr, sc), (R * wide, wide, 1)
+            if wide == C:
+                codes, cp = _out(None, size, torch.float8_e4m3fn, "", x0, stream)
+            else:  # rows start at multiples of 16 bytes
+                codes = _empty_strided(size, strides, torch.float8_e4m3fn, x0.device, stream)
+                cp = codes.data_ptr()
+            scales, sp = _out(None, ssize, torch.uint8, "", x0, stream)
+            desc[k] = ctypes.byref(_abi.MaoFp8(cp, sp, R, C, wide, sc, batch, _BLOCKS[k]))
+            out += (codes, scales)
     else:
         if len(out) != 2 * len(kinds):
             raise ValueError("out needs codes and scales for each kind of blocks")
         for i, k in enumerate(kinds):
             desc[k] = ctypes.byref(_fp8(out[2 * i], out[2 * i + 1], k, k))
-    st = lib().fp8_quantize(mats, batch, stride, index, n_index,
-                            int(copies) if rows is not None else 0, desc["row"], desc["col"],
-                            desc["tile"], _raw_stream(stream, x0))
-    _abi.check("fp8_quantize", st)
+    st = lib().fp8_quantize(mats, batch, stride, index, n_index, copies, desc.get("row"),
+                            desc.get("col"), desc.get("tile"), _raw_stream(stream, x0))
+    if st:
+        _abi.check("fp8_quantize", st)
     return tuple(out)
 
 
@@ -586,14 +620,20 @@ def fp8_product(A, a_scales, B, b_scales, form, offsets=None, out=None, out_dtyp
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = _empty(shape, out_dtype, A.device, stream)
-    if tuple(out.shape) != shape and not (tn and groups == 1 and tuple(out.shape) == shape[1:]):
-        raise ValueError("out must have shape %s" % (shape,))
-    d = out
-    if out.dim() == 3:
-        if groups > 1 and out.stride(0) != a.cols * out.stride(1):
-            raise ValueError("the groups' matrices follow each other without gaps")
-        d = out.as_strided((groups * a.cols, b.cols), (out.stride(1), out.stride(2)))
+        if out_dtype not in _FLOATS:
+            raise ValueError("out_dtype must be float32 or bfloat16")
+        out, op = _out(None, shape, out_dtype, "", A, stream)
+        d = _abi.MaoMat(op, groups * a.cols if tn else a.rows, shape[-1], shape[-1],
+                        _FLOATS[out_dtype], 0)
+    else:
+        if tuple(out.shape) != shape and not (tn and groups == 1 and tuple(out.shape) == shape[1:]):
+            raise ValueError("out must have shape %s" % (shape,))
+        flat = out
+        if out.dim() == 3:
+            if groups > 1 and out.stride(0) != a.cols * out.stride(1):
+                raise ValueError("the groups' matrices follow each other without gaps")
+            flat = out.as_strided((groups * a.cols, b.cols), (out.stride(1), out.stride(2)))
+        d = _desc(flat)
     ra, rb = ctypes.byref(a), ctypes.byref(b)
     wptr, wbytes = None, 0
     if ws is not None:
@@ -602,7 +642,7 @@ def fp8_product(A, a_scales, B, b_scales, form, offsets=None, out=None, out_dtyp
         wbytes = lib().fp8_product_workspace_bytes(ra, rb, _FORM[form])
         if wbytes:
             ws, wptr = _out(None, wbytes, torch.uint8, "", A, stream)
-    st = lib().fp8_product(ra, rb, ctypes.byref(_mat(d)), _FORM[form], off, groups,
+    st = lib().fp8_product(ra, rb, ctypes.byref(d), _FORM[form], off, groups,
                            bool(accumulate), wptr, wbytes, _raw_stream(stream, A))
     if st:
         _abi.check("fp8_product", st)
@@ -619,7 +659,7 @@ def expert_route(logits, top_k, score="softmax", bias=None, groups=1, keep_group
     are divided by their sum. Masked experts (logit -inf) are never chosen; ids -1 with
     weight 0 fill the places that are left.
     """
-    m = _mat(logits)
+    m = _desc(logits)
     shape = (m.rows, top_k)
     weights, wp = _out(weights, shape, torch.float32, "weights", logits, stream)
     ids, ip = _out(ids, shape, torch.int32, "ids", logits, stream)
@@ -636,7 +676,7 @@ def expert_route_backward(logits, ids, dweights, score="softmax", renorm=True, s
                           dlogits=None, stream=None):
     """Gradient of expert_route's weights with respect to the logits (dlogits: of the logits'
     shape and dtype unless given)."""
-    m = _mat(logits)
+    m = _desc(logits)
     if ids.dim() != 2 or ids.shape[0] != m.rows:
         raise ValueError("ids must be [T, top_k]")
     k = ids.shape[1]
@@ -645,7 +685,7 @@ def expert_route_backward(logits, ids, dweights, score="softmax", renorm=True, s
     st = lib().expert_route_backward(
         ctypes.byref(m), _dense_ptr(ids, torch.int32, (m.rows, k), "ids"),
         _dense_ptr(dweights, torch.float32, (m.rows, k), "dweights"), k, _SCORE[score],
-        int(bool(renorm)), float(scale), ctypes.byref(_mat(dlogits)), _raw_stream(stream, logits))
+        int(bool(renorm)), float(scale), ctypes.byref(_desc(dlogits)), _raw_stream(stream, logits))
     _abi.check("expert_route_backward", st)
     return dlogits
 
@@ -703,12 +743,12 @@ def expert_combine(Z, row_of, weights=None, out=None, stream=None):
     all 1), summed in fp32; out: of Z's dtype unless given."""
     shape = row_of.shape
     T, k = shape
-    z = _mat(Z)
+    z = _desc(Z)
     if out is None:
         out, yp = _out(None, (T, z.cols), Z.dtype, "", Z, stream)
         y = _abi.MaoMat(yp, T, z.cols, z.cols, z.dtype, 0)
     else:
-        y = _mat(out)
+        y = _desc(out)
     st = lib().expert_combine(
         ctypes.byref(z), _dense_ptr(row_of, torch.int32, shape, "row_of"),
         _dense_ptr(weights, torch.float32, shape, "weights"), T, k, ctypes.byref(y),
@@ -730,10 +770,10 @@ def expert_combine_backward(dY, Z, row_of, slot_of, weights=None, dZ=None, dweig
     if dweights is None:
         dweights = _empty((T, k), torch.float32, Z.device, stream)
     st = lib().expert_combine_backward(
-        ctypes.byref(_mat(dY)), ctypes.byref(_mat(Z)),
+        ctypes.byref(_desc(dY)), ctypes.byref(_desc(Z)),
         _dense_ptr(row_of, torch.int32, (T, k), "row_of"),
         _dense_ptr(slot_of, torch.int32, (Z.shape[0],), "slot_of"),
-        _dense_ptr(weights, torch.float32, (T, k), "weights"), k, ctypes.byref(_mat(dZ)),
+        _dense_ptr(weights, torch.float32, (T, k), "weights"), k, ctypes.byref(_desc(dZ)),
         _dense_ptr(dweights, torch.float32, (T, k), "dweights"), _raw_stream(stream, Z))
     _abi.check("expert_combine_backward", st)
     return dZ, dweights
