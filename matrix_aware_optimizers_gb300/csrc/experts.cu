@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_place_kernel(const PlanPara
 
 // ------------------------------------------------------------------ combination
 
-// Eight columns from c on (VEC: one 16-byte load for bf16, two for fp32); columns from `cols`
+// Eight columns from c on (VEC: one 16-byte access for bf16, two for fp32); columns from `cols`
 // on read as 0.
 template <bool VEC>
 __device__ __forceinline__ void load_cols(const void* base, int64_t row, int64_t ld, int dtype,
@@ -492,6 +492,44 @@ __device__ __forceinline__ void store_cols(void* base, int64_t row, int64_t ld, 
   }
 }
 
+// Eight columns as they are in memory, so that loads can be issued ahead of their use.
+struct RawCols {
+  uint4 a, b;  // b: fp32 only
+};
+template <bool VEC>
+__device__ __forceinline__ void load_raw(const void* base, int64_t row, int64_t ld, int dtype,
+                                         int64_t c, int64_t cols, RawCols& r) {
+  if (VEC) {
+    if (dtype == MAO_BF16) {
+      r.a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + row * ld + c);
+    } else {
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + row * ld + c);
+      r.a = q[0];
+      r.b = q[1];
+    }
+  } else {
+    float v[8];
+    load_cols<false>(base, row, ld, dtype, c, cols, v);
+    r.a = *reinterpret_cast<const uint4*>(&v[0]);
+    r.b = *reinterpret_cast<const uint4*>(&v[4]);
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void unpack_raw(const RawCols& r, int dtype, float (&v)[8]) {
+  if (VEC && dtype == MAO_BF16) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+  }
+}
+
 struct CombineParams {
   const void* z;
   void* y;
@@ -502,7 +540,7 @@ struct CombineParams {
 };
 
 // Threads of a row own eight columns each; a block holds as many tokens as fit. HBM bounds it:
-// 8192 tokens of 8 x 2048 bf16 take 55 us (5.5 TB/s).
+// 8192 tokens of 8 x 2048 bf16 take 52 us (5.8 TB/s; 56 and 68 with two and eight rows ahead).
 template <bool VEC>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
   wait_for_previous();
@@ -510,16 +548,30 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
   const int64_t c = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * 8;
   if (t >= p.tokens || c >= p.cols) return;
   float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int j = 0; j < p.top_k; ++j) {
-    const int64_t i = t * p.top_k + j;
-    const int32_t row = p.row_of[i];
-    if (row < 0 || row >= p.zrows) continue;
-    const float w = p.weights ? p.weights[i] : 1.0f;
-    float v[8];
-    load_cols<VEC>(p.z, row, p.zld, p.zdt, c, p.cols, v);
+  constexpr int AHEAD = 4;  // rows asked for before the first is used
+  for (int j0 = 0; j0 < p.top_k; j0 += AHEAD) {
+    int32_t row[AHEAD];
+    float w[AHEAD];
+    RawCols r[AHEAD];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) acc[q] = fmaf(w, v[q], acc[q]);
+    for (int q = 0; q < AHEAD; ++q) {
+      const int64_t i = t * p.top_k + j0 + q;
+      const bool in = j0 + q < p.top_k;
+      row[q] = in ? p.row_of[i] : -1;
+      w[q] = !in ? 0.0f : p.weights ? p.weights[i] : 1.0f;
+      if (row[q] >= p.zrows) row[q] = -1;
+    }
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q)
+      if (row[q] >= 0) load_raw<VEC>(p.z, row[q], p.zld, p.zdt, c, p.cols, r[q]);
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      if (row[q] < 0) continue;
+      float v[8];
+      unpack_raw<VEC>(r[q], p.zdt, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[q], v[e], acc[e]);
+    }
   }
   store_cols<VEC>(p.y, t, p.yld, p.ydt, c, p.cols, acc);
 }
@@ -537,10 +589,12 @@ struct CombineBackParams {
 };
 
 // One warp per row of Z: its copy's token gives dZ's row, and the dot product of the two rows
-// the copy's weight's gradient; no sums across warps, and none over copies. HBM bounds it: the
-// gradient of the case above takes 119 us (5.4 TB/s; 126 and 163 with the column loop unrolled
-// twice and four times, which costs resident warps).
-template <bool VEC>
+// the copy's weight's gradient; no sums across warps, and none over copies. AHEAD pieces of Z's
+// row (512 bytes each for bf16, from HBM; dY's rows come from L2) are asked for before the first
+// is used. HBM bounds it: the gradient of combine_kernel's case takes 116 us (5.5 TB/s) with two
+// pieces ahead, 127 with one, 120 with four and 131 with eight, which cost resident warps; a
+// block per row instead of a warp took 256.
+template <bool VEC, int AHEAD>
 __global__ void __launch_bounds__(256) combine_back_kernel(const CombineBackParams p) {
   wait_for_previous();
   const int lane = threadIdx.x & 31;
@@ -553,30 +607,42 @@ __global__ void __launch_bounds__(256) combine_back_kernel(const CombineBackPara
     }
   }
   if (r >= p.rows) return;
-  const int64_t slot = p.slot_of[r];
-  const bool used = slot >= 0 && slot < p.copies;
-  const int64_t t = used ? slot / p.top_k : 0;
-  const float w = used ? (p.weights ? p.weights[slot] : 1.0f) : 0.0f;
+  const int32_t slot = p.slot_of[r];
+  if (slot < 0 || slot >= p.copies) {
+    const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t c = lane * 8; c < p.cols; c += 256) store_cols<VEC>(p.dz, r, p.dzld, p.dzdt, c, p.cols, zero);
+    return;
+  }
+  const int64_t t = uint32_t(slot) / uint32_t(p.top_k);
+  const float w = p.weights ? p.weights[slot] : 1.0f;
+  const int zdt = AHEAD > 1 ? int(MAO_BF16) : p.zdt;  // several ahead: all of it is bf16
+  const int dydt = AHEAD > 1 ? int(MAO_BF16) : p.dydt;
   float dot = 0.0f;
 #pragma unroll 1
-  for (int64_t c = lane * 8; c < p.cols; c += 256) {
-    float g[8], v[8];
-    if (used) {
-      load_cols<VEC>(p.dy, t, p.dyld, p.dydt, c, p.cols, g);
+  for (int64_t c0 = lane * 8; c0 < p.cols; c0 += 256 * AHEAD) {
+    RawCols z[AHEAD];
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a)
+      if (p.dweights && c0 + 256 * a < p.cols) load_raw<VEC>(p.z, r, p.zld, zdt, c0 + 256 * a, p.cols, z[a]);
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      const int64_t c = c0 + 256 * a;
+      if (c >= p.cols) break;
+      float g[8], v[8];
+      RawCols y;
+      load_raw<VEC>(p.dy, t, p.dyld, dydt, c, p.cols, y);
+      unpack_raw<VEC>(y, dydt, g);
       if (p.dweights) {
-        load_cols<VEC>(p.z, r, p.zld, p.zdt, c, p.cols, v);
+        unpack_raw<VEC>(z[a], zdt, v);
 #pragma unroll
         for (int q = 0; q < 8; ++q) dot = fmaf(g[q], v[q], dot);
       }
 #pragma unroll
       for (int q = 0; q < 8; ++q) g[q] *= w;
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) g[q] = 0.0f;
+      store_cols<VEC>(p.dz, r, p.dzld, p.dzdt, c, p.cols, g);
     }
-    store_cols<VEC>(p.dz, r, p.dzld, p.dzdt, c, p.cols, g);
   }
-  if (!p.dweights || !used) return;
+  if (!p.dweights) return;
   dot = warp_sum(dot);
   if (lane == 0) p.dweights[slot] = dot;
 }
@@ -642,8 +708,11 @@ mao_status combine_backward_launch(const mao_mat& dY, const mao_mat& Z, const in
   const CombineBackParams p{dY.data, Z.data, dZ.data, row_of, slot_of, weights, dweights, Z.rows,
                             Z.cols, dY.ld, Z.ld, dZ.ld, copies, dY.dtype, Z.dtype, dZ.dtype, top_k};
   const bool vec = vec8_ok(dY) && vec8_ok(Z) && vec8_ok(dZ);
+  const bool bf = Z.dtype == MAO_BF16 && dY.dtype == MAO_BF16;
+  using Kernel = void (*)(const CombineBackParams);
+  const Kernel k = !vec ? combine_back_kernel<false, 1> : bf ? combine_back_kernel<true, 2> : combine_back_kernel<true, 1>;
   const unsigned grid = unsigned(ceil_div(Z.rows > 0 ? Z.rows : 1, 8));
-  return launch_dependent(vec ? combine_back_kernel<true> : combine_back_kernel<false>, grid, 256, 0, stream, p);
+  return launch_dependent(k, grid, 256, 0, stream, p);
 }
 
 }  // namespace mao
