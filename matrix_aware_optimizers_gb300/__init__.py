@@ -434,13 +434,13 @@ def _empty_strided(shape, strides, dtype, device, stream):
 _FLOATS = {torch.float32: _abi.MAO_F32, torch.bfloat16: _abi.MAO_BF16}
 
 
-def _desc(t):
-    """_mat of a float32 or bfloat16 matrix, with as few calls as it takes."""
+def _desc(t, dims=2):
+    """_mat of a float32 or bfloat16 matrix, with as few calls as it takes; with dims = 3 of the
+    first of stacked matrices."""
     shape, st = t.shape, t.stride()
-    if len(shape) != 2 or (st[1] != 1 and shape[1] > 1) or not t.is_cuda:
-        raise ValueError("expected a 2-D CUDA tensor with unit column stride")
-    rows, cols = shape
-    ld = st[0]
+    if len(shape) != dims or (st[-1] != 1 and shape[-1] > 1) or not t.is_cuda:
+        raise ValueError("expected a %d-D CUDA tensor with unit column stride" % dims)
+    rows, cols, ld = shape[-2], shape[-1], st[-2]
     if ld < cols:
         if rows > 1:
             raise ValueError("expected a tensor whose rows do not overlap")
@@ -539,7 +539,7 @@ def fp8_quantize(X, blocks, rows=None, copies=1, out=None, stream=None):
         batch, R, C = x0.shape
         if batch == 0:
             raise ValueError("no matrices")
-        m = _desc(x0[0])
+        m = _desc(x0, 3)
         stride = x0.stride(0) if batch > 1 else 0
         if batch > 1 and stride < 1:
             raise ValueError("stacked matrices need a positive stride")
