@@ -681,9 +681,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const uint32_t dp = p_mn ? 4096 >> 4 : 32 >> 4, dq = q_mn ? 4096 >> 4 : 32 >> 4;
       int stage = 0, local = 0, before_n = 0;
       uint32_t phase = 0;
-      bool ok = true, issued = false, started = false, ready = false;
-      // Scale words: the slot of the blocks being multiplied (every three groups of blocks the
-      // phase flips), the set of TMEM columns that holds them, and the slot copied next.
+      bool ok = true, issued = false, ready = false;
+      // Scale words: the slot of the blocks being multiplied, the set of TMEM columns that holds
+      // them, and the slot copied next (copied just before its products; earlier copies, one to
+      // three blocks ahead, were up to 3% slower).
       int slot = 0, set = 0, copied = 0;
       uint32_t copied_phase = 0, before_phase = 1;
       int before = SF_SLOTS - 2;  // slot of the group two before the one copied next
@@ -692,9 +693,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!wait_warp<false>(&sf_empty_bar[before], before_phase, abort_flag, limit) ||
             !wait_warp<true>(&sf_full_bar[copied], copied_phase, abort_flag, limit))
           return false;
-        copy_scales(elected, tmem_base + uint32_t(SF_COL + SF_COLS * (set ^ (started ? 1 : 0))),
+        copy_scales(elected, tmem_base + uint32_t(SF_COL + SF_COLS * set),
                     sf_desc + uint64_t(copied * (SF_BYTES >> 4)));
-        started = issued = true;
+        issued = true;
         if (++copied == SF_SLOTS) {
           copied = 0;
           copied_phase ^= 1u;
@@ -743,23 +744,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     kb != 0 ? 1u : 0u);
           issued = true;
           commit_both(elected, empty);
-          const bool last = (kb & 3) == 3 || kb + 1 == t.nkb;
-          // the next scale words follow two or three blocks behind the current ones: by then
-          // the slot's last products are done, and the copy is done before it is needed
-          if (((kb & 3) == 2 || (last && (kb & 3) < 2)) && ((kb | 3) + 1 < t.nkb || after < total)) {
-            if (!copy_next()) {
+          if ((kb & 3) == 3 || kb + 1 == t.nkb) {  // the last block of its scale words
+            commit_both(elected, smem_u32(&sf_empty_bar[slot]));
+            if (++slot == SF_SLOTS) slot = 0;
+            set ^= 1;
+            if (kb + 1 < t.nkb && !copy_next()) {
               ok = false;
               break;
             }
           }
-          if (last) {
-            commit_both(elected, smem_u32(&sf_empty_bar[slot]));
-            if (++slot == SF_SLOTS) slot = 0;
-            set ^= 1;
-          }
         }
         if (!ok) break;
         commit_both(elected, smem_u32(&tfull_bar[acc]));
+        if (after < total) ok = copy_next();
         ++local;
         tile = after;
         t = next;
