@@ -314,7 +314,7 @@ struct PickBack {
 // warp find each other by ballots), which also ranks every copy within its warp. A copy's row
 // is the expert's offset plus the counts of the blocks and warps before it plus its rank.
 // Integer sums only: the result does not depend on the order in which blocks run. Latency
-// bounds it: 131,072 copies among 256 experts take 6.5 us to count and 11 to place; up to
+// bounds it: 131,072 copies among 256 experts take 7 us to count and 8.3 to place; up to
 // 4096 copies one block does both.
 
 constexpr int PLAN_WARPS = 16;
@@ -364,66 +364,45 @@ struct PlanParams {
   const int32_t* ids;
   int64_t n, n_slots;
   int32_t experts, blocks;
-  int32_t* block_counts;
+  int32_t* block_counts;  // [blocks][experts]
+  int32_t* ranks;         // [n]: each copy's rank among its block's copies of its expert
   int32_t* counts;
   int32_t* offsets;
   int32_t* row_of;
   int32_t* slot_of;
 };
 
-__global__ void __launch_bounds__(PLAN_THREADS) plan_count_kernel(const PlanParams p) {
-  extern __shared__ int cnt[];
-  wait_for_previous();
-  const int experts = p.experts;
-  const int64_t n_slots = p.n_slots;
-  int ex[PLAN_ROUNDS], rank[PLAN_ROUNDS];
-  plan_count(p.ids, p.n, experts, cnt, ex, rank);
+// cnt[warp][expert] becomes the number of copies of the expert in the warps before; total[expert]
+// their sum over all warps.
+__device__ __forceinline__ void plan_sum_warps(int experts, int* cnt, int* total) {
   for (int e = threadIdx.x; e < experts; e += PLAN_THREADS) {
-    int c = 0;
+    int c[PLAN_WARPS], sum = 0;
 #pragma unroll
-    for (int w = 0; w < PLAN_WARPS; ++w) c += cnt[w * experts + e];
-    p.block_counts[int64_t(blockIdx.x) * experts + e] = c;
+    for (int w = 0; w < PLAN_WARPS; ++w) c[w] = cnt[w * experts + e];
+#pragma unroll
+    for (int w = 0; w < PLAN_WARPS; ++w) {
+      cnt[w * experts + e] = sum;
+      sum += c[w];
+    }
+    total[e] = sum;
   }
-  const int64_t step = int64_t(gridDim.x) * PLAN_THREADS;
-  for (int64_t i = int64_t(blockIdx.x) * PLAN_THREADS + threadIdx.x; i < n_slots; i += step)
-    p.slot_of[i] = -1;
+  __syncthreads();
 }
 
-// block_counts == nullptr: the grid is one block, which also clears slot_of.
-__global__ void __launch_bounds__(PLAN_THREADS) plan_place_kernel(const PlanParams p) {
-  extern __shared__ int cnt[];
-  wait_for_previous();
-  const int experts = p.experts, blocks = p.blocks;
-  const int64_t n = p.n, n_slots = p.n_slots;
-  const int32_t* block_counts = p.block_counts;
-  int32_t* slot_of = p.slot_of;
-  __shared__ int warp_total[PLAN_WARPS];
-  int ex[PLAN_ROUNDS], rank[PLAN_ROUNDS];
-  if (!block_counts)
-    for (int64_t i = threadIdx.x; i < n_slots; i += PLAN_THREADS) slot_of[i] = -1;
-  plan_count(p.ids, p.n, experts, cnt, ex, rank);
-  // thread i owns experts PER i .. PER i + PER - 1
+// Offsets of the experts' runs from their counts (thread i owns experts PER i .. of `all`; they
+// are written if `write`), and base[e] = offset + before[e].
+__device__ __forceinline__ void plan_offsets(const PlanParams& p, const int* all, const int* before,
+                                             int* base, bool write) {
   constexpr int PER = (PLAN_MAX_EXPERTS + PLAN_THREADS - 1) / PLAN_THREADS;
+  __shared__ int warp_total[PLAN_WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = (experts + PLAN_THREADS - 1) / PLAN_THREADS;
-  int total[PER], before[PER], own = 0;
+  const int per = (p.experts + PLAN_THREADS - 1) / PLAN_THREADS;
+  int size[PER], own = 0;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const int e = int(threadIdx.x) * per + q;
-    total[q] = before[q] = 0;
-    if (q >= per || e >= experts) continue;
-    if (block_counts) {
-#pragma unroll 8
-      for (int b = 0; b < blocks; ++b) {
-        const int c = block_counts[int64_t(b) * experts + e];
-        total[q] += c;
-        before[q] += b < int(blockIdx.x) ? c : 0;
-      }
-    } else {
-#pragma unroll
-      for (int w = 0; w < PLAN_WARPS; ++w) total[q] += cnt[w * experts + e];
-    }
-    own += (total[q] + 127) & ~127;
+    size[q] = q < per && e < p.experts ? (all[e] + 127) & ~127 : 0;
+    own += size[q];
   }
   int scan = own;  // inclusive over the warp, then over the warps
 #pragma unroll
@@ -438,31 +417,102 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_place_kernel(const PlanPara
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const int e = int(threadIdx.x) * per + q;
-    if (q >= per || e >= experts) continue;
-    if (blockIdx.x == 0) {
-      p.counts[e] = total[q];
+    if (q >= per || e >= p.experts) continue;
+    if (write) {
+      p.counts[e] = all[e];
       p.offsets[e] = off;
-      if (e == experts - 1) p.offsets[experts] = off + ((total[q] + 127) & ~127);
+      if (e == p.experts - 1) p.offsets[p.experts] = off + size[q];
     }
-    // the counts become the first row of each warp's copies
-    int at = off + before[q];
-#pragma unroll
-    for (int w = 0; w < PLAN_WARPS; ++w) {
-      const int c = cnt[w * experts + e];
-      cnt[w * experts + e] = at;
-      at += c;
-    }
-    off += (total[q] + 127) & ~127;
+    base[e] = off + (before ? before[e] : 0);
+    off += size[q];
   }
   __syncthreads();
-  const int64_t first = int64_t(blockIdx.x) * PLAN_CHUNK + warp * 32 * PLAN_ROUNDS + lane;
+}
+
+// The first copy of this thread (then every 32nd).
+__device__ __forceinline__ int64_t plan_first() {
+  return int64_t(blockIdx.x) * PLAN_CHUNK + (threadIdx.x >> 5) * 32 * PLAN_ROUNDS + (threadIdx.x & 31);
+}
+
+// Up to PLAN_CHUNK copies: one block does it all.
+__global__ void __launch_bounds__(PLAN_THREADS) plan_alone_kernel(const PlanParams p) {
+  extern __shared__ int cnt[];
+  int* total = cnt + PLAN_WARPS * p.experts;
+  int* base = total + p.experts;
+  wait_for_previous();
+  for (int64_t i = threadIdx.x; i < p.n_slots; i += PLAN_THREADS) p.slot_of[i] = -1;
+  int ex[PLAN_ROUNDS], rank[PLAN_ROUNDS];
+  plan_count(p.ids, p.n, p.experts, cnt, ex, rank);
+  plan_sum_warps(p.experts, cnt, total);
+  plan_offsets(p, total, nullptr, base, true);
+  const int64_t first = plan_first();
 #pragma unroll
   for (int r = 0; r < PLAN_ROUNDS; ++r) {
     const int64_t i = first + 32 * r;
-    if (i >= n) continue;
-    const int row = ex[r] < 0 ? -1 : cnt[warp * experts + ex[r]] + rank[r];
+    if (i >= p.n) continue;
+    const int e = ex[r];
+    const int row = e < 0 ? -1 : base[e] + cnt[(threadIdx.x >> 5) * p.experts + e] + rank[r];
     p.row_of[i] = row;
-    if (row >= 0) slot_of[row] = int32_t(i);
+    if (row >= 0) p.slot_of[row] = int32_t(i);
+  }
+}
+
+// More: every block counts its copies and ranks them among themselves ..
+__global__ void __launch_bounds__(PLAN_THREADS) plan_count_kernel(const PlanParams p) {
+  extern __shared__ int cnt[];
+  int* total = cnt + PLAN_WARPS * p.experts;
+  wait_for_previous();
+  int ex[PLAN_ROUNDS], rank[PLAN_ROUNDS];
+  plan_count(p.ids, p.n, p.experts, cnt, ex, rank);
+  plan_sum_warps(p.experts, cnt, total);
+  for (int e = threadIdx.x; e < p.experts; e += PLAN_THREADS)
+    p.block_counts[int64_t(blockIdx.x) * p.experts + e] = total[e];
+  const int64_t first = plan_first();
+#pragma unroll
+  for (int r = 0; r < PLAN_ROUNDS; ++r) {
+    const int64_t i = first + 32 * r;
+    if (i < p.n && ex[r] >= 0) p.ranks[i] = cnt[(threadIdx.x >> 5) * p.experts + ex[r]] + rank[r];
+  }
+  const int64_t step = int64_t(gridDim.x) * PLAN_THREADS;
+  for (int64_t i = int64_t(blockIdx.x) * PLAN_THREADS + threadIdx.x; i < p.n_slots; i += step)
+    p.slot_of[i] = -1;
+}
+
+// .. and places them after the copies of the blocks before.
+__global__ void __launch_bounds__(PLAN_THREADS) plan_place_kernel(const PlanParams p) {
+  extern __shared__ int all[];
+  int* before = all + p.experts;
+  int* base = before + p.experts;
+  wait_for_previous();
+  for (int e = threadIdx.x; e < p.experts; e += PLAN_THREADS) {
+    int sum = 0, mine = 0;
+#pragma unroll 16
+    for (int b = 0; b < p.blocks; ++b) {
+      const int c = p.block_counts[int64_t(b) * p.experts + e];
+      sum += c;
+      mine += b < int(blockIdx.x) ? c : 0;
+    }
+    all[e] = sum;
+    before[e] = mine;
+  }
+  const int64_t first = plan_first();
+  int ex[PLAN_ROUNDS], rank[PLAN_ROUNDS];
+#pragma unroll
+  for (int r = 0; r < PLAN_ROUNDS; ++r) {
+    const int64_t i = first + 32 * r;
+    ex[r] = i < p.n ? p.ids[i] : -1;
+    if (ex[r] >= p.experts) ex[r] = -1;
+    rank[r] = i < p.n && ex[r] >= 0 ? p.ranks[i] : 0;
+  }
+  __syncthreads();
+  plan_offsets(p, all, before, base, blockIdx.x == 0);
+#pragma unroll
+  for (int r = 0; r < PLAN_ROUNDS; ++r) {
+    const int64_t i = first + 32 * r;
+    if (i >= p.n) continue;
+    const int row = ex[r] < 0 ? -1 : base[ex[r]] + rank[r];
+    p.row_of[i] = row;
+    if (row >= 0) p.slot_of[row] = int32_t(i);
   }
 }
 
@@ -659,7 +709,7 @@ mao_status route_backward_launch(const RouteBackParams& p, cudaStream_t stream) 
 
 size_t plan_workspace_size(int64_t n, int32_t experts) {
   const int64_t blocks = ceil_div(n, PLAN_CHUNK);
-  return size_t(round_up((blocks > 1 ? blocks : 1) * experts * 4, 256));
+  return size_t(round_up(blocks > 1 ? blocks * experts * 4 : 0, 256) + round_up(n * 4, 256) + 256);
 }
 
 mao_status plan_launch(const int32_t* ids, int64_t n, int32_t experts, int32_t* counts,
@@ -670,21 +720,21 @@ mao_status plan_launch(const int32_t* ids, int64_t n, int32_t experts, int32_t* 
   if (cudaGetDevice(&dev) != cudaSuccess) return MAO_ERR_CUDA;
   cudaError_t attr = cudaSuccess;
   std::call_once(once[dev & 63], [&] {
-    const int most = PLAN_WARPS * PLAN_MAX_EXPERTS * int(sizeof(int));
-    attr = cudaFuncSetAttribute(plan_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    const int most = (PLAN_WARPS + 2) * PLAN_MAX_EXPERTS * int(sizeof(int));
+    attr = cudaFuncSetAttribute(plan_alone_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (attr == cudaSuccess)
-      attr = cudaFuncSetAttribute(plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+      attr = cudaFuncSetAttribute(plan_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   });
   if (attr != cudaSuccess) return MAO_ERR_CUDA;
   const int blocks = int(ceil_div(n, PLAN_CHUNK));
-  const size_t smem = size_t(PLAN_WARPS) * experts * sizeof(int);
-  PlanParams p{ids, n, n_slots, experts, blocks, nullptr, counts, offsets, row_of, slot_of};
-  if (blocks > 1) {
-    p.block_counts = static_cast<int32_t*>(workspace);
-    const mao_status st = launch_dependent(plan_count_kernel, blocks, PLAN_THREADS, smem, stream, p);
-    if (st != MAO_OK) return st;
-  }
-  return launch_dependent(plan_place_kernel, blocks > 1 ? blocks : 1, PLAN_THREADS, smem, stream, p);
+  const size_t row = size_t(experts) * sizeof(int);
+  PlanParams p{ids, n, n_slots, experts, blocks, nullptr, nullptr, counts, offsets, row_of, slot_of};
+  if (blocks <= 1) return launch_dependent(plan_alone_kernel, 1, PLAN_THREADS, (PLAN_WARPS + 2) * row, stream, p);
+  p.block_counts = static_cast<int32_t*>(workspace);
+  p.ranks = p.block_counts + round_up(int64_t(blocks) * experts, 64);
+  const mao_status st = launch_dependent(plan_count_kernel, blocks, PLAN_THREADS, (PLAN_WARPS + 1) * row, stream, p);
+  if (st != MAO_OK) return st;
+  return launch_dependent(plan_place_kernel, blocks, PLAN_THREADS, 3 * row, stream, p);
 }
 
 mao_status combine_launch(const mao_mat& Z, const int32_t* row_of, const float* weights,
