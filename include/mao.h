@@ -546,7 +546,7 @@ mao_status expert_route_backward(const mao_mat* logits, const int32_t* ids,
  *   row_of    device, n int32: the row of copy i, -1 if dropped.
  *   slot_of   device, n_slots int32: the copy in each row, -1 in padding rows; n_slots >=
  *             expert_rows(n, experts).
- *   Limits: n <= 2^27, experts <= 1024; n = 0 writes counts, offsets and slot_of.
+ *   Limits: n <= 2^24, experts <= 1024; n = 0 writes counts, offsets and slot_of.
  *   workspace >= expert_plan_workspace_bytes(n, experts) bytes, 256-byte aligned; up to 4096
  *             copies need none (NULL).
  */

@@ -710,7 +710,7 @@ def _plan_sizes(n, experts):
     """(rows, workspace bytes or 0 where none is needed) of a plan."""
     nb = lib().expert_plan_workspace_bytes(n, experts)
     if nb == 0:
-        raise ValueError("expert_plan takes up to 2^27 copies and 1 to 1024 experts")
+        raise ValueError("expert_plan takes up to 2^24 copies and 1 to 1024 experts")
     return expert_rows(n, experts), nb if n > 4096 else 0
 
 

@@ -152,7 +152,7 @@ int64_t expert_rows(int64_t n, int32_t experts) {
 }
 
 size_t expert_plan_workspace_bytes(int64_t n, int32_t experts) {
-  if (n < 0 || n > (int64_t(1) << 27) || experts < 1 || experts > 1024) return 0;
+  if (n < 0 || n > (int64_t(1) << 24) || experts < 1 || experts > 1024) return 0;
   return plan_workspace_size(n, experts);
 }
 
@@ -160,7 +160,7 @@ mao_status expert_plan(const int32_t* ids, int64_t n, int32_t experts, int32_t* 
                        int32_t* offsets, int32_t* row_of, int32_t* slot_of, int64_t n_slots,
                        void* workspace, size_t workspace_bytes, void* stream) {
   if (n < 0 || experts < 1 || !counts || !offsets) return MAO_ERR_INVALID_ARG;
-  if (n > (int64_t(1) << 27) || experts > 1024) return MAO_ERR_UNSUPPORTED;
+  if (n > (int64_t(1) << 24) || experts > 1024) return MAO_ERR_UNSUPPORTED;
   if ((n > 0 && (!ids || !row_of)) || (n_slots > 0 && !slot_of)) return MAO_ERR_INVALID_ARG;
   if (n_slots < expert_rows(n, experts)) return MAO_ERR_INVALID_ARG;
   if (!aligned(ids, 4) || !aligned(counts, 4) || !aligned(offsets, 4) || !aligned(row_of, 4) ||

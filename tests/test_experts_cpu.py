@@ -193,7 +193,7 @@ def test_route_plan_combine_refusals(lib):
     def plan(n=8, e=4, slots=1024, ids=FAKE, ws=FAKE, wsb=1 << 20, off=FAKE):
         return lib.expert_plan(ids, n, e, FAKE, off, FAKE, FAKE, slots, ws, wsb, None)
 
-    assert plan(n=-1) == bad and plan(e=0) == bad and plan(e=1025) == uns and plan(n=(1 << 27) + 1, slots=1 << 31) == uns
+    assert plan(n=-1) == bad and plan(e=0) == bad and plan(e=1025) == uns and plan(n=(1 << 24) + 1, slots=1 << 31) == uns
     assert plan(slots=256) == bad and plan(ids=None) == bad and plan(off=None) == bad
     assert plan(ws=FAKE + 16) == mis and plan(off=FAKE + 2) == mis
     assert plan(n=5000, slots=8192, ws=None) == bad and plan(n=5000, slots=8192, wsb=0) == wsp
