@@ -39,10 +39,10 @@
 // What bounds it: a pair's block of 256 x 256 x 128 takes 512 cycles of the tensor cores and
 // brings 32 KB into each SM, which near 55 bytes per cycle and SM takes as long; products
 // that run back to back also meet the power limit. Measured alone (CUDA events) and in a run
-// of 0.15 s, on experts 128 x [1536 x 2048], 65,536 rows:
-//   dense 8192 x 14336 x 4096, bf16 out     290 us (3.3 PFLOP/s), 343 us in a run
-//   forward (nt), bf16 out                  177 us (2.3 PFLOP/s), 206 us in a run
-//   input gradient (nn, 128 x [2048 x 768]) 94 us, 103 us in a run
+// of 0.15 s (a range: on different cards), on experts 128 x [1536 x 2048], 65,536 rows:
+//   dense 8192 x 14336 x 4096, bf16 out     290 us (3.3 PFLOP/s), 329 to 344 us in a run
+//   forward (nt), bf16 out                  177 us (2.3 PFLOP/s), 193 to 206 us in a run
+//   input gradient (nn, 128 x [2048 x 768]) 94 us, 99 to 103 us in a run
 //   weight gradient (tn), fp32 out          325 us (5.7 TB/s, the outputs' 1.6 GB bound it)
 // Parts of the work taken out, to see what they cost (forward, 174 us): no stores 156, no loads
 // of Q 165, all loads from the same L2 lines 154. The tensor pipe is active 58% of the time.

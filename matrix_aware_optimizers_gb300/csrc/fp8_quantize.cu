@@ -16,7 +16,7 @@
 // gathered both-direction pass took 133 us instead of 87. Blocks of 512 and 1024 threads were
 // slower everywhere (80 and 150 us against 61 for bf16 rows). Measured, 65,536 x 2048: bf16 row 60
 // us (6.8 TB/s), column 59, tile 59, both 80 (6.8 TB/s); fp32 row 100 us (6.7 TB/s), both 125;
-// 81,792 rows gathered from 8192, bf16, both: 87 us; 128 matrices of 1536 x 2048, bf16, tile: 168
+// 81,792 rows gathered from 8192, bf16, both: 85 us; 128 matrices of 1536 x 2048, bf16, tile: 166
 // us (7.2 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
