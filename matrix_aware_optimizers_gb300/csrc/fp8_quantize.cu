@@ -8,16 +8,19 @@
 // With y = x 2^-e exact, the only rounding is that of the code, and the code and scale do not
 // depend on how or where they are computed.
 //
-// HBM bounds it, except for both directions of gathered bf16 rows, which instructions and
-// their latency bound (twelve per entry, 60% of the issue slots). So bf16 maxima are taken two
-// to a register and products two to an instruction, an entry is unpacked once for both
-// directions, tiles that reach over an edge or hold NaN or infinities take a path out of line, and
-// registers are kept to 64 for four blocks per SM (bf16; two for fp32): with 121 registers the
-// gathered both-direction pass took 133 us instead of 87. Blocks of 512 and 1024 threads were
-// slower everywhere (80 and 150 us against 61 for bf16 rows). Measured, 65,536 x 2048: bf16 row 60
-// us (6.8 TB/s), column 59, tile 59, both 80 (6.8 TB/s); fp32 row 100 us (6.7 TB/s), both 125;
-// 81,792 rows gathered from 8192, bf16, both: 85 us; 128 matrices of 1536 x 2048, bf16, tile: 166
-// us (7.2 TB/s).
+// HBM bounds it, except for gathered rows, which instructions and latency bound (bf16: eight per
+// entry in one direction and eleven in both, 60% of the issue slots). So bf16 maxima and the
+// rows' scales are taken two to a register and products two to an instruction, an entry is
+// unpacked once for both directions, places are divided by multiplications, tiles that reach
+// over an edge or hold NaN or infinities take a path out of line, and registers are kept to 64
+// for four blocks per SM (bf16; two for fp32): with 121 registers the gathered both-direction
+// pass took 133 us instead of 84. Blocks of 512 and 1024 threads were slower everywhere (80 and
+// 150 us against 61 for bf16 rows). Measured, 65,536 x 2048: bf16 row 59 us (6.8 TB/s), column
+// 59, tile 58, both 80 (6.7 TB/s); fp32 row 100 us (6.7 TB/s), both 124; 81,792 rows gathered
+// from 8192, bf16: row 59 us, both 84 (fp32: 104, 141); 128 matrices of 1536 x 2048, bf16, tile:
+// 166 us (7.3 TB/s). For gathered rows, a block that copies its next tile's rows into shared
+// memory while it encodes (98 us), or takes several tiles in a row (119), was slower: registers
+// spill.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -42,6 +45,20 @@ struct Out {
   int64_t ld, scale_ld;
 };
 
+// n / d for n < 2^31 by a multiplication (Granlund and Montgomery): with 2^(s-1) < d <= 2^s and
+// m = ceil(2^(31+s) / d), m d - 2^(31+s) < 2^s, so n m / 2^(31+s) stays below the next integer.
+struct Divisor {
+  uint32_t m, s;
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return uint32_t((uint64_t(n) * m) >> s);
+  }
+};
+Divisor divisor(uint32_t d) {
+  uint32_t s = 0;
+  while ((uint64_t(1) << s) < d) ++s;
+  return {uint32_t(((uint64_t(1) << (31 + s)) + d - 1) / d), 31 + s};
+}
+
 struct QuantParams {
   const void* base;           // matrix 0 (stride > 0)
   int64_t stride;             // elements between matrices; 0: ptr and lds below
@@ -49,8 +66,8 @@ struct QuantParams {
   int64_t rows, cols;         // of the result
   int64_t src_rows;           // of X
   const int32_t* index;       // source rows (times copies), or null
-  int32_t copies;
   int32_t row_tiles, col_tiles;
+  Divisor by_copies, by_tiles, by_cols;  // copies, tiles of a matrix, col_tiles
   int64_t first;              // number of matrix 0 among the results
   Out row, col, tile;
   const void* ptr[TABLE];
@@ -160,7 +177,7 @@ template <bool BF16, bool ROW, bool COL, bool TILE>
 __device__ __noinline__ void quantize_tile(const QuantParams& p, int64_t matrix, int rb, int cb,
                                               const uint8_t* base, int64_t ld, bool vec,
                                               uint32_t (*part)[128], uint8_t* col_byte,
-                                              const int32_t* src) {
+                                              const int64_t* src) {
   constexpr int ES = BF16 ? 2 : 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cg = tid & 15, rr = tid >> 4;  // columns 8 cg .., rows rr + STEP it
@@ -176,9 +193,9 @@ __device__ __noinline__ void quantize_tile(const QuantParams& p, int64_t matrix,
     const uint8_t* a;
     bool have = r < nr && nc > 0;
     if (src) {
-      const int32_t i = src[r];
-      have = have && i >= 0;
-      a = base + (int64_t(i) * ld + c0) * ES;
+      const int64_t from = src[r];
+      have = have && from >= 0;
+      a = base + from + c0 * ES;
     } else {
       a = at + r * ld * ES;
     }
@@ -345,19 +362,22 @@ __device__ __forceinline__ uint32_t codes4(float2 a, float2 b) {
 template <bool BF16, bool ROW, bool COL, bool TILE>
 __device__ __forceinline__ bool quantize_full(const QuantParams& p, int64_t matrix, int rb, int cb,
                                               const uint8_t* base, int64_t ld, uint32_t (*part)[128],
-                                              uint8_t* byte_of, const int32_t* src) {
+                                              uint8_t* byte_of, const int64_t* src, bool gaps) {
   constexpr int ES = BF16 ? 2 : 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cg = tid & 15, rr = tid >> 4;  // columns 8 cg .., rows rr + STEP it
   Raw<BF16> x[IT];
   const uint8_t* at = base + (int64_t(cb) * 128 + 8 * cg) * ES;
-  if (src) {
+  if (src && gaps) {
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
-      const int32_t i = src[STEP * it + rr];
+      const int64_t from = src[STEP * it + rr];
       x[it].zero();
-      if (i >= 0) x[it].load(at + int64_t(i) * ld * ES);
+      if (from >= 0) x[it].load(at + from);
     }
+  } else if (src) {
+#pragma unroll
+    for (int it = 0; it < IT; ++it) x[it].load(at + src[STEP * it + rr]);
   } else {
     at += (int64_t(rb) * 128 + rr) * ld * ES;
 #pragma unroll
@@ -431,6 +451,14 @@ __device__ __forceinline__ bool quantize_full(const QuantParams& p, int64_t matr
         rmax[h] = BF16 ? max2(rmax[h], other) : max(rmax[h], other);
       }
   }
+  uint32_t row_inv[NR];  // bf16: of two rows; fp32: see below
+  if constexpr (ROW && BF16) {
+    // scale_byte and scale_inverse on the upper halves of two maxima at once: 15 bits each, and
+    // (262 - exponent) << 7 is the upper half of 2^-(byte - 127)
+#pragma unroll
+    for (int h = 0; h < NR; ++h)
+      row_inv[h] = 0x83008300u - __vmaxu2((rmax[h] + 0x001F001Fu) & 0xFF80FF80u, 0x04000400u);
+  }
   float2 inv[4];  // of the columns, or of the tile
   if constexpr (COL) {
     __syncthreads();
@@ -459,12 +487,13 @@ __device__ __forceinline__ bool quantize_full(const QuantParams& p, int64_t matr
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = make_float2(x[it].value(2 * i), x[it].value(2 * i + 1));
     if constexpr (ROW) {
-      const uint32_t m = !BF16 ? rmax[it % NR] : (it & 1) ? rmax[it / 2] & 0xFFFF0000u : rmax[it / 2] << 16;
-      const int byte = scale_byte(m);
-      const float2 s = make_float2(scale_inverse(byte), scale_inverse(byte));
+      float si;
+      if constexpr (BF16) si = __uint_as_float((it & 1) ? row_inv[it / 2] & 0xFFFF0000u : row_inv[it / 2] << 16);
+      else si = scale_inverse(scale_byte(rmax[it]));
+      const float2 s = make_float2(si, si);
       *reinterpret_cast<uint2*>(dr + int64_t(STEP * it) * p.row.ld) =
           make_uint2(codes4(mul2(v[0], s), mul2(v[1], s)), codes4(mul2(v[2], s), mul2(v[3], s)));
-      if (cg == 0) row_byte[STEP * it + rr] = uint8_t(byte);
+      if (cg == 0) row_byte[STEP * it + rr] = uint8_t(254u - (__float_as_uint(si) >> 23));
     }
     if constexpr (COL || TILE)
       *reinterpret_cast<uint2*>(d + int64_t(STEP * it) * o.ld) =
@@ -481,29 +510,31 @@ template <bool BF16, bool ROW, bool COL, bool TILE>
 __global__ void __launch_bounds__(THREADS, BF16 ? 4 : 2) quantize_kernel(const __grid_constant__ QuantParams p) {
   __shared__ uint32_t part[WARPS][128];
   __shared__ __align__(8) uint8_t byte_of[256];  // scale bytes of the columns, of the rows
-  __shared__ int32_t src[128];  // source rows of the tile, -1: zeros
+  __shared__ int64_t src[128];  // where the tile's source rows begin (bytes), -1: zeros
   wait_for_previous();
   const unsigned tiles = unsigned(p.row_tiles) * unsigned(p.col_tiles);
-  const unsigned z = blockIdx.x / tiles, in = blockIdx.x - z * tiles;
-  const int rb = int(in / unsigned(p.col_tiles)), cb = int(in - unsigned(rb) * unsigned(p.col_tiles));
+  const unsigned z = p.by_tiles(blockIdx.x), in = blockIdx.x - z * tiles;
+  const int rb = int(p.by_cols(in)), cb = int(in - unsigned(rb) * unsigned(p.col_tiles));
   constexpr int ES = BF16 ? 2 : 4;
   const uint8_t* base = static_cast<const uint8_t*>(p.stride ? p.base : p.ptr[z]);
   if (p.stride) base += int64_t(z) * p.stride * ES;
   const int64_t ld = p.stride ? p.ld : p.lds[z];
   const bool vec = reinterpret_cast<uintptr_t>(base) % 16 == 0 && (ld * ES) % 16 == 0;
   const bool full = vec && int64_t(rb + 1) * 128 <= p.rows && int64_t(cb + 1) * 128 <= p.cols;
+  bool gaps = false;
   if (p.index) {
     const int64_t r = int64_t(rb) * 128 + threadIdx.x;
     if (threadIdx.x < 128) {
-      int32_t i = r < p.rows ? p.index[r] : -1;
-      if (i >= 0 && p.copies > 1) i /= p.copies;
-      src[threadIdx.x] = i < p.src_rows ? i : -1;
+      const int32_t i = r < p.rows ? p.index[r] : -1;
+      const int64_t row = p.by_copies(uint32_t(i));
+      gaps = i < 0 || row >= p.src_rows;
+      src[threadIdx.x] = gaps ? -1 : row * ld * ES;
     }
-    __syncthreads();
+    gaps = __syncthreads_or(gaps) != 0;
   }
   const int64_t matrix = p.first + z;
-  const int32_t* rows = p.index ? src : nullptr;
-  if (full && quantize_full<BF16, ROW, COL, TILE>(p, matrix, rb, cb, base, ld, part, byte_of, rows)) return;
+  const int64_t* rows = p.index ? src : nullptr;
+  if (full && quantize_full<BF16, ROW, COL, TILE>(p, matrix, rb, cb, base, ld, part, byte_of, rows, gaps)) return;
   __syncthreads();  // the shared memory is used again
   quantize_tile<BF16, ROW, COL, TILE>(p, matrix, rb, cb, base, ld, vec, part, byte_of, rows);
 }
@@ -524,7 +555,7 @@ mao_status quantize_launch(const mao_mat* X, int32_t batch, int64_t batch_stride
   p.src_rows = X[0].rows;
   if (p.rows == 0) return MAO_OK;
   p.index = copies > 0 ? index : nullptr;
-  p.copies = copies;
+  p.by_copies = divisor(copies > 0 ? copies : 1);
   const int64_t rt = ceil_div(p.rows, 128), ct = ceil_div(p.cols, 128);
   p.row = out_of(row);
   p.col = out_of(col);
@@ -533,6 +564,8 @@ mao_status quantize_launch(const mao_mat* X, int32_t batch, int64_t batch_stride
   if (rt * ct > most) return MAO_ERR_UNSUPPORTED;
   p.row_tiles = int32_t(rt);
   p.col_tiles = int32_t(ct);
+  p.by_tiles = divisor(uint32_t(rt * ct));
+  p.by_cols = divisor(uint32_t(ct));
   const bool bf = X[0].dtype == MAO_BF16;
   using Kernel = void (*)(const QuantParams);
   const Kernel k =

@@ -123,6 +123,26 @@ def test_quantize_gather(cuda, copies):
     assert none[0].shape == (0, 200) and none[1].shape == (0, 2)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("blocks", ["row", "col", "both"])
+@pytest.mark.parametrize("copies", [1, 7, 2 ** 20 + 1])
+def test_quantize_gather_whole_tiles(cuda, dtype, blocks, copies):
+    """Blocks of rows that all exist, some that do not, and a ragged last one."""
+    x = spread(6, 33, 256).to(dtype).to(cuda)
+    g = torch.Generator().manual_seed(2)
+    rows = torch.randint(0, 33 * copies, (330,), generator=g)
+    rows[:4] = torch.tensor([0, copies - 1, copies, 33 * copies - 1])  # ends of runs of copies
+    rows[130], rows[200], rows[201] = -1, 33 * copies, 2 ** 31 - 1
+    src = torch.div(rows, copies, rounding_mode="floor")
+    have = (rows >= 0) & (src < 33)
+    y = torch.where(have[:, None], x.cpu()[torch.where(have, src, 0)], torch.zeros((), dtype=dtype))
+    out = mao.fp8_quantize(x, blocks, rows=rows.to(torch.int32).to(cuda), copies=copies)
+    if blocks != "col":
+        check_quantized(out[0], out[1], np64(y), "row")
+    if blocks != "row":
+        check_quantized(out[-2], out[-1], np64(y), "col")
+
+
 # ------------------------------------------------------------------------------ products
 
 
