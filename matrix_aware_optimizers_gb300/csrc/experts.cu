@@ -542,20 +542,22 @@ __device__ __forceinline__ void store_cols(void* base, int64_t row, int64_t ld, 
   }
 }
 
-// Eight columns as they are in memory, so that loads can be issued ahead of their use.
+// Eight columns as they are in memory, so that loads can be issued ahead of their use. STREAM:
+// the row is read once by this call, and leaves the caches before what is read again.
 struct RawCols {
   uint4 a, b;  // b: fp32 only
 };
-template <bool VEC>
+template <bool VEC, bool STREAM = false>
 __device__ __forceinline__ void load_raw(const void* base, int64_t row, int64_t ld, int dtype,
                                          int64_t c, int64_t cols, RawCols& r) {
   if (VEC) {
     if (dtype == MAO_BF16) {
-      r.a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + row * ld + c);
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + row * ld + c);
+      r.a = STREAM ? __ldcs(q) : *q;
     } else {
       const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + row * ld + c);
-      r.a = q[0];
-      r.b = q[1];
+      r.a = STREAM ? __ldcs(q) : q[0];
+      r.b = STREAM ? __ldcs(q + 1) : q[1];
     }
   } else {
     float v[8];
@@ -590,7 +592,9 @@ struct CombineParams {
 };
 
 // Threads of a row own eight columns each; a block holds as many tokens as fit. HBM bounds it:
-// 8192 tokens of 8 x 2048 bf16 take 52 us (5.8 TB/s; 56 and 68 with two and eight rows ahead).
+// 8192 tokens of 8 x 2048 bf16 take 45 us in a row of calls and 58 after others have filled the
+// L2 (52 and 62 without the streaming loads, and then 56 and 68 in a row of calls with two and
+// eight rows ahead).
 template <bool VEC>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
   wait_for_previous();
@@ -613,7 +617,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
     }
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q)
-      if (row[q] >= 0) load_raw<VEC>(p.z, row[q], p.zld, p.zdt, c, p.cols, r[q]);
+      if (row[q] >= 0) load_raw<VEC, true>(p.z, row[q], p.zld, p.zdt, c, p.cols, r[q]);
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) {
       if (row[q] < 0) continue;
@@ -641,9 +645,10 @@ struct CombineBackParams {
 // One warp per row of Z: its copy's token gives dZ's row, and the dot product of the two rows
 // the copy's weight's gradient; no sums across warps, and none over copies. AHEAD pieces of Z's
 // row (512 bytes each for bf16, from HBM; dY's rows come from L2) are asked for before the first
-// is used. HBM bounds it: the gradient of combine_kernel's case takes 116 us (5.5 TB/s) with two
-// pieces ahead, 127 with one, 120 with four and 131 with eight, which cost resident warps; a
-// block per row instead of a warp took 256.
+// is used. HBM bounds it: the gradient of combine_kernel's case takes 111 us (5.7 TB/s) with two
+// pieces ahead. Without streaming loads of Z it took 115, and then 127 with one piece ahead, 120
+// with four and 131 with eight, which cost resident warps; a block per row instead of a warp
+// took 256.
 template <bool VEC, int AHEAD>
 __global__ void __launch_bounds__(256) combine_back_kernel(const CombineBackParams p) {
   wait_for_previous();
@@ -673,7 +678,7 @@ __global__ void __launch_bounds__(256) combine_back_kernel(const CombineBackPara
     RawCols z[AHEAD];
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a)
-      if (p.dweights && c0 + 256 * a < p.cols) load_raw<VEC>(p.z, r, p.zld, zdt, c0 + 256 * a, p.cols, z[a]);
+      if (p.dweights && c0 + 256 * a < p.cols) load_raw<VEC, true>(p.z, r, p.zld, zdt, c0 + 256 * a, p.cols, z[a]);
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a) {
       const int64_t c = c0 + 256 * a;
