@@ -81,7 +81,7 @@ constexpr int SHARED = TILE - ACC1;        // columns that both accumulators use
 constexpr int SF_COL = ACC1 + TILE;        // scale words: 12 columns per set
 constexpr int SF_COLS = 12;
 constexpr int TMEM_COLS = 512;
-constexpr int Q_BOXES = 8;                 // heights of boxes of Q: 16 (b + 1) rows
+constexpr int Q_BOXES = 4;                 // heights of boxes of Q: 16 << b rows
 constexpr int BAND = 8;                    // tiles of j that share a pass over i
 constexpr size_t TABLE_BYTES = size_t(2) * (MAX_GROUPS + 2) * 4;
 constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + SF_SLOTS * SF_BYTES + TABLE_BYTES + 256;
@@ -90,7 +90,7 @@ static_assert(SF_COL + SF_SETS * SF_COLS <= TMEM_COLS, "TMEM budget");
 
 struct ProductParams {
   CUtensorMap map_p;
-  CUtensorMap map_q[Q_BOXES];  // boxes of 16, 32, .. 128 rows (MAO_TN: the last only)
+  CUtensorMap map_q[Q_BOXES];  // boxes of 16, 32, 64, 128 rows (MAO_TN: the last only)
   const uint8_t* sp;        // scales of P and Q
   const uint8_t* sq;
   const int32_t* offsets;
@@ -636,9 +636,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       decode<FORM>(p, lo, begin, tile, t);
       const int i = t.i0 + HALF * int(cta), j = t.j0 + (t.n >> 1) * int(cta);
       const int z = FORM != MAO_TN ? t.g : 0;
-      // the box that holds this CTA's n / 2 rows of Q
-      const int box = q_mn ? Q_BOXES - 1 : (t.n >> 5) - 1;
-      const uint32_t q_bytes = uint32_t(box + 1) * (OP_BYTES / Q_BOXES);
+      // this CTA's n / 2 rows of Q, a multiple of 16: one box each for its bits
+      const int q_rows = q_mn ? HALF : t.n >> 1;
+      const uint32_t q_bytes = uint32_t(q_rows) * BK;
       for (int kb = 0; kb < t.nkb; ++kb) {
         if (!wait_warp<false>(&empty_bar[stage], phase ^ 1u, abort_flag, limit)) {
           ok = false;
@@ -651,7 +651,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (p_mn) tma_load_3d_pair(dst, &p.map_p, fb, i, k, z);
           else tma_load_3d_pair(dst, &p.map_p, fb, k, i, z);
           if (q_mn) tma_load_3d_pair(dst + OP_BYTES, &p.map_q[Q_BOXES - 1], fb, j, k, 0);
-          else tma_load_3d_pair(dst + OP_BYTES, &p.map_q[box], fb, k, j, 0);
+          else if (q_rows == HALF) tma_load_3d_pair(dst + OP_BYTES, &p.map_q[Q_BOXES - 1], fb, k, j, 0);
+          else
+            for (int b = Q_BOXES - 2, at = 0; b >= 0; --b)
+              if (q_rows & (16 << b)) {
+                tma_load_3d_pair(dst + OP_BYTES + at * BK, &p.map_q[b], fb, k, j + at, 0);
+                at += 16 << b;
+              }
         }
         armed |= 1u << stage;
         armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
@@ -987,7 +993,7 @@ mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, 
   ProductParams p = {};
   mao_status st = tc_encode_code_map(&p.map_p, B.codes, B.cols, B.rows, B.ld, B.count, HALF);
   for (int b = tn ? Q_BOXES - 1 : 0; b < Q_BOXES && st == MAO_OK; ++b)
-    st = tc_encode_code_map(&p.map_q[b], A.codes, A.cols, A.rows, A.ld, 1, 16 * (b + 1));
+    st = tc_encode_code_map(&p.map_q[b], A.codes, A.cols, A.rows, A.ld, 1, 16 << b);
   if (st != MAO_OK) return st;
   p.sp = B.scales;
   p.sq = A.scales;
