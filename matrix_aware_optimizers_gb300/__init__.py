@@ -677,16 +677,20 @@ def expert_route_backward(logits, ids, dweights, score="softmax", renorm=True, s
     """Gradient of expert_route's weights with respect to the logits (dlogits: of the logits'
     shape and dtype unless given)."""
     m = _desc(logits)
-    if ids.dim() != 2 or ids.shape[0] != m.rows:
+    shape = ids.shape
+    if len(shape) != 2 or shape[0] != m.rows:
         raise ValueError("ids must be [T, top_k]")
-    k = ids.shape[1]
     if dlogits is None:
-        dlogits = _empty(tuple(logits.shape), logits.dtype, logits.device, stream)
+        dlogits, dp = _out(None, logits.shape, logits.dtype, "", logits, stream)
+        d = _abi.MaoMat(dp, m.rows, m.cols, m.cols, m.dtype, 0)
+    else:
+        d = _desc(dlogits)
     st = lib().expert_route_backward(
-        ctypes.byref(m), _dense_ptr(ids, torch.int32, (m.rows, k), "ids"),
-        _dense_ptr(dweights, torch.float32, (m.rows, k), "dweights"), k, _SCORE[score],
-        int(bool(renorm)), float(scale), ctypes.byref(_desc(dlogits)), _raw_stream(stream, logits))
-    _abi.check("expert_route_backward", st)
+        ctypes.byref(m), _dense_ptr(ids, torch.int32, shape, "ids"),
+        _dense_ptr(dweights, torch.float32, shape, "dweights"), shape[1], _SCORE[score],
+        bool(renorm), scale, ctypes.byref(d), _raw_stream(stream, logits))
+    if st:
+        _abi.check("expert_route_backward", st)
     return dlogits
 
 
@@ -762,20 +766,24 @@ def expert_combine_backward(dY, Z, row_of, slot_of, weights=None, dZ=None, dweig
                             stream=None):
     """Gradients (dZ of Z's shape and dtype unless given, dweights float32 [T, k]) of
     expert_combine."""
-    T, k = row_of.shape
-    if dY.dim() != 2 or dY.shape[0] != T:
+    shape = row_of.shape
+    T, k = shape
+    dy, z = _desc(dY), _desc(Z)
+    if dy.rows != T:
         raise ValueError("dY needs one row per token")
     if dZ is None:
-        dZ = _empty(tuple(Z.shape), Z.dtype, Z.device, stream)
-    if dweights is None:
-        dweights = _empty((T, k), torch.float32, Z.device, stream)
+        dZ, dp = _out(None, Z.shape, Z.dtype, "", Z, stream)
+        d = _abi.MaoMat(dp, z.rows, z.cols, z.cols, z.dtype, 0)
+    else:
+        d = _desc(dZ)
+    dweights, wp = _out(dweights, shape, torch.float32, "dweights", Z, stream)
     st = lib().expert_combine_backward(
-        ctypes.byref(_desc(dY)), ctypes.byref(_desc(Z)),
-        _dense_ptr(row_of, torch.int32, (T, k), "row_of"),
-        _dense_ptr(slot_of, torch.int32, (Z.shape[0],), "slot_of"),
-        _dense_ptr(weights, torch.float32, (T, k), "weights"), k, ctypes.byref(_desc(dZ)),
-        _dense_ptr(dweights, torch.float32, (T, k), "dweights"), _raw_stream(stream, Z))
-    _abi.check("expert_combine_backward", st)
+        ctypes.byref(dy), ctypes.byref(z), _dense_ptr(row_of, torch.int32, shape, "row_of"),
+        _dense_ptr(slot_of, torch.int32, (z.rows,), "slot_of"),
+        _dense_ptr(weights, torch.float32, shape, "weights"), k, ctypes.byref(d), wp,
+        _raw_stream(stream, Z))
+    if st:
+        _abi.check("expert_combine_backward", st)
     return dZ, dweights
 
 
