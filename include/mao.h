@@ -524,10 +524,11 @@ mao_status expert_route(const mao_mat* logits, const float* bias, int32_t top_k,
 /*
  * Gradient of expert_route's weights: dlogits (T x E, f32 or bf16) from dweights (T x top_k
  * floats), the logits and the ids that the call gave; choosing has no gradient. With S =
- * sum of chosen s, r = s / S, g = scale * dweights (0 where the id is -1):
+ * sum of chosen s + 1e-20, r = s / S, g = scale * dweights (0 where the id is -1):
  *   ds_j = g_j, or with renorm (g_j - sum_i g_i r_i) / S
  *   softmax: dl_i = s_i (ds_i - sum_j ds_j s_j)     sigmoid: dl_i = ds_i s_i (1 - s_i)
- * where ds is 0 for experts that were not chosen (with softmax and renorm the sum is 0).
+ * where ds is 0 for experts that were not chosen (with softmax and renorm the sum is 1e-20 / S
+ * times that of g_i r_i: nothing unless a bias has chosen experts of tiny scores).
  * A masked expert's gradient is 0.
  */
 mao_status expert_route_backward(const mao_mat* logits, const int32_t* ids,

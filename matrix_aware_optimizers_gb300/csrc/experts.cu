@@ -259,15 +259,19 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_back_kernel(const Rout
   for (int i = 0; i < VPL; ++i) ds_sm[32 * i + lane] = 0.0f;
   __syncwarp();
   float ds = id >= 0 ? p.scale * p.dweights[t * p.top_k + lane] : 0.0f;
+  float dot = 0.0f;  // softmax: the sum of ds_j s_j
   if (p.renorm) {
     // divided, not multiplied by a reciprocal: a lone expert's share is then exactly 1, and
     // its gradient exactly 0
-    const float total = warp_sum(sj) + 1e-20f;
+    const float sum = warp_sum(sj), total = sum + 1e-20f;
     const float mean = warp_sum(ds * (sj / total));
     ds = id >= 0 ? (ds - mean) / total : 0.0f;
+    // sum of ds_j s_j = (mean total - mean sum) / total: nothing where 1e-20 is below the sum's
+    // rounding, but not where a bias has chosen experts of tiny scores
+    if (total > sum) dot = mean * (1e-20f / total);
+  } else if (!sigmoid) {
+    dot = warp_sum(ds * sj);
   }
-  // with renorm the weights do not change when all chosen scores grow alike: the sum is 0
-  const float dot = !sigmoid && !p.renorm ? warp_sum(ds * sj) : 0.0f;
   if (id >= 0) ds_sm[id] = sigmoid ? ds * slope : ds;
   __syncwarp();
 #pragma unroll

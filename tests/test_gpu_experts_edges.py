@@ -1,0 +1,54 @@
+"""Expert-layer operators at the ends of their ranges, against the fp64 oracle.
+
+u = 2^-23 bounds fp32's roundings: a softmax over E experts, its sums and the few products and
+divisions after it are within (E + 64) u of their terms' magnitudes.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import matrix_aware_optimizers_gb300 as mao
+from oracle import experts as ox
+
+pytestmark = pytest.mark.gpu
+
+U23 = 2.0 ** -23
+
+
+def np64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+# ------------------------------------------------------------------------------ routing
+
+
+@pytest.mark.parametrize("top_k", [1, 2, 3])
+def test_route_gradient_of_experts_of_tiny_probability(cuda, top_k):
+    """A bias chooses experts whose scores are as small as the 1e-20 of the weights'
+    denominator: then the weights do depend on the sum of the scores."""
+    low = -np.log(10.0) * np.array([18, 19, 19.5, 20, 20.5, 21, 22])
+    x = np.zeros((7, 12), np.float32)
+    x[:, 0], x[:, 1] = 1.0, -2.0
+    for t in range(7):
+        x[t, 2:9] = np.roll(low, t)
+    x[:, 9:] = -30.0
+    bias = np.zeros(12, np.float32)
+    bias[2:5] = [8.0, 6.0, 4.0]
+    g = np.random.default_rng(top_k).normal(size=(7, top_k)).astype(np.float32)
+    X, G = torch.from_numpy(x).to(cuda), torch.from_numpy(g).to(cuda)
+    w, ids = mao.expert_route(X, top_k, bias=torch.from_numpy(bias).to(cuda), scale=1.5)
+    assert ids.tolist() == [list(range(2, 2 + top_k))] * 7
+    ww, _, _ = ox.route(x, top_k, bias=bias, scale=1.5)
+    assert (np.abs(np64(w) - ww) <= (12 + 64) * U23 * ww).all()
+    d = np64(mao.expert_route_backward(X, ids, G, scale=1.5))
+    want = ox.route_backward(x, ids.cpu().numpy(), g, scale=1.5)
+    s = ox.scores(x, "softmax")
+    chosen = np.zeros_like(s)
+    chosen[:, 2:2 + top_k] = 1.0
+    total = (s * chosen).sum(1, keepdims=True) + 1e-20
+    size = 1.5 * np.abs(g).sum(1, keepdims=True)
+    # s_j (ds_j - dot) of the chosen, s_i dot of the others, with dot = mean 1e-20 / total
+    tol = (12 + 64) * U23 * s * size / total * np.where(chosen > 0, 1.0, 1e-20)
+    assert (np.abs(d - want) <= tol + 1e-37).all(), np.abs(d - want).max()
+    assert np.abs(want[:, 0]).min() > 1e-4  # the expert that was not chosen has a gradient
