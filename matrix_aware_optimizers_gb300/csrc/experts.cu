@@ -58,7 +58,17 @@ template <int VPL>
 __device__ __forceinline__ void scores_of(const float (&x)[VPL], int score, float (&p)[VPL]) {
   if (score == MAO_SCORE_SIGMOID) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) p[i] = __fdividef(1.0f, 1.0f + expf(-x[i]));  // within 2 ulp
+    for (int i = 0; i < VPL; ++i) p[i] = __fdividef(1.0f, 1.0f + expf(-x[i]));
+    // the quotient is within 4 units in the last place, but 0 once its divisor passes 2^126: from
+    // x = -87.4 down the score is e^x
+    bool low = false;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) low = low || (p[i] == 0.0f && x[i] > -INFINITY);
+    if (low) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (p[i] == 0.0f) p[i] = expf(x[i]);
+    }
     return;
   }
   float m = -INFINITY;

@@ -52,3 +52,18 @@ def test_route_gradient_of_experts_of_tiny_probability(cuda, top_k):
     tol = (12 + 64) * U23 * s * size / total * np.where(chosen > 0, 1.0, 1e-20)
     assert (np.abs(d - want) <= tol + 1e-37).all(), np.abs(d - want).max()
     assert np.abs(want[:, 0]).min() > 1e-4  # the expert that was not chosen has a gradient
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_sigmoid_far_below_zero(cuda, dtype):
+    """Scores down to fp32's smallest numbers, in the order of the logits. An exponential (2 units
+    in the last place), a sum and a quotient (2 more): 5 u, and below 2^-126 units of 2^-149."""
+    x = torch.arange(-100.0, -68.0, 0.5)[torch.randperm(64, generator=torch.Generator().manual_seed(1))]
+    x = x.view(2, 32).to(dtype)  # halves below 128 are exact in bf16
+    want = ox.scores(np64(x), "sigmoid")
+    for opts in (dict(groups=2, keep_groups=2), dict(bias=torch.zeros(32, device=cuda)), {}):
+        w, ids = mao.expert_route(x.to(cuda), 32, score="sigmoid", renorm=False, **opts)
+        order = np.argsort(-np64(x), 1)
+        np.testing.assert_array_equal(ids.cpu().numpy(), order)
+        s = np.take_along_axis(want, order, 1)
+        assert (np.abs(np64(w) - s) <= 5 * U23 * s + 2 * 2.0 ** -149).all()
