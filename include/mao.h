@@ -469,16 +469,16 @@ enum {
  * Product of two 8-bit matrices on the tensor cores, fp32 sums, over groups of rows t.
  *
  *   offsets    NULL (groups must be 1): one group of all R rows. Otherwise a device array of
- *              groups + 1 int32, rising from 0 to at most R: group g is rows offsets[g] ..
+ *              groups + 1 int32, rising within 0 .. R: group g is rows offsets[g] ..
  *              offsets[g+1] - 1 and, for MAO_NT and MAO_NN, multiplies matrix g of B
  *              (B->count = groups); for MAO_TN it gives matrix g of D, and the offsets must
  *              be multiples of 128 (expert_plan's are; blocks do not cross groups). Values
  *              outside 0 .. R are cut to that range.
- *   D          f32 or bf16. MAO_NT: R x N; MAO_NN: R x K; both: rows past the last group are
- *              set to zero. MAO_TN: the groups' N x K matrices stacked, (groups*N) x K; an
+ *   D          f32 or bf16. MAO_NT: R x N; MAO_NN: R x K; both: rows without a group are set
+ *              to zero. MAO_TN: the groups' N x K matrices stacked, (groups*N) x K; an
  *              empty group's matrix is zero.
- *   accumulate nonzero: D <- D + product (in fp32, rounded to D's dtype once; rows past the
- *              last group and empty groups' matrices keep their values).
+ *   accumulate nonzero: D <- D + product (in fp32, rounded to D's dtype once; rows without
+ *              a group and empty groups' matrices keep their values).
  *   workspace  NULL, or a device buffer, 256-byte aligned: without groups a product with few
  *              outputs and a long sum is then split over the sum, if the buffer has
  *              fp8_product_workspace_bytes(A, B, form) bytes (0 where a split would not pay),

@@ -600,7 +600,7 @@ def fp8_product(A, a_scales, B, b_scales, form, offsets=None, out=None, out_dtyp
     offsets: int32 tensor of groups + 1 row numbers (expert_plan's; for "tn" multiples of
     128): g is the group of row t, and "tn" sums over the rows of group g. None: one group, and
     B may then be [N, K]. out: a float32 or bfloat16 tensor to fill, or with accumulate to add
-    to; by default a new one of out_dtype. Rows past the last group become zero. ws: a uint8
+    to; by default a new one of out_dtype. Rows without a group become zero. ws: a uint8
     buffer for products without groups whose sum is split (fp8_product_workspace_bytes);
     allocated when needed.
     """

@@ -231,8 +231,8 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 
 // ------------------------------------------------------------------ tiles
 //
-// lo[g] (g <= groups) is the first row of group g, cut to 0 .. rows and made rising; lo[groups]
-// is where the rows without a group begin. begin[g] counts the tiles of j before group g
+// lo[g] (g <= groups) is the first row of group g, cut to 0 .. rows and made rising; the rows before
+// lo[0] and from lo[groups] on have no group. begin[g] counts the tiles of j before group g
 // (MAO_NT, MAO_NN: of its rows; MAO_TN: the same number for every group), begin[groups] all.
 
 template <int FORM>
@@ -782,10 +782,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                 mapa_shared(smem_u32(&tempty_bar[1]), 0)};
     const uint32_t tshared[2] = {mapa_shared(smem_u32(&tshared_bar[0]), 0),
                                  mapa_shared(smem_u32(&tshared_bar[1]), 0)};
-    // rows past the last group are cleared while the first tiles are multiplied
-    if (FORM != MAO_TN && !p.accumulate)
-      clear_rows(p, lo[p.groups] + int64_t(blockIdx.x) * EPI_WARPS + warp - 2, p.rows,
-                 int64_t(gridDim.x) * EPI_WARPS, 0, p.I, lane);
+    // rows before the first group and past the last are cleared while the first tiles are multiplied
+    if (FORM != MAO_TN && !p.accumulate) {
+      const int64_t turn = int64_t(blockIdx.x) * EPI_WARPS + warp - 2, turns = int64_t(gridDim.x) * EPI_WARPS;
+      clear_rows(p, turn, lo[0], turns, 0, p.I, lane);
+      clear_rows(p, lo[p.groups] + turn, p.rows, turns, 0, p.I, lane);
+    }
     int local = 0;
     Tile t;
     for (int tile = pair; tile < total; tile += npairs) {

@@ -67,3 +67,28 @@ def test_route_sigmoid_far_below_zero(cuda, dtype):
         np.testing.assert_array_equal(ids.cpu().numpy(), order)
         s = np.take_along_axis(want, order, 1)
         assert (np.abs(np64(w) - s) <= 5 * U23 * s + 2 * 2.0 ** -149).all()
+
+
+# ------------------------------------------------------------------------------ products
+
+
+@pytest.mark.parametrize("form", ["nt", "nn"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("off", [[200, 456, 600], [700, 700, 700], [1, 1, 2]])
+def test_product_rows_before_the_first_group_are_zero(cuda, form, dtype, off):
+    """They belong to no group, like the rows past the last; with accumulate both stay."""
+    g = torch.Generator().manual_seed(off[0])
+    a, b = torch.randn(700, 200, generator=g).to(cuda), torch.randn(2, 200, 200, generator=g).to(cuda)
+    A, B = mao.fp8_quantize(a, "row"), mao.fp8_quantize(b, "tile")
+    o = torch.tensor(off, dtype=torch.int32, device=cuda)
+    alone = mao.fp8_product(*A, *B, form, offsets=torch.tensor([0] + off[1:], dtype=torch.int32, device=cuda),
+                            out_dtype=dtype)
+    y = torch.full((700, 200), 7.0, dtype=dtype, device=cuda)
+    z = y.clone()
+    mao.fp8_product(*A, *B, form, offsets=o, out=y)
+    mao.fp8_product(*A, *B, form, offsets=o, out=z, accumulate=True)
+    mao.sync_status()
+    lo, hi = off[0], off[-1]
+    assert torch.equal(y[lo:hi], alone[lo:hi])
+    assert (y[:lo] == 0).all() and (y[hi:] == 0).all()
+    assert (z[:lo] == 7).all() and (z[hi:] == 7).all()
