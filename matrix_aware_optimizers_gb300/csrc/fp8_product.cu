@@ -341,7 +341,8 @@ __device__ __forceinline__ void decode(const ProductParams& p, const int* lo, co
   t.k0 = 0;
   // a group's tiles are of even height: those of up to 224 rows do not share TMEM columns
   const int rows = lo[a + 1] - lo[a];
-  const int height = count > 1 ? ((rows + count - 1) / count + 31) & ~31 : TILE;
+  // ((rows - 1) / count + 1 is the quotient rounded up: rows + count may pass 2^31)
+  const int height = count > 1 ? ((rows - 1) / count + 32) & ~31 : TILE;
   t.j0 = lo[a] + jt * height;
   t.j_end = min(t.j0 + height, lo[a + 1]);
   t.nkb = (p.depth + BK - 1) / BK;

@@ -92,3 +92,26 @@ def test_product_rows_before_the_first_group_are_zero(cuda, form, dtype, off):
     assert torch.equal(y[lo:hi], alone[lo:hi])
     assert (y[:lo] == 0).all() and (y[hi:] == 0).all()
     assert (z[:lo] == 7).all() and (z[hi:] == 7).all()
+
+
+@pytest.mark.parametrize("form", ["nt", "nn"])
+def test_product_of_the_most_rows(cuda, form):
+    """2^31 - 1024 rows, in more tiles than fit beside them in 32 bits: rows here and there against
+    the oracle's values, all others zero."""
+    R = 2 ** 31 - 1024
+    free, _ = torch.cuda.mem_get_info()
+    if free < 70e9:
+        pytest.skip("needs 70 GB of device memory")
+    A = torch.zeros(R, 16, dtype=torch.uint8, device=cuda)
+    As = torch.full((R, 1), 127, dtype=torch.uint8, device=cuda)
+    some = torch.tensor([0, 1, 255, 256, 2 ** 30 - 1, 2 ** 30, 2139127680, R - 257, R - 256, R - 1], device=cuda)
+    A[some] = torch.arange(1, 17, dtype=torch.uint8, device=cuda) + 0x38 + some[:, None].to(torch.uint8) % 8
+    B, Bs = mao.fp8_quantize(torch.arange(1.0, 3.0, device=cuda)[:, None].expand(2, 16).contiguous() if form == "nt"
+                             else torch.arange(1.0, 3.0, device=cuda).expand(16, 2).contiguous(), "tile")
+    y = mao.fp8_product(A, As, B, Bs, form, out_dtype=torch.bfloat16)
+    mao.sync_status()
+    v = np64(A[some].view(torch.float8_e4m3fn)).sum(1)[:, None] * np.array([1.0, 2.0])
+    np.testing.assert_allclose(np64(y[some]), v, rtol=2.0 ** -8, atol=0)
+    y[some] = 0
+    for at in range(0, R, 2 ** 28):
+        assert not y[at:at + 2 ** 28].any()
