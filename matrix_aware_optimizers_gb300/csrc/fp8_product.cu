@@ -50,6 +50,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -961,6 +962,9 @@ Split choose_split(int64_t tiles, int64_t nkb, int64_t outputs) {
   return best;
 }
 
+// Set for good by the first product, captured ones included: from then on the error word is read.
+std::atomic<bool> g_launched{false};
+
 struct Shape {
   int64_t rows, cols, depth;  // of D (one group) and the product
 };
@@ -1050,6 +1054,7 @@ mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, 
     p.dtype = MAO_F32;
     p.accumulate = p.paired = 0;
   }
+  g_launched.store(true, std::memory_order_release);
   const int64_t units = tiles * p.splits;
   const int64_t pairs = units < num_sms() / 2 ? units : num_sms() / 2;
   st = launch_dependent(kernels[form], unsigned(2 * pairs), THREADS, SMEM, stream, p);
@@ -1062,6 +1067,9 @@ mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, 
                           256, 0, stream, sum);
 }
 
-mao_status product_read_and_clear_error(cudaStream_t stream) { return read_and_clear_error(stream); }
+mao_status product_read_and_clear_error(cudaStream_t stream) {
+  // a copy and a synchronisation that programs without 8-bit products do not wait for
+  return g_launched.load(std::memory_order_acquire) ? read_and_clear_error(stream) : MAO_OK;
+}
 
 }  // namespace mao
