@@ -49,6 +49,7 @@ void count_launch();
 
 // Launches a kernel that may start before the previous one in the stream has finished: it
 // begins with griddepcontrol.wait, before which it touches no global memory.
+// Judged by its own result: an error that other code left pending is not this launch's.
 template <typename P>
 mao_status launch_dependent(void (*kernel)(const P), dim3 grid, dim3 block, size_t smem,
                             cudaStream_t stream, const P& params) {
@@ -64,7 +65,9 @@ mao_status launch_dependent(void (*kernel)(const P), dim3 grid, dim3 block, size
   cfg.numAttrs = 1;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, params);
   count_launch();
-  return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? MAO_OK : MAO_ERR_CUDA;
+  if (err == cudaSuccess) return MAO_OK;
+  cudaGetLastError();  // reported here: the next call finds no error of this one
+  return MAO_ERR_CUDA;
 }
 // Optional timing of launches (see mao_profile_begin); tag 0 = tensor-core product kernel,
 // other tags name the Dion CUDA-core kernels (mao_profile_end_tagged).
