@@ -2,7 +2,7 @@
 // the combination of the experts' outputs, and the gradients.
 #include <cuda_bf16.h>
 
-#include <mutex>
+#include <atomic>
 
 #include "common.cuh"
 #include "experts.h"
@@ -734,17 +734,13 @@ size_t plan_workspace_size(int64_t n, int32_t experts) {
 mao_status plan_launch(const int32_t* ids, int64_t n, int32_t experts, int32_t* counts,
                        int32_t* offsets, int32_t* row_of, int32_t* slot_of, int64_t n_slots,
                        void* workspace, cudaStream_t stream) {
-  static std::once_flag once[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MAO_ERR_CUDA;
-  cudaError_t attr = cudaSuccess;
-  std::call_once(once[dev & 63], [&] {
+  static std::atomic<bool> ready[64];
+  const mao_status attr = once_per_device(ready, [] {
     const int most = (PLAN_WARPS + 2) * PLAN_MAX_EXPERTS * int(sizeof(int));
-    attr = cudaFuncSetAttribute(plan_alone_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (attr == cudaSuccess)
-      attr = cudaFuncSetAttribute(plan_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    const cudaError_t err = cudaFuncSetAttribute(plan_alone_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    return err != cudaSuccess ? err : cudaFuncSetAttribute(plan_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   });
-  if (attr != cudaSuccess) return MAO_ERR_CUDA;
+  if (attr != MAO_OK) return attr;
   const int blocks = int(ceil_div(n, PLAN_CHUNK));
   const size_t row = size_t(experts) * sizeof(int);
   PlanParams p{ids, n, n_slots, experts, blocks, nullptr, nullptr, counts, offsets, row_of, slot_of};

@@ -51,7 +51,6 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
-#include <mutex>
 
 #include "common.cuh"
 #include "experts.h"
@@ -1025,19 +1024,16 @@ mao_status product_launch(const mao_fp8& A, const mao_fp8& B, const mao_mat& D, 
   // tiles at most: every group may end in a part of one
   const int64_t tiles = (tn ? ceil_div(p.J, TILE) * groups : ceil_div(A.rows, TILE) + groups) * p.tiles_i;
   if (tiles > 0x7FFF0000 || p.tiles_i > (1 << 17)) return MAO_ERR_UNSUPPORTED;
-  static std::once_flag once[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MAO_ERR_CUDA;
-  cudaError_t attr = cudaSuccess;
   using Kernel = void (*)(const ProductParams);
   const Kernel kernels[3] = {product_kernel<MAO_NT>, product_kernel<MAO_NN>, product_kernel<MAO_TN>};
-  std::call_once(once[dev & 63], [&] {
-    for (const Kernel k : kernels) {
-      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM));
-      if (e != cudaSuccess) attr = e;
-    }
+  static std::atomic<bool> ready[64];
+  st = once_per_device(ready, [&] {
+    cudaError_t err = cudaSuccess;
+    for (int f = 0; f < 3 && err == cudaSuccess; ++f)
+      err = cudaFuncSetAttribute(kernels[f], cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM));
+    return err;
   });
-  if (attr != cudaSuccess) return MAO_ERR_CUDA;
+  if (st != MAO_OK) return st;
   p.splits = 1;
   const Shape shape = shape_of(A, B, form);
   Split split{1, 0};

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "mao.h"
 
 namespace mao {
@@ -69,6 +71,24 @@ mao_status launch_dependent(void (*kernel)(const P), dim3 grid, dim3 block, size
   cudaGetLastError();  // reported here: the next call finds no error of this one
   return MAO_ERR_CUDA;
 }
+
+// Runs `set` (cudaError_t()) once on each device, again at the next call if it failed; two threads
+// may both run it.
+template <typename Set>
+mao_status once_per_device(std::atomic<bool> (&done)[64], Set&& set) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  std::atomic<bool>& ready = done[dev & 63];
+  if (err == cudaSuccess && ready.load(std::memory_order_acquire)) return MAO_OK;
+  if (err == cudaSuccess) err = set();
+  if (err != cudaSuccess) {
+    cudaGetLastError();  // reported here
+    return MAO_ERR_CUDA;
+  }
+  ready.store(true, std::memory_order_release);
+  return MAO_OK;
+}
+
 // Optional timing of launches (see mao_profile_begin); tag 0 = tensor-core product kernel,
 // other tags name the Dion CUDA-core kernels (mao_profile_end_tagged).
 void profile_before_launch(cudaStream_t stream, int tag = 0);

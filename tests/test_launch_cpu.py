@@ -13,12 +13,16 @@ RUNTIME = r"""
 #include <cuda_runtime_api.h>
 
 cudaError_t g_next = cudaSuccess, g_last = cudaSuccess;
-int g_launches = 0;
+int g_launches = 0, g_device = 0;
 
 extern "C" cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t*, const void*, void**) {
   if (g_next != cudaSuccess) g_last = g_next;
   else ++g_launches;
   return g_next;
+}
+extern "C" cudaError_t cudaGetDevice(int* device) {
+  *device = g_device;
+  return cudaSuccess;
 }
 extern "C" cudaError_t cudaGetLastError(void) {
   const cudaError_t e = g_last;
@@ -32,7 +36,7 @@ PROGRAM = r"""
 #include "internal.h"
 
 extern cudaError_t g_next, g_last;
-extern int g_launches;
+extern int g_launches, g_device;
 namespace mao {
 void count_launch() {}
 }
@@ -55,6 +59,18 @@ int main() {
   std::printf("its own error %d\n", launch(cudaErrorInvalidConfiguration));
   std::printf("left behind %d\n", int(g_last));
   std::printf("launches %d\n", g_launches);
+  // what a device is set up with: tried again after a failure, and once for each device
+  static std::atomic<bool> ready[64];
+  int calls = 0;
+  auto once = [&](cudaError_t result) {
+    g_last = result;
+    return mao::once_per_device(ready, [&] { return ++calls, result; });
+  };
+  const int first = once(cudaErrorInvalidValue), pending = int(g_last);
+  const int second = once(cudaSuccess), third = once(cudaSuccess);
+  g_device = 1;
+  const int other = once(cudaSuccess);
+  std::printf("set up %d %d %d %d %d calls %d\n", first, pending, second, third, other, calls);
 }
 """
 
@@ -86,3 +102,7 @@ def test_a_launch_is_judged_by_its_own_result(answers):
 
 def test_a_failed_launch_leaves_no_error(answers):
     assert answers[4] == "its own error %d" % _abi.MAO_ERR_CUDA and answers[5] == "left behind 0"
+
+
+def test_setting_up_a_device_is_tried_again_after_a_failure(answers):
+    assert answers[7] == "set up %d 0 0 0 0 calls 3" % _abi.MAO_ERR_CUDA
