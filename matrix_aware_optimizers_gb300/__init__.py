@@ -451,12 +451,19 @@ def _desc(t, dims=2):
     return _abi.MaoMat(t.data_ptr(), rows, cols, ld, dt, 0)
 
 
-def _raw_stream(stream, t):
-    """The stream's handle, or that of the stream current on t's device (these calls may be
-    as short as a kernel launch, so the handle is fetched without a Stream object)."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _raw_stream(stream, *operands):
+    """The handle of a call's stream, by default the current one. The library launches on the
+    current device, so its operands (None: not given) and its stream have to be there. (These calls
+    may be as short as a kernel launch, so the handle is fetched without a Stream object.)"""
+    device = torch._C._cuda_getDevice()
+    for t in operands:
+        if t is not None and t.get_device() != device:
+            raise ValueError("expected tensors of the current CUDA device, %d" % device)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError("expected a stream of the current CUDA device, %d" % device)
+    return stream.cuda_stream
 
 
 def _dense_ptr(t, dtype, shape, name):
@@ -583,7 +590,8 @@ def fp8_quantize(X, blocks, rows=None, copies=1, out=None, stream=None):
         for i, k in enumerate(kinds):
             desc[k] = ctypes.byref(_fp8(out[2 * i], out[2 * i + 1], k, k))
     st = lib().fp8_quantize(mats, batch, stride, index, n_index, copies, desc.get("row"),
-                            desc.get("col"), desc.get("tile"), _raw_stream(stream, x0))
+                            desc.get("col"), desc.get("tile"),
+                            _raw_stream(stream, rows, *(X if many else (X,)), *out))
     if st:
         _abi.check("fp8_quantize", st)
     return tuple(out)
@@ -643,7 +651,8 @@ def fp8_product(A, a_scales, B, b_scales, form, offsets=None, out=None, out_dtyp
         if wbytes:
             ws, wptr = _out(None, wbytes, torch.uint8, "", A, stream)
     st = lib().fp8_product(ra, rb, ctypes.byref(d), _FORM[form], off, groups,
-                           bool(accumulate), wptr, wbytes, _raw_stream(stream, A))
+                           bool(accumulate), wptr, wbytes,
+                           _raw_stream(stream, A, a_scales, B, b_scales, offsets, out, ws))
     if st:
         _abi.check("fp8_product", st)
     return out
@@ -666,7 +675,7 @@ def expert_route(logits, top_k, score="softmax", bias=None, groups=1, keep_group
     st = lib().expert_route(
         ctypes.byref(m), _dense_ptr(bias, torch.float32, (m.cols,), "bias"), top_k, _SCORE[score],
         groups, groups if keep_groups is None else keep_groups, _GROUP_SCORE[group_score],
-        bool(renorm), scale, wp, ip, _raw_stream(stream, logits))
+        bool(renorm), scale, wp, ip, _raw_stream(stream, logits, bias, weights, ids))
     if st:
         _abi.check("expert_route", st)
     return weights, ids
@@ -688,7 +697,7 @@ def expert_route_backward(logits, ids, dweights, score="softmax", renorm=True, s
     st = lib().expert_route_backward(
         ctypes.byref(m), _dense_ptr(ids, torch.int32, shape, "ids"),
         _dense_ptr(dweights, torch.float32, shape, "dweights"), shape[1], _SCORE[score],
-        bool(renorm), scale, ctypes.byref(d), _raw_stream(stream, logits))
+        bool(renorm), scale, ctypes.byref(d), _raw_stream(stream, logits, ids, dweights, dlogits))
     if st:
         _abi.check("expert_route_backward", st)
     return dlogits
@@ -736,7 +745,7 @@ def expert_plan(ids, experts, ws=None, stream=None):
     elif nb:
         ws, wptr = _out(None, nb, torch.uint8, "", ids, stream)
     st = lib().expert_plan(p_ids, n, experts, p_counts, p_off, p_row, p_slot, rows, wptr, nb,
-                           _raw_stream(stream, ids))
+                           _raw_stream(stream, ids, ws))
     if st:
         _abi.check("expert_plan", st)
     return ExpertPlan(counts, offsets, row_of, slot_of)
@@ -756,7 +765,7 @@ def expert_combine(Z, row_of, weights=None, out=None, stream=None):
     st = lib().expert_combine(
         ctypes.byref(z), _dense_ptr(row_of, torch.int32, shape, "row_of"),
         _dense_ptr(weights, torch.float32, shape, "weights"), T, k, ctypes.byref(y),
-        _raw_stream(stream, Z))
+        _raw_stream(stream, Z, row_of, weights, out))
     if st:
         _abi.check("expert_combine", st)
     return out
@@ -781,7 +790,7 @@ def expert_combine_backward(dY, Z, row_of, slot_of, weights=None, dZ=None, dweig
         ctypes.byref(dy), ctypes.byref(z), _dense_ptr(row_of, torch.int32, shape, "row_of"),
         _dense_ptr(slot_of, torch.int32, (z.rows,), "slot_of"),
         _dense_ptr(weights, torch.float32, shape, "weights"), k, ctypes.byref(d), wp,
-        _raw_stream(stream, Z))
+        _raw_stream(stream, dY, Z, row_of, slot_of, weights, dZ, dweights))
     if st:
         _abi.check("expert_combine_backward", st)
     return dZ, dweights
