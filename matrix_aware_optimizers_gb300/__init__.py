@@ -485,6 +485,13 @@ def _out(t, shape, dtype, name, like, stream):
     return t, t.data_ptr()
 
 
+def _buffer(ws):
+    """Device pointer and bytes of a caller's workspace."""
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous CUDA tensor")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _scale_shape(rows, cols, blocks):
     br = 1 if blocks == "row" else 128
     bc = 1 if blocks == "col" else 128
@@ -645,7 +652,7 @@ def fp8_product(A, a_scales, B, b_scales, form, offsets=None, out=None, out_dtyp
     ra, rb = ctypes.byref(a), ctypes.byref(b)
     wptr, wbytes = None, 0
     if ws is not None:
-        wptr, wbytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        wptr, wbytes = _buffer(ws)
     elif off is None:
         wbytes = lib().fp8_product_workspace_bytes(ra, rb, _FORM[form])
         if wbytes:
@@ -741,7 +748,7 @@ def expert_plan(ids, experts, ws=None, stream=None):
     slot_of, p_slot = _out(None, rows, i32, "", ids, stream)
     wptr = None
     if ws is not None:
-        wptr, nb = ws.data_ptr(), ws.numel() * ws.element_size()
+        wptr, nb = _buffer(ws)
     elif nb:
         ws, wptr = _out(None, nb, torch.uint8, "", ids, stream)
     st = lib().expert_plan(p_ids, n, experts, p_counts, p_off, p_row, p_slot, rows, wptr, nb,

@@ -127,3 +127,20 @@ def test_tensors_of_another_device_are_refused(calls, name):
     with pytest.raises(ValueError):
         call(**tensors, **rest, stream=Stream(1))
     assert len(calls) == 2
+
+
+class Gaps(Stand):
+    def is_contiguous(self):
+        return False
+
+    def on(self, device):
+        return Gaps(self.shape, self.dtype, device)
+
+
+@pytest.mark.parametrize("name", ["fp8_product", "expert_plan"])
+def test_workspaces_on_the_host_or_with_gaps_are_refused(calls, name):
+    call, tensors, rest = CALLS[name]
+    for ws in (Stand((1 << 20,), U8, -1), Gaps((1 << 20,), U8)):
+        with pytest.raises(ValueError):
+            call(**dict(tensors, ws=ws), **rest)
+    assert not calls
