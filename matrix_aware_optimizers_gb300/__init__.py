@@ -675,13 +675,16 @@ def expert_route(logits, top_k, score="softmax", bias=None, groups=1, keep_group
     are divided by their sum. Masked experts (logit -inf) are never chosen; ids -1 with
     weight 0 fill the places that are left.
     """
+    kind, run = _SCORE.get(score), _GROUP_SCORE.get(group_score)
+    if kind is None or run is None:
+        raise ValueError("score must be softmax or sigmoid, group_score max or top2")
     m = _desc(logits)
     shape = (m.rows, top_k)
     weights, wp = _out(weights, shape, torch.float32, "weights", logits, stream)
     ids, ip = _out(ids, shape, torch.int32, "ids", logits, stream)
     st = lib().expert_route(
-        ctypes.byref(m), _dense_ptr(bias, torch.float32, (m.cols,), "bias"), top_k, _SCORE[score],
-        groups, groups if keep_groups is None else keep_groups, _GROUP_SCORE[group_score],
+        ctypes.byref(m), _dense_ptr(bias, torch.float32, (m.cols,), "bias"), top_k, kind,
+        groups, groups if keep_groups is None else keep_groups, run,
         bool(renorm), scale, wp, ip, _raw_stream(stream, logits, bias, weights, ids))
     if st:
         _abi.check("expert_route", st)
@@ -692,6 +695,9 @@ def expert_route_backward(logits, ids, dweights, score="softmax", renorm=True, s
                           dlogits=None, stream=None):
     """Gradient of expert_route's weights with respect to the logits (dlogits: of the logits'
     shape and dtype unless given)."""
+    kind = _SCORE.get(score)
+    if kind is None:
+        raise ValueError("score must be softmax or sigmoid")
     m = _desc(logits)
     shape = ids.shape
     if len(shape) != 2 or shape[0] != m.rows:
@@ -703,7 +709,7 @@ def expert_route_backward(logits, ids, dweights, score="softmax", renorm=True, s
         d = _desc(dlogits)
     st = lib().expert_route_backward(
         ctypes.byref(m), _dense_ptr(ids, torch.int32, shape, "ids"),
-        _dense_ptr(dweights, torch.float32, shape, "dweights"), shape[1], _SCORE[score],
+        _dense_ptr(dweights, torch.float32, shape, "dweights"), shape[1], kind,
         bool(renorm), scale, ctypes.byref(d), _raw_stream(stream, logits, ids, dweights, dlogits))
     if st:
         _abi.check("expert_route_backward", st)

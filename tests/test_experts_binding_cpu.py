@@ -144,3 +144,14 @@ def test_workspaces_on_the_host_or_with_gaps_are_refused(calls, name):
         with pytest.raises(ValueError):
             call(**dict(tensors, ws=ws), **rest)
     assert not calls
+
+
+def test_unknown_kinds_of_scores_are_refused(calls):
+    """With ValueError, as the other calls refuse an unknown kind."""
+    x, ids, g = Stand((5, 16)), Stand((5, 2), I32), Stand((5, 2))
+    for opts in (dict(score="tanh"), dict(score=None), dict(group_score="mean"), dict(group_score=2)):
+        with pytest.raises(ValueError):
+            mao.expert_route(x, 2, **opts)
+    with pytest.raises(ValueError):
+        mao.expert_route_backward(x, ids, g, score="tanh")
+    assert not calls
