@@ -544,6 +544,8 @@ def fp8_quantize(X, blocks, rows=None, copies=1, out=None, stream=None):
     rows[i] // copies of X, or zeros where rows[i] < 0. out: a tuple of tensors to fill.
     """
     many = isinstance(X, (list, tuple))
+    if many and not X:
+        raise ValueError("no matrices")
     x0 = X[0] if many else X
     stacked = many or x0.dim() == 3
     if many:

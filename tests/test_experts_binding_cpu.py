@@ -155,3 +155,10 @@ def test_unknown_kinds_of_scores_are_refused(calls):
     with pytest.raises(ValueError):
         mao.expert_route_backward(x, ids, g, score="tanh")
     assert not calls
+
+
+def test_no_matrices_to_quantise_are_refused(calls):
+    for X in ([], ()):
+        with pytest.raises(ValueError):
+            mao.fp8_quantize(X, "row")
+    assert not calls
