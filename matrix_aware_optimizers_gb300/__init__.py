@@ -570,8 +570,8 @@ def fp8_quantize(X, blocks, rows=None, copies=1, out=None, stream=None):
     else:
         if batch != 1:
             raise ValueError("rows go with a single matrix")
-        if copies < 1:
-            raise ValueError("copies must be at least 1")
+        if not 1 <= copies < 2 ** 31:
+            raise ValueError("copies must be at least 1 and below 2^31")
         n_index = R = rows.numel()
         index = _dense_ptr(rows, torch.int32, rows.shape, "rows")
     kinds = _KINDS.get(blocks)

@@ -162,3 +162,11 @@ def test_no_matrices_to_quantise_are_refused(calls):
         with pytest.raises(ValueError):
             mao.fp8_quantize(X, "row")
     assert not calls
+
+
+@pytest.mark.parametrize("copies", [0, -1, 2 ** 31, 2 ** 32 + 1])
+def test_copies_that_no_row_number_reaches_are_refused(calls, copies):
+    """Passed on in 32 bits, 2^32 + 1 copies would be taken for one."""
+    with pytest.raises(ValueError):
+        mao.fp8_quantize(Stand((40, 256)), "row", rows=Stand((9,), I32), copies=copies)
+    assert not calls
