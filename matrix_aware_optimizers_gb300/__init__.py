@@ -77,14 +77,18 @@ def _mat(t, allow_none=False, like=None):
         return _abi.MaoMat(None, like.shape[0], like.shape[1], like.shape[1], _abi.MAO_F32, 0)
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    if t.dim() != 2 or t.stride(1) != 1:
+    shape, st = t.shape, t.stride()  # one look at each: steps of many matrices come here often
+    if len(shape) != 2 or st[1] != 1:
         raise ValueError("expected a 2-D tensor with unit column stride")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError("expected a tensor whose rows do not overlap")
-    if t.dtype not in _DT:
+    (rows, cols), ld = shape, st[0]
+    if ld < cols:
+        if rows > 1:
+            raise ValueError("expected a tensor whose rows do not overlap")
+        ld = cols
+    dt = _DT.get(t.dtype)
+    if dt is None:
         raise ValueError("dtype must be float32, bfloat16 or int8")
-    return _abi.MaoMat(t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]),
-                       _DT[t.dtype], 0)
+    return _abi.MaoMat(t.data_ptr(), rows, cols, ld, dt, 0)
 
 
 def _mats(ts, allow_none=False, like=None):

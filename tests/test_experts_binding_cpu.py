@@ -17,7 +17,6 @@ class Stand:
         self.shape, self.dtype, self.index = torch.Size(shape), dtype, device
         self.is_cuda = device >= 0
         self.device = torch.device("cuda", device) if device >= 0 else torch.device("cpu")
-        self.looks = {"shape": 0, "stride": 0}
 
     def dim(self):
         return len(self.shape)
@@ -170,3 +169,41 @@ def test_copies_that_no_row_number_reaches_are_refused(calls, copies):
     with pytest.raises(ValueError):
         mao.fp8_quantize(Stand((40, 256)), "row", rows=Stand((9,), I32), copies=copies)
     assert not calls
+
+
+class Watched(Stand):
+    """Counts the looks at its shape and strides, which cost a real tensor about 0.3 us each."""
+
+    def __init__(self, *args):
+        self.seen = dict(shape=0, stride=0)
+        super().__init__(*args)
+
+    def __getattribute__(self, name):
+        if name in ("shape", "stride", "dim"):
+            self.seen["stride" if name == "stride" else "shape"] += 1
+        return super().__getattribute__(name)
+
+
+def test_a_matrix_is_looked_at_once():
+    """One descriptor per matrix and step: a step of many matrices makes over a thousand."""
+    t = Watched((4, 8))
+    t.stride = lambda i=None: (8, 1) if i is None else (8, 1)[i]
+    t.seen.update(shape=0, stride=0)
+    m = mao._mat(t)
+    assert (m.rows, m.cols, m.ld) == (4, 8, 8)
+    assert t.seen == dict(shape=1, stride=1)
+
+
+@pytest.mark.parametrize("shape,strides,ld", [((4, 8), (8, 1), 8), ((4, 8), (11, 1), 11), ((1, 8), (0, 1), 8),
+                                              ((1, 8), (3, 1), 8), ((4, 1), (1, 1), 1), ((4, 8), (7, 1), None),
+                                              ((4, 8), (0, 1), None), ((4, 8), (1, 4), None), ((4,), (1,), None),
+                                              ((2, 4, 8), (32, 8, 1), None)])
+def test_descriptors_of_matrices(shape, strides, ld):
+    t = Stand(shape)
+    t.stride = lambda i=None: strides if i is None else strides[i]
+    if ld is None:
+        with pytest.raises(ValueError):
+            mao._mat(t)
+    else:
+        m = mao._mat(t)
+        assert (m.data, m.rows, m.cols, m.ld, m.dtype) == (0x10000,) + shape + (ld, 0)
