@@ -532,18 +532,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_place_kernel(const PlanPara
 
 // ------------------------------------------------------------------ combination
 
-// Eight columns from c on (VEC: one 16-byte access for bf16, two for fp32); columns from `cols`
-// on read as 0.
-template <bool VEC>
-__device__ __forceinline__ void load_cols(const void* base, int64_t row, int64_t ld, int dtype,
-                                          int64_t c, int64_t cols, float (&v)[8]) {
-  if (VEC) {
-    load8(base, row * ld + c, dtype, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? load_elem(base, row * ld + c + i, dtype) : 0.0f;
-  }
-}
+// Stores eight columns from c on (VEC: one 16-byte access for bf16, two for fp32), those below `cols`.
 template <bool VEC>
 __device__ __forceinline__ void store_cols(void* base, int64_t row, int64_t ld, int dtype,
                                            int64_t c, int64_t cols, const float (&v)[8]) {
@@ -556,8 +545,9 @@ __device__ __forceinline__ void store_cols(void* base, int64_t row, int64_t ld, 
   }
 }
 
-// Eight columns as they are in memory, so that loads can be issued ahead of their use. STREAM:
-// the row is read once by this call, and leaves the caches before what is read again.
+// Eight columns as they are in memory (!VEC: as fp32, 0 from `cols` on), so that loads can be issued
+// ahead of their use. STREAM: the row is read once by this call, and leaves the caches before what
+// is read again.
 struct RawCols {
   uint4 a, b;  // b: fp32 only
 };
@@ -575,7 +565,8 @@ __device__ __forceinline__ void load_raw(const void* base, int64_t row, int64_t 
     }
   } else {
     float v[8];
-    load_cols<false>(base, row, ld, dtype, c, cols, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? load_elem(base, row * ld + c + i, dtype) : 0.0f;
     r.a = *reinterpret_cast<const uint4*>(&v[0]);
     r.b = *reinterpret_cast<const uint4*>(&v[4]);
   }

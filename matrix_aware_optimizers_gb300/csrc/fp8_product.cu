@@ -100,7 +100,6 @@ struct ProductParams {
   int32_t rows;             // t
   int32_t I, J;             // D's columns; D's rows (of a group, for MAO_TN)
   int32_t depth;            // K (MAO_TN: the group's rows)
-  int32_t sp_rows;          // rows of scales of one matrix of P
   int32_t tiles_i, groups, dtype, accumulate, paired;
   int32_t sp_words, sq_words;  // scales allow 4-byte loads
   int32_t splits, split_kb;    // parts of the depth (one group), blocks of each
