@@ -115,3 +115,82 @@ def test_product_of_the_most_rows(cuda, form):
     y[some] = 0
     for at in range(0, R, 2 ** 28):
         assert not y[at:at + 2 ** 28].any()
+
+
+# ------------------------------------------------------------------------------ combination
+
+
+@pytest.mark.parametrize("zt,yt", [("f32", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("H", [24, 770, 2056])
+def test_combine_of_mixed_types(cuda, zt, yt, H):
+    """Z, Y and the gradients each of its own type: one rounding, to the result's."""
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}
+    T, k, E = 70, 5, 9
+    g = torch.Generator().manual_seed(H)
+    p = mao.expert_plan(torch.randint(-1, E, (T, k), generator=g).to(torch.int32).to(cuda), E)
+    rows = p.slot_of.numel()
+    z = torch.randn(rows, H, generator=g).to(dt[zt]).to(cuda)
+    w = torch.randn(T, k, generator=g).to(cuda)
+    dy = torch.randn(T, H, generator=g).to(dt[yt]).to(cuda)
+    y = mao.expert_combine(z, p.row_of, w, out=torch.empty(T, H, dtype=dt[yt], device=cuda))
+    row_of, wn = p.row_of.cpu().numpy(), w.cpu().numpy()
+    step = {"f32": U23, "bf16": 2.0 ** -8}
+    want, mag = ox.combine(np64(z), row_of, wn), ox.combine(np.abs(np64(z)), row_of, np.abs(wn))
+    assert (np.abs(np64(y) - want) <= (k + 1) * U23 * mag + step[yt] * np.abs(want)).all()
+    want_z, want_w = ox.combine_backward(np64(dy), np64(z), row_of, wn)
+    _, mag = ox.combine_backward(np.abs(np64(dy)), np.abs(np64(z)), row_of, wn)
+    for dzt in dt:
+        dz, dw = mao.expert_combine_backward(dy, z, p.row_of, p.slot_of, w,
+                                             dZ=torch.empty(rows, H, dtype=dt[dzt], device=cuda))
+        mao.sync_status()
+        assert (np.abs(np64(dz) - want_z) <= step[dzt] * np.abs(want_z)).all()
+        assert (np.abs(np64(dw) - want_w) <= (H + 1) * U23 * mag).all()
+
+
+# ------------------------------------------------------------------------------ graphs
+
+
+def test_every_call_in_one_graph(cuda):
+    """A layer's calls captured once: each replay works on what its inputs hold then, as the same
+    calls outside the graph do."""
+    T, H, N, E, k = 130, 256, 192, 8, 2
+    g = torch.Generator(device="cuda")
+    W8 = mao.fp8_quantize(torch.randn(E, N, H, generator=g.manual_seed(1), device=cuda), "tile")
+    x = torch.empty(T, H, device=cuda)
+    logits = torch.empty(T, E, device=cuda)
+    dy = torch.empty(T, N, device=cuda)
+
+    def fill(seed):
+        for t in (x, logits, dy):
+            t.copy_(torch.randn(t.shape, generator=g.manual_seed(seed), device=cuda))
+
+    def layer():
+        w, ids = mao.expert_route(logits, k)
+        p = mao.expert_plan(ids, E)
+        xr, xrs, xc, xcs = mao.fp8_quantize(x, "both", rows=p.slot_of, copies=k)
+        z = mao.fp8_product(xr, xrs, *W8, "nt", offsets=p.offsets, out_dtype=torch.float32)
+        y = mao.expert_combine(z, p.row_of, w)
+        dz, dw = mao.expert_combine_backward(dy, z, p.row_of, p.slot_of, w)
+        zr, zrs, zc, zcs = mao.fp8_quantize(dz, "both")
+        dx = mao.expert_combine(mao.fp8_product(zr, zrs, *W8, "nn", offsets=p.offsets), p.row_of)
+        dW = mao.fp8_product(zc, zcs, xc, xcs, "tn", offsets=p.offsets)
+        return [w, ids, p.counts, p.offsets, p.row_of, p.slot_of, y, dx, dW,
+                mao.expert_route_backward(logits, ids, dw)]
+
+    fill(2)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        layer()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = layer()
+    for seed in (3, 4, 5):
+        fill(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = layer()
+        mao.sync_status()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
