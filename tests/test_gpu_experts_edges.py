@@ -16,6 +16,12 @@ pytestmark = pytest.mark.gpu
 U23 = 2.0 ** -23
 
 
+@pytest.fixture(scope="module", autouse=True)
+def give_memory_back():
+    yield
+    torch.cuda.empty_cache()
+
+
 def np64(t):
     return t.detach().float().cpu().numpy().astype(np.float64)
 
@@ -194,3 +200,108 @@ def test_every_call_in_one_graph(cuda):
         mao.sync_status()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------------------ long tensors
+#
+# More than 2^31 entries: the last rows come out as in a call on them alone.
+
+LONG = 1_050_240  # rows; a multiple of 256, and with 2048 columns or more past 2^31
+
+
+def long_matrix(cols, dtype, seed, rows=LONG):
+    free, _ = torch.cuda.mem_get_info()
+    if free < 60e9:
+        pytest.skip("needs 60 GB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.empty(rows, cols, dtype=dtype, device="cuda")
+    x.normal_(generator=g)
+    assert x.numel() > 2 ** 31
+    return x
+
+
+@pytest.mark.parametrize("blocks", ["row", "col", "tile", "both"])
+def test_quantize_of_many_entries(cuda, blocks):
+    x = long_matrix(2048, torch.bfloat16, 1)
+    out = mao.fp8_quantize(x, blocks)
+    tail = mao.fp8_quantize(x[-256:], blocks)
+    mao.sync_status()
+    for a, b in zip(out, tail):
+        assert torch.equal(a[-b.shape[0]:].view(torch.uint8), b.view(torch.uint8))
+    if blocks in ("row", "both"):
+        rows = torch.tensor([LONG - 1, 0, LONG - 5, -1, LONG], dtype=torch.int32, device=cuda)
+        got = mao.fp8_quantize(x, "row", rows=rows)[0].view(torch.uint8)
+        want = mao.fp8_quantize(x[[LONG - 1, 0, LONG - 5]], "row")[0].view(torch.uint8)
+        assert torch.equal(got[:3], want) and not got[3:].any()
+
+
+def test_route_of_many_entries(cuda):
+    x = long_matrix(2 ** 8, torch.float32, 2, rows=8 * LONG)
+    w, ids = mao.expert_route(x, 4)
+    d = mao.expert_route_backward(x, ids, w, renorm=False)
+    w2, ids2 = mao.expert_route(x[-100:], 4)
+    mao.sync_status()
+    assert torch.equal(w[-100:], w2) and torch.equal(ids[-100:], ids2)
+    assert torch.equal(d[-100:], mao.expert_route_backward(x[-100:], ids2, w2, renorm=False))
+
+
+def test_combine_of_many_entries(cuda):
+    z = long_matrix(2056, torch.bfloat16, 3)
+    row_of = torch.tensor([[LONG - 1, 7], [LONG - 300, -1], [0, LONG - 2]], dtype=torch.int32, device=cuda)
+    w = torch.tensor([[0.5, 2.0], [1.5, 3.0], [0.25, 1.0]], device=cuda)
+    y = mao.expert_combine(z, row_of, w)
+    want = w[:, :1] * z[row_of[:, 0].long()].float() + w[:, 1:] * z[row_of[:, 1].clamp_min(0).long()].float()
+    want[1] = 1.5 * z[LONG - 300].float()
+    assert (y.float() - want).abs().le(2.0 ** -8 * want.abs() + 4 * U23 * 8).all()
+    slot_of = torch.full((LONG,), -1, dtype=torch.int32, device=cuda)
+    for t, j in ((0, 0), (0, 1), (1, 0), (2, 0), (2, 1)):
+        slot_of[row_of[t, j].long()] = 2 * t + j
+    dy = torch.randn(3, 2056, device=cuda).bfloat16()
+    dz, dw = mao.expert_combine_backward(dy, z, row_of, slot_of, w)
+    mao.sync_status()
+    for t, j in ((0, 0), (0, 1), (1, 0), (2, 0), (2, 1)):
+        r = int(row_of[t, j])
+        assert torch.equal(dz[r], (w[t, j] * dy[t].float()).bfloat16())
+        dz[r] = 0
+        dot, mag = (dy[t].double() * z[r].double()).sum(), (dy[t].double() * z[r].double()).abs().sum()
+        assert abs(float(dw[t, j]) - float(dot)) <= 2057 * U23 * float(mag)
+    assert dw[1, 1] == 0
+    for at in range(0, LONG, 65536):
+        assert not dz[at:at + 65536].any()
+
+
+@pytest.mark.parametrize("form", ["nt", "nn"])
+def test_product_of_many_entries(cuda, form):
+    free, _ = torch.cuda.mem_get_info()
+    if free < 60e9:
+        pytest.skip("needs 60 GB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    A = mao.fp8_quantize(torch.randn(LONG, 128, generator=g, device=cuda), "row")
+    b = torch.randn(2050, 128, generator=g, device=cuda)
+    B = mao.fp8_quantize(b if form == "nt" else b.T.contiguous(), "tile")
+    y = mao.fp8_product(*A, *B, form)
+    assert y.numel() > 2 ** 31
+    tail = mao.fp8_product(A[0][-256:], A[1][-256:], *B, form)
+    mao.sync_status()
+    assert torch.equal(y[-256:], tail)
+
+
+def test_weight_gradients_of_many_entries(cuda):
+    free, _ = torch.cuda.mem_get_info()
+    if free < 60e9:
+        pytest.skip("needs 60 GB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    A = mao.fp8_quantize(torch.randn(256, 2048, generator=g, device=cuda), "col")
+    B = mao.fp8_quantize(torch.randn(256, 2100, generator=g, device=cuda), "col")
+    off = torch.zeros(513, dtype=torch.int32, device=cuda)
+    off[300:], off[512:] = 128, 256  # group 299 has the first block, group 511 the second
+    y = mao.fp8_product(*A, *B, "tn", offsets=off, out_dtype=torch.float32)
+    assert y.numel() > 2 ** 31
+    mao.sync_status()
+    for e, lo in ((299, 0), (511, 128)):
+        alone = mao.fp8_product(A[0][lo:lo + 128], A[1][lo // 128:lo // 128 + 1], B[0][lo:lo + 128],
+                                B[1][lo // 128:lo // 128 + 1], "tn", out_dtype=torch.float32)
+        assert torch.equal(y[e], alone[0])
+        y[e] = 0
+    for e in range(512):
+        assert not y[e].any()
