@@ -36,10 +36,11 @@ __device__ __forceinline__ uint32_t order_of(float key) {
 // One warp per token; lane l holds experts 32 i + l. The softmax is one maximum, one sum. Keys
 // are compared as ordered integers.
 //
-// The instructions bound it (about 1070 per token of 256 experts in 8 runs with sigmoid scores,
-// 70% of the issue slots), not its 17 MB: 16,384 tokens take 20 us, and the gradient, which for
-// sigmoid scores reads only the chosen logits, 8.8 us. Choosing the best one by one over all
-// keys took 35 us.
+// The instructions bound it (1097 per token of 256 experts in 8 runs with sigmoid scores and a bias,
+// 89% of the issue slots), not its 17 MB: 16,384 tokens take 17.7 us in a graph of calls, and 12.4 with
+// softmax scores and neither bias nor runs. The gradient takes 6.6 us for sigmoid scores, of which it
+// reads only the chosen logits, and 8.6 for softmax. Choosing the best one by one over all keys took
+// 35 us against 20 (both with a filled L2).
 
 constexpr int ROUTE_WARPS = 4;
 
@@ -328,8 +329,8 @@ struct PickBack {
 // warp find each other by ballots), which also ranks every copy within its warp. A copy's row
 // is the expert's offset plus the counts of the blocks and warps before it plus its rank.
 // Integer sums only: the result does not depend on the order in which blocks run. Latency
-// bounds it: 131,072 copies among 256 experts take 7 us to count and 8.3 to place; up to
-// 4096 copies one block does both.
+// bounds it: 131,072 copies among 256 experts take 7 us to count and 8.3 to place, 10.4 in all in a
+// graph of calls; up to 4096 copies one block does both.
 
 constexpr int PLAN_WARPS = 16;
 constexpr int PLAN_ROUNDS = 8;
@@ -599,7 +600,8 @@ struct CombineParams {
 // Threads of a row own eight columns each; a block holds as many tokens as fit. HBM bounds it:
 // 8192 tokens of 8 x 2048 bf16 take 45 us in a row of calls and 58 after others have filled the
 // L2 (52 and 62 without the streaming loads, and then 56 and 68 in a row of calls with two and
-// eight rows ahead).
+// eight rows ahead). fp32 takes 88 us. Widths that are no multiple of eight, whose threads read eight
+// neighbours one by one, take 114 (2050 columns, bf16) and 149 (fp32).
 template <bool VEC>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
   wait_for_previous();
@@ -650,10 +652,13 @@ struct CombineBackParams {
 // One warp per row of Z: its copy's token gives dZ's row, and the dot product of the two rows
 // the copy's weight's gradient; no sums across warps, and none over copies. AHEAD pieces of Z's
 // row (512 bytes each for bf16, from HBM; dY's rows come from L2) are asked for before the first
-// is used. HBM bounds it: the gradient of combine_kernel's case takes 111 us (5.7 TB/s) with two
+// is used. HBM bounds it: the gradient of combine_kernel's case takes 110 us (5.7 TB/s) with two
 // pieces ahead. Without streaming loads of Z it took 115, and then 127 with one piece ahead, 120
 // with four and 131 with eight, which cost resident warps; a block per row instead of a warp
-// took 256.
+// took 256. Two ahead pay where the types are fixed when compiled, as for bf16 throughout; with types
+// looked up, one and two pieces ahead take 125 and 131 us (bf16), 238 and 230 (fp32), 204 and 209 (Z
+// fp32, dY bf16), 160 and 144 (Z bf16, dY fp32), so the others have one. Widths that are no multiple
+// of eight: 343 to 347 us (2050 columns, bf16) and 480 (fp32), with one piece or two.
 template <bool VEC, int AHEAD>
 __global__ void __launch_bounds__(256) combine_back_kernel(const CombineBackParams p) {
   wait_for_previous();

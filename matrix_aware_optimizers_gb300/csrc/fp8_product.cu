@@ -37,15 +37,18 @@
 // slower (320 against 301 us dense), as every block of P then serves fewer columns.
 //
 // What bounds it: a pair's block of 256 x 256 x 128 takes 512 cycles of the tensor cores and
-// brings 32 KB into each SM, which near 55 bytes per cycle and SM takes as long; products
-// that run back to back also meet the power limit. Measured alone (CUDA events) and in a run
-// of 0.15 s (a range: on different cards), on experts 128 x [1536 x 2048], 65,536 rows:
-//   dense 8192 x 14336 x 4096, bf16 out     290 us (3.3 PFLOP/s), 329 to 344 us in a run
-//   forward (nt), bf16 out                  177 us (2.3 PFLOP/s), 193 to 206 us in a run
-//   input gradient (nn, 128 x [2048 x 768]) 94 us, 99 to 103 us in a run
-//   weight gradient (tn), fp32 out          325 us (5.7 TB/s, the outputs' 1.6 GB bound it)
-// Parts of the work taken out, to see what they cost (forward, 174 us): no stores 156, no loads
-// of Q 165, all loads from the same L2 lines 154. The tensor pipe is active 58% of the time.
+// brings 32 KB into each SM. Dense products that run back to back meet the power limit. Over groups,
+// forward, the tensor cores' cycles are 106 us at 1.76 GHz and 12.6 MB come into each SM (41 bytes per
+// cycle over the kernel's time); what fills the rest of its 175 us is known in part only. Parts of the
+// work taken out (of 174 us): no stores 156, no loads of Q 165, all loads from the same L2 lines 154;
+// the tensor pipe is active 58% of the time. Measured in a graph of ten calls and in a run of
+// 0.15 s (ranges: on different cards), on experts 128 x [1536 x 2048], 65,536 rows:
+//   dense 8192 x 14336 x 4096, bf16 out     288 to 293 us (3.3 PFLOP/s), 329 to 344 us in a run
+//   forward (nt), bf16 out                  175 us (2.3 PFLOP/s), 193 to 206 us in a run
+//   input gradient (nn, 128 x [2048 x 768], 60,007 rows)  92 us, 99 to 103 us in a run
+//   weight gradient (tn), fp32 out          316 us, 324 to 330 in a run (5.7 TB/s: its 1.6 GB of outputs)
+// Dense nn and tn of the same sizes take 307 and (fp32) 313 us. Adding to D reads and writes it entry
+// by entry, each after the one before: 760 us for that tn, 4.7 ms for the experts'.
 // Barriers and their bounded waits are as in the Newton–Schulz product kernel.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -937,11 +940,13 @@ __global__ void __launch_bounds__(256) split_sum_kernel(const SumParams p) {
   }
 }
 
-// 768 x 768 over 32,768 rows: 26 us in eight parts, 76 whole; 1 x 4096 over 14,336: 15 and 32.
 // How many parts the depth of a product without groups is split into when its tiles leave
 // pairs of SMs idle: the number with the least time by a model of the two kernels (about
 // 0.25 us per block of the depth; 2.5 us for the second kernel and 3 TB/s for the partial
-// sums, which stay in L2), parts of whole scale words.
+// sums, which stay in L2), parts of whole scale words. In parts and whole (us, fp32 out): 768 x 768
+// over 32,768 rows 26.5 and 75.7, over 8192 16.2 and 25.2; 256 x 256 over 4096 11.9 and 16.0; 2048 x
+// 768 over 131,072 129 and 280; 1 x 4096 over 14,336 18.0 and 35.3, 16 rows 16.2 and 31.0; 128 x 768
+// over 4096 11.1 and 13.5; 1 x 768 over 2048 8.7 and 9.2.
 struct Split {
   int splits, kb;
 };

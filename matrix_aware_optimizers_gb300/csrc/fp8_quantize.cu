@@ -9,7 +9,7 @@
 // depend on how or where they are computed.
 //
 // HBM bounds it, except for gathered rows, which instructions and latency bound (bf16: eight per
-// entry in one direction and eleven in both, 60% of the issue slots). So bf16 maxima and the
+// entry in one direction and eleven in both, 58% of the issue slots). So bf16 maxima and the
 // rows' scales are taken two to a register and products two to an instruction, an entry is
 // unpacked once for both directions, places are divided by multiplications, tiles that reach
 // over an edge or hold NaN or infinities take a path out of line, and registers are kept to 64
