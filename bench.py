@@ -1144,7 +1144,7 @@ def finish_line(args, line, wl, step, K, world, rank, dev, barrier, max_over_ran
             line["e2e"] = run_e2e_dist(step, K, dev, barrier, max_over_ranks)
         else:
             line["e2e"] = run_e2e(step, K, world, dev, barrier, max_over_ranks, line["scaling"],
-                                  warmup=max(3, args.warmup))
+                                  warmup=line["warmup"])
 
     # ---------------- CPU baseline: the oracle on a bounded sample (rank 0, N = 1)
     if world == 1 and rank == 0 and not args.no_cpu_baseline:
