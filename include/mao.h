@@ -580,6 +580,120 @@ mao_status expert_combine_backward(const mao_mat* dY, const mao_mat* Z, const in
                                    const mao_mat* dZ, float* dweights, void* stream);
 
 /*
+ * ------------------------------------------------------------------ feed-forward blocks
+ *
+ * A gated feed-forward block y = (act(x Wg^T) * (x Wu^T)) Wd^T, trained and served in bf16, or
+ * served in 8-bit integers; dense, or as the networks of an expert layer over the runs of rows
+ * that expert_plan lays out. As the calls above they take zero rows, read no argument after they
+ * return and keep nothing between calls.
+ *
+ *   Y, Z <- gated_ffn(X, up, down)                   a training step (without Z: serving)
+ *   dX, dup, ddown <- gated_ffn_backward(dY, X, up, down, Z)
+ *   muon_step(up, M, dup); muon_step(down, M', ddown)
+ *
+ *   up8 <- int8_quantize(up); down8 <- int8_quantize(down)      serving in 8-bit integers
+ *   x8 <- int8_quantize(x); z <- int8_product(x8, up8)
+ *   h8 <- int8_quantize(z, gated); y <- int8_product(h8, down8)
+ *
+ * Runs of rows (gated_ffn, gated_ffn_backward, int8_product): offsets is NULL (groups must be
+ * 1): one run of all R rows. Otherwise a device array of groups + 1 int32, rising within 0 ..
+ * R (values outside are cut to that range): run g is rows offsets[g] .. offsets[g+1] - 1 and
+ * is multiplied by matrix g. counts is NULL, or a device array of groups int32: only the first
+ * counts[g] rows of run g hold tokens (values outside 0 .. its length are cut), and the time
+ * goes by those. Output rows outside the runs, and in a run from its count on, are zero.
+ */
+
+enum { MAO_SILU = 0, MAO_GELU = 1, MAO_GELU_TANH = 2 };
+
+/*
+ * Gated feed-forward block: G = X Wg^T, U = X Wu^T, H = act(G) * U, Y = H Wd^T.
+ *
+ *   act       MAO_SILU: g / (1 + e^-g); MAO_GELU: g Phi(g); MAO_GELU_TANH: the same with
+ *             Phi(g) ~ (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2.
+ *   X         bf16, R x K (R >= 0).
+ *   up        bf16, (groups * 2 N) x K: for each group the N rows of Wg, then those of Wu.
+ *   down      bf16, (groups * C) x N.
+ *   Z         NULL, or bf16, R x 2 N: G and U, which gated_ffn_backward takes.
+ *   Y         f32 or bf16, R x C.
+ * Sums are in fp32; G and U are rounded to bf16 in Z only, H once, to the bf16 operand of the
+ * second product. An infinite G gives what the formulas give (NaN at -inf).
+ * The first kernel computes both projections, the activation and the product; few rows are
+ * split over the sums' length, the parts added in a fixed order. Results are the same each time.
+ *   workspace >= gated_ffn_workspace_bytes(X, up, down, groups, offsets != NULL) bytes, 256-byte
+ *   aligned; it depends on the descriptors' shapes, row strides and alignment: operands whose rows
+ *   do not start at multiples of 16 bytes are copied there first. Clobbered.
+ *   Limits: groups <= 1024, R <= 2^31 - 1024, N, K, C <= 2^20, matrices of less than 2^40 bytes.
+ */
+mao_status gated_ffn(const mao_mat* X, const mao_mat* up, const mao_mat* down, int32_t act,
+                     const int32_t* offsets, const int32_t* counts, int32_t groups, const mao_mat* Z,
+                     const mao_mat* Y, void* workspace, size_t workspace_bytes, void* stream);
+size_t gated_ffn_workspace_bytes(const mao_mat* X, const mao_mat* up, const mao_mat* down,
+                                 int32_t groups, int32_t grouped);
+
+/*
+ * Its gradients, from dY (bf16, R x C), the call's X, up, down and the Z that it gave:
+ *   dH = dY Wd, dG = dH * U * act'(G), dU = dH * act(G), H = act(G) * U
+ *   dX = dG Wg + dU Wu (R x K); dup = [dG^T X; dU^T X] and ddown = dY^T H, shaped as up and down.
+ * dG, dU and H are rounded to bf16 once, as operands of the products after them; sums are in
+ * fp32. dX, dup and ddown are f32 or bf16 each, or NULL: not wanted.
+ * Offsets must be multiples of 128 (expert_plan's are) but for the last, which may be R. With
+ * counts, rows of X and dY in a run from its count on must be finite (they are multiplied by
+ * zero); without, they count as rows. A run without rows gives matrices of zeros.
+ *   workspace >= gated_ffn_backward_workspace_bytes(dY, X, up, down, groups, offsets != NULL).
+ */
+mao_status gated_ffn_backward(const mao_mat* dY, const mao_mat* X, const mao_mat* up,
+                              const mao_mat* down, const mao_mat* Z, int32_t act,
+                              const int32_t* offsets, const int32_t* counts, int32_t groups,
+                              const mao_mat* dX, const mao_mat* dup, const mao_mat* ddown,
+                              void* workspace, size_t workspace_bytes, void* stream);
+size_t gated_ffn_backward_workspace_bytes(const mao_mat* dY, const mao_mat* X, const mao_mat* up,
+                                          const mao_mat* down, int32_t groups, int32_t grouped);
+
+/*
+ * Rows in 8-bit integers: entry (i, j) of matrix b is codes[(b*rows + i)*ld + j] *
+ * scales[b*rows + i].
+ */
+typedef struct mao_int8 {
+  int8_t* codes;   /* device, 16-byte aligned */
+  float* scales;   /* device, count * rows floats */
+  int64_t rows;    /* R >= 0 (of one matrix) */
+  int64_t cols;    /* C >= 1 */
+  int64_t ld;      /* codes between row starts: >= cols, a multiple of 16 */
+  int32_t count;   /* stacked matrices, >= 1 */
+  int32_t reserved;
+} mao_int8;
+
+/*
+ * Quantises the rows of matrices to 8-bit integers. For a row x with largest magnitude a: scale
+ * = a / 127 in fp32, and code = 127 x / a rounded to the nearest integer, ties to even, as if
+ * computed exactly. A row of zeros gets scale 0 and codes 0. A row that holds a NaN or an
+ * infinity gets scale NaN and codes 0: products that read it are NaN, not saturated.
+ *   X      as in fp8_quantize: *X and a stride, or an array of descriptors. f32 or bf16.
+ *   gated  0: the rows of X (act is not looked at). Nonzero: X is R x 2 C, and row x is act(X[:C])
+ *          * X[C:], in fp32, each operation rounded as it stands: silu g / (1 + exp(-g)), gelu
+ *          (0.5 g) * (1 + erf(g * sqrt(0.5))), gelu_tanh (0.5 g) * (1 + tanh(sqrt(2/pi) *
+ *          (g + ((0.044715 g) * g) * g))), with CUDA's expf, erff and tanhf.
+ *   out    count = batch, rows = X's, cols = C.
+ */
+mao_status int8_quantize(const mao_mat* X, int32_t batch, int64_t batch_stride, int32_t gated,
+                         int32_t act, const mao_int8* out, void* stream);
+
+/*
+ * Product of 8-bit integers: D[t][n] = sA[t] sB[g][n] sum_k A[t][k] B[g][n][k] for the rows t of
+ * run g, D f32 or bf16, R x N.
+ *   A      R x K, count 1. B: N x K, count = groups.
+ * Products of codes are exact and summed in fp32: the sum is exact while its parts stay below
+ * 2^24 (K <= 1040 for any codes). It is scaled by sA, then by sB, and rounded to D's type.
+ *   workspace  NULL, or a device buffer, 256-byte aligned, of int8_product_workspace_bytes(A, B,
+ *              offsets != NULL) bytes (0: none is used): few rows are then split over the sum.
+ *   Limits: groups <= 1024, R <= 2^31 - 1024, N, K <= 2^20.
+ */
+mao_status int8_product(const mao_int8* A, const mao_int8* B, const mao_mat* D,
+                        const int32_t* offsets, const int32_t* counts, int32_t groups,
+                        void* workspace, size_t workspace_bytes, void* stream);
+size_t int8_product_workspace_bytes(const mao_int8* A, const mao_int8* B, int32_t grouped);
+
+/*
  * Bound of every device-side wait of the tensor-core kernels (default 4 s), used by launches
  * enqueued after the call; process-wide. A wait that runs past it makes the kernel stop
  * early (its outputs are then incomplete) and mao_sync_status() report MAO_ERR_TIMEOUT.

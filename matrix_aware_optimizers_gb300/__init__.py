@@ -25,6 +25,10 @@ Functions (same names as the C ABI):
   expert_plan(ids, experts)                          places of the copies among the experts' rows
   expert_combine(Z, row_of, weights)                 weighted sum of a token's expert outputs
   expert_combine_backward(dY, Z, row_of, ...)        its gradients
+  gated_ffn(X, up, down, act, ...)                   gated feed-forward block, bf16, grouped rows
+  gated_ffn_backward(dY, X, up, down, Z, act, ...)   its gradients
+  int8_quantize(X, gate, ...)                        rows (or gated rows) in 8-bit integers
+  int8_product(A, a_scales, B, b_scales, ...)        products of 8-bit integers, grouped rows
   sync_status()                                      stream sync + device error word
 """
 
@@ -416,6 +420,7 @@ _BLOCKS = {"row": _abi.MAO_BLOCKS_ROW, "col": _abi.MAO_BLOCKS_COL, "tile": _abi.
 _KINDS = {"row": ("row",), "col": ("col",), "tile": ("tile",), "both": ("row", "col")}
 _FORM = {"nt": _abi.MAO_NT, "nn": _abi.MAO_NN, "tn": _abi.MAO_TN}
 _SCORE = {"softmax": _abi.MAO_SCORE_SOFTMAX, "sigmoid": _abi.MAO_SCORE_SIGMOID}
+_ACT = {"silu": _abi.MAO_SILU, "gelu": _abi.MAO_GELU, "gelu_tanh": _abi.MAO_GELU_TANH}
 _GROUP_SCORE = {"max": _abi.MAO_GROUP_MAX, "top2": _abi.MAO_GROUP_TOP2}
 
 
@@ -813,6 +818,279 @@ def expert_combine_backward(dY, Z, row_of, slot_of, weights=None, dZ=None, dweig
     if st:
         _abi.check("expert_combine_backward", st)
     return dZ, dweights
+
+
+def _act(name):
+    kind = _ACT.get(name)
+    if kind is None:
+        raise ValueError("the activation must be silu, gelu or gelu_tanh")
+    return kind
+
+
+def _stack(t, groups, rows, cols, name):
+    """MaoMat of stacked matrices [groups, rows, cols] (or one, [rows, cols]) as one tall matrix."""
+    shape, st = t.shape, t.stride()
+    if tuple(shape) != (groups, rows, cols) and not (groups == 1 and tuple(shape) == (rows, cols)):
+        raise ValueError("%s must have shape %s" % (name, (groups, rows, cols)))
+    dt = _FLOATS.get(t.dtype)
+    if dt is None or not t.is_cuda or (st[-1] != 1 and cols > 1):
+        raise ValueError("%s must be a float32 or bfloat16 CUDA tensor with unit column stride" % name)
+    ld = st[-2] if rows > 1 else max(st[0], cols) if groups > 1 and len(shape) == 3 else cols
+    if ld < cols and rows > 1:
+        raise ValueError("%s: expected a tensor whose rows do not overlap" % name)
+    if groups > 1 and st[0] != rows * ld:
+        raise ValueError("%s: stacked matrices follow each other without gaps" % name)
+    return _abi.MaoMat(t.data_ptr(), groups * rows, cols, ld, dt, 0)
+
+
+def _runs(offsets, counts):
+    """Device pointers of a call's runs of rows, and their number."""
+    if offsets is None:
+        if counts is not None:
+            raise ValueError("counts go with offsets")
+        return None, None, 1
+    groups = offsets.numel() - 1
+    if groups < 1:
+        raise ValueError("offsets needs at least two entries")
+    return (_dense_ptr(offsets, torch.int32, (groups + 1,), "offsets"),
+            _dense_ptr(counts, torch.int32, (groups,), "counts"), groups)
+
+
+def _block(X, up, down, groups):
+    """MaoMats of a block's X, up and down, and its widths (K, N, C)."""
+    if X.dtype != torch.bfloat16 or up.dtype != torch.bfloat16 or down.dtype != torch.bfloat16:
+        raise ValueError("X, up and down must be bfloat16")
+    if down.dim() not in (2, 3) or up.dim() != down.dim():
+        raise ValueError("up and down must be matrices, or stacked ones for each run of rows")
+    x = _desc(X)
+    C, N = down.shape[-2:]
+    return (x, _stack(up, groups, 2 * N, x.cols, "up"), _stack(down, groups, C, N, "down"),
+            x.cols, N, C)
+
+
+def _ws(ws, nbytes, like, stream):
+    """The caller's workspace or a new one of nbytes; its device pointer and bytes."""
+    if ws is not None:
+        return (ws,) + _buffer(ws)
+    if not nbytes:
+        return None, None, 0
+    ws, ptr = _out(None, nbytes, torch.uint8, "", like, stream)
+    return ws, ptr, nbytes
+
+
+def gated_ffn(X, up, down, act="silu", offsets=None, counts=None, save=False, out=None,
+              out_dtype=torch.bfloat16, Z=None, ws=None, stream=None):
+    """Y = (act(X Wg^T) * (X Wu^T)) Wd^T, sums in fp32; with save (or a tensor Z to fill), (Y, Z): Z
+    holds the rows of [X Wg^T, X Wu^T], which gated_ffn_backward takes.
+
+    X: bfloat16 [T, K]. up: bfloat16 [2 N, K], the N rows of Wg, then those of Wu. down:
+    bfloat16 [C, N]. act: "silu", "gelu" or "gelu_tanh". offsets: int32 tensor of groups + 1
+    row numbers (expert_plan's); up and down are then stacked, [groups, 2 N, K] and [groups, C,
+    N], one for each run of rows. counts: int32 tensor of groups numbers (expert_plan's): the
+    rows of each run that hold tokens; the others are not computed. Rows without a run, or past
+    their run's count, become zero. out: a float32 or bfloat16 tensor to fill, by default a
+    new one of out_dtype. ws: a uint8 buffer of gated_ffn_workspace_bytes; allocated by default.
+    """
+    kind = _act(act)
+    off, cnt, groups = _runs(offsets, counts)
+    x, u, d, K, N, C = _block(X, up, down, groups)
+    if out is None:
+        if out_dtype not in _FLOATS:
+            raise ValueError("out_dtype must be float32 or bfloat16")
+        out, yp = _out(None, (x.rows, C), out_dtype, "", X, stream)
+        y = _abi.MaoMat(yp, x.rows, C, C, _FLOATS[out_dtype], 0)
+    else:
+        y = _desc(out)
+    z = None
+    if Z is not None:
+        z = _desc(Z)
+    elif save:
+        Z, zp = _out(None, (x.rows, 2 * N), torch.bfloat16, "", X, stream)
+        z = _abi.MaoMat(zp, x.rows, 2 * N, 2 * N, _abi.MAO_BF16, 0)
+    refs = ctypes.byref(x), ctypes.byref(u), ctypes.byref(d)
+    need = 0 if ws is not None else \
+        lib().gated_ffn_workspace_bytes(*refs, groups, off is not None)
+    ws, wptr, wbytes = _ws(ws, need, X, stream)
+    st = lib().gated_ffn(*refs, kind, off, cnt, groups, None if z is None else ctypes.byref(z),
+                         ctypes.byref(y), wptr, wbytes,
+                         _raw_stream(stream, X, up, down, offsets, counts, out, Z, ws))
+    if st:
+        _abi.check("gated_ffn", st)
+    return out if z is None else (out, Z)
+
+
+def gated_ffn_backward(dY, X, up, down, Z, act="silu", offsets=None, counts=None, dX=None,
+                       dup=None, ddown=None, grad_dtype=torch.bfloat16, ws=None, stream=None):
+    """Gradients (dX, dup, ddown) of gated_ffn for the gradient dY (bfloat16 [T, C]) of its output,
+    from the call's arguments and its Z.
+
+    dX, dup, ddown: float32 or bfloat16 tensors to fill, by default new ones of grad_dtype,
+    shaped as X, up and down; False: not wanted (None is returned in its place). offsets must
+    be multiples of 128 (expert_plan's), but for the last. With counts, rows of X and dY past
+    their run's count must be finite.
+    """
+    kind = _act(act)
+    off, cnt, groups = _runs(offsets, counts)
+    x, u, d, K, N, C = _block(X, up, down, groups)
+    if dY.dtype != torch.bfloat16 or Z.dtype != torch.bfloat16:
+        raise ValueError("dY and Z must be bfloat16")
+    dy, z = _desc(dY), _desc(Z)
+    if grad_dtype not in _FLOATS:
+        raise ValueError("grad_dtype must be float32 or bfloat16")
+    outs, descs = [], []
+    for t, like, rows, cols in ((dX, X, x.rows, K), (dup, up, u.rows, K), (ddown, down, d.rows, N)):
+        if t is False:
+            outs.append(None)
+            descs.append(None)
+            continue
+        if t is None:
+            t, ptr = _out(None, like.shape, grad_dtype, "", X, stream)
+            m = _abi.MaoMat(ptr, rows, cols, cols, _FLOATS[grad_dtype], 0)
+        elif t.dim() == 3:
+            m = _stack(t, groups, rows // groups, cols, "the gradient of up or down")
+        else:
+            m = _desc(t)
+        outs.append(t)
+        descs.append(ctypes.byref(m))
+    refs = ctypes.byref(dy), ctypes.byref(x), ctypes.byref(u), ctypes.byref(d)
+    need = 0 if ws is not None else \
+        lib().gated_ffn_backward_workspace_bytes(*refs, groups, off is not None)
+    ws, wptr, wbytes = _ws(ws, need, X, stream)
+    st = lib().gated_ffn_backward(
+        *refs, ctypes.byref(z), kind, off, cnt, groups, *descs, wptr, wbytes,
+        _raw_stream(stream, dY, X, up, down, Z, offsets, counts, *outs, ws))
+    if st:
+        _abi.check("gated_ffn_backward", st)
+    return tuple(outs)
+
+
+def gated_ffn_workspace_bytes(X, up, down, groups=None):
+    """Workspace of gated_ffn for these tensors (groups: the number of runs, None without
+    offsets)."""
+    x, u, d = _block(X, up, down, groups or 1)[:3]
+    return int(lib().gated_ffn_workspace_bytes(ctypes.byref(x), ctypes.byref(u), ctypes.byref(d),
+                                               groups or 1, groups is not None))
+
+
+def gated_ffn_backward_workspace_bytes(dY, X, up, down, groups=None):
+    """Workspace of gated_ffn_backward for these tensors."""
+    x, u, d = _block(X, up, down, groups or 1)[:3]
+    dy = _desc(dY)
+    return int(lib().gated_ffn_backward_workspace_bytes(
+        ctypes.byref(dy), ctypes.byref(x), ctypes.byref(u), ctypes.byref(d), groups or 1,
+        groups is not None))
+
+
+def _int8(codes, scales, name):
+    """MaoInt8 of a code tensor [R, C] or [B, R, C] and its scales [R] or [B, R]."""
+    shape = codes.shape
+    if codes.dtype != torch.int8 or len(shape) not in (2, 3) or not codes.is_cuda:
+        raise ValueError("%s: codes are int8 CUDA tensors of two or three dimensions" % name)
+    sp = _dense_ptr(scales, torch.float32, shape[:-1], "%s: scales" % name)
+    rows, cols = shape[-2], shape[-1]
+    count = shape[0] if len(shape) == 3 else 1
+    st = codes.stride()
+    if st[-1] != 1 and cols > 1:
+        raise ValueError("%s: expected unit column stride" % name)
+    # the row stride of a single row may be anything
+    ld = st[-2] if rows > 1 else -(-cols // 16) * 16
+    if count > 1 and rows:
+        if rows == 1:
+            ld = st[0]
+        if st[0] != rows * ld:
+            raise ValueError("%s: stacked matrices follow each other without gaps" % name)
+    return _abi.MaoInt8(codes.data_ptr(), sp, rows, cols, ld, count, 0)
+
+
+def int8_quantize(X, gate=None, out=None, stream=None):
+    """Codes (int8) and scales (float32) of the rows of X: codes * scale, scale = largest
+    magnitude / 127, codes rounded to nearest even.
+
+    X: a float32 or bfloat16 matrix [R, C], stacked matrices [B, R, C], or a list of B matrices
+    of one shape. gate: "silu", "gelu" or "gelu_tanh": X is [R, 2 C], and the rows act(X[:, :C])
+    * X[:, C:] (in float32) are quantised. Returns (codes, scales), stacked as X is; code rows
+    are 16-byte aligned. A row with a NaN or an infinity gets scale NaN and codes 0. out: a pair
+    of tensors to fill.
+    """
+    many = isinstance(X, (list, tuple))
+    if many and not X:
+        raise ValueError("no matrices")
+    x0 = X[0] if many else X
+    stacked = many or x0.dim() == 3
+    if many:
+        mats, batch, stride = _mats(list(X)), len(X), 0
+        R, C = x0.shape
+    elif stacked:
+        batch, R, C = x0.shape
+        if batch == 0:
+            raise ValueError("no matrices")
+        m = _desc(x0, 3)
+        stride = x0.stride(0) if batch > 1 else 0
+        if batch > 1 and stride < 1:
+            raise ValueError("stacked matrices need a positive stride")
+        mats = ctypes.byref(m)
+    else:
+        m = _desc(x0)
+        mats, batch, stride = ctypes.byref(m), 1, 0
+        R, C = m.rows, m.cols
+    kind = 0
+    if gate is not None:
+        kind = _act(gate)
+        if C % 2:
+            raise ValueError("gated rows have an even number of columns")
+        C //= 2
+    if out is None:
+        wide = (C + 15) // 16 * 16
+        size, strides = (R, C), (wide, 1)
+        if stacked:
+            size, strides = (batch, R, C), (R * wide, wide, 1)
+        if wide == C:
+            codes, cp = _out(None, size, torch.int8, "", x0, stream)
+        else:  # rows start at multiples of 16 bytes
+            codes = _empty_strided(size, strides, torch.int8, x0.device, stream)
+            cp = codes.data_ptr()
+        scales, sp = _out(None, size[:-1], torch.float32, "", x0, stream)
+        d = _abi.MaoInt8(cp, sp, R, C, wide, batch, 0)
+    else:
+        codes, scales = out
+        d = _int8(codes, scales, "out")
+    st = lib().int8_quantize(mats, batch, stride, gate is not None, kind, ctypes.byref(d),
+                             _raw_stream(stream, *(X if many else (X,)), codes, scales))
+    if st:
+        _abi.check("int8_quantize", st)
+    return codes, scales
+
+
+def int8_product(A, a_scales, B, b_scales, offsets=None, counts=None, out=None,
+                 out_dtype=torch.bfloat16, ws=None, stream=None):
+    """out[t, n] = a_scales[t] b_scales[n] sum_k A[t, k] B[n, k] of int8 codes (int8_quantize's of
+    the tokens and of the weights), sums in fp32.
+
+    A: int8 [T, K]. B: int8 [N, K], or [groups, N, K] with offsets and counts, which are as in
+    gated_ffn. out: a float32 or bfloat16 tensor to fill, by default a new one of out_dtype. ws:
+    a uint8 buffer for few rows, whose sums are split (int8_product_workspace_bytes); allocated
+    when needed.
+    """
+    off, cnt, groups = _runs(offsets, counts)
+    if A.dim() != 2:
+        raise ValueError("A must be a matrix")
+    a, b = _int8(A, a_scales, "A"), _int8(B, b_scales, "B")
+    if out is None:
+        if out_dtype not in _FLOATS:
+            raise ValueError("out_dtype must be float32 or bfloat16")
+        out, op = _out(None, (a.rows, b.rows), out_dtype, "", A, stream)
+        d = _abi.MaoMat(op, a.rows, b.rows, b.rows, _FLOATS[out_dtype], 0)
+    else:
+        d = _desc(out)
+    ra, rb = ctypes.byref(a), ctypes.byref(b)
+    need = 0 if ws is not None or off is not None else \
+        lib().int8_product_workspace_bytes(ra, rb, False)
+    ws, wptr, wbytes = _ws(ws, need, A, stream)
+    st = lib().int8_product(ra, rb, ctypes.byref(d), off, cnt, groups, wptr, wbytes,
+                            _raw_stream(stream, A, a_scales, B, b_scales, offsets, counts, out, ws))
+    if st:
+        _abi.check("int8_product", st)
+    return out
 
 
 def set_wait_limit(ns):

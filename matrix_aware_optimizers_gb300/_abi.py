@@ -29,6 +29,9 @@ MAO_SCORE_SOFTMAX = 0
 MAO_SCORE_SIGMOID = 1
 MAO_GROUP_MAX = 0
 MAO_GROUP_TOP2 = 1
+MAO_SILU = 0
+MAO_GELU = 1
+MAO_GELU_TANH = 2
 
 # every symbol include/mao.h declares
 EXPORTS = (
@@ -61,6 +64,13 @@ EXPORTS = (
     "expert_plan",
     "expert_combine",
     "expert_combine_backward",
+    "gated_ffn",
+    "gated_ffn_workspace_bytes",
+    "gated_ffn_backward",
+    "gated_ffn_backward_workspace_bytes",
+    "int8_quantize",
+    "int8_product",
+    "int8_product_workspace_bytes",
     "mao_set_wait_limit",
     "mao_get_wait_limit",
     "mao_sync_status",
@@ -94,6 +104,18 @@ class MaoFp8(ctypes.Structure):
         ("scale_ld", ctypes.c_int64),
         ("count", ctypes.c_int32),
         ("blocks", ctypes.c_int32),
+    ]
+
+
+class MaoInt8(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("count", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -200,7 +222,21 @@ def load():
              [vp, i64, i32, vp, vp, vp, vp, i64, vp, ctypes.c_size_t, vp]),
             ("expert_combine", ctypes.c_int, [P(MaoMat), vp, vp, i64, i32, P(MaoMat), vp]),
             ("expert_combine_backward", ctypes.c_int,
-             [P(MaoMat), P(MaoMat), vp, vp, vp, i32, P(MaoMat), vp, vp])):
+             [P(MaoMat), P(MaoMat), vp, vp, vp, i32, P(MaoMat), vp, vp]),
+            ("gated_ffn", ctypes.c_int,
+             [P(MaoMat), P(MaoMat), P(MaoMat), i32, vp, vp, i32, P(MaoMat), P(MaoMat), vp,
+              ctypes.c_size_t, vp]),
+            ("gated_ffn_workspace_bytes", ctypes.c_size_t,
+             [P(MaoMat), P(MaoMat), P(MaoMat), i32, i32]),
+            ("gated_ffn_backward", ctypes.c_int,
+             [P(MaoMat), P(MaoMat), P(MaoMat), P(MaoMat), P(MaoMat), i32, vp, vp, i32, P(MaoMat),
+              P(MaoMat), P(MaoMat), vp, ctypes.c_size_t, vp]),
+            ("gated_ffn_backward_workspace_bytes", ctypes.c_size_t,
+             [P(MaoMat), P(MaoMat), P(MaoMat), P(MaoMat), i32, i32]),
+            ("int8_quantize", ctypes.c_int, [P(MaoMat), i32, i64, i32, i32, P(MaoInt8), vp]),
+            ("int8_product", ctypes.c_int,
+             [P(MaoInt8), P(MaoInt8), P(MaoMat), vp, vp, i32, vp, ctypes.c_size_t, vp]),
+            ("int8_product_workspace_bytes", ctypes.c_size_t, [P(MaoInt8), P(MaoInt8), i32])):
         getattr(lib, name).restype = res
         getattr(lib, name).argtypes = args
     lib.mao_set_wait_limit.restype = None

@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "experts.h"
+#include "ffn.h"
 #include "internal.h"
 #include "ns_small.h"
 
@@ -373,9 +374,12 @@ mao_status mao_sync_status(void* stream) {
   const mao_status b = dion_read_and_clear_error(static_cast<cudaStream_t>(stream));
   const mao_status c = small_read_and_clear_error(static_cast<cudaStream_t>(stream));
   const mao_status d = product_read_and_clear_error(static_cast<cudaStream_t>(stream));
-  if (a == MAO_ERR_CUDA || b == MAO_ERR_CUDA || c == MAO_ERR_CUDA || d == MAO_ERR_CUDA)
-    return MAO_ERR_CUDA;
-  return a != MAO_OK ? a : b != MAO_OK ? b : c != MAO_OK ? c : d;
+  const mao_status e = ffn_read_and_clear_error(static_cast<cudaStream_t>(stream));
+  const mao_status f = int8_read_and_clear_error(static_cast<cudaStream_t>(stream));
+  mao_status st = MAO_OK;
+  for (const mao_status s : {a, b, c, d, e, f})
+    if (s == MAO_ERR_CUDA || st == MAO_OK) st = s;
+  return st;
 }
 
 int64_t mao_launch_count(void) { return g_launches.load(); }

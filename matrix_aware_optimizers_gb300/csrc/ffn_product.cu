@@ -1,0 +1,912 @@
+// Products of the gated feed-forward block in bf16 on the 5th-generation tensor cores, fp32 sums,
+// over runs of rows.
+//
+// Every product is D[j][i] = sum_k Q[j][k] P[i][k]: i runs along D's rows in memory. An operand
+// whose depth runs along its rows is loaded K-major, one whose depth runs down its columns
+// MN-major, so no operand is transposed in memory:
+//   GATE       H = act(X Wg^T) * (X Wu^T)        P = [Wg; Wu], Q = X               nt
+//   down       Y = H Wd^T                        P = Wd, Q = H                     nt
+//   GATE_BACK  dG, dU, H from dH = dY Wd, G, U   P = Wd, Q = dY                    nn
+//   dX         dG Wg + dU Wu                     P = [Wg; Wu], Q = [dG, dU]        nn, depth 2 N
+//   dup        dG^T X, dU^T X                    P = X, Q = dG or dU               tn
+//   ddown      dY^T H                            P = H, Q = dY                     tn
+// dH never reaches memory: the epilogue of its product turns it into dG, dU and H. For GATE each
+// 32 lanes of the accumulator hold 16 rows of Wg and the same 16 of Wu (sixteen-row boxes, loaded
+// that way), so that a channel's G and U meet by one exchange within a warp.
+//
+// Tiles of 256 x 256 (GATE: 128 channels, twice) by a pair of CTAs (tcgen05 cta_group::2, M = 256
+// values of i, N up to 256 values of j). Roles per CTA (320 threads):
+//   warp 0      TMA producer: 64-deep stages, 128 rows of P and the tile's half of Q, ring of six
+//   warp 1      TMEM allocation; in the even CTA it issues the products (converged, one lane)
+//   warps 2..9  epilogue: two warps per 32-lane quadrant of TMEM; lane = i
+// TMEM holds two accumulators of 256 columns: a tile's epilogue runs under the next one's products.
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "ffn.h"
+#include "ffn_act.cuh"
+#include "ffn_tiles.cuh"
+#include "internal.h"
+#include "ns_plan.h"
+#include "tc_ptx.cuh"
+
+namespace mao {
+namespace {
+
+using namespace ptx;
+using namespace ffn;
+
+constexpr int BK = 64;                // depth per stage: rows of 128 bytes
+constexpr int OP_BYTES = HALF * BK * 2;
+constexpr int STAGE_BYTES = 2 * OP_BYTES;
+constexpr int CHUNK_BYTES = 64 * BK * 2;  // 64 values of i or j of an MN-major operand
+constexpr int STAGES = 6;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int TMEM_COLS = 512;
+constexpr int Q_BOXES = 4;            // heights of boxes of a K-major Q: 16 << b rows
+constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + TABLE_BYTES + 256;
+static_assert(SMEM <= 232448, "shared memory budget of one CTA");
+
+enum Epilogue { PLAIN, GATE, GATE_BACK };
+
+struct FfnParams : TileParams {
+  CUtensorMap map_p;
+  CUtensorMap map_q[Q_BOXES];  // boxes of 16, 32, 64, 128 rows (TN: the last only, 64 x 64)
+  void* d;                     // PLAIN: D; GATE, GATE_BACK: H
+  __nv_bfloat16* z;            // G and U: GATE writes them (null: not wanted), GATE_BACK reads them
+  __nv_bfloat16* dz;           // GATE_BACK: dG and dU
+  int64_t ld, ldz, lddz;
+  int32_t dz_half;             // columns from dG to dU
+  int32_t dtype, act;
+  int32_t paired, paired_z;  // entries 2 i, 2 i + 1 of a row are one 4-byte word
+  int32_t part_half;           // GATE: columns from G's parts to U's
+};
+
+// Instruction descriptor of kind::f16: bf16 operands, fp32 sums, M = 256.
+__device__ __forceinline__ uint32_t instr_desc(int p_mn, int q_mn, int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(p_mn) << 15) | (uint32_t(q_mn) << 16) |
+         (uint32_t(n >> 3) << 17) | (uint32_t(TILE >> 4) << 24);
+}
+
+// The four 16-deep products of a block, issued by the elected lane of a converged warp: the
+// operands' descriptors advance by dp and dq (in 16-byte units) from one to the next.
+__device__ __forceinline__ void mma_block(uint32_t elected, uint32_t d, uint64_t p, uint64_t q,
+                                          uint32_t dp, uint32_t dq, uint32_t idesc,
+                                          uint32_t accumulate) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    asm volatile(
+        "{\n\t.reg .pred a, e;\n\t"
+        "setp.ne.b32 a, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, a;\n\t}\n" ::"r"(d),
+        "l"(p + uint64_t(k) * dp), "l"(q + uint64_t(k) * dq), "r"(idesc),
+        "r"(k ? 1u : accumulate), "r"(elected)
+        : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ output
+
+// Sixteen rows of D (from row j on, those below j_end) at column i of this lane.
+__device__ __forceinline__ void store16(const FfnParams& p, const Tile& t, int j, int i,
+                                        const float (&v)[16], int lane) {
+  const bool in = i < p.I;
+  const int64_t row = t.row0 + j;
+  if (p.dtype == MAO_F32) {
+    float* d = static_cast<float*>(p.d) + row * p.ld + i;
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      if (in && j + c < t.j_end)
+        asm volatile("st.global.L1::no_allocate.f32 [%0], %1;" ::"l"(d + c * p.ld), "f"(v[c]) : "memory");
+    return;
+  }
+  __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + row * p.ld + i;
+  if (p.paired) {
+    const int odd = lane & 1;
+    d += odd ? p.ld - 1 : 0;
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+      const uint32_t both = swap_pair(v[c], v[c + 1], odd);
+      if (in && j + c + odd < t.j_end)  // an even number of columns: both or none are there
+        store_word(d, both);
+      d += 2 * p.ld;
+    }
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    if (in && j + c < t.j_end) d[c * p.ld] = __float2bfloat16_rn(v[c]);
+}
+
+// The same of a split of GATE: lanes 0 .. 15 hold G, lanes 16 .. 31 U, of channel i.
+__device__ __forceinline__ void store16_gate_parts(const FfnParams& p, const Tile& t, int j, int i,
+                                                   const float (&v)[16], int lane) {
+  float* d = static_cast<float*>(p.d) + (t.row0 + j) * p.ld + i + (lane & 16 ? p.part_half : 0);
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    if (i < p.I && j + c < t.j_end)
+      asm volatile("st.global.L1::no_allocate.f32 [%0], %1;" ::"l"(d + c * p.ld), "f"(v[c]) : "memory");
+}
+
+// GATE: lanes 0 .. 15 hold G and lanes 16 .. 31 U of sixteen rows at channel i (the same for l and
+// l + 16). Of each four rows the lower lanes take two and the upper ones two; then the lanes of
+// a pair take one row each.
+__device__ __forceinline__ void gate16(const FfnParams& p, const Tile& t, int j, int i,
+                                       const float (&v)[16], int lane) {
+  const int up = lane >> 4, odd = lane & 1;
+  const bool in = i < p.I;
+  __nv_bfloat16* h = static_cast<__nv_bfloat16*>(p.d);
+#pragma unroll
+  for (int c = 0; c < 16; c += 4) {
+    const float s0 = up ? v[c] : v[c + 2], s1 = up ? v[c + 1] : v[c + 3];
+    const float r0 = __shfl_xor_sync(0xFFFFFFFFu, s0, 16), r1 = __shfl_xor_sync(0xFFFFFFFFu, s1, 16);
+    const float g0 = up ? r0 : v[c], g1 = up ? r1 : v[c + 1];
+    const float u0 = up ? v[c + 2] : r0, u1 = up ? v[c + 3] : r1;
+    const float h0 = activate(g0, p.act) * u0, h1 = activate(g1, p.act) * u1;
+    const int r = j + c + 2 * up;  // the lane's two rows
+    if (p.paired) {
+      const uint32_t wh = swap_pair(h0, h1, odd);
+      const int64_t row = r + odd;
+      const bool ok = in && row < t.j_end;
+      if (ok) store_word(h + row * p.ld + i - odd, wh);
+    } else {
+      if (in && r < t.j_end) h[int64_t(r) * p.ld + i] = __float2bfloat16_rn(h0);
+      if (in && r + 1 < t.j_end) h[int64_t(r + 1) * p.ld + i] = __float2bfloat16_rn(h1);
+    }
+    if (p.z) {
+      if (p.paired_z) {
+        const uint32_t wg = swap_pair(g0, g1, odd), wu = swap_pair(u0, u1, odd);
+        const int64_t row = r + odd;
+        if (in && row < t.j_end) {
+          store_word(p.z + row * p.ldz + i - odd, wg);
+          store_word(p.z + row * p.ldz + p.I + i - odd, wu);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (in && r + q < t.j_end) {
+            __nv_bfloat16* z = p.z + int64_t(r + q) * p.ldz + i;
+            z[0] = __float2bfloat16_rn(q ? g1 : g0);
+            z[p.I] = __float2bfloat16_rn(q ? u1 : u0);
+          }
+      }
+    }
+  }
+}
+
+// GATE_BACK: G and U of the sixteen rows at column i, two columns of every second row if paired
+// (even lanes of rows j, j + 2, ..., odd lanes of the others).
+struct Saved {
+  uint32_t g[8], u[8];
+};
+__device__ __forceinline__ void load_saved(const FfnParams& p, const Tile& t, int j, int i, int lane,
+                                           Saved& s) {
+  const int odd = lane & 1;
+  if (p.paired_z) {
+    const __nv_bfloat16* z = p.z + int64_t(j + odd) * p.ldz + i - odd;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const bool ok = i < p.I && j + 2 * c + odd < t.j_end;
+      s.g[c] = ok ? __ldg(reinterpret_cast<const uint32_t*>(z)) : 0u;
+      s.u[c] = ok ? __ldg(reinterpret_cast<const uint32_t*>(z + p.I)) : 0u;
+      z += 2 * p.ldz;
+    }
+    return;
+  }
+  // entry by entry: the two columns of this lane's rows
+  const int col = i - odd;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const int row = j + 2 * c + odd;
+    const uint16_t* z = reinterpret_cast<const uint16_t*>(p.z) + int64_t(row) * p.ldz + col;
+    const bool a = col < p.I && row < t.j_end, b = col + 1 < p.I && row < t.j_end;
+    s.g[c] = (a ? uint32_t(z[0]) : 0u) | (b ? uint32_t(z[1]) << 16 : 0u);
+    s.u[c] = (a ? uint32_t(z[p.I]) : 0u) | (b ? uint32_t(z[p.I + 1]) << 16 : 0u);
+  }
+}
+
+// dG, dU and H of sixteen rows of dH. The buffers' rows are padded to whole words.
+__device__ __forceinline__ void gate_back16(const FfnParams& p, const Tile& t, int j, int i,
+                                            const float (&v)[16], const Saved& s, int lane) {
+  const int odd = lane & 1, col = i - odd;
+  __nv_bfloat16* h = static_cast<__nv_bfloat16*>(p.d);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float o = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[2 * c] : v[2 * c + 1], 1);
+    const float d0 = odd ? o : v[2 * c], d1 = odd ? v[2 * c + 1] : o;
+    float a0, a1, s0, s1;
+    activate(low_half(s.g[c]), p.act, a0, s0);
+    activate(high_half(s.g[c]), p.act, a1, s1);
+    const float u0 = low_half(s.u[c]), u1 = high_half(s.u[c]);
+    const int64_t row = j + 2 * c + odd;
+    if (col < p.I && row < t.j_end) {
+      store_word(p.dz + row * p.lddz + col, pack(d0 * u0 * s0, d1 * u1 * s1));
+      store_word(p.dz + row * p.lddz + p.dz_half + col, pack(d0 * a0, d1 * a1));
+      store_word(h + row * p.ld + col, pack(a0 * u0, a1 * u1));
+    }
+  }
+}
+
+// Rows from j0 below j1 of the outputs hold no tokens.
+template <int EPI>
+__device__ __forceinline__ void clear_unused(const FfnParams& p, int64_t j0, int64_t j1, int64_t turn,
+                                             int64_t turns, int lane) {
+  const int es = p.dtype == MAO_F32 ? 4 : 2;
+  if (EPI != GATE) clear_rows(p.d, p.ld * es, int64_t(p.I) * es, j0 + turn, j1, turns, lane);
+  if (EPI == GATE && p.z) clear_rows(p.z, p.ldz * 2, int64_t(p.I) * 4, j0 + turn, j1, turns, lane);
+  if (EPI == GATE_BACK) {
+    clear_rows(p.dz, p.lddz * 2, int64_t(p.I) * 2, j0 + turn, j1, turns, lane);
+    clear_rows(p.dz + p.dz_half, p.lddz * 2, int64_t(p.I) * 2, j0 + turn, j1, turns, lane);
+  }
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int FORM, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    ffn_kernel(const __grid_constant__ FfnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  int* lo = reinterpret_cast<int*>(ring + STAGES * STAGE_BYTES);
+  int* cnt = lo + MAX_GROUPS + 2;
+  int* begin = cnt + MAX_GROUPS + 2;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + STAGES * STAGE_BYTES + TABLE_BYTES);
+  uint64_t* full_bar = bars;                  // [STAGES]  (used in the even CTA)
+  uint64_t* empty_bar = full_bar + STAGES;    // [STAGES]
+  uint64_t* tfull_bar = empty_bar + STAGES;   // [2]
+  uint64_t* tempty_bar = tfull_bar + 2;       // [2]       (even CTA)
+  uint64_t* drain_bar = tempty_bar + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t cta = cluster_ctarank();
+  const bool leader = cta == 0;
+  const int pair = blockIdx.x >> 1;
+  const int npairs = gridDim.x >> 1;
+  const uint64_t limit = p.timeout_ns;
+  constexpr int p_mn = FORM != NT, q_mn = FORM == TN;
+  constexpr int STEP_I = EPI == GATE ? HALF : TILE;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&tfull_bar[a]), 1);
+      mbar_init(smem_u32(&tempty_bar[a]), 2 * EPI_WARPS);
+    }
+    mbar_init(smem_u32(drain_bar), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_holder)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (warp == 0 && lane < 2) {
+    const CUtensorMap* map = lane ? &p.map_q[Q_BOXES - 1] : &p.map_p;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+  }
+  // launched as a programmatic dependent: the set-up so far may overlap the previous kernel
+  wait_for_previous();
+  make_table<THREADS>(p, lo, cnt, begin, reinterpret_cast<int*>(bars + 24));
+  tc_fence_before();
+  __syncthreads();
+  const int total = FORM == TN ? (p.J + TILE - 1) / TILE * p.tiles_i * p.groups * p.halves * p.splits
+                               : begin[p.groups] * p.tiles_i * p.splits;
+  cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA arrival
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
+    // P's rows i0 + 128 cta .. and Q's rows j0 + n/2 cta .. (each CTA supplies half of the
+    // tile's n values of j). The whole warp runs the loop, converged; one lane issues.
+    const uint32_t elected = elect_one();
+    const uint32_t full0 = mapa_shared(smem_u32(full_bar), 0);
+    const uint32_t ring0 = smem_u32(ring);
+    const int half_kb = (p.depth + BK - 1) / BK;  // NN: blocks of a half of the depth
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    uint32_t armed = 0, armed_phase = 0;
+    Tile t;
+    for (int tile = pair; ok && tile < total; tile += npairs) {
+      decode<FORM, STEP_I, BK>(p, lo, cnt, begin, tile, t);
+      const int i = t.i0 + (EPI == GATE ? HALF / 2 : HALF) * int(cta);
+      const int j = t.j0 + (t.n >> 1) * int(cta);
+      const int z = FORM != TN ? t.g : 0;
+      const int q_rows = t.n >> 1;  // a multiple of 16
+      const int q_chunks = (q_rows + 63) >> 6;
+      const uint32_t q_bytes = q_mn ? uint32_t(q_chunks) * CHUNK_BYTES : uint32_t(q_rows) * BK * 2;
+      for (int kb = 0; kb < t.nkb; ++kb) {
+        if (!wait_warp<false>(&empty_bar[stage], phase ^ 1u, abort_flag, limit)) {
+          ok = false;
+          break;
+        }
+        const uint32_t fb = full0 + 8 * stage, dst = ring0 + stage * STAGE_BYTES;
+        const int b = t.kb0 + kb;
+        const int second = FORM == NN && b >= half_kb;  // half of the depth
+        const int k = t.k0 + (second ? b - half_kb : b) * BK;
+        if (elected) {
+          if (leader) mbar_expect_tx(smem_u32(&full_bar[stage]), 2 * (OP_BYTES + q_bytes));
+          if (EPI == GATE) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r)  // 16 rows of Wg, the same 16 of Wu, ...
+              tma_load_4d_pair(dst + r * (16 * BK * 2), &p.map_p, fb, k, i + 16 * (r >> 1), r & 1, z);
+          } else if (p_mn) {
+            tma_load_4d_pair(dst, &p.map_p, fb, i, k, second, z);
+            tma_load_4d_pair(dst + CHUNK_BYTES, &p.map_p, fb, i + 64, k, second, z);
+          } else {
+            tma_load_4d_pair(dst, &p.map_p, fb, k, i, 0, z);
+          }
+          if (q_mn) {
+            for (int c = 0; c < q_chunks; ++c)
+              tma_load_4d_pair(dst + OP_BYTES + c * CHUNK_BYTES, &p.map_q[Q_BOXES - 1], fb, j + 64 * c, k, t.half, 0);
+          } else if (q_rows == HALF) {
+            tma_load_4d_pair(dst + OP_BYTES, &p.map_q[Q_BOXES - 1], fb, k, j, second, 0);
+          } else {
+            for (int box = Q_BOXES - 2, at = 0; box >= 0; --box)
+              if (q_rows & (16 << box)) {
+                tma_load_4d_pair(dst + OP_BYTES + at * (BK * 2), &p.map_q[box], fb, k, j + at, second, 0);
+                at += 16 << box;
+              }
+          }
+        }
+        armed |= 1u << stage;
+        armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // after an abort, the loads already issued land before the CTA leaves
+    if (*abort_flag && leader && lane == 0) {
+      for (int s = 0; s < STAGES; ++s)
+        if ((armed >> s) & 1u) mbar_drain(smem_u32(&full_bar[s]), (armed_phase >> s) & 1u, 20000000ull);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (leader) {
+      const uint32_t elected = elect_one();
+      // K-major: rows of 128 bytes, 1024 between groups of eight; 32 bytes along them per product.
+      // MN-major: eight rows of the depth per 1024 bytes, 64 values of i or j per chunk; two
+      // groups of eight per product.
+      const uint64_t p_desc = desc_of(smem_u32(ring), p_mn ? CHUNK_BYTES : 16, 1024, 2);
+      const uint64_t q_desc = desc_of(smem_u32(ring) + OP_BYTES, q_mn ? CHUNK_BYTES : 16, 1024, 2);
+      const uint32_t dp = p_mn ? 2048 >> 4 : 32 >> 4, dq = q_mn ? 2048 >> 4 : 32 >> 4;
+      int stage = 0, local = 0;
+      uint32_t phase = 0;
+      bool ok = true, issued = false, ready = false;
+      Tile t;
+      for (int tile = pair; ok && tile < total; tile += npairs) {
+        decode<FORM, STEP_I, BK>(p, lo, cnt, begin, tile, t);
+        if (t.nkb == 0) continue;
+        const int acc = local & 1;
+        if (!wait_warp<true>(&tempty_bar[acc], (uint32_t(local >> 1) & 1u) ^ 1u, abort_flag, limit)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem_base + uint32_t(acc * TILE);
+        const uint32_t idesc = instr_desc(p_mn, q_mn, t.n);
+        for (int kb = 0; kb < t.nkb; ++kb) {
+          // the stage was looked at while the products before were issued
+          if (!__all_sync(0xFFFFFFFFu, ready) && !wait_warp<false>(&full_bar[stage], phase, abort_flag, limit)) {
+            ok = false;
+            break;
+          }
+          const uint32_t empty = smem_u32(&empty_bar[stage]);
+          const uint64_t at = uint64_t(stage * (STAGE_BYTES >> 4));
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          ready = limit != 0 && mbar_test_wait(smem_u32(&full_bar[stage]), phase);
+          mma_block(elected, d, p_desc + at, q_desc + at, dp, dq, idesc, kb != 0 ? 1u : 0u);
+          issued = true;
+          commit_both(elected, empty);
+        }
+        if (!ok) break;
+        commit_both(elected, smem_u32(&tfull_bar[acc]));
+        ++local;
+      }
+      if (!ok && issued) {  // wait for everything in flight before TMEM is freed
+        if (elected) umma_commit_pair(smem_u32(drain_bar), 1);
+        __syncwarp();
+        mbar_drain(smem_u32(drain_bar), 0u, 1000000000ull);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int quad = warp & 3;         // TMEM lanes 32 quad ..
+    const int part = (warp - 2) >> 2;  // which of the quadrant's two warps
+    const uint32_t tempty[2] = {mapa_shared(smem_u32(&tempty_bar[0]), 0),
+                                mapa_shared(smem_u32(&tempty_bar[1]), 0)};
+    // rows that hold no tokens are cleared while the first tiles are multiplied
+    if (FORM != TN && p.splits == 1) {
+      const int64_t turn = int64_t(blockIdx.x) * EPI_WARPS + warp - 2, turns = int64_t(gridDim.x) * EPI_WARPS;
+      clear_unused<EPI>(p, 0, lo[0], turn, turns, lane);
+      if (p.counts)
+        for (int g = 0; g < p.groups; ++g) clear_unused<EPI>(p, lo[g] + cnt[g], lo[g + 1], turn, turns, lane);
+      clear_unused<EPI>(p, lo[p.groups], p.rows, turn, turns, lane);
+    }
+    int local = 0;
+    Tile t;
+    for (int tile = pair; tile < total; tile += npairs) {
+      decode<FORM, STEP_I, BK>(p, lo, cnt, begin, tile, t);
+      const int i = EPI == GATE ? t.i0 + HALF / 2 * int(cta) + 16 * quad + (lane & 15)
+                                : t.i0 + HALF * int(cta) + 32 * quad + lane;
+      if (t.nkb == 0) {  // TN: an empty run's matrix is zero
+        const int es = p.dtype == MAO_F32 ? 4 : 2, i0 = t.i0 + HALF * int(cta);
+        clear_rows(static_cast<uint8_t*>(p.d) + int64_t(i0) * es, p.ld * es, int64_t(min(HALF, p.I - i0)) * es,
+                   t.row0 + t.j0 + warp - 2, t.row0 + t.j_end, EPI_WARPS, lane);
+        continue;
+      }
+      const int acc = local & 1;
+      const int n = t.j_end - t.j0;
+      // this warp's 128 columns in eight steps, every second sixteen
+      auto column = [&](int s) { return 32 * s + 16 * part; };
+      Saved sa, sb;
+      if (EPI == GATE_BACK && p.splits == 1) load_saved(p, t, t.j0 + column(0), i, lane, sa);
+      // every lane waits; the warp goes on only if all of them saw the accumulator
+      if (!wait_warp<false>(&tfull_bar[acc], uint32_t(local >> 1) & 1u, abort_flag, limit)) break;
+      tc_fence_after();
+      const uint32_t trow = tmem_base + (uint32_t(32 * quad) << 16) + uint32_t(acc * TILE);
+      auto out = [&](int s, const float(&v)[16], const Saved& z) {
+        const int c = column(s);
+        if (c >= n) return;
+        if (EPI == GATE && p.splits > 1) store16_gate_parts(p, t, t.j0 + c, i, v, lane);
+        else if (EPI == GATE) gate16(p, t, t.j0 + c, i, v, lane);
+        else if (EPI == GATE_BACK && p.splits == 1) gate_back16(p, t, t.j0 + c, i, v, z, lane);
+        else store16(p, t, t.j0 + c, i, v, lane);
+      };
+      // a step's columns are loaded while the step before is stored
+      float va[16], vb[16];
+      if (column(0) < n) tmem_ld16(trow + uint32_t(column(0)), va);
+#pragma unroll 1
+      for (int s = 0; s < 8; s += 2) {
+        if (EPI == GATE_BACK && p.splits == 1 && column(s + 1) < n) load_saved(p, t, t.j0 + column(s + 1), i, lane, sb);
+        tmem_wait(va);
+        if (column(s + 1) < n) tmem_ld16(trow + uint32_t(column(s + 1)), vb);
+        out(s, va, sa);
+        if (EPI == GATE_BACK && p.splits == 1 && s < 6 && column(s + 2) < n)
+          load_saved(p, t, t.j0 + column(s + 2), i, lane, sa);
+        tmem_wait(vb);
+        if (s == 6) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty[acc]);
+        } else if (column(s + 2) < n) {
+          tmem_ld16(trow + uint32_t(column(s + 2)), va);
+        }
+        out(s + 1, vb, sb);
+      }
+      ++local;
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {  // an aborted CTA also gives the peer's copies in flight 50 us to land
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 50000ull) {
+    }
+  }
+  cluster_sync_all();  // no CTA leaves while its peer may still touch its shared memory
+  tc_fence_after();
+  if (warp == 1) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ sums of the splits' parts
+
+// The splits' parts added up in their order, then what the product's epilogue does; four columns
+// per thread. q.d, q.dtype, q.ld, q.paired are those of the whole product.
+struct SumParams {
+  FfnParams q;
+  const float* parts;
+  int64_t prows, pld;  // rows and row stride of one part
+};
+
+__device__ __forceinline__ void add_parts(const SumParams& p, int64_t j, int64_t i, float (&v)[4]) {
+  v[0] = v[1] = v[2] = v[3] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < p.q.splits; ++s) {
+    const float4 x = *reinterpret_cast<const float4*>(p.parts + (s * p.prows + j) * p.pld + i);
+    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+  }
+}
+
+// Four bf16 columns, those below n, of a row that starts at d.
+__device__ __forceinline__ void store4(__nv_bfloat16* d, int64_t i, int n, bool words, const float (&v)[4]) {
+  if (words && i + 4 <= n) {
+    *reinterpret_cast<uint32_t*>(d + i) = pack(v[0], v[1]);
+    *reinterpret_cast<uint32_t*>(d + i + 2) = pack(v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (i + c < n) d[i + c] = __float2bfloat16_rn(v[c]);
+  }
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(256) ffn_sum_kernel(const __grid_constant__ SumParams p) {
+  wait_for_previous();
+  const FfnParams& q = p.q;
+  const int64_t quads = (q.I + 3) / 4, all = p.prows * quads;
+  for (int64_t x = int64_t(blockIdx.x) * 256 + threadIdx.x; x < all; x += int64_t(gridDim.x) * 256) {
+    const int64_t j = x / quads, i = 4 * (x - j * quads);
+    float v[4];
+    add_parts(p, j, i, v);
+    if (EPI == PLAIN) {
+      if (q.dtype == MAO_F32) {
+        float* d = static_cast<float*>(q.d) + j * q.ld + i;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (i + c < q.I) d[c] = v[c];
+      } else {
+        store4(static_cast<__nv_bfloat16*>(q.d) + j * q.ld, i, q.I, q.paired, v);
+      }
+    } else if (EPI == GATE) {
+      float u[4], h[4];
+      add_parts(p, j, q.part_half + i, u);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) h[c] = activate(v[c], q.act) * u[c];
+      store4(static_cast<__nv_bfloat16*>(q.d) + j * q.ld, i, q.I, q.paired, h);
+      if (q.z) {
+        store4(q.z + j * q.ldz, i, q.I, q.paired_z, v);
+        store4(q.z + j * q.ldz + q.I, i, q.I, q.paired_z, u);
+      }
+    } else {
+      float h[4], dg[4], du[4];
+      const __nv_bfloat16* z = q.z + j * q.ldz + i;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool in = i + c < q.I;
+        const float g = in ? __bfloat162float(z[c]) : 0.0f, u = in ? __bfloat162float(z[q.I + c]) : 0.0f;
+        float a, slope;
+        activate(g, q.act, a, slope);
+        h[c] = a * u;
+        dg[c] = v[c] * u * slope;
+        du[c] = v[c] * a;
+      }
+      store4(static_cast<__nv_bfloat16*>(q.d) + j * q.ld, i, q.I, true, h);
+      store4(q.dz + j * q.lddz, i, q.I, true, dg);
+      store4(q.dz + j * q.lddz + q.dz_half, i, q.I, true, du);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ copies of unaligned operands
+
+struct CopyParams {
+  const uint16_t* src;
+  uint16_t* dst;
+  int64_t rows, cols, ld, dld;
+};
+__global__ void __launch_bounds__(256) copy_kernel(const CopyParams p) {
+  wait_for_previous();
+  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x)
+    for (int64_t c = threadIdx.x; c < p.cols; c += 256) p.dst[r * p.dld + c] = p.src[r * p.ld + c];
+}
+
+// ------------------------------------------------------------------ host
+
+std::atomic<bool> g_launched{false};
+
+// A bf16 operand as the kernels see it: rows that start at multiples of 16 bytes.
+struct Operand {
+  const void* data;
+  int64_t rows, cols, ld;
+  bool copied;
+  size_t bytes() const { return copied ? size_t(round_up(rows * ld * 2, 256)) : 0; }
+};
+Operand operand(const mao_mat& m) {
+  const bool whole = reinterpret_cast<uintptr_t>(m.data) % 16 == 0 && (m.ld % 8 == 0 || m.rows <= 1);
+  // a single row's stride may be anything, but a map wants a multiple of 16 bytes
+  if (whole) return Operand{m.data, m.rows, m.cols, round_up(m.rows <= 1 ? m.cols : m.ld, 8), false};
+  return Operand{nullptr, m.rows, m.cols, round_up(m.cols, 8), true};
+}
+mao_status place(Operand& o, const mao_mat& m, uint8_t*& at, cudaStream_t stream) {
+  if (!o.copied || o.rows == 0) return MAO_OK;
+  o.data = at;
+  at += o.bytes();
+  const CopyParams c{static_cast<const uint16_t*>(m.data), static_cast<uint16_t*>(const_cast<void*>(o.data)),
+                     m.rows, m.cols, m.ld, o.ld};
+  return launch_dependent(copy_kernel, unsigned(m.rows < 16 * num_sms() ? m.rows : 16 * num_sms()), 256, 0,
+                          stream, c);
+}
+
+// The products of a call, with the sizes that their splits and parts go by.
+struct Plan {
+  int form, epi;
+  int64_t I, J, depth;  // of D: columns (GATE: channels), rows (one matrix's for TN); depth per half
+  int32_t halves;
+  Split split{1, 0};
+  int64_t prows = 0, pld = 0;
+
+  int64_t tiles_i() const { return ceil_div(I, epi == GATE ? HALF : TILE); }
+  int64_t matrices() const { return form == TN ? halves : 1; }
+  void choose(bool grouped) {
+    if (grouped) return;
+    const int64_t nkb = ceil_div(depth, BK) * (form == NN ? halves : 1);
+    const int64_t outputs = J * matrices() * I * (epi == GATE ? 2 : 1);
+    // a block takes a pair 0.27 us (the tensor cores) or, where few rows leave the operands' bytes
+    // to bound it, 0.37 us
+    split = choose_split(tiles_i() * ceil_div(J, TILE) * matrices(), nkb, J < 128 ? 0.37 : 0.27, outputs, 4);
+    prows = J * matrices();
+    pld = round_up(I, 4) * (epi == GATE ? 2 : 1);
+  }
+  size_t bytes() const { return split.splits > 1 ? size_t(round_up(split.splits * prows * pld * 4, 256)) : 0; }
+};
+
+using Kernel = void (*)(const FfnParams);
+using SumKernel = void (*)(const SumParams);
+
+mao_status run(const Plan& plan, FfnParams& p, const Runs& runs, int64_t rows, void* parts, cudaStream_t stream) {
+  p.offsets = runs.offsets;
+  p.counts = runs.offsets ? runs.counts : nullptr;
+  p.groups = runs.groups;
+  p.rows = int32_t(rows);
+  p.I = int32_t(plan.I);
+  p.J = int32_t(plan.J);
+  p.depth = int32_t(plan.depth);
+  p.halves = plan.halves;
+  p.tiles_i = int32_t(plan.tiles_i());
+  p.timeout_ns = wait_limit_ns();
+  p.splits = plan.split.splits;
+  p.split_kb = plan.split.kb;
+  p.part_half = int32_t(round_up(plan.I, 4));
+  const bool tn = plan.form == TN;
+  const int64_t tiles = (tn ? ceil_div(plan.J, TILE) * runs.groups * plan.halves
+                            : ceil_div(rows, TILE) + (runs.offsets ? runs.groups : 0)) * plan.tiles_i();
+  if (tiles * p.splits > 0x7FFF0000) return MAO_ERR_UNSUPPORTED;
+  const int k = plan.epi == GATE ? 0 : plan.epi == GATE_BACK ? 1 : plan.form == NT ? 2 : plan.form == NN ? 3 : 4;
+  static const Kernel kernels[5] = {ffn_kernel<NT, GATE>, ffn_kernel<NN, GATE_BACK>, ffn_kernel<NT, PLAIN>,
+                                    ffn_kernel<NN, PLAIN>, ffn_kernel<TN, PLAIN>};
+  static const SumKernel sums[3] = {ffn_sum_kernel<PLAIN>, ffn_sum_kernel<GATE>, ffn_sum_kernel<GATE_BACK>};
+  static std::atomic<bool> ready[64];
+  mao_status st = once_per_device(ready, [&] {
+    cudaError_t err = cudaSuccess;
+    for (int f = 0; f < 5 && err == cudaSuccess; ++f)
+      err = cudaFuncSetAttribute(kernels[f], cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM));
+    return err;
+  });
+  if (st != MAO_OK) return st;
+  g_launched.store(true, std::memory_order_release);
+  const int64_t units = tiles * p.splits;
+  const unsigned grid = unsigned(2 * (units < num_sms() / 2 ? units : num_sms() / 2));
+  if (p.splits == 1) return launch_dependent(kernels[k], grid, THREADS, SMEM, stream, p);
+  SumParams sum;
+  sum.q = p;
+  sum.parts = static_cast<const float*>(parts);
+  sum.prows = plan.prows;
+  sum.pld = plan.pld;
+  p.d = parts;
+  p.ld = plan.pld;
+  p.dtype = MAO_F32;
+  st = launch_dependent(kernels[k], grid, THREADS, SMEM, stream, p);
+  if (st != MAO_OK) return st;
+  const int64_t blocks = ceil_div(plan.prows * ceil_div(plan.I, 4), 256);
+  return launch_dependent(sums[plan.epi], unsigned(blocks < 8 * num_sms() ? blocks : 8 * num_sms()), 256, 0,
+                          stream, sum);
+}
+
+bool words(const void* data, int64_t ld, int64_t cols) {
+  return reinterpret_cast<uintptr_t>(data) % 4 == 0 && ld % 2 == 0 && cols % 2 == 0;
+}
+void set_out(FfnParams& p, const mao_mat& D) {
+  p.d = D.data;
+  p.ld = D.ld;
+  p.dtype = D.dtype;
+  p.paired = words(D.data, D.ld, D.cols);
+}
+
+struct Sizes {
+  int64_t R, K, N, C;
+};
+
+// Buffers of the workspace, in order: the intermediate rows, copies of operands, parts.
+struct Forward {
+  Sizes s;
+  int64_t ldh;
+  Operand x, up, down;
+  Plan gate, out;
+  Forward(const mao_mat& X, const mao_mat& Up, const mao_mat& Down, int32_t groups, bool grouped)
+      : s{X.rows, X.cols, Down.cols, Down.rows / groups}, ldh(round_up(s.N, 8)), x(operand(X)), up(operand(Up)),
+        down(operand(Down)), gate{NT, GATE, s.N, s.R, s.K, 1}, out{NT, PLAIN, s.C, s.R, s.N, 1} {
+    gate.choose(grouped);
+    out.choose(grouped);
+  }
+  size_t h_bytes() const { return size_t(round_up(s.R * ldh * 2, 256)); }
+  size_t parts_bytes() const { return gate.bytes() > out.bytes() ? gate.bytes() : out.bytes(); }
+  size_t bytes() const { return h_bytes() + x.bytes() + up.bytes() + down.bytes() + parts_bytes(); }
+};
+
+struct Backward {
+  Sizes s;
+  int64_t ldh;
+  Operand dy, x, up, down;
+  Plan back, dx, dup, ddown;
+  Backward(const mao_mat& dY, const mao_mat& X, const mao_mat& Up, const mao_mat& Down, int32_t groups, bool grouped)
+      : s{X.rows, X.cols, Down.cols, Down.rows / groups}, ldh(round_up(s.N, 8)), dy(operand(dY)), x(operand(X)),
+        up(operand(Up)), down(operand(Down)), back{NN, GATE_BACK, s.N, s.R, s.C, 1}, dx{NN, PLAIN, s.K, s.R, s.N, 2},
+        dup{TN, PLAIN, s.K, s.N, s.R, 2}, ddown{TN, PLAIN, s.N, s.C, s.R, 1} {
+    for (Plan* q : {&back, &dx, &dup, &ddown}) q->choose(grouped);
+  }
+  size_t h_bytes() const { return size_t(round_up(s.R * ldh * 2, 256)); }
+  size_t dz_bytes() const { return size_t(round_up(s.R * ldh * 4, 256)); }
+  size_t parts_bytes() const {
+    size_t most = 0;
+    for (const Plan* q : {&back, &dx, &dup, &ddown}) most = q->bytes() > most ? q->bytes() : most;
+    return most;
+  }
+  size_t bytes() const {
+    return h_bytes() + dz_bytes() + dy.bytes() + x.bytes() + up.bytes() + down.bytes() + parts_bytes();
+  }
+};
+
+// Maps of a K-major Q: boxes of 16, 32, 64, 128 rows.
+mao_status encode_q(FfnParams& p, const void* base, int64_t cols, int64_t rows, int64_t halves, int64_t ld,
+                    int64_t half_stride) {
+  mao_status st = MAO_OK;
+  for (int b = 0; b < Q_BOXES && st == MAO_OK; ++b)
+    st = tc_encode_bf16_map(&p.map_q[b], base, cols, rows, halves, 1, ld, half_stride, rows * ld, 16 << b);
+  return st;
+}
+
+}  // namespace
+
+size_t gated_ffn_workspace_size(const mao_mat& X, const mao_mat& up, const mao_mat& down, int32_t groups,
+                                bool grouped) {
+  return X.rows == 0 ? 0 : Forward(X, up, down, groups, grouped).bytes();
+}
+
+mao_status gated_ffn_launch(const mao_mat& X, const mao_mat& up, const mao_mat& down, int32_t act,
+                            const Runs& runs, const mao_mat* Z, const mao_mat& Y, void* workspace,
+                            cudaStream_t stream) {
+  if (X.rows == 0) return MAO_OK;
+  Forward f(X, up, down, runs.groups, runs.offsets != nullptr);
+  const Sizes& s = f.s;
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  uint8_t* h = at;
+  at += f.h_bytes();
+  mao_status st = place(f.x, X, at, stream);
+  if (st == MAO_OK) st = place(f.up, up, at, stream);
+  if (st == MAO_OK) st = place(f.down, down, at, stream);
+  if (st != MAO_OK) return st;
+
+  FfnParams p = {};
+  st = tc_encode_bf16_map(&p.map_p, f.up.data, s.K, s.N, 2, runs.groups, f.up.ld, s.N * f.up.ld, 2 * s.N * f.up.ld, 16);
+  if (st == MAO_OK) st = encode_q(p, f.x.data, s.K, s.R, 1, f.x.ld, s.R * f.x.ld);
+  if (st != MAO_OK) return st;
+  p.d = h;
+  p.ld = f.ldh;
+  p.dtype = MAO_BF16;
+  p.paired = s.N % 2 == 0;
+  p.act = act;
+  if (Z) {
+    p.z = static_cast<__nv_bfloat16*>(Z->data);
+    p.ldz = Z->ld;
+    p.paired_z = words(Z->data, Z->ld, s.N);
+  }
+  st = run(f.gate, p, runs, s.R, at, stream);
+  if (st != MAO_OK) return st;
+
+  FfnParams q = {};
+  st = tc_encode_bf16_map(&q.map_p, f.down.data, s.N, s.C, 1, runs.groups, f.down.ld, s.C * f.down.ld, s.C * f.down.ld, HALF);
+  if (st == MAO_OK) st = encode_q(q, h, s.N, s.R, 1, f.ldh, s.R * f.ldh);
+  if (st != MAO_OK) return st;
+  set_out(q, Y);
+  return run(f.out, q, runs, s.R, at, stream);
+}
+
+size_t gated_ffn_backward_workspace_size(const mao_mat& dY, const mao_mat& X, const mao_mat& up,
+                                         const mao_mat& down, int32_t groups, bool grouped) {
+  return X.rows == 0 ? 0 : Backward(dY, X, up, down, groups, grouped).bytes();
+}
+
+mao_status gated_ffn_backward_launch(const mao_mat& dY, const mao_mat& X, const mao_mat& up,
+                                     const mao_mat& down, const mao_mat& Z, int32_t act, const Runs& runs,
+                                     const mao_mat* dX, const mao_mat* dup, const mao_mat* ddown,
+                                     void* workspace, cudaStream_t stream) {
+  if (X.rows == 0) {  // sums over nothing
+    for (const mao_mat* D : {dup, ddown}) {
+      if (!D) continue;
+      const int es = elem_size(D->dtype);
+      const cudaError_t err = cudaMemset2DAsync(D->data, size_t(D->ld) * es, 0, size_t(D->cols) * es,
+                                                size_t(D->rows), stream);
+      if (err != cudaSuccess) return MAO_ERR_CUDA;
+    }
+    return MAO_OK;
+  }
+  Backward b(dY, X, up, down, runs.groups, runs.offsets != nullptr);
+  const Sizes& s = b.s;
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  uint8_t* h = at;
+  at += b.h_bytes();
+  uint8_t* dz = at;
+  at += b.dz_bytes();
+  mao_status st = place(b.dy, dY, at, stream);
+  if (st == MAO_OK) st = place(b.x, X, at, stream);
+  if (st == MAO_OK) st = place(b.up, up, at, stream);
+  if (st == MAO_OK) st = place(b.down, down, at, stream);
+  if (st != MAO_OK) return st;
+
+  {
+    FfnParams p = {};
+    st = tc_encode_bf16_map(&p.map_p, b.down.data, s.N, s.C, 1, runs.groups, b.down.ld, s.C * b.down.ld, s.C * b.down.ld, BK);
+    if (st == MAO_OK) st = encode_q(p, b.dy.data, s.C, s.R, 1, b.dy.ld, s.R * b.dy.ld);
+    if (st != MAO_OK) return st;
+    p.d = h;
+    p.ld = b.ldh;
+    p.dtype = MAO_BF16;
+    p.paired = 1;
+    p.z = static_cast<__nv_bfloat16*>(Z.data);
+    p.ldz = Z.ld;
+    p.paired_z = words(Z.data, Z.ld, s.N);
+    p.dz = reinterpret_cast<__nv_bfloat16*>(dz);
+    p.lddz = 2 * b.ldh;
+    p.dz_half = int32_t(b.ldh);
+    p.act = act;
+    st = run(b.back, p, runs, s.R, at, stream);
+    if (st != MAO_OK) return st;
+  }
+  if (dX) {
+    FfnParams p = {};
+    st = tc_encode_bf16_map(&p.map_p, b.up.data, s.K, s.N, 2, runs.groups, b.up.ld, s.N * b.up.ld, 2 * s.N * b.up.ld, BK);
+    if (st == MAO_OK) st = encode_q(p, dz, s.N, s.R, 2, 2 * b.ldh, b.ldh);
+    if (st != MAO_OK) return st;
+    set_out(p, *dX);
+    st = run(b.dx, p, runs, s.R, at, stream);
+    if (st != MAO_OK) return st;
+  }
+  if (dup) {
+    FfnParams p = {};
+    st = tc_encode_bf16_map(&p.map_p, b.x.data, s.K, s.R, 1, 1, b.x.ld, s.R * b.x.ld, s.R * b.x.ld, BK);
+    if (st == MAO_OK)
+      st = tc_encode_bf16_map(&p.map_q[Q_BOXES - 1], dz, s.N, s.R, 2, 1, 2 * b.ldh, b.ldh, s.R * 2 * b.ldh, BK);
+    if (st != MAO_OK) return st;
+    set_out(p, *dup);
+    st = run(b.dup, p, runs, s.R, at, stream);
+    if (st != MAO_OK) return st;
+  }
+  if (ddown) {
+    FfnParams p = {};
+    st = tc_encode_bf16_map(&p.map_p, h, s.N, s.R, 1, 1, b.ldh, s.R * b.ldh, s.R * b.ldh, BK);
+    if (st == MAO_OK)
+      st = tc_encode_bf16_map(&p.map_q[Q_BOXES - 1], b.dy.data, s.C, s.R, 1, 1, b.dy.ld, s.R * b.dy.ld, s.R * b.dy.ld, BK);
+    if (st != MAO_OK) return st;
+    set_out(p, *ddown);
+    st = run(b.ddown, p, runs, s.R, at, stream);
+  }
+  return st;
+}
+
+mao_status ffn_read_and_clear_error(cudaStream_t stream) {
+  // a copy and a synchronisation that programs without these products do not wait for
+  return g_launched.load(std::memory_order_acquire) ? read_and_clear_error(stream) : MAO_OK;
+}
+
+}  // namespace mao

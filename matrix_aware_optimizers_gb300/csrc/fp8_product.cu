@@ -120,12 +120,6 @@ struct Tile {
   int64_t row0; // row of the output that j counts from
 };
 
-__device__ __forceinline__ uint64_t desc_of(uint32_t saddr, uint32_t lbo, uint32_t sbo,
-                                            uint32_t swizzle) {
-  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(lbo >> 4) << 16) |
-         (uint64_t(sbo >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(swizzle) << 61);
-}
-
 // Instruction descriptor of kind::mxf8f6f4: e4m3 operands, scales of type ue8m0, M = 256.
 __device__ __forceinline__ uint32_t instr_desc(int p_mn, int q_mn, int n, int byte) {
   return (uint32_t(byte) << 4) | (uint32_t(p_mn) << 15) | (uint32_t(q_mn) << 16) |
@@ -152,17 +146,6 @@ __device__ __forceinline__ void mma_block(uint32_t elected, uint32_t d, uint64_t
   }
 }
 
-// One lane of a converged warp.
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t e;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xFFFFFFFF;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(e));
-  return e;
-}
-
 // 128 scale words (512 bytes of each CTA's shared memory) into four TMEM columns of both, for
 // the three sets of words of a slot.
 __device__ __forceinline__ void copy_scales(uint32_t elected, uint32_t taddr, uint64_t desc) {
@@ -176,17 +159,6 @@ __device__ __forceinline__ void copy_scales(uint32_t elected, uint32_t taddr, ui
         : "memory");
 }
 
-// umma_commit_pair to both CTAs by the elected lane of a converged warp.
-__device__ __forceinline__ void commit_both(uint32_t elected, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "setp.ne.b32 e, %2, 0;\n\t"
-      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;\n\t}\n" ::"r"(bar),
-      "h"(uint16_t(3)), "r"(elected)
-      : "memory");
-}
-
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map,
                                                  uint32_t bar_cluster, int32_t x, int32_t y,
                                                  int32_t z) {
@@ -195,40 +167,6 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
       : "memory");
-}
-
-// Arrive that makes this thread's earlier writes visible to the leader CTA's waiter.
-__device__ __forceinline__ void mbar_arrive_release(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
-
-// Sixteen columns of this thread's TMEM lane: the load is issued, and its registers may be
-// used after tmem_wait.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
-        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
-        "=f"(v[14]), "=f"(v[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait(float (&v)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
-                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
-                 "+f"(v[14]), "+f"(v[15])
-               :
-               : "memory");
-}
-
-// A wait of a whole warp: true once every lane has seen the phase complete.
-template <bool CLUSTER>
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          uint64_t limit) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait_fast<CLUSTER>(smem_u32(bar), parity, abort_flag, limit));
 }
 
 // ------------------------------------------------------------------ tiles

@@ -171,6 +171,11 @@ mao_status tc_encode_map(CUtensorMap* map, const void* base, int64_t rows, int64
 // row; what lies outside reads as zeros): boxes of 128 columns x box_rows rows.
 mao_status tc_encode_code_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
                               int64_t ld, int64_t count, int32_t box_rows);
+// Operand map of bf16 entries [count][halves][rows][cols], strides in elements (multiples of 8;
+// what lies outside reads as zeros): boxes of 64 columns x box_rows rows.
+mao_status tc_encode_bf16_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
+                              int64_t halves, int64_t count, int64_t ld, int64_t half_stride,
+                              int64_t stride, int32_t box_rows);
 // Bulk-store map of a workspace output buffer [count][rows][ld] bf16 (64 x 32 blocks).
 // fp32 [count][rows][ld] for bulk stores of 32 x 32 blocks (128-byte swizzle)
 mao_status tc_encode_store_map_f32(CUtensorMap* map, const void* base, int64_t rows, int64_t ld,

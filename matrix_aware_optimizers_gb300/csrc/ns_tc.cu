@@ -1153,6 +1153,22 @@ mao_status tc_encode_code_map(CUtensorMap* map, const void* base, int64_t cols, 
   return r == CUDA_SUCCESS ? MAO_OK : MAO_ERR_UNSUPPORTED;
 }
 
+mao_status tc_encode_bf16_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
+                              int64_t halves, int64_t count, int64_t ld, int64_t half_stride,
+                              int64_t stride, int32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return MAO_ERR_UNSUPPORTED;
+  const cuuint64_t dims[4] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(halves), cuuint64_t(count)};
+  const cuuint64_t strides[3] = {cuuint64_t(ld) * 2, cuuint64_t(half_stride) * 2, cuuint64_t(stride) * 2};
+  const cuuint32_t box[4] = {CHUNK, cuuint32_t(box_rows), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MAO_OK : MAO_ERR_UNSUPPORTED;
+}
+
 mao_status tc_encode_store_map_f32(CUtensorMap* map, const void* base, int64_t rows, int64_t ld,
                                    int64_t count) {
   auto fn = encode_fn();

@@ -217,6 +217,69 @@ static __device__ __forceinline__ void umma_commit_pair(uint32_t bar, uint16_t m
       : "memory");
 }
 
+// Shared-memory matrix descriptor (version field 0b001 at bit 46); swizzle 2: rows of 128 bytes.
+static __device__ __forceinline__ uint64_t desc_of(uint32_t saddr, uint32_t lbo, uint32_t sbo,
+                                            uint32_t swizzle) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(lbo >> 4) << 16) |
+         (uint64_t(sbo >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(swizzle) << 61);
+}
+
+// One lane of a converged warp.
+static __device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(e));
+  return e;
+}
+
+// umma_commit_pair to both CTAs by the elected lane of a converged warp.
+static __device__ __forceinline__ void commit_both(uint32_t elected, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %2, 0;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n\t}\n" ::"r"(bar),
+      "h"(uint16_t(3)), "r"(elected)
+      : "memory");
+}
+
+// Arrive that makes this thread's earlier writes visible to the leader CTA's waiter.
+static __device__ __forceinline__ void mbar_arrive_release(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
+// Sixteen columns of this thread's TMEM lane: the load is issued, and its registers may be
+// used after tmem_wait.
+static __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+static __device__ __forceinline__ void tmem_wait(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+                 "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+
+// A wait of a whole warp: true once every lane has seen the phase complete.
+template <bool CLUSTER>
+static __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          uint64_t limit) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_fast<CLUSTER>(smem_u32(bar), parity, abort_flag, limit));
+}
+
 // Reads and clears this translation unit's error word (after a stream sync).
 static inline mao_status read_and_clear_error(cudaStream_t stream) {
   unsigned int v = 0;
