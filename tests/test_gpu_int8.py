@@ -196,13 +196,22 @@ def test_product_few_rows(cuda, T):
 
 
 def test_product_exact_at_the_limit(cuda):
-    """Every partial sum of 1040 products of the largest codes is exact."""
+    """Sums of the largest codes are exact up to 2^24: 1040 products of 127 * 127 (codes of
+    int8_quantize), 1024 of 128 * 128 (any codes)."""
+    one = lambda n: torch.ones(n, device=cuda)  # noqa: E731
+    for K, x, z in ((1040, 127, 127), (1040, -127, 127), (1024, -128, -128), (1024, 127, -128)):
+        a = torch.full((40, K), x, dtype=torch.int8, device=cuda)
+        b = torch.full((300, K), z, dtype=torch.int8, device=cuda)
+        b[:, 1] += 1 if z < 0 else -1
+        y = mao.int8_product(a, one(40), b, one(300), out_dtype=F32)
+        assert (y == float(x * (z * K + (1 if z < 0 else -1)))).all()
+    # 1039 of 127 * -128 and one of 127 * 127: 16,873,855 is odd and above 2^24, where fp32 holds even
+    # numbers only; the two sums at the end that pass 2^24 may each be cut by less than 2
     a = torch.full((40, 1040), 127, dtype=torch.int8, device=cuda)
     b = torch.full((300, 1040), -128, dtype=torch.int8, device=cuda)
     b[:, 1] = 127
-    one = lambda n: torch.ones(n, device=cuda)  # noqa: E731
     y = mao.int8_product(a, one(40), b, one(300), out_dtype=F32)
-    assert (y == 127.0 * (-128.0 * 1039 + 127)).all()
+    assert ((y.double() - 127.0 * (-128.0 * 1039 + 127)).abs() <= 4).all()
 
 
 @pytest.mark.parametrize("use_counts", [False, True])
@@ -266,10 +275,13 @@ def test_served_block(cuda):
     y = mao.int8_product(h8, hs, d8, ds, out_dtype=F32)
     mao.sync_status()
     val = lambda c, s: np64(c) * np64(s)[:, None]  # noqa: E731
-    zz = val(x8, xs) @ val(u8, us).T
+    # sums of codes first: whole numbers, exact in 64 bits too (sums of scaled values are not: where
+    # the codes' sum is 0 they leave some 2^-53)
+    prod = lambda a, sa, b, sb: (np64(a) @ np64(b).T) * np64(sa)[:, None] * np64(sb)  # noqa: E731
+    zz = prod(x8, xs, u8, us)
     np.testing.assert_allclose(np64(z), zz, rtol=2.0 ** -21, atol=0)  # three roundings
     h = of.act(np64(z)[:, :N], "silu") * np64(z)[:, N:]
     # a code is off by half a step and what the gate's arithmetic adds
     step = np.abs(h).max(1, keepdims=True) / 127.0
     assert (np.abs(val(h8, hs) - h) <= 0.5001 * step + 1e-30).all()
-    np.testing.assert_allclose(np64(y), val(h8, hs) @ val(d8, ds).T, rtol=2.0 ** -21, atol=0)
+    np.testing.assert_allclose(np64(y), prod(h8, hs, d8, ds), rtol=2.0 ** -21, atol=0)
