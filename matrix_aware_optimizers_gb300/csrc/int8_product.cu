@@ -44,7 +44,8 @@ constexpr int RAW_STAGES = 4;
 constexpr int HK = 64;                    // depth of a converted stage
 constexpr int Q_BYTES = HALF * HK * 2;
 constexpr int STAGES = 4;
-constexpr int EPI_WARPS = 8, CONV_WARPS = 4;  // converting warps of each operand
+constexpr int EPI_WARPS = 8;
+constexpr int CONV_WARPS = 8;             // of each operand, four for each half of a raw stage
 constexpr int THREADS = 64 + 32 * (EPI_WARPS + 2 * CONV_WARPS);
 constexpr int TMEM_COLS = 512;
 constexpr int ACC1 = 128;                 // first column of the second accumulator
@@ -168,6 +169,14 @@ __device__ __forceinline__ void store16(const Int8Params& p, const Tile& t, int 
     if (in && j + c < t.j_end) d[c * p.ld] = __float2bfloat16_rn(v[c]);
 }
 
+// Arrive on a barrier of the leader CTA, ordered after this warp's writes to its own shared memory
+// at cluster scope. Only shared memory is fenced: a plain cluster-scope release also waits
+// for global memory, some 2000 cycles (8192 x 14336 x 4096: 1093 us instead of 647).
+__device__ __forceinline__ void mbar_arrive_shared_release(uint32_t cluster_addr) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     int8_kernel(const __grid_constant__ Int8Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -203,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&rempty_bar[s]), 2 * CONV_WARPS);
     }
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 4 * CONV_WARPS);
+      mbar_init(smem_u32(&full_bar[s]), 2 * CONV_WARPS);
       mbar_init(smem_u32(&empty_bar[s]), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -368,79 +377,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const int c0 = ((acc ^ half) ? 0 : ACC1) + 16 * part;
-        float v[4][16];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (c0 + 32 * q < n) tmem_ld16(trow + uint32_t(c0 + 32 * q), v[q]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_wait(v[q]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(half ? tempty[acc] : tshared[acc]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (c0 + 32 * q < n) store16(p, t, t.j0 + c0 + 32 * q, i, sb, v[q], lane);
+#pragma unroll 1
+        for (int q = 0; q < 4; q += 2) {
+          const int c = c0 + 32 * q;
+          float va[16], vb[16];
+          if (c < n) tmem_ld16(trow + uint32_t(c), va);
+          if (c + 32 < n) tmem_ld16(trow + uint32_t(c + 32), vb);
+          tmem_wait(va);
+          tmem_wait(vb);
+          if (q == 2) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(half ? tempty[acc] : tshared[acc]);
+          }
+          if (c < n) store16(p, t, t.j0 + c, i, sb, va, lane);
+          if (c + 32 < n) store16(p, t, t.j0 + c + 32, i, sb, vb, lane);
+        }
       }
       ++local;
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ conversion (both CTAs)
+    // A warp takes the same half of every raw stage (every second converted one), so that its
+    // loads, its arithmetic and the hand-over have the time of two stages' products.
     const bool of_b = warp < 2 + EPI_WARPS + CONV_WARPS;
+    const int h = ((warp - 2 - EPI_WARPS) >> 2) & 1;
     // B's rows by TMEM's lanes: a warp reaches the quadrant of its number
-    const int r = (of_b ? 32 * (warp & 3) : 32 * (warp - 2 - EPI_WARPS - CONV_WARPS)) + lane;
+    const int r = 32 * (of_b ? warp & 3 : (warp - 2 - EPI_WARPS) & 3) + lane;
     const uint32_t full0 = mapa_shared(smem_u32(full_bar), 0);
     const uint32_t tcol = tmem_base + (uint32_t(32 * (warp & 3)) << 16) + B_COL;
-    int rstage = 0, stage = 0;
+    int rstage = 0, stage = h;
     uint32_t rphase = 0, phase = 0;
     bool ok = true;
     Tile t;
     for (int tile = pair; ok && tile < total; tile += npairs) {
       decode<NT, TILE, BK>(p, lo, cnt, begin, tile, t);
       const bool mine = of_b || r < (t.n >> 1);
-      for (int kb = 0; ok && kb < t.nkb; ++kb) {
+      for (int kb = 0; kb < t.nkb; ++kb) {
         if (!wait_warp<false>(&rfull_bar[rstage], rphase, abort_flag, limit)) {
           ok = false;
           break;
         }
-        const uint8_t* from = raw + rstage * RAW_BYTES + (of_b ? 0 : RAW_OP);
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
-          if (mine) load_row(from, r, h, w);
-          if (h) {  // the raw stage has been read
-            __syncwarp();
-            if (lane == 0)
-              asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&rempty_bar[rstage])) : "memory");
-          }
-          if (!wait_warp<false>(&empty_bar[stage], phase ^ 1u, abort_flag, limit)) {
-            ok = false;
-            break;
-          }
-          if (of_b) {
-            tc_fence_after();
-            tmem_st32(tcol + uint32_t(stage * B_COLS), w);
-            tc_fence_before();
-          } else {
-            if (mine) {
-              uint8_t* to = qst + stage * Q_BYTES + r * (HK * 2);
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                *reinterpret_cast<uint4*>(to + 16 * (q ^ (r & 7))) =
-                    make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-            }
-            fence_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_release(full0 + 8 * stage);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
+        uint32_t w[32];
+        if (mine) load_row(raw + rstage * RAW_BYTES + (of_b ? 0 : RAW_OP), r, h, w);
+        __syncwarp();
+        if (lane == 0)  // this half of the raw stage has been read
+          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&rempty_bar[rstage])) : "memory");
         if (++rstage == RAW_STAGES) {
           rstage = 0;
           rphase ^= 1u;
+        }
+        if (!wait_warp<false>(&empty_bar[stage], phase ^ 1u, abort_flag, limit)) {
+          ok = false;
+          break;
+        }
+        if (of_b) {
+          tc_fence_after();
+          tmem_st32(tcol + uint32_t(stage * B_COLS), w);
+          tc_fence_before();
+        } else {
+          if (mine) {
+            uint8_t* to = qst + stage * Q_BYTES + r * (HK * 2);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<uint4*>(to + 16 * (q ^ (r & 7))) =
+                  make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          }
+          fence_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_shared_release(full0 + 8 * stage);
+        stage += 2;
+        if (stage >= STAGES) {
+          stage -= STAGES;
+          phase ^= 1u;
         }
       }
     }
