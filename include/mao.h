@@ -684,8 +684,8 @@ mao_status int8_quantize(const mao_mat* X, int32_t batch, int64_t batch_stride, 
  *   A      R x K, count 1. B: N x K, count = groups.
  * Products of codes are exact and summed in fp32: the sum is exact while its parts stay below
  * 2^24 (for any codes while K <= 1024). It is scaled by sA, then by sB, and rounded to D's type.
- *   workspace  NULL, or a device buffer, 256-byte aligned, of int8_product_workspace_bytes(A, B,
- *              offsets != NULL) bytes (0: none is used): few rows are then split over the sum.
+ *   workspace >= int8_product_workspace_bytes(A, B, offsets != NULL) bytes, 256-byte aligned (A in
+ *   fp16; parts of few rows' sums, which are split). Clobbered.
  *   Limits: groups <= 1024, R <= 2^31 - 1024, N, K <= 2^20.
  */
 mao_status int8_product(const mao_int8* A, const mao_int8* B, const mao_mat* D,

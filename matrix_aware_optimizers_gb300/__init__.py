@@ -1068,8 +1068,7 @@ def int8_product(A, a_scales, B, b_scales, offsets=None, counts=None, out=None,
 
     A: int8 [T, K]. B: int8 [N, K], or [groups, N, K] with offsets and counts, which are as in
     gated_ffn. out: a float32 or bfloat16 tensor to fill, by default a new one of out_dtype. ws:
-    a uint8 buffer for few rows, whose sums are split (int8_product_workspace_bytes); allocated
-    when needed.
+    a uint8 buffer of int8_product_workspace_bytes; allocated by default.
     """
     off, cnt, groups = _runs(offsets, counts)
     if A.dim() != 2:
@@ -1083,14 +1082,19 @@ def int8_product(A, a_scales, B, b_scales, offsets=None, counts=None, out=None,
     else:
         d = _desc(out)
     ra, rb = ctypes.byref(a), ctypes.byref(b)
-    need = 0 if ws is not None or off is not None else \
-        lib().int8_product_workspace_bytes(ra, rb, False)
+    need = 0 if ws is not None else lib().int8_product_workspace_bytes(ra, rb, off is not None)
     ws, wptr, wbytes = _ws(ws, need, A, stream)
     st = lib().int8_product(ra, rb, ctypes.byref(d), off, cnt, groups, wptr, wbytes,
                             _raw_stream(stream, A, a_scales, B, b_scales, offsets, counts, out, ws))
     if st:
         _abi.check("int8_product", st)
     return out
+
+
+def int8_product_workspace_bytes(A, a_scales, B, b_scales, grouped=False):
+    """Workspace of int8_product for these tensors (grouped: with offsets)."""
+    a, b = _int8(A, a_scales, "A"), _int8(B, b_scales, "B")
+    return int(lib().int8_product_workspace_bytes(ctypes.byref(a), ctypes.byref(b), bool(grouped)))
 
 
 def set_wait_limit(ns):

@@ -32,7 +32,7 @@ mao_status int8_quantize_launch(const mao_mat* X, int32_t batch, int64_t batch_s
                                 bool gated, const mao_int8& out, cudaStream_t stream);
 size_t int8_product_workspace_size(const mao_int8& A, const mao_int8& B, bool grouped);
 mao_status int8_product_launch(const mao_int8& A, const mao_int8& B, const mao_mat& D, const Runs& runs,
-                               void* workspace, size_t workspace_bytes, cudaStream_t stream);
+                               void* workspace, cudaStream_t stream);
 // Read and clear the device error words of the products (after a stream sync).
 mao_status ffn_read_and_clear_error(cudaStream_t stream);
 mao_status int8_read_and_clear_error(cudaStream_t stream);

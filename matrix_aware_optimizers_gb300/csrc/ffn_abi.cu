@@ -150,9 +150,10 @@ mao_status int8_product(const mao_int8* A, const mao_int8* B, const mao_mat* D,
   if (A->count != 1 || B->count != groups || B->rows < 1 || B->cols != A->cols || !shaped(D, A->rows, B->rows))
     return MAO_ERR_INVALID_ARG;
   if (B->rows > kMaxCols) return MAO_ERR_UNSUPPORTED;
-  if (!aligned(workspace, 256)) return MAO_ERR_MISALIGNED;
   if (device_cc() / 10 != 10) return MAO_ERR_UNSUPPORTED;
-  return int8_product_launch(*A, *B, *D, Runs{offsets, counts, groups}, workspace, workspace_bytes,
+  st = check_ws(workspace, workspace_bytes, int8_product_workspace_size(*A, *B, offsets != nullptr));
+  if (st != MAO_OK) return st;
+  return int8_product_launch(*A, *B, *D, Runs{offsets, counts, groups}, workspace,
                              static_cast<cudaStream_t>(stream));
 }
 

@@ -232,16 +232,15 @@ __device__ __forceinline__ void gate_back16(const FfnParams& p, const Tile& t, i
   }
 }
 
-// Rows from j0 below j1 of the outputs hold no tokens.
+// Rows j0, j0 + step, ... below j1 of the outputs hold no tokens.
 template <int EPI>
-__device__ __forceinline__ void clear_unused(const FfnParams& p, int64_t j0, int64_t j1, int64_t turn,
-                                             int64_t turns, int lane) {
+__device__ __forceinline__ void clear_unused(const FfnParams& p, int64_t j0, int64_t j1, int64_t step, int lane) {
   const int es = p.dtype == MAO_F32 ? 4 : 2;
-  if (EPI != GATE) clear_rows(p.d, p.ld * es, int64_t(p.I) * es, j0 + turn, j1, turns, lane);
-  if (EPI == GATE && p.z) clear_rows(p.z, p.ldz * 2, int64_t(p.I) * 4, j0 + turn, j1, turns, lane);
+  if (EPI != GATE) clear_rows(p.d, p.ld * es, int64_t(p.I) * es, j0, j1, step, lane);
+  if (EPI == GATE && p.z) clear_rows(p.z, p.ldz * 2, int64_t(p.I) * 4, j0, j1, step, lane);
   if (EPI == GATE_BACK) {
-    clear_rows(p.dz, p.lddz * 2, int64_t(p.I) * 2, j0 + turn, j1, turns, lane);
-    clear_rows(p.dz + p.dz_half, p.lddz * 2, int64_t(p.I) * 2, j0 + turn, j1, turns, lane);
+    clear_rows(p.dz, p.lddz * 2, int64_t(p.I) * 2, j0, j1, step, lane);
+    clear_rows(p.dz + p.dz_half, p.lddz * 2, int64_t(p.I) * 2, j0, j1, step, lane);
   }
 }
 
@@ -441,11 +440,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                 mapa_shared(smem_u32(&tempty_bar[1]), 0)};
     // rows that hold no tokens are cleared while the first tiles are multiplied
     if (FORM != TN && p.splits == 1) {
-      const int64_t turn = int64_t(blockIdx.x) * EPI_WARPS + warp - 2, turns = int64_t(gridDim.x) * EPI_WARPS;
-      clear_unused<EPI>(p, 0, lo[0], turn, turns, lane);
-      if (p.counts)
-        for (int g = 0; g < p.groups; ++g) clear_unused<EPI>(p, lo[g] + cnt[g], lo[g + 1], turn, turns, lane);
-      clear_unused<EPI>(p, lo[p.groups], p.rows, turn, turns, lane);
+      for_unused_rows(p, lo, cnt, int(blockIdx.x) * EPI_WARPS + warp - 2, int(gridDim.x) * EPI_WARPS,
+                      [&](int64_t j0, int64_t j1, int64_t step) { clear_unused<EPI>(p, j0, j1, step, lane); });
     }
     int local = 0;
     Tile t;

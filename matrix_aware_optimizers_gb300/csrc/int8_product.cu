@@ -2,22 +2,24 @@
 // cores, over runs of rows: D[j][i] = sA[j] sB[i] sum_k A[j][k] B[i][k].
 //
 // This part's tensor cores multiply 16-bit floating point many times faster than 8-bit integers,
-// and fp16 holds every code, so the codes become fp16 on their way from shared memory to the
-// tensor core: memory and L2 move 8 bits per entry, the products are exact in the fp32 sums (below
-// 2^24). One operand is converted into TMEM, from where tcgen05.mma reads it as its M side, the
-// other into shared memory. (Through shared memory both, a 64-deep block of 256 x 256 moves
-// 96 KB of an SM's shared memory in the 512 cycles of its products; so it moves 64 KB.)
+// and fp16 holds every code, so codes become fp16 on their way to the tensor core; the products
+// are exact in the fp32 sums (below 2^24). The weights B stay 8 bits wide in memory and L2: they
+// are converted between shared memory and TMEM, from where tcgen05.mma reads them as its M
+// side. The rows A are converted once, by a kernel of their own, into the workspace: done in this
+// kernel as well, tile by tile, their way back through shared memory (a fence of the asynchronous
+// proxy per stage, some 400 cycles of a stage's 512) held up the tensor cores.
 //
 // Tiles of 256 x 256 by a pair of CTAs (cta_group::2, M = 256 channels i, N up to 256 rows j).
-// Roles per CTA (576 threads):
-//   warp 0        TMA producer: raw codes, 128-deep stages, ring of four
+// Roles per CTA (608 threads):
+//   warp 0        TMA producer of A: 64-deep stages of fp16, ring of six
 //   warp 1        TMEM allocation; in the even CTA it issues the products (converged, one lane)
 //   warps 2..9    epilogue: two warps per 32-lane quadrant of TMEM; lane = i
-//   warps 10..13  B's rows, one per lane: 64 codes to 32 words of TMEM
-//   warps 14..17  A's rows: 64 codes to 128 bytes of shared memory, swizzled
+//   warps 10..17  B's rows, one per lane: 64 codes to 32 words of TMEM; four warps for each half of
+//                 a stage of codes
+//   warp 18       TMA producer of B: 128-deep stages of codes, ring of six
 // TMEM: two accumulators of 256 columns that share 128 (columns 0..255 and 128..383), and four
-// stages of B (32 columns each from 384 on). The shared columns are read into registers first,
-// so the next tile's products wait for that only.
+// stages of B (32 columns each from 384 on). The shared columns are read first, so the next
+// tile's products wait for that only.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -37,24 +39,24 @@ namespace {
 using namespace ptx;
 using namespace ffn;
 
-constexpr int BK = 128;                   // depth of a raw stage: rows of 128 bytes
-constexpr int RAW_OP = HALF * BK;
-constexpr int RAW_BYTES = 2 * RAW_OP;
-constexpr int RAW_STAGES = 4;
-constexpr int HK = 64;                    // depth of a converted stage
-constexpr int Q_BYTES = HALF * HK * 2;
-constexpr int STAGES = 4;
+constexpr int BK = 128;                   // depth of a stage of codes: rows of 128 bytes
+constexpr int RAW_BYTES = HALF * BK;
+constexpr int RAW_STAGES = 6;
+constexpr int HK = 64;                    // depth of a stage of fp16: rows of 128 bytes
+constexpr int A_BYTES = HALF * HK * 2;
+constexpr int A_STAGES = 6;
+constexpr int B_STAGES = 4;
 constexpr int EPI_WARPS = 8;
-constexpr int CONV_WARPS = 8;             // of each operand, four for each half of a raw stage
-constexpr int THREADS = 64 + 32 * (EPI_WARPS + 2 * CONV_WARPS);
+constexpr int CONV_WARPS = 8;
+constexpr int THREADS = 32 * (3 + EPI_WARPS + CONV_WARPS);
 constexpr int TMEM_COLS = 512;
 constexpr int ACC1 = 128;                 // first column of the second accumulator
 constexpr int B_COL = ACC1 + TILE;        // B's stages
 constexpr int B_COLS = HK / 2;
 constexpr int Q_BOXES = 4;                // heights of boxes of A: 16 << b rows
-constexpr size_t SMEM = 1024 + size_t(RAW_STAGES) * RAW_BYTES + size_t(STAGES) * Q_BYTES + TABLE_BYTES + 512;
+constexpr size_t SMEM = 1024 + size_t(RAW_STAGES) * RAW_BYTES + size_t(A_STAGES) * A_BYTES + TABLE_BYTES + 512;
 static_assert(SMEM <= 232448, "shared memory budget of one CTA");
-static_assert(B_COL + STAGES * B_COLS <= TMEM_COLS, "TMEM budget");
+static_assert(B_COL + B_STAGES * B_COLS <= TMEM_COLS, "TMEM budget");
 
 struct Int8Params : TileParams {
   CUtensorMap map_p;
@@ -169,29 +171,23 @@ __device__ __forceinline__ void store16(const Int8Params& p, const Tile& t, int 
     if (in && j + c < t.j_end) d[c * p.ld] = __float2bfloat16_rn(v[c]);
 }
 
-// Arrive on a barrier of the leader CTA, ordered after this warp's writes to its own shared memory
-// at cluster scope. Only shared memory is fenced: a plain cluster-scope release also waits
-// for global memory, some 2000 cycles (8192 x 14336 x 4096: 1093 us instead of 647).
-__device__ __forceinline__ void mbar_arrive_shared_release(uint32_t cluster_addr) {
-  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     int8_kernel(const __grid_constant__ Int8Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* raw = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* qst = raw + RAW_STAGES * RAW_BYTES;
-  int* lo = reinterpret_cast<int*>(qst + STAGES * Q_BYTES);
+  uint8_t* ast = raw + RAW_STAGES * RAW_BYTES;
+  int* lo = reinterpret_cast<int*>(ast + A_STAGES * A_BYTES);
   int* cnt = lo + MAX_GROUPS + 2;
   int* begin = cnt + MAX_GROUPS + 2;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(qst + STAGES * Q_BYTES + TABLE_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ast + A_STAGES * A_BYTES + TABLE_BYTES);
   uint64_t* rfull_bar = bars;                       // [RAW_STAGES]
   uint64_t* rempty_bar = rfull_bar + RAW_STAGES;    // [RAW_STAGES]
-  uint64_t* full_bar = rempty_bar + RAW_STAGES;     // [STAGES]  (used in the even CTA)
-  uint64_t* empty_bar = full_bar + STAGES;          // [STAGES]
-  uint64_t* tfull_bar = empty_bar + STAGES;         // [2]
+  uint64_t* afull_bar = rempty_bar + RAW_STAGES;    // [A_STAGES]  (used in the even CTA)
+  uint64_t* aempty_bar = afull_bar + A_STAGES;      // [A_STAGES]
+  uint64_t* bfull_bar = aempty_bar + A_STAGES;      // [B_STAGES]  (used in the even CTA)
+  uint64_t* bempty_bar = bfull_bar + B_STAGES;      // [B_STAGES]
+  uint64_t* tfull_bar = bempty_bar + B_STAGES;      // [2]
   uint64_t* tempty_bar = tfull_bar + 2;             // [2]  all columns read    (even CTA)
   uint64_t* tshared_bar = tempty_bar + 2;           // [2]  shared columns read (even CTA)
   uint64_t* drain_bar = tshared_bar + 2;
@@ -209,11 +205,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < RAW_STAGES; ++s) {
       mbar_init(smem_u32(&rfull_bar[s]), 1);
-      mbar_init(smem_u32(&rempty_bar[s]), 2 * CONV_WARPS);
+      mbar_init(smem_u32(&rempty_bar[s]), CONV_WARPS);
     }
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 2 * CONV_WARPS);
-      mbar_init(smem_u32(&empty_bar[s]), 1);
+    for (int s = 0; s < A_STAGES; ++s) {
+      mbar_init(smem_u32(&afull_bar[s]), 1);
+      mbar_init(smem_u32(&aempty_bar[s]), 1);
+    }
+    for (int s = 0; s < B_STAGES; ++s) {
+      mbar_init(smem_u32(&bfull_bar[s]), CONV_WARPS);  // four warps of each CTA
+      mbar_init(smem_u32(&bempty_bar[s]), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&tfull_bar[a]), 1);
@@ -238,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   // launched as a programmatic dependent: the set-up so far may overlap the previous kernel
   wait_for_previous();
-  make_table<THREADS>(p, lo, cnt, begin, reinterpret_cast<int*>(bars + 32));
+  make_table<THREADS>(p, lo, cnt, begin, reinterpret_cast<int*>(bars + 48));
   tc_fence_before();
   __syncthreads();
   const int total = begin[p.groups] * p.tiles_i * p.splits;
@@ -247,9 +247,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t tmem_base = *tmem_holder;
 
   if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer (both CTAs)
-    // B's rows i0 + 128 cta .. and A's rows j0 + n/2 cta .. (each CTA supplies half of the
-    // tile's n values of j). The whole warp runs the loop, converged; one lane issues.
+    // ------------------------------------------------------------ TMA producer of A (both CTAs)
+    // A's rows j0 + n/2 cta .. (each CTA supplies half of the tile's n values of j). The whole
+    // warp runs the loop, converged; one lane issues.
+    const uint32_t elected = elect_one();
+    const uint32_t full0 = mapa_shared(smem_u32(afull_bar), 0);
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_phase = 0;
+    bool ok = true;
+    Tile t;
+    for (int tile = pair; ok && tile < total; tile += npairs) {
+      decode<NT, TILE, BK>(p, lo, cnt, begin, tile, t);
+      const int j = t.j0 + (t.n >> 1) * int(cta);
+      const int q_rows = t.n >> 1;  // a multiple of 16
+      for (int kb = 0; kb < 2 * t.nkb; ++kb) {
+        if (!wait_warp<false>(&aempty_bar[stage], phase ^ 1u, abort_flag, limit)) {
+          ok = false;
+          break;
+        }
+        const uint32_t fb = full0 + 8 * stage, dst = smem_u32(ast) + stage * A_BYTES;
+        const int k = (2 * t.kb0 + kb) * HK;
+        if (elected) {
+          if (leader) mbar_expect_tx(smem_u32(&afull_bar[stage]), uint32_t(t.n) * HK * 2);
+          for (int box = Q_BOXES - 1, at = 0; box >= 0; --box)
+            if (q_rows & (16 << box)) {
+              tma_load_4d_pair(dst + at * (HK * 2), &p.map_q[box], fb, k, j + at, 0, 0);
+              at += 16 << box;
+            }
+        }
+        armed |= 1u << stage;
+        armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == A_STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // after an abort, the loads already issued land before the CTA leaves
+    if (*abort_flag && leader && lane == 0) {
+      for (int s = 0; s < A_STAGES; ++s)
+        if ((armed >> s) & 1u) mbar_drain(smem_u32(&afull_bar[s]), (armed_phase >> s) & 1u, 20000000ull);
+    }
+    __syncwarp();
+  } else if (warp == 2 + EPI_WARPS + CONV_WARPS) {
+    // ------------------------------------------------------------ TMA producer of B (both CTAs)
     const uint32_t elected = elect_one();
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_phase = 0;
@@ -257,23 +298,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     Tile t;
     for (int tile = pair; ok && tile < total; tile += npairs) {
       decode<NT, TILE, BK>(p, lo, cnt, begin, tile, t);
-      const int i = t.i0 + HALF * int(cta), j = t.j0 + (t.n >> 1) * int(cta);
-      const int q_rows = t.n >> 1;  // a multiple of 16
+      const int i = t.i0 + HALF * int(cta);
       for (int kb = 0; kb < t.nkb; ++kb) {
         if (!wait_warp<false>(&rempty_bar[stage], phase ^ 1u, abort_flag, limit)) {
           ok = false;
           break;
         }
-        const uint32_t fb = smem_u32(&rfull_bar[stage]), dst = smem_u32(raw) + stage * RAW_BYTES;
-        const int k = (t.kb0 + kb) * BK;
         if (elected) {
-          mbar_expect_tx(fb, RAW_OP + uint32_t(q_rows) * BK);
-          tma_load_3d(dst, &p.map_p, fb, k, i, t.g);
-          for (int box = Q_BOXES - 1, at = 0; box >= 0; --box)
-            if (q_rows & (16 << box)) {
-              tma_load_3d(dst + RAW_OP + at * BK, &p.map_q[box], fb, k, j + at, 0);
-              at += 16 << box;
-            }
+          const uint32_t fb = smem_u32(&rfull_bar[stage]);
+          mbar_expect_tx(fb, RAW_BYTES);
+          tma_load_3d(smem_u32(raw) + stage * RAW_BYTES, &p.map_p, fb, (t.kb0 + kb) * BK, i, t.g);
         }
         armed |= 1u << stage;
         armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
@@ -283,7 +317,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
     }
-    // after an abort, the loads already issued land before the CTA leaves
     if (*abort_flag && lane == 0) {
       for (int s = 0; s < RAW_STAGES; ++s)
         if ((armed >> s) & 1u) mbar_drain(smem_u32(&rfull_bar[s]), (armed_phase >> s) & 1u, 20000000ull);
@@ -293,9 +326,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (leader) {
       const uint32_t elected = elect_one();
-      const uint64_t a_desc = desc_of(smem_u32(qst), 16, 1024, 2);
-      int stage = 0, local = 0, before_n = 0;
-      uint32_t phase = 0;
+      const uint64_t a_desc = desc_of(smem_u32(ast), 16, 1024, 2);
+      int sa = 0, sb = 0, local = 0, before_n = 0;
+      uint32_t pa = 0, pb = 0;
       bool ok = true, issued = false;
       Tile t;
       for (int tile = pair; ok && tile < total; tile += npairs) {
@@ -315,18 +348,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint32_t d = tmem_base + uint32_t(acc * ACC1);
         const uint32_t idesc = instr_desc(t.n);
         for (int kb = 0; kb < 2 * t.nkb; ++kb) {
-          if (!wait_warp<true>(&full_bar[stage], phase, abort_flag, limit)) {
+          if (!wait_warp<false>(&afull_bar[sa], pa, abort_flag, limit) ||
+              !wait_warp<true>(&bfull_bar[sb], pb, abort_flag, limit)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          mma_stage(elected, d, tmem_base + uint32_t(B_COL + stage * B_COLS),
-                    a_desc + uint64_t(stage * (Q_BYTES >> 4)), idesc, kb != 0 ? 1u : 0u);
+          mma_stage(elected, d, tmem_base + uint32_t(B_COL + sb * B_COLS),
+                    a_desc + uint64_t(sa * (A_BYTES >> 4)), idesc, kb != 0 ? 1u : 0u);
           issued = true;
-          commit_both(elected, smem_u32(&empty_bar[stage]));
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+          commit_both(elected, smem_u32(&bempty_bar[sb]));
+          commit_both(elected, smem_u32(&aempty_bar[sa]));
+          if (++sa == A_STAGES) {
+            sa = 0;
+            pa ^= 1u;
+          }
+          if (++sb == B_STAGES) {
+            sb = 0;
+            pb ^= 1u;
           }
         }
         if (!ok) break;
@@ -351,14 +390,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // rows that hold no tokens are cleared while the first tiles are multiplied
     if (p.splits == 1) {
       const int es = p.dtype == MAO_F32 ? 4 : 2;
-      const int64_t turn = int64_t(blockIdx.x) * EPI_WARPS + warp - 2, turns = int64_t(gridDim.x) * EPI_WARPS;
-      auto clear = [&](int64_t j0, int64_t j1) {
-        clear_rows(p.d, p.ld * es, int64_t(p.I) * es, j0 + turn, j1, turns, lane);
-      };
-      clear(0, lo[0]);
-      if (p.counts)
-        for (int g = 0; g < p.groups; ++g) clear(lo[g] + cnt[g], lo[g + 1]);
-      clear(lo[p.groups], p.rows);
+      for_unused_rows(p, lo, cnt, int(blockIdx.x) * EPI_WARPS + warp - 2, int(gridDim.x) * EPI_WARPS,
+                      [&](int64_t j0, int64_t j1, int64_t step) {
+                        clear_rows(p.d, p.ld * es, int64_t(p.I) * es, j0, j1, step, lane);
+                      });
     }
     int local = 0;
     Tile t;
@@ -399,13 +434,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ conversion (both CTAs)
-    // A warp takes the same half of every raw stage (every second converted one), so that its
-    // loads, its arithmetic and the hand-over have the time of two stages' products.
-    const bool of_b = warp < 2 + EPI_WARPS + CONV_WARPS;
-    const int h = ((warp - 2 - EPI_WARPS) >> 2) & 1;
-    // B's rows by TMEM's lanes: a warp reaches the quadrant of its number
-    const int r = 32 * (of_b ? warp & 3 : (warp - 2 - EPI_WARPS) & 3) + lane;
-    const uint32_t full0 = mapa_shared(smem_u32(full_bar), 0);
+    // A warp takes the same half of every stage of codes (every second stage of fp16), so that
+    // its loads, its arithmetic and the hand-over have the time of two stages' products.
+    const int h = (warp - 2 - EPI_WARPS) >> 2;
+    const int r = 32 * (warp & 3) + lane;  // TMEM's lane: a warp reaches the quadrant of its number
+    const uint32_t full0 = mapa_shared(smem_u32(bfull_bar), 0);
     const uint32_t tcol = tmem_base + (uint32_t(32 * (warp & 3)) << 16) + B_COL;
     int rstage = 0, stage = h;
     uint32_t rphase = 0, phase = 0;
@@ -413,44 +446,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     Tile t;
     for (int tile = pair; ok && tile < total; tile += npairs) {
       decode<NT, TILE, BK>(p, lo, cnt, begin, tile, t);
-      const bool mine = of_b || r < (t.n >> 1);
       for (int kb = 0; kb < t.nkb; ++kb) {
         if (!wait_warp<false>(&rfull_bar[rstage], rphase, abort_flag, limit)) {
           ok = false;
           break;
         }
         uint32_t w[32];
-        if (mine) load_row(raw + rstage * RAW_BYTES + (of_b ? 0 : RAW_OP), r, h, w);
+        load_row(raw + rstage * RAW_BYTES, r, h, w);
         __syncwarp();
-        if (lane == 0)  // this half of the raw stage has been read
+        if (lane == 0)  // this half of the stage has been read
           asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&rempty_bar[rstage])) : "memory");
         if (++rstage == RAW_STAGES) {
           rstage = 0;
           rphase ^= 1u;
         }
-        if (!wait_warp<false>(&empty_bar[stage], phase ^ 1u, abort_flag, limit)) {
+        if (!wait_warp<false>(&bempty_bar[stage], phase ^ 1u, abort_flag, limit)) {
           ok = false;
           break;
         }
-        if (of_b) {
-          tc_fence_after();
-          tmem_st32(tcol + uint32_t(stage * B_COLS), w);
-          tc_fence_before();
-        } else {
-          if (mine) {
-            uint8_t* to = qst + stage * Q_BYTES + r * (HK * 2);
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<uint4*>(to + 16 * (q ^ (r & 7))) =
-                  make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-          }
-          fence_async_smem();
-        }
+        tc_fence_after();
+        tmem_st32(tcol + uint32_t(stage * B_COLS), w);
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_shared_release(full0 + 8 * stage);
+        // the words are in this SM's TMEM (tcgen05.wait::st, the fence before): as for an
+        // accumulator's reads, the arrive only carries that
+        if (lane == 0) mbar_arrive_cluster(full0 + 8 * stage);
         stage += 2;
-        if (stage >= STAGES) {
-          stage -= STAGES;
+        if (stage >= B_STAGES) {
+          stage -= B_STAGES;
           phase ^= 1u;
         }
       }
@@ -501,29 +524,63 @@ __global__ void __launch_bounds__(256) int8_sum_kernel(const SumParams p) {
   }
 }
 
+// A's codes in fp16, sixteen per thread and step.
+struct HalfParams {
+  const int8_t* src;
+  uint16_t* dst;
+  int64_t rows, ld, dld;
+  int32_t cols, groups16;
+};
+__global__ void __launch_bounds__(256) to_half_kernel(const HalfParams p) {
+  wait_for_previous();
+  const int64_t all = p.rows * p.groups16;
+  for (int64_t x = int64_t(blockIdx.x) * 256 + threadIdx.x; x < all; x += int64_t(gridDim.x) * 256) {
+    const int64_t r = x / p.groups16;
+    const int c = 16 * int(x - r * p.groups16);
+    const int8_t* s = p.src + r * p.ld + c;
+    uint16_t* d = p.dst + r * p.dld + c;
+    if (c + 16 <= p.cols) {
+      const uint4 v = *reinterpret_cast<const uint4*>(s);
+      uint4 a, b;
+      to_half(v.x, a.x, a.y);
+      to_half(v.y, a.z, a.w);
+      to_half(v.z, b.x, b.y);
+      to_half(v.w, b.z, b.w);
+      reinterpret_cast<uint4*>(d)[0] = a;
+      reinterpret_cast<uint4*>(d)[1] = b;
+    } else {
+      for (int q = 0; c + q < p.cols; ++q) d[q] = __half_as_ushort(__int2half_rn(s[q]));
+    }
+  }
+}
+
 std::atomic<bool> g_launched{false};
 
-// A block of 128 takes a pair 0.6 us, or 0.4 us (the operands' bytes) with few rows.
+// A block of 128 takes a pair 0.55 us, or 0.4 us (the operands' bytes) with few rows.
 Split split_of(const mao_int8& A, const mao_int8& B) {
   return choose_split(ceil_div(A.rows, TILE) * ceil_div(B.rows, TILE), ceil_div(A.cols, BK),
-                      A.rows < 128 ? 0.4 : 0.6, A.rows * B.rows, 2);
+                      A.rows < 128 ? 0.4 : 0.55, A.rows * B.rows, 2);
 }
+
+// The workspace: A in fp16, then the parts of split sums.
+int64_t half_ld(const mao_int8& A) { return round_up(A.cols, 8); }
+size_t half_bytes(const mao_int8& A) { return size_t(round_up(A.rows * half_ld(A) * 2, 256)); }
 
 }  // namespace
 
 size_t int8_product_workspace_size(const mao_int8& A, const mao_int8& B, bool grouped) {
-  if (A.rows == 0 || grouped) return 0;
-  const Split s = split_of(A, B);
-  return s.splits > 1 ? size_t(round_up(int64_t(s.splits) * A.rows * round_up(B.rows, 4) * 4, 256)) : 0;
+  if (A.rows == 0) return 0;
+  const Split s = grouped ? Split{1, 0} : split_of(A, B);
+  return half_bytes(A) + (s.splits > 1 ? size_t(round_up(int64_t(s.splits) * A.rows * round_up(B.rows, 4) * 4, 256)) : 0);
 }
-
 mao_status int8_product_launch(const mao_int8& A, const mao_int8& B, const mao_mat& D, const Runs& runs,
-                               void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+                               void* workspace, cudaStream_t stream) {
   if (A.rows == 0) return MAO_OK;
   Int8Params p = {};
   mao_status st = tc_encode_code_map(&p.map_p, B.codes, B.cols, B.rows, B.ld, B.count, HALF);
   for (int b = 0; b < Q_BOXES && st == MAO_OK; ++b)
-    st = tc_encode_code_map(&p.map_q[b], A.codes, A.cols, A.rows, A.ld, 1, 16 << b);
+    st = tc_encode_bf16_map(&p.map_q[b], workspace, A.cols, A.rows, 1, 1, half_ld(A), A.rows * half_ld(A),
+                            A.rows * half_ld(A), 16 << b);
   if (st != MAO_OK) return st;
   p.offsets = runs.offsets;
   p.counts = runs.offsets ? runs.counts : nullptr;
@@ -541,9 +598,8 @@ mao_status int8_product_launch(const mao_int8& A, const mao_int8& B, const mao_m
   p.ld = D.ld;
   p.dtype = D.dtype;
   p.paired = D.dtype == MAO_BF16 && D.cols % 2 == 0 && reinterpret_cast<uintptr_t>(D.data) % 4 == 0 && D.ld % 2 == 0;
-  Split split{1, 0};
-  const size_t need = int8_product_workspace_size(A, B, runs.offsets != nullptr);
-  if (need && workspace && workspace_bytes >= need) split = split_of(A, B);
+  const Split split = runs.offsets ? Split{1, 0} : split_of(A, B);
+  void* parts = static_cast<uint8_t*>(workspace) + half_bytes(A);
   p.splits = split.splits;
   p.split_kb = split.kb;
   const int64_t tiles = (ceil_div(A.rows, TILE) + (runs.offsets ? runs.groups : 0)) * p.tiles_i;
@@ -555,17 +611,24 @@ mao_status int8_product_launch(const mao_int8& A, const mao_int8& B, const mao_m
   if (st != MAO_OK) return st;
   if (p.splits > 1) {
     p.sa = p.sb = nullptr;
-    p.d = workspace;
+    p.d = parts;
     p.ld = round_up(D.cols, 4);
     p.dtype = MAO_F32;
   }
+  const HalfParams half{A.codes, static_cast<uint16_t*>(workspace), A.rows, A.ld, half_ld(A), int32_t(A.cols),
+                        int32_t(ceil_div(A.cols, 16))};
+  const int64_t vectors = ceil_div(A.rows * half.groups16, 256);
+  using Half = void (*)(const HalfParams);
+  st = launch_dependent(static_cast<Half>(to_half_kernel), unsigned(vectors < 16 * num_sms() ? vectors : 16 * num_sms()),
+                        256, 0, stream, half);
+  if (st != MAO_OK) return st;
   g_launched.store(true, std::memory_order_release);
   const int64_t units = tiles * p.splits;
   const unsigned grid = unsigned(2 * (units < num_sms() / 2 ? units : num_sms() / 2));
   using Kernel = void (*)(const Int8Params);
   st = launch_dependent(static_cast<Kernel>(int8_kernel), grid, THREADS, SMEM, stream, p);
   if (st != MAO_OK || p.splits == 1) return st;
-  const SumParams sum{static_cast<const float*>(workspace), A.scales, B.scales, D.data, A.rows, D.cols,
+  const SumParams sum{static_cast<const float*>(parts), A.scales, B.scales, D.data, A.rows, D.cols,
                       p.ld, D.ld, p.splits, D.dtype};
   const int64_t blocks = ceil_div(A.rows * (p.ld / 4), 256);
   using Sum = void (*)(const SumParams);
