@@ -11,14 +11,14 @@
 //
 // Tiles of 256 x 256 by a pair of CTAs (cta_group::2, M = 256 channels i, N up to 256 rows j).
 // Roles per CTA (608 threads):
-//   warp 0        TMA producer of A: 64-deep stages of fp16, ring of six
+//   warp 0        TMA producer of A: 128-deep stages of fp16, ring of three
 //   warp 1        TMEM allocation; in the even CTA it issues the products (converged, one lane)
 //   warps 2..9    epilogue: two warps per 32-lane quadrant of TMEM; lane = i
 //   warps 10..17  B's rows, one per lane: 64 codes to 32 words of TMEM; four warps for each half of
-//                 a stage of codes
+//                 a stage
 //   warp 18       TMA producer of B: 128-deep stages of codes, ring of six
-// TMEM: two accumulators of 256 columns that share 128 (columns 0..255 and 128..383), and four
-// stages of B (32 columns each from 384 on). The shared columns are read first, so the next
+// TMEM: two accumulators of 256 columns that share 128 (columns 0..255 and 128..383), and two
+// stages of B (64 columns each from 384 on). The shared columns are read first, so the next
 // tile's products wait for that only.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -39,20 +39,21 @@ namespace {
 using namespace ptx;
 using namespace ffn;
 
-constexpr int BK = 128;                   // depth of a stage of codes: rows of 128 bytes
+constexpr int BK = 128;                   // depth of a stage: rows of 128 bytes of codes
 constexpr int RAW_BYTES = HALF * BK;
 constexpr int RAW_STAGES = 6;
-constexpr int HK = 64;                    // depth of a stage of fp16: rows of 128 bytes
-constexpr int A_BYTES = HALF * HK * 2;
-constexpr int A_STAGES = 6;
-constexpr int B_STAGES = 4;
+constexpr int HK = 64;                    // half of it: rows of 128 bytes of fp16
+constexpr int HALF_BYTES = HALF * HK * 2;
+constexpr int A_BYTES = 2 * HALF_BYTES;
+constexpr int A_STAGES = 3;
+constexpr int B_STAGES = 2;
 constexpr int EPI_WARPS = 8;
 constexpr int CONV_WARPS = 8;
 constexpr int THREADS = 32 * (3 + EPI_WARPS + CONV_WARPS);
 constexpr int TMEM_COLS = 512;
 constexpr int ACC1 = 128;                 // first column of the second accumulator
 constexpr int B_COL = ACC1 + TILE;        // B's stages
-constexpr int B_COLS = HK / 2;
+constexpr int B_COLS = BK / 2;
 constexpr int Q_BOXES = 4;                // heights of boxes of A: 16 << b rows
 constexpr size_t SMEM = 1024 + size_t(RAW_STAGES) * RAW_BYTES + size_t(A_STAGES) * A_BYTES + TABLE_BYTES + 512;
 static_assert(SMEM <= 232448, "shared memory budget of one CTA");
@@ -73,18 +74,19 @@ __device__ __forceinline__ uint32_t instr_desc(int n) {
   return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(TILE >> 4) << 24);
 }
 
-// The four 16-deep products of a converted stage: B from TMEM (8 columns each), A from shared
-// memory (32 bytes along its rows each).
+// The eight 16-deep products of a stage: B from TMEM (8 columns each), A from shared memory (32
+// bytes along its rows each).
 __device__ __forceinline__ void mma_stage(uint32_t elected, uint32_t d, uint32_t b, uint64_t a,
                                           uint32_t idesc, uint32_t accumulate) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < 8; ++k) {
     asm volatile(
         "{\n\t.reg .pred a, e;\n\t"
         "setp.ne.b32 a, %4, 0;\n\t"
         "setp.ne.b32 e, %5, 0;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, a;\n\t}\n" ::"r"(d),
-        "r"(b + 8 * k), "l"(a + uint64_t(2 * k)), "r"(idesc), "r"(k ? 1u : accumulate), "r"(elected)
+        "r"(b + 8 * k), "l"(a + uint64_t(k < 4 ? 2 * k : (HALF_BYTES >> 4) + 2 * (k - 4))), "r"(idesc),
+        "r"(k ? 1u : accumulate), "r"(elected)
         : "memory");
   }
 }
@@ -212,7 +214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&aempty_bar[s]), 1);
     }
     for (int s = 0; s < B_STAGES; ++s) {
-      mbar_init(smem_u32(&bfull_bar[s]), CONV_WARPS);  // four warps of each CTA
+      mbar_init(smem_u32(&bfull_bar[s]), 2 * CONV_WARPS);
       mbar_init(smem_u32(&bempty_bar[s]), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -260,18 +262,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       decode<NT, TILE, BK>(p, lo, cnt, begin, tile, t);
       const int j = t.j0 + (t.n >> 1) * int(cta);
       const int q_rows = t.n >> 1;  // a multiple of 16
-      for (int kb = 0; kb < 2 * t.nkb; ++kb) {
+      for (int kb = 0; kb < t.nkb; ++kb) {
         if (!wait_warp<false>(&aempty_bar[stage], phase ^ 1u, abort_flag, limit)) {
           ok = false;
           break;
         }
         const uint32_t fb = full0 + 8 * stage, dst = smem_u32(ast) + stage * A_BYTES;
-        const int k = (2 * t.kb0 + kb) * HK;
+        const int k = (t.kb0 + kb) * BK;
         if (elected) {
-          if (leader) mbar_expect_tx(smem_u32(&afull_bar[stage]), uint32_t(t.n) * HK * 2);
+          if (leader) mbar_expect_tx(smem_u32(&afull_bar[stage]), uint32_t(t.n) * BK * 2);
           for (int box = Q_BOXES - 1, at = 0; box >= 0; --box)
             if (q_rows & (16 << box)) {
               tma_load_4d_pair(dst + at * (HK * 2), &p.map_q[box], fb, k, j + at, 0, 0);
+              tma_load_4d_pair(dst + HALF_BYTES + at * (HK * 2), &p.map_q[box], fb, k + HK, j + at, 0, 0);
               at += 16 << box;
             }
         }
@@ -329,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const uint64_t a_desc = desc_of(smem_u32(ast), 16, 1024, 2);
       int sa = 0, sb = 0, local = 0, before_n = 0;
       uint32_t pa = 0, pb = 0;
-      bool ok = true, issued = false;
+      bool ok = true, issued = false, ready = false;
       Tile t;
       for (int tile = pair; ok && tile < total; tile += npairs) {
         decode<NT, TILE, BK>(p, lo, cnt, begin, tile, t);
@@ -347,18 +350,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const uint32_t d = tmem_base + uint32_t(acc * ACC1);
         const uint32_t idesc = instr_desc(t.n);
-        for (int kb = 0; kb < 2 * t.nkb; ++kb) {
-          if (!wait_warp<false>(&afull_bar[sa], pa, abort_flag, limit) ||
-              !wait_warp<true>(&bfull_bar[sb], pb, abort_flag, limit)) {
+        for (int kb = 0; kb < t.nkb; ++kb) {
+          // the stage was looked at while the products before were issued
+          if (!__all_sync(0xFFFFFFFFu, ready) &&
+              (!wait_warp<false>(&afull_bar[sa], pa, abort_flag, limit) ||
+               !wait_warp<true>(&bfull_bar[sb], pb, abort_flag, limit))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          mma_stage(elected, d, tmem_base + uint32_t(B_COL + sb * B_COLS),
-                    a_desc + uint64_t(sa * (A_BYTES >> 4)), idesc, kb != 0 ? 1u : 0u);
-          issued = true;
-          commit_both(elected, smem_u32(&bempty_bar[sb]));
-          commit_both(elected, smem_u32(&aempty_bar[sa]));
+          const uint32_t b = tmem_base + uint32_t(B_COL + sb * B_COLS);
+          const uint64_t a = a_desc + uint64_t(sa * (A_BYTES >> 4));
+          const uint32_t aempty = smem_u32(&aempty_bar[sa]), bempty = smem_u32(&bempty_bar[sb]);
           if (++sa == A_STAGES) {
             sa = 0;
             pa ^= 1u;
@@ -367,6 +370,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             sb = 0;
             pb ^= 1u;
           }
+          ready = limit != 0 && mbar_test_wait(smem_u32(&afull_bar[sa]), pa) &&
+                  mbar_test_wait_cluster(smem_u32(&bfull_bar[sb]), pb);
+          mma_stage(elected, d, b, a, idesc, kb != 0 ? 1u : 0u);
+          issued = true;
+          commit_both(elected, bempty);
+          commit_both(elected, aempty);
         }
         if (!ok) break;
         commit_both(elected, smem_u32(&tfull_bar[acc]));
@@ -434,13 +443,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ conversion (both CTAs)
-    // A warp takes the same half of every stage of codes (every second stage of fp16), so that
-    // its loads, its arithmetic and the hand-over have the time of two stages' products.
     const int h = (warp - 2 - EPI_WARPS) >> 2;
     const int r = 32 * (warp & 3) + lane;  // TMEM's lane: a warp reaches the quadrant of its number
     const uint32_t full0 = mapa_shared(smem_u32(bfull_bar), 0);
     const uint32_t tcol = tmem_base + (uint32_t(32 * (warp & 3)) << 16) + B_COL;
-    int rstage = 0, stage = h;
+    int rstage = 0, stage = 0;
     uint32_t rphase = 0, phase = 0;
     bool ok = true;
     Tile t;
@@ -465,15 +472,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           break;
         }
         tc_fence_after();
-        tmem_st32(tcol + uint32_t(stage * B_COLS), w);
+        tmem_st32(tcol + uint32_t(stage * B_COLS + h * (B_COLS / 2)), w);
         tc_fence_before();
         __syncwarp();
         // the words are in this SM's TMEM (tcgen05.wait::st, the fence before): as for an
         // accumulator's reads, the arrive only carries that
         if (lane == 0) mbar_arrive_cluster(full0 + 8 * stage);
-        stage += 2;
-        if (stage >= B_STAGES) {
-          stage -= B_STAGES;
+        if (++stage == B_STAGES) {
+          stage = 0;
           phase ^= 1u;
         }
       }
