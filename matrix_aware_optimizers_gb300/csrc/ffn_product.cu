@@ -61,8 +61,8 @@ struct FfnParams : TileParams {
   __nv_bfloat16* dz;           // GATE_BACK: dG and dU
   int64_t ld, ldz, lddz;
   int32_t dz_half;             // columns from dG to dU
-  int32_t dtype, act;
-  int32_t paired, paired_z;  // entries 2 i, 2 i + 1 of a row are one 4-byte word
+  int32_t dtype;
+  int32_t paired, paired_z;  // entries 2 i, 2 i + 1 of a row are one 4-byte word (D; Z)
   int32_t part_half;           // GATE: columns from G's parts to U's
 };
 
@@ -136,45 +136,43 @@ __device__ __forceinline__ void store16_gate_parts(const FfnParams& p, const Til
 // GATE: lanes 0 .. 15 hold G and lanes 16 .. 31 U of sixteen rows at channel i (the same for l and
 // l + 16). Of each four rows the lower lanes take two and the upper ones two; then the lanes of
 // a pair take one row each.
+template <int ACT>
 __device__ __forceinline__ void gate16(const FfnParams& p, const Tile& t, int j, int i,
                                        const float (&v)[16], int lane) {
-  const int up = lane >> 4, odd = lane & 1;
-  const bool in = i < p.I;
-  __nv_bfloat16* h = static_cast<__nv_bfloat16*>(p.d);
+  const int up = lane >> 4, odd = lane & 1, col = i - odd;
+  const bool in = col < p.I;
+  const int left = t.j_end - j - 2 * up - odd;  // rows from this lane's first on
+  const int64_t row = j + 2 * up + odd;
+  // H's rows are padded to whole words
+  __nv_bfloat16* h = static_cast<__nv_bfloat16*>(p.d) + row * p.ld + col;
+  __nv_bfloat16* z = p.z + row * p.ldz + col;
 #pragma unroll
   for (int c = 0; c < 16; c += 4) {
     const float s0 = up ? v[c] : v[c + 2], s1 = up ? v[c + 1] : v[c + 3];
     const float r0 = __shfl_xor_sync(0xFFFFFFFFu, s0, 16), r1 = __shfl_xor_sync(0xFFFFFFFFu, s1, 16);
     const float g0 = up ? r0 : v[c], g1 = up ? r1 : v[c + 1];
     const float u0 = up ? v[c + 2] : r0, u1 = up ? v[c + 3] : r1;
-    const float h0 = activate(g0, p.act) * u0, h1 = activate(g1, p.act) * u1;
-    const int r = j + c + 2 * up;  // the lane's two rows
-    if (p.paired) {
-      const uint32_t wh = swap_pair(h0, h1, odd);
-      const int64_t row = r + odd;
-      const bool ok = in && row < t.j_end;
-      if (ok) store_word(h + row * p.ld + i - odd, wh);
-    } else {
-      if (in && r < t.j_end) h[int64_t(r) * p.ld + i] = __float2bfloat16_rn(h0);
-      if (in && r + 1 < t.j_end) h[int64_t(r + 1) * p.ld + i] = __float2bfloat16_rn(h1);
-    }
+    const uint32_t wh = swap_pair(activate<ACT>(g0) * u0, activate<ACT>(g1) * u1, odd);
+    const bool ok = in && c < left;
+    if (ok) store_word(h, wh);
+    h += 4 * p.ld;
     if (p.z) {
+      const uint32_t wg = swap_pair(g0, g1, odd), wu = swap_pair(u0, u1, odd);
       if (p.paired_z) {
-        const uint32_t wg = swap_pair(g0, g1, odd), wu = swap_pair(u0, u1, odd);
-        const int64_t row = r + odd;
-        if (in && row < t.j_end) {
-          store_word(p.z + row * p.ldz + i - odd, wg);
-          store_word(p.z + row * p.ldz + p.I + i - odd, wu);
+        if (ok) {
+          store_word(z, wg);
+          store_word(z + p.I, wu);
         }
-      } else {
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (in && r + q < t.j_end) {
-            __nv_bfloat16* z = p.z + int64_t(r + q) * p.ldz + i;
-            z[0] = __float2bfloat16_rn(q ? g1 : g0);
-            z[p.I] = __float2bfloat16_rn(q ? u1 : u0);
-          }
+      } else if (ok) {
+        uint16_t* z16 = reinterpret_cast<uint16_t*>(z);
+        z16[0] = uint16_t(wg);
+        z16[p.I] = uint16_t(wu);
+        if (col + 1 < p.I) {
+          z16[1] = uint16_t(wg >> 16);
+          z16[p.I + 1] = uint16_t(wu >> 16);
+        }
       }
+      z += 4 * p.ldz;
     }
   }
 }
@@ -211,24 +209,31 @@ __device__ __forceinline__ void load_saved(const FfnParams& p, const Tile& t, in
 }
 
 // dG, dU and H of sixteen rows of dH. The buffers' rows are padded to whole words.
+template <int ACT>
 __device__ __forceinline__ void gate_back16(const FfnParams& p, const Tile& t, int j, int i,
                                             const float (&v)[16], const Saved& s, int lane) {
   const int odd = lane & 1, col = i - odd;
-  __nv_bfloat16* h = static_cast<__nv_bfloat16*>(p.d);
+  const int left = col < p.I ? t.j_end - j - odd : 0;  // rows from this lane's first on
+  const int64_t row = j + odd;
+  __nv_bfloat16* h = static_cast<__nv_bfloat16*>(p.d) + row * p.ld + col;
+  __nv_bfloat16* dg = p.dz + row * p.lddz + col;
+  __nv_bfloat16* du = dg + p.dz_half;
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     const float o = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[2 * c] : v[2 * c + 1], 1);
     const float d0 = odd ? o : v[2 * c], d1 = odd ? v[2 * c + 1] : o;
     float a0, a1, s0, s1;
-    activate(low_half(s.g[c]), p.act, a0, s0);
-    activate(high_half(s.g[c]), p.act, a1, s1);
+    activate<ACT>(low_half(s.g[c]), a0, s0);
+    activate<ACT>(high_half(s.g[c]), a1, s1);
     const float u0 = low_half(s.u[c]), u1 = high_half(s.u[c]);
-    const int64_t row = j + 2 * c + odd;
-    if (col < p.I && row < t.j_end) {
-      store_word(p.dz + row * p.lddz + col, pack(d0 * u0 * s0, d1 * u1 * s1));
-      store_word(p.dz + row * p.lddz + p.dz_half + col, pack(d0 * a0, d1 * a1));
-      store_word(h + row * p.ld + col, pack(a0 * u0, a1 * u1));
+    if (2 * c < left) {
+      store_word(dg, pack(d0 * u0 * s0, d1 * u1 * s1));
+      store_word(du, pack(d0 * a0, d1 * a1));
+      store_word(h, pack(a0 * u0, a1 * u1));
     }
+    dg += 2 * p.lddz;
+    du += 2 * p.lddz;
+    h += 2 * p.ld;
   }
 }
 
@@ -246,7 +251,7 @@ __device__ __forceinline__ void clear_unused(const FfnParams& p, int64_t j0, int
 
 // ------------------------------------------------------------------ the kernel
 
-template <int FORM, int EPI>
+template <int FORM, int EPI, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     ffn_kernel(const __grid_constant__ FfnParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -469,8 +474,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int c = column(s);
         if (c >= n) return;
         if (EPI == GATE && p.splits > 1) store16_gate_parts(p, t, t.j0 + c, i, v, lane);
-        else if (EPI == GATE) gate16(p, t, t.j0 + c, i, v, lane);
-        else if (EPI == GATE_BACK && p.splits == 1) gate_back16(p, t, t.j0 + c, i, v, z, lane);
+        else if (EPI == GATE) gate16<ACT>(p, t, t.j0 + c, i, v, lane);
+        else if (EPI == GATE_BACK && p.splits == 1) gate_back16<ACT>(p, t, t.j0 + c, i, v, z, lane);
         else store16(p, t, t.j0 + c, i, v, lane);
       };
       // a step's columns are loaded while the step before is stored
@@ -546,7 +551,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16* d, int64_t i, int n, bool 
   }
 }
 
-template <int EPI>
+template <int EPI, int ACT>
 __global__ void __launch_bounds__(256) ffn_sum_kernel(const __grid_constant__ SumParams p) {
   wait_for_previous();
   const FfnParams& q = p.q;
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(256) ffn_sum_kernel(const __grid_constant__ Su
       float u[4], h[4];
       add_parts(p, j, q.part_half + i, u);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) h[c] = activate(v[c], q.act) * u[c];
+      for (int c = 0; c < 4; ++c) h[c] = activate<ACT>(v[c]) * u[c];
       store4(static_cast<__nv_bfloat16*>(q.d) + j * q.ld, i, q.I, q.paired, h);
       if (q.z) {
         store4(q.z + j * q.ldz, i, q.I, q.paired_z, v);
@@ -582,7 +587,7 @@ __global__ void __launch_bounds__(256) ffn_sum_kernel(const __grid_constant__ Su
         const bool in = i + c < q.I;
         const float g = in ? __bfloat162float(z[c]) : 0.0f, u = in ? __bfloat162float(z[q.I + c]) : 0.0f;
         float a, slope;
-        activate(g, q.act, a, slope);
+        activate<ACT>(g, a, slope);
         h[c] = a * u;
         dg[c] = v[c] * u * slope;
         du[c] = v[c] * a;
@@ -660,7 +665,8 @@ struct Plan {
 using Kernel = void (*)(const FfnParams);
 using SumKernel = void (*)(const SumParams);
 
-mao_status run(const Plan& plan, FfnParams& p, const Runs& runs, int64_t rows, void* parts, cudaStream_t stream) {
+mao_status run(const Plan& plan, int32_t act, FfnParams& p, const Runs& runs, int64_t rows, void* parts,
+               cudaStream_t stream) {
   p.offsets = runs.offsets;
   p.counts = runs.offsets ? runs.counts : nullptr;
   p.groups = runs.groups;
@@ -678,14 +684,21 @@ mao_status run(const Plan& plan, FfnParams& p, const Runs& runs, int64_t rows, v
   const int64_t tiles = (tn ? ceil_div(plan.J, TILE) * runs.groups * plan.halves
                             : ceil_div(rows, TILE) + (runs.offsets ? runs.groups : 0)) * plan.tiles_i();
   if (tiles * p.splits > 0x7FFF0000) return MAO_ERR_UNSUPPORTED;
-  const int k = plan.epi == GATE ? 0 : plan.epi == GATE_BACK ? 1 : plan.form == NT ? 2 : plan.form == NN ? 3 : 4;
-  static const Kernel kernels[5] = {ffn_kernel<NT, GATE>, ffn_kernel<NN, GATE_BACK>, ffn_kernel<NT, PLAIN>,
-                                    ffn_kernel<NN, PLAIN>, ffn_kernel<TN, PLAIN>};
-  static const SumKernel sums[3] = {ffn_sum_kernel<PLAIN>, ffn_sum_kernel<GATE>, ffn_sum_kernel<GATE_BACK>};
+  // the plain products, then those of each activation
+  static const Kernel kernels[9] = {
+      ffn_kernel<NT, PLAIN, 0>, ffn_kernel<NN, PLAIN, 0>, ffn_kernel<TN, PLAIN, 0>,
+      ffn_kernel<NT, GATE, MAO_SILU>, ffn_kernel<NT, GATE, MAO_GELU>, ffn_kernel<NT, GATE, MAO_GELU_TANH>,
+      ffn_kernel<NN, GATE_BACK, MAO_SILU>, ffn_kernel<NN, GATE_BACK, MAO_GELU>, ffn_kernel<NN, GATE_BACK, MAO_GELU_TANH>};
+  static const SumKernel sums[7] = {
+      ffn_sum_kernel<PLAIN, 0>,
+      ffn_sum_kernel<GATE, MAO_SILU>, ffn_sum_kernel<GATE, MAO_GELU>, ffn_sum_kernel<GATE, MAO_GELU_TANH>,
+      ffn_sum_kernel<GATE_BACK, MAO_SILU>, ffn_sum_kernel<GATE_BACK, MAO_GELU>, ffn_sum_kernel<GATE_BACK, MAO_GELU_TANH>};
+  const int k = plan.epi == GATE ? 3 + act : plan.epi == GATE_BACK ? 6 + act : plan.form;
+  const int ks = plan.epi == GATE ? 1 + act : plan.epi == GATE_BACK ? 4 + act : 0;
   static std::atomic<bool> ready[64];
   mao_status st = once_per_device(ready, [&] {
     cudaError_t err = cudaSuccess;
-    for (int f = 0; f < 5 && err == cudaSuccess; ++f)
+    for (int f = 0; f < 9 && err == cudaSuccess; ++f)
       err = cudaFuncSetAttribute(kernels[f], cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM));
     return err;
   });
@@ -705,7 +718,7 @@ mao_status run(const Plan& plan, FfnParams& p, const Runs& runs, int64_t rows, v
   st = launch_dependent(kernels[k], grid, THREADS, SMEM, stream, p);
   if (st != MAO_OK) return st;
   const int64_t blocks = ceil_div(plan.prows * ceil_div(plan.I, 4), 256);
-  return launch_dependent(sums[plan.epi], unsigned(blocks < 8 * num_sms() ? blocks : 8 * num_sms()), 256, 0,
+  return launch_dependent(sums[ks], unsigned(blocks < 8 * num_sms() ? blocks : 8 * num_sms()), 256, 0,
                           stream, sum);
 }
 
@@ -800,14 +813,13 @@ mao_status gated_ffn_launch(const mao_mat& X, const mao_mat& up, const mao_mat& 
   p.d = h;
   p.ld = f.ldh;
   p.dtype = MAO_BF16;
-  p.paired = s.N % 2 == 0;
-  p.act = act;
+  p.paired = 1;
   if (Z) {
     p.z = static_cast<__nv_bfloat16*>(Z->data);
     p.ldz = Z->ld;
     p.paired_z = words(Z->data, Z->ld, s.N);
   }
-  st = run(f.gate, p, runs, s.R, at, stream);
+  st = run(f.gate, act, p, runs, s.R, at, stream);
   if (st != MAO_OK) return st;
 
   FfnParams q = {};
@@ -815,7 +827,7 @@ mao_status gated_ffn_launch(const mao_mat& X, const mao_mat& up, const mao_mat& 
   if (st == MAO_OK) st = encode_q(q, h, s.N, s.R, 1, f.ldh, s.R * f.ldh);
   if (st != MAO_OK) return st;
   set_out(q, Y);
-  return run(f.out, q, runs, s.R, at, stream);
+  return run(f.out, act, q, runs, s.R, at, stream);
 }
 
 size_t gated_ffn_backward_workspace_size(const mao_mat& dY, const mao_mat& X, const mao_mat& up,
@@ -865,8 +877,7 @@ mao_status gated_ffn_backward_launch(const mao_mat& dY, const mao_mat& X, const 
     p.dz = reinterpret_cast<__nv_bfloat16*>(dz);
     p.lddz = 2 * b.ldh;
     p.dz_half = int32_t(b.ldh);
-    p.act = act;
-    st = run(b.back, p, runs, s.R, at, stream);
+      st = run(b.back, act, p, runs, s.R, at, stream);
     if (st != MAO_OK) return st;
   }
   if (dX) {
@@ -875,7 +886,7 @@ mao_status gated_ffn_backward_launch(const mao_mat& dY, const mao_mat& X, const 
     if (st == MAO_OK) st = encode_q(p, dz, s.N, s.R, 2, 2 * b.ldh, b.ldh);
     if (st != MAO_OK) return st;
     set_out(p, *dX);
-    st = run(b.dx, p, runs, s.R, at, stream);
+    st = run(b.dx, act, p, runs, s.R, at, stream);
     if (st != MAO_OK) return st;
   }
   if (dup) {
@@ -885,7 +896,7 @@ mao_status gated_ffn_backward_launch(const mao_mat& dY, const mao_mat& X, const 
       st = tc_encode_bf16_map(&p.map_q[Q_BOXES - 1], dz, s.N, s.R, 2, 1, 2 * b.ldh, b.ldh, s.R * 2 * b.ldh, BK);
     if (st != MAO_OK) return st;
     set_out(p, *dup);
-    st = run(b.dup, p, runs, s.R, at, stream);
+    st = run(b.dup, act, p, runs, s.R, at, stream);
     if (st != MAO_OK) return st;
   }
   if (ddown) {
@@ -895,7 +906,7 @@ mao_status gated_ffn_backward_launch(const mao_mat& dY, const mao_mat& X, const 
       st = tc_encode_bf16_map(&p.map_q[Q_BOXES - 1], b.dy.data, s.C, s.R, 1, 1, b.dy.ld, s.R * b.dy.ld, s.R * b.dy.ld, BK);
     if (st != MAO_OK) return st;
     set_out(p, *ddown);
-    st = run(b.ddown, p, runs, s.R, at, stream);
+    st = run(b.ddown, act, p, runs, s.R, at, stream);
   }
   return st;
 }
