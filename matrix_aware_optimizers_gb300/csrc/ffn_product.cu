@@ -15,10 +15,11 @@
 // that way), so that a channel's G and U meet by one exchange within a warp.
 //
 // Tiles of 256 x 256 (GATE: 128 channels, twice) by a pair of CTAs (tcgen05 cta_group::2, M = 256
-// values of i, N up to 256 values of j). Roles per CTA (320 threads):
+// values of i, N up to 256 values of j). Roles per CTA (576 threads):
 //   warp 0      TMA producer: 64-deep stages, 128 rows of P and the tile's half of Q, ring of six
 //   warp 1      TMEM allocation; in the even CTA it issues the products (converged, one lane)
-//   warps 2..9  epilogue: two warps per 32-lane quadrant of TMEM; lane = i
+//   warps 2..17 epilogue: four warps per 32-lane quadrant of TMEM; lane = i. Its loops are kept
+//               short: unrolled over two steps the code left the instruction cache
 // TMEM holds two accumulators of 256 columns: a tile's epilogue runs under the next one's products.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -44,11 +45,11 @@ constexpr int OP_BYTES = HALF * BK * 2;
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
 constexpr int CHUNK_BYTES = 64 * BK * 2;  // 64 values of i or j of an MN-major operand
 constexpr int STAGES = 6;
-constexpr int EPI_WARPS = 8;
+constexpr int EPI_WARPS = 16;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 512;
 constexpr int Q_BOXES = 4;            // heights of boxes of a K-major Q: 16 << b rows
-constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + TABLE_BYTES + 256;
+constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + TABLE_BYTES + 512;
 static_assert(SMEM <= 232448, "shared memory budget of one CTA");
 
 enum Epilogue { PLAIN, GATE, GATE_BACK };
@@ -206,6 +207,15 @@ __device__ __forceinline__ void load_saved(const FfnParams& p, const Tile& t, in
     s.g[c] = (a ? uint32_t(z[0]) : 0u) | (b ? uint32_t(z[1]) << 16 : 0u);
     s.u[c] = (a ? uint32_t(z[p.I]) : 0u) | (b ? uint32_t(z[p.I + 1]) << 16 : 0u);
   }
+}
+
+// Asks L2 for a tile's G and U (this CTA's columns), two threads per row.
+__device__ __forceinline__ void prefetch_saved(const FfnParams& p, const Tile& t, int cta, int thread) {
+  const int i = t.i0 + HALF * cta, row = t.j0 + (thread >> 1);
+  if (row >= t.j_end) return;
+  const __nv_bfloat16* z = p.z + int64_t(row) * p.ldz + (thread & 1 ? p.I : 0);
+  if (i < p.I) prefetch_l2(z + i);
+  if (i + 64 < p.I) prefetch_l2(z + i + 64);
 }
 
 // dG, dU and H of sixteen rows of dH. The buffers' rows are padded to whole words.
@@ -440,7 +450,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int quad = warp & 3;         // TMEM lanes 32 quad ..
-    const int part = (warp - 2) >> 2;  // which of the quadrant's two warps
+    const int part = (warp - 2) >> 2;  // which of the quadrant's four warps
+    const bool saved = EPI == GATE_BACK && p.splits == 1;
     const uint32_t tempty[2] = {mapa_shared(smem_u32(&tempty_bar[0]), 0),
                                 mapa_shared(smem_u32(&tempty_bar[1]), 0)};
     // rows that hold no tokens are cleared while the first tiles are multiplied
@@ -452,6 +463,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     Tile t;
     for (int tile = pair; tile < total; tile += npairs) {
       decode<FORM, STEP_I, BK>(p, lo, cnt, begin, tile, t);
+      if (saved) {
+        // this tile's G and U if it is the first, and the next one's: they have a tile's time
+        if (tile == pair) prefetch_saved(p, t, int(cta), int(threadIdx.x) - 64);
+        if (tile + npairs < total) {
+          Tile u = t;
+          decode<FORM, STEP_I, BK>(p, lo, cnt, begin, tile + npairs, u);
+          prefetch_saved(p, u, int(cta), int(threadIdx.x) - 64);
+        }
+      }
       const int i = EPI == GATE ? t.i0 + HALF / 2 * int(cta) + 16 * quad + (lane & 15)
                                 : t.i0 + HALF * int(cta) + 32 * quad + lane;
       if (t.nkb == 0) {  // TN: an empty run's matrix is zero
@@ -462,43 +482,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       const int acc = local & 1;
       const int n = t.j_end - t.j0;
-      // this warp's 128 columns in eight steps, every second sixteen
-      auto column = [&](int s) { return 32 * s + 16 * part; };
-      Saved sa, sb;
-      if (EPI == GATE_BACK && p.splits == 1) load_saved(p, t, t.j0 + column(0), i, lane, sa);
+      // this warp's 64 columns in four steps, every fourth sixteen
+      Saved z, next;
+      if (saved) load_saved(p, t, t.j0 + 16 * part, i, lane, z);
       // every lane waits; the warp goes on only if all of them saw the accumulator
       if (!wait_warp<false>(&tfull_bar[acc], uint32_t(local >> 1) & 1u, abort_flag, limit)) break;
       tc_fence_after();
       const uint32_t trow = tmem_base + (uint32_t(32 * quad) << 16) + uint32_t(acc * TILE);
-      auto out = [&](int s, const float(&v)[16], const Saved& z) {
-        const int c = column(s);
-        if (c >= n) return;
+#pragma unroll 1
+      for (int c = 16 * part; c < n; c += 64) {
+        float v[16];
+        tmem_ld16(trow + uint32_t(c), v);
+        // the next step's G and U are on their way while this one is worked on
+        if (saved && c + 64 < n) load_saved(p, t, t.j0 + c + 64, i, lane, next);
+        tmem_wait(v);
         if (EPI == GATE && p.splits > 1) store16_gate_parts(p, t, t.j0 + c, i, v, lane);
         else if (EPI == GATE) gate16<ACT>(p, t, t.j0 + c, i, v, lane);
-        else if (EPI == GATE_BACK && p.splits == 1) gate_back16<ACT>(p, t, t.j0 + c, i, v, z, lane);
+        else if (saved) gate_back16<ACT>(p, t, t.j0 + c, i, v, z, lane);
         else store16(p, t, t.j0 + c, i, v, lane);
-      };
-      // a step's columns are loaded while the step before is stored
-      float va[16], vb[16];
-      if (column(0) < n) tmem_ld16(trow + uint32_t(column(0)), va);
-#pragma unroll 1
-      for (int s = 0; s < 8; s += 2) {
-        if (EPI == GATE_BACK && p.splits == 1 && column(s + 1) < n) load_saved(p, t, t.j0 + column(s + 1), i, lane, sb);
-        tmem_wait(va);
-        if (column(s + 1) < n) tmem_ld16(trow + uint32_t(column(s + 1)), vb);
-        out(s, va, sa);
-        if (EPI == GATE_BACK && p.splits == 1 && s < 6 && column(s + 2) < n)
-          load_saved(p, t, t.j0 + column(s + 2), i, lane, sa);
-        tmem_wait(vb);
-        if (s == 6) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tempty[acc]);
-        } else if (column(s + 2) < n) {
-          tmem_ld16(trow + uint32_t(column(s + 2)), va);
-        }
-        out(s + 1, vb, sb);
+        if (saved) z = next;
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty[acc]);
       ++local;
     }
     __syncwarp();
