@@ -319,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   make_table<THREADS>(p, lo, cnt, begin, reinterpret_cast<int*>(bars + 24));
   tc_fence_before();
   __syncthreads();
-  const int total = FORM == TN ? (p.J + TILE - 1) / TILE * p.tiles_i * p.groups * p.halves * p.splits
+  const int total = FORM == TN ? (p.J + p.height - 1) / p.height * p.tiles_i * p.groups * p.halves * p.splits
                                : begin[p.groups] * p.tiles_i * p.splits;
   cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA arrival
   tc_fence_after();
@@ -607,15 +607,34 @@ __global__ void __launch_bounds__(256) ffn_sum_kernel(const __grid_constant__ Su
 
 // ------------------------------------------------------------------ copies of unaligned operands
 
+// Up to four operands to rows that start at multiples of 16 bytes, in one launch: eight entries per
+// thread and step.
 struct CopyParams {
-  const uint16_t* src;
-  uint16_t* dst;
-  int64_t rows, cols, ld, dld;
+  struct Part {
+    const uint16_t* src;
+    uint16_t* dst;
+    int64_t ld, dld, first, groups;  // first of all groups of eight, their number
+    int32_t cols, per_row;
+  } part[4];
+  int32_t n;
 };
 __global__ void __launch_bounds__(256) copy_kernel(const CopyParams p) {
   wait_for_previous();
-  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x)
-    for (int64_t c = threadIdx.x; c < p.cols; c += 256) p.dst[r * p.dld + c] = p.src[r * p.ld + c];
+  int64_t all = 0;
+  for (int q = 0; q < p.n; ++q) all += p.part[q].groups;
+  for (int64_t x = int64_t(blockIdx.x) * 256 + threadIdx.x; x < all; x += int64_t(gridDim.x) * 256) {
+    int q = 0;
+    while (q + 1 < p.n && x >= p.part[q + 1].first) ++q;
+    const CopyParams::Part& c = p.part[q];
+    const int64_t y = x - c.first, r = y / c.per_row;
+    const int col = 8 * int(y - r * c.per_row);
+    const uint16_t* s = c.src + r * c.ld + col;
+    uint32_t e[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = col + k < c.cols ? uint32_t(s[k]) : 0u;
+    *reinterpret_cast<uint4*>(c.dst + r * c.dld + col) =
+        make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -635,22 +654,32 @@ Operand operand(const mao_mat& m) {
   if (whole) return Operand{m.data, m.rows, m.cols, round_up(m.rows <= 1 ? m.cols : m.ld, 8), false};
   return Operand{nullptr, m.rows, m.cols, round_up(m.cols, 8), true};
 }
-mao_status place(Operand& o, const mao_mat& m, uint8_t*& at, cudaStream_t stream) {
-  if (!o.copied || o.rows == 0) return MAO_OK;
-  o.data = at;
-  at += o.bytes();
-  const CopyParams c{static_cast<const uint16_t*>(m.data), static_cast<uint16_t*>(const_cast<void*>(o.data)),
-                     m.rows, m.cols, m.ld, o.ld};
-  return launch_dependent(copy_kernel, unsigned(m.rows < 16 * num_sms() ? m.rows : 16 * num_sms()), 256, 0,
-                          stream, c);
-}
+// Copies of operands, in one launch; at: the workspace from there on.
+struct Copies {
+  CopyParams p = {};
+  int64_t all = 0;
+  void add(Operand& o, const mao_mat& m, uint8_t*& at) {
+    if (!o.copied || o.rows == 0) return;
+    o.data = at;
+    const int64_t per_row = o.ld / 8;
+    p.part[p.n++] = {static_cast<const uint16_t*>(m.data), reinterpret_cast<uint16_t*>(at), m.ld, o.ld, all,
+                     m.rows * per_row, int32_t(m.cols), int32_t(per_row)};
+    all += m.rows * per_row;
+    at += o.bytes();
+  }
+  mao_status launch(cudaStream_t stream) const {
+    if (p.n == 0) return MAO_OK;
+    const int64_t blocks = ceil_div(all, 256);
+    return launch_dependent(copy_kernel, unsigned(blocks < 16 * num_sms() ? blocks : 16 * num_sms()), 256, 0, stream, p);
+  }
+};
 
 // The products of a call, with the sizes that their splits and parts go by.
 struct Plan {
   int form, epi;
   int64_t I, J, depth;  // of D: columns (GATE: channels), rows (one matrix's for TN); depth per half
   int32_t halves;
-  Split split{1, 0};
+  Cut split{TILE, 1, 0};
   int64_t prows = 0, pld = 0;
 
   int64_t tiles_i() const { return ceil_div(I, epi == GATE ? HALF : TILE); }
@@ -659,9 +688,10 @@ struct Plan {
     if (grouped) return;
     const int64_t nkb = ceil_div(depth, BK) * (form == NN ? halves : 1);
     const int64_t outputs = J * matrices() * I * (epi == GATE ? 2 : 1);
-    // a block takes a pair 0.27 us (the tensor cores) or, where few rows leave the operands' bytes
-    // to bound it, 0.37 us
-    split = choose_split(tiles_i() * ceil_div(J, TILE) * matrices(), nkb, J < 128 ? 0.37 : 0.27, outputs, 4);
+    // A block takes a pair 0.27 us (the tensor cores), at least 0.14 (its copies and their waits),
+    // or 0.37 where few rows leave the operands' bytes to bound it.
+    split = choose_cut(tiles_i() * matrices(), J, nkb, 0.27, form != TN && J < 128 ? 0.37 : 0.14,
+                       epi == GATE_BACK ? 9.5 : epi == GATE ? 3.5 : 1.7, outputs, 4);
     prows = J * matrices();
     pld = round_up(I, 4) * (epi == GATE ? 2 : 1);
   }
@@ -683,12 +713,13 @@ mao_status run(const Plan& plan, int32_t act, FfnParams& p, const Runs& runs, in
   p.halves = plan.halves;
   p.tiles_i = int32_t(plan.tiles_i());
   p.timeout_ns = wait_limit_ns();
+  p.height = plan.split.height;
   p.splits = plan.split.splits;
   p.split_kb = plan.split.kb;
   p.part_half = int32_t(round_up(plan.I, 4));
   const bool tn = plan.form == TN;
-  const int64_t tiles = (tn ? ceil_div(plan.J, TILE) * runs.groups * plan.halves
-                            : ceil_div(rows, TILE) + (runs.offsets ? runs.groups : 0)) * plan.tiles_i();
+  const int64_t tiles = (tn ? ceil_div(plan.J, p.height) * runs.groups * plan.halves
+                            : ceil_div(rows, p.height) + (runs.offsets ? runs.groups : 0)) * plan.tiles_i();
   if (tiles * p.splits > 0x7FFF0000) return MAO_ERR_UNSUPPORTED;
   // the plain products, then those of each activation
   static const Kernel kernels[9] = {
@@ -807,9 +838,11 @@ mao_status gated_ffn_launch(const mao_mat& X, const mao_mat& up, const mao_mat& 
   uint8_t* at = static_cast<uint8_t*>(workspace);
   uint8_t* h = at;
   at += f.h_bytes();
-  mao_status st = place(f.x, X, at, stream);
-  if (st == MAO_OK) st = place(f.up, up, at, stream);
-  if (st == MAO_OK) st = place(f.down, down, at, stream);
+  Copies copies;
+  copies.add(f.x, X, at);
+  copies.add(f.up, up, at);
+  copies.add(f.down, down, at);
+  mao_status st = copies.launch(stream);
   if (st != MAO_OK) return st;
 
   FfnParams p = {};
@@ -862,10 +895,12 @@ mao_status gated_ffn_backward_launch(const mao_mat& dY, const mao_mat& X, const 
   at += b.h_bytes();
   uint8_t* dz = at;
   at += b.dz_bytes();
-  mao_status st = place(b.dy, dY, at, stream);
-  if (st == MAO_OK) st = place(b.x, X, at, stream);
-  if (st == MAO_OK) st = place(b.up, up, at, stream);
-  if (st == MAO_OK) st = place(b.down, down, at, stream);
+  Copies copies;
+  copies.add(b.dy, dY, at);
+  copies.add(b.x, X, at);
+  copies.add(b.up, up, at);
+  copies.add(b.down, down, at);
+  mao_status st = copies.launch(stream);
   if (st != MAO_OK) return st;
 
   {

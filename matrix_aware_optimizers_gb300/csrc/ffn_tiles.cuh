@@ -9,7 +9,7 @@
 namespace mao {
 namespace ffn {
 
-constexpr int TILE = 256;  // i and j per tile
+constexpr int TILE = 256;  // i and (at most) j per tile
 constexpr int HALF = 128;  // of each per CTA
 constexpr int MAX_GROUPS = 1024;
 constexpr int BAND = 8;    // tiles of j that share a pass over i
@@ -25,6 +25,7 @@ struct TileParams {
   int32_t depth;             // per half of the depth (TN: the run's rows)
   int32_t halves;            // NN: halves of the depth; TN: matrices per run
   int32_t tiles_i, groups;
+  int32_t height;            // j per tile, at most: a multiple of 32
   int32_t splits, split_kb;  // parts of the depth (one run), blocks of each: D are fp32 parts
   unsigned long long timeout_ns;
 };
@@ -74,7 +75,7 @@ __device__ __forceinline__ void make_table(const TileParams& p, int* lo, int* cn
       const int all = lo[g + 1] - lo[g];
       const int used = p.counts ? max(0, min(p.counts[g], all)) : all;
       cnt[g] = used;
-      c[q] = (used + TILE - 1) / TILE;
+      c[q] = (used - 1) / p.height + (used > 0);  // (used + height may pass 2^31)
     }
     own += c[q];
   }
@@ -114,7 +115,7 @@ __device__ __forceinline__ void decode(const TileParams& p, const int* lo, const
                                        const int* begin, int tile, Tile& t) {
   if (FORM == TN) {
     // i runs fastest: the pairs at work at one time write whole rows of a matrix
-    const int tiles_j = (p.J + TILE - 1) / TILE, each = tiles_j * p.tiles_i;
+    const int tiles_j = (p.J + p.height - 1) / p.height, each = tiles_j * p.tiles_i;
     int m = tile / each;  // split, run, half
     const int local = tile - m * each;
     const int jt = local / p.tiles_i;
@@ -123,8 +124,8 @@ __device__ __forceinline__ void decode(const TileParams& p, const int* lo, const
     t.g = m / p.halves;
     t.half = m - t.g * p.halves;
     t.i0 = (local - jt * p.tiles_i) * TILE;
-    t.j0 = jt * TILE;
-    t.j_end = min(t.j0 + TILE, p.J);
+    t.j0 = jt * p.height;
+    t.j_end = min(t.j0 + p.height, p.J);
     t.k0 = lo[t.g];
     t.nkb = (cnt[t.g] + BK - 1) / BK;
     t.row0 = int64_t(m) * p.J;
@@ -165,7 +166,7 @@ __device__ __forceinline__ void decode(const TileParams& p, const int* lo, const
   t.k0 = 0;
   // a run's tiles are of even height
   const int rows = cnt[a];
-  const int height = count > 1 ? ((rows - 1) / count + 32) & ~31 : TILE;
+  const int height = count > 1 ? ((rows - 1) / count + 32) & ~31 : p.height;
   t.j0 = lo[a] + jt * height;
   t.j_end = min(t.j0 + height, lo[a] + rows);
   t.nkb = (p.depth + BK - 1) / BK * (FORM == NN ? p.halves : 1);
@@ -232,22 +233,32 @@ __device__ __forceinline__ void for_unused_rows(const TileParams& p, const int* 
   range(lo[p.groups], p.rows);
 }
 
-struct Split {
-  int splits, kb;
+// How a product of one run is cut: the height of its tiles, and the parts of its depth with their
+// blocks.
+struct Cut {
+  int height, splits, kb;
 };
-// How many parts the depth of a product of one run is split into, each at least `least_kb` blocks,
-// by a model of the two kernels: `block` us per block of the depth and pair; 2.5 us and 3 TB/s for
-// the sum of the fp32 parts, which stay in L2.
-inline Split choose_split(int64_t tiles, int64_t nkb, double block, int64_t outputs, int64_t least_kb) {
+// The cut with the least time by a model of the kernels, in us: `block` per block of the depth for a
+// tile of 256, less for a lower one down to `least_block`; `epilogue` for a tile of 256; 2.5 us and
+// 3 TB/s for the sum of the fp32 parts, which stay in L2. tiles_i: tiles of i (of all matrices).
+inline Cut choose_cut(int64_t tiles_i, int64_t J, int64_t nkb, double block, double least_block, double epilogue,
+                      int64_t outputs, int64_t least_kb) {
   const int64_t pairs = num_sms() / 2;
-  Split best{1, int(nkb)};
-  double least = block * double(nkb * ceil_div(tiles, pairs));
-  for (int64_t s = 2; s <= 32 && least_kb * s <= nkb; ++s) {
-    const int64_t kb = ceil_div(nkb, s), parts = ceil_div(nkb, kb);
-    const double t = block * double(kb * ceil_div(tiles * parts, pairs)) + 2.5 + double(parts) * double(outputs) * 8.0 / 3e6;
-    if (parts > 1 && t < 0.95 * least) {
-      least = t;
-      best = Split{int(parts), int(kb)};
+  Cut best{TILE, 1, int(nkb)};
+  double least = 1e30;
+  for (int h = TILE; h >= 32; h /= 2) {
+    if (h < TILE && J <= h / 2) break;  // (a lower tile than the rows need changes nothing)
+    const int64_t tiles = tiles_i * ceil_div(J, h);
+    const double part = double(J < h ? round_up(J, 32) : h) / TILE;
+    const double each = block * part > least_block ? block * part : least_block;
+    for (int64_t s = 1; s <= 32 && (s == 1 || least_kb * s <= nkb); ++s) {
+      const int64_t kb = ceil_div(nkb, s), parts = ceil_div(nkb, kb);
+      double t = each * double(kb * ceil_div(tiles * parts, pairs)) + epilogue * part;
+      if (parts > 1) t += 2.5 + double(parts) * double(outputs) * 8.0 / 3e6;
+      if (t < 0.95 * least) {
+        least = t;
+        best = Cut{h, int(parts), int(kb)};
+      }
     }
   }
   return best;

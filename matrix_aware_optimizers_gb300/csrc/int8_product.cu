@@ -577,10 +577,9 @@ __global__ void __launch_bounds__(128) to_half_kernel(const HalfParams p) {
 
 std::atomic<bool> g_launched{false};
 
-// A block of 128 takes a pair 0.55 us, or 0.4 us (the operands' bytes) with few rows.
-Split split_of(const mao_int8& A, const mao_int8& B) {
-  return choose_split(ceil_div(A.rows, TILE) * ceil_div(B.rows, TILE), ceil_div(A.cols, BK),
-                      A.rows < 128 ? 0.4 : 0.55, A.rows * B.rows, 2);
+// A block of 128 takes a pair 0.55 us, at least 0.4 (the conversion; with few rows the bytes).
+Cut cut_of(const mao_int8& A, const mao_int8& B) {
+  return choose_cut(ceil_div(B.rows, TILE), A.rows, ceil_div(A.cols, BK), 0.55, 0.4, 1.7, A.rows * B.rows, 2);
 }
 
 // The workspace: A in fp16, then the parts of split sums.
@@ -591,7 +590,7 @@ size_t half_bytes(const mao_int8& A) { return size_t(round_up(A.rows * half_ld(A
 
 size_t int8_product_workspace_size(const mao_int8& A, const mao_int8& B, bool grouped) {
   if (A.rows == 0) return 0;
-  const Split s = grouped ? Split{1, 0} : split_of(A, B);
+  const Cut s = grouped ? Cut{TILE, 1, 0} : cut_of(A, B);
   return half_bytes(A) + (s.splits > 1 ? size_t(round_up(int64_t(s.splits) * A.rows * round_up(B.rows, 4) * 4, 256)) : 0);
 }
 mao_status int8_product_launch(const mao_int8& A, const mao_int8& B, const mao_mat& D, const Runs& runs,
@@ -619,11 +618,12 @@ mao_status int8_product_launch(const mao_int8& A, const mao_int8& B, const mao_m
   p.ld = D.ld;
   p.dtype = D.dtype;
   p.paired = D.dtype == MAO_BF16 && D.cols % 2 == 0 && reinterpret_cast<uintptr_t>(D.data) % 4 == 0 && D.ld % 2 == 0;
-  const Split split = runs.offsets ? Split{1, 0} : split_of(A, B);
+  const Cut cut = runs.offsets ? Cut{TILE, 1, 0} : cut_of(A, B);
   void* parts = static_cast<uint8_t*>(workspace) + half_bytes(A);
-  p.splits = split.splits;
-  p.split_kb = split.kb;
-  const int64_t tiles = (ceil_div(A.rows, TILE) + (runs.offsets ? runs.groups : 0)) * p.tiles_i;
+  p.height = cut.height;
+  p.splits = cut.splits;
+  p.split_kb = cut.kb;
+  const int64_t tiles = (ceil_div(A.rows, p.height) + (runs.offsets ? runs.groups : 0)) * p.tiles_i;
   if (tiles * p.splits > 0x7FFF0000) return MAO_ERR_UNSUPPORTED;
   static std::atomic<bool> ready[64];
   st = once_per_device(ready, [&] {
