@@ -8,6 +8,7 @@
 #include "common.cuh"
 #include "experts.h"
 #include "ffn.h"
+#include "ffn_few.h"
 #include "internal.h"
 #include "ns_small.h"
 
@@ -376,8 +377,9 @@ mao_status mao_sync_status(void* stream) {
   const mao_status d = product_read_and_clear_error(static_cast<cudaStream_t>(stream));
   const mao_status e = ffn_read_and_clear_error(static_cast<cudaStream_t>(stream));
   const mao_status f = int8_read_and_clear_error(static_cast<cudaStream_t>(stream));
+  const mao_status g = few_read_and_clear_error(static_cast<cudaStream_t>(stream));
   mao_status st = MAO_OK;
-  for (const mao_status s : {a, b, c, d, e, f})
+  for (const mao_status s : {a, b, c, d, e, f, g})
     if (s == MAO_ERR_CUDA || st == MAO_OK) st = s;
   return st;
 }

@@ -1,0 +1,320 @@
+// The feed-forward products for few rows: Y = X W^T (W's rows are channels), the gated pair of them,
+// and the same of 8-bit integers. Reading W bounds them: each weight is read once, and nothing
+// may hold the reads up. A block per SM works on sixteen channels at a time, whose sums' length its
+// eight warps share, 128 bytes of each row at a time; every warp has a ring of its own in shared
+// memory that its TMA loads keep full across the ends of sums (24 KB per warp: 192 KB under way
+// per SM), so no warp waits for another but where a sum ends.
+//
+// Up to sixteen rows of X meet the weights in mma.sync m16n8k16 with fp32 sums: with so few rows the
+// tensor cores' rate does not count, and the fragments come straight from the ring. Any order of the
+// products within a sum does, so a lane takes 32 bytes in a row of W's row and the same 32 of X's and
+// hands out four of their entries per product. 8-bit codes become fp16 on the way, exactly. The
+// warps' sums are added in their order.
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "ffn.h"
+#include "ffn_act.cuh"
+#include "ffn_few.h"
+#include "ffn_tiles.cuh"
+#include "internal.h"
+#include "ns_plan.h"
+#include "tc_ptx.cuh"
+
+namespace mao {
+namespace {
+
+using namespace ptx;
+using namespace ffn;
+
+constexpr int WARPS = 8;
+constexpr int THREADS = 32 * WARPS;
+constexpr int CHANNELS = 16;           // per unit
+constexpr int BOX_BYTES = 16 * 128;    // sixteen rows of 128 bytes
+// A warp's ring; the gated sums of sixteen rows need more room elsewhere.
+constexpr int ring_bytes(bool gate, int nt) { return gate && nt == 2 ? 20 * 1024 : 24 * 1024; }
+
+struct FewKernelParams : FewParams {
+  CUtensorMap map_w;
+  CUtensorMap map_x;
+  int32_t x_rows;  // rows of an X box
+};
+
+// A lane's 32 bytes of a row as words of two 16-bit entries.
+template <bool INT8>
+struct Entries {
+  static constexpr int WORDS = INT8 ? 16 : 8;
+  uint32_t w[WORDS];
+};
+
+__device__ __forceinline__ void codes_to_half(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = codes ^ 0x80808080u;  // code + 128 into the low byte of 1024, less 1152
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// Bytes 32 (lane % 4) .. + 31 of row r of a box (128-byte rows, swizzled).
+template <bool INT8>
+__device__ __forceinline__ Entries<INT8> entries(const uint8_t* box, int r, int lane) {
+  Entries<INT8> e;
+  const int c = 2 * (lane & 3);
+  const uint4 a = *reinterpret_cast<const uint4*>(box + r * 128 + 16 * (c ^ (r & 7)));
+  const uint4 b = *reinterpret_cast<const uint4*>(box + r * 128 + 16 * ((c + 1) ^ (r & 7)));
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    if (INT8) codes_to_half(w[q], e.w[INT8 ? 2 * q : 0], e.w[INT8 ? 2 * q + 1 : 0]);
+    else e.w[q] = w[q];
+  }
+  return e;
+}
+
+__device__ __forceinline__ void tma_load(bool codes, uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                         int32_t y, int32_t z, int32_t w) {
+  if (codes)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(w), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+template <bool INT8>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  if (INT8) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+
+// Unit number `unit`: sixteen channels for up to 8 NT rows of a run.
+struct Unit {
+  int run = 0;  // at or before the unit's (units come in rising order)
+  int i0, n;
+  int64_t j0;
+};
+template <int NT>
+__device__ __forceinline__ void decode_unit(const FewParams& p, const int* lo, const int* cnt, const int* begin,
+                                            int unit, Unit& u) {
+  int local = unit, count = (p.rows + 8 * NT - 1) / (8 * NT);
+  int64_t first = 0;
+  int rows = p.rows;
+  if (p.offsets) {
+    while (begin[u.run + 1] * p.tiles_i <= unit) ++u.run;
+    local = unit - begin[u.run] * p.tiles_i;
+    count = begin[u.run + 1] - begin[u.run];
+    first = lo[u.run];
+    rows = cnt[u.run];
+  }
+  const int it = local / count, jt = local - it * count;
+  u.i0 = it * CHANNELS;
+  u.j0 = first + jt * (8 * NT);
+  u.n = min(8 * NT, rows - jt * (8 * NT));
+}
+
+template <bool INT8, bool GATE, int ACT, int NT>
+__global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__ FewKernelParams p) {
+  constexpr int MATS = GATE ? 2 : 1;
+  constexpr int STAGE = MATS * BOX_BYTES + NT * 1024;  // a multiple of 1024
+  constexpr int RING = ring_bytes(GATE, NT), STAGES = RING / STAGE;
+  static_assert(RING % 1024 == 0 && STAGE % 1024 == 0, "swizzled boxes");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ float parts[2][WARPS][MATS][NT][32][4];
+  __shared__ int table[3 * (MAX_GROUPS + 2)];
+  __shared__ int scratch[WARPS];
+  __shared__ uint64_t bars[WARPS][STAGES];
+  __shared__ int abort_word;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &abort_word;
+  int* lo = table;
+  int* cnt = lo + MAX_GROUPS + 2;
+  int* begin = cnt + MAX_GROUPS + 2;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)) +
+                  warp * RING;
+  if (threadIdx.x == 0) abort_word = 0;
+  if (lane == 0) {
+    for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&bars[warp][s]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  __syncthreads();
+  // launched as a programmatic dependent: the set-up so far may overlap the previous kernel
+  wait_for_previous();
+  int units = p.tiles_i * ((p.rows + 8 * NT - 1) / (8 * NT));
+  if (p.offsets) {
+    make_table<THREADS>(p, lo, cnt, begin, scratch);
+    __syncthreads();
+    units = begin[p.groups] * p.tiles_i;
+  }
+  const int chunks = (p.depth * (INT8 ? 1 : 2) + 127) / 128;
+  const int step = INT8 ? 128 : 64;  // entries of a chunk
+
+  // The warp's items: chunks warp, warp + 8, ... of each of the block's units. The next one to load:
+  Unit next;
+  int next_unit = blockIdx.x, next_chunk = warp, loaded = 0;
+  if (next_chunk >= chunks) next_unit = units;  // no chunk of any sum is this warp's
+  if (next_unit < units) decode_unit<NT>(p, lo, cnt, begin, next_unit, next);
+  auto load_next = [&]() {
+    if (next_unit >= units) return;
+    const int stage = loaded % STAGES;
+    if (lane == 0) {
+      const uint32_t bar = smem_u32(&bars[warp][stage]), dst = smem_u32(ring) + stage * STAGE;
+      const int k = next_chunk * step;
+      mbar_expect_tx(bar, MATS * BOX_BYTES + p.x_rows * 128);
+#pragma unroll
+      for (int m = 0; m < MATS; ++m) tma_load(INT8, dst + m * BOX_BYTES, &p.map_w, bar, k, next.i0, m, next.run);
+      tma_load(INT8, dst + MATS * BOX_BYTES, &p.map_x, bar, k, int(next.j0), 0, 0);
+    }
+    ++loaded;
+    next_chunk += WARPS;
+    if (next_chunk >= chunks) {
+      next_chunk = warp;
+      next_unit += gridDim.x;
+      if (next_unit < units) decode_unit<NT>(p, lo, cnt, begin, next_unit, next);
+    }
+  };
+  for (int s = 0; s < STAGES; ++s) load_next();
+
+  if (p.offsets) {  // rows that hold no tokens, while the first loads are under way
+    const int turn = int(blockIdx.x) * WARPS + warp, turns = int(gridDim.x) * WARPS;
+    const int es = p.dtype == MAO_F32 ? 4 : 2;
+    for_unused_rows(p, lo, cnt, turn, turns, [&](int64_t j0, int64_t j1, int64_t every) {
+      if (!GATE) clear_rows(p.d, p.ld * es, int64_t(p.I) * es, j0, j1, every, lane);
+      else if (p.z) clear_rows(p.z, p.ldz * 2, int64_t(p.I) * 4, j0, j1, every, lane);
+    });
+  }
+
+  Unit u;
+  int used = 0, flip = 0;
+  bool ok = true;
+  for (int unit = blockIdx.x; unit < units; unit += gridDim.x, flip ^= 1) {
+    decode_unit<NT>(p, lo, cnt, begin, unit, u);
+    float acc[MATS][NT][4] = {};
+    for (int c = warp; c < chunks; c += WARPS) {
+      const int stage = used % STAGES;
+      ok = ok && wait_warp<false>(&bars[warp][stage], uint32_t(used / STAGES) & 1u, abort_flag, p.timeout_ns);
+      if (!ok) break;
+      const uint8_t* box = ring + stage * STAGE;
+      const int r = lane >> 2;
+      Entries<INT8> x[NT];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) x[q] = entries<INT8>(box + MATS * BOX_BYTES, r + 8 * q, lane);
+#pragma unroll
+      for (int m = 0; m < MATS; ++m) {
+        const Entries<INT8> a = entries<INT8>(box + m * BOX_BYTES, r, lane);
+        const Entries<INT8> b = entries<INT8>(box + m * BOX_BYTES, r + 8, lane);
+#pragma unroll
+        for (int s = 0; s < Entries<INT8>::WORDS; s += 2)
+#pragma unroll
+          for (int q = 0; q < NT; ++q) mma<INT8>(acc[m][q], a.w[s], b.w[s], a.w[s + 1], b.w[s + 1], x[q].w[s], x[q].w[s + 1]);
+      }
+      ++used;
+      __syncwarp();  // every lane has read the stage
+      load_next();
+    }
+#pragma unroll
+    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+        *reinterpret_cast<float4*>(parts[flip][warp][m][q][lane]) =
+            make_float4(acc[m][q][0], acc[m][q][1], acc[m][q][2], acc[m][q][3]);
+    // (the other half of `parts` was read before this barrier's last use but one)
+    __syncthreads();
+    // thread: row j0 + r of X, channel i0 + c
+    const int c = threadIdx.x % CHANNELS, r = threadIdx.x / CHANNELS, i = u.i0 + c;
+    if (r < u.n && i < p.I) {
+      float v[MATS] = {};
+      const int from = (c & 7) * 4 + ((r & 7) >> 1), e = (c >> 3) * 2 + (r & 1);
+#pragma unroll
+      for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) v[m] += parts[flip][w][m][NT == 1 ? 0 : r >> 3][from][e];
+      const int64_t j = u.j0 + r;
+      if (GATE) {
+        static_cast<__nv_bfloat16*>(p.d)[j * p.ld + i] = __float2bfloat16_rn(activate<ACT>(v[0]) * v[MATS - 1]);
+        if (p.z) {
+          p.z[j * p.ldz + i] = __float2bfloat16_rn(v[0]);
+          p.z[j * p.ldz + p.I + i] = __float2bfloat16_rn(v[MATS - 1]);
+        }
+      } else {
+        if (INT8) v[0] = v[0] * __ldg(p.sa + j) * __ldg(p.sb + int64_t(u.run) * p.I + i);
+        store_elem(p.d, j * p.ld + i, p.dtype, v[0]);
+      }
+    }
+  }
+  // after an abort, the loads already issued land before the block leaves
+  if (*abort_flag && lane == 0)
+    for (; used < loaded; ++used)
+      mbar_drain(smem_u32(&bars[warp][used % STAGES]), uint32_t(used / STAGES) & 1u, 20000000ull);
+}
+
+using Kernel = void (*)(const FewKernelParams);
+
+std::atomic<bool> g_launched{false};
+
+}  // namespace
+
+mao_status few_launch(const FewParams& params, bool int8, bool gate, int32_t act, cudaStream_t stream) {
+  FewKernelParams p = {};
+  static_cast<FewParams&>(p) = params;
+  p.tiles_i = int32_t(ceil_div(p.I, CHANNELS));
+  p.timeout_ns = wait_limit_ns();
+  const int two = !p.offsets && p.rows > 8;
+  p.height = two ? 16 : 8;
+  p.x_rows = p.rows < p.height ? p.rows : p.height;
+  const int64_t mats = gate ? 2 : 1, w_rows = int64_t(p.I);
+  mao_status st = int8 ? tc_encode_code_map(&p.map_w, p.w, p.depth, w_rows, p.ldw, p.groups, CHANNELS)
+                       : tc_encode_bf16_map(&p.map_w, p.w, p.depth, w_rows, mats, p.groups, p.ldw, w_rows * p.ldw,
+                                            mats * w_rows * p.ldw, CHANNELS);
+  if (st == MAO_OK)
+    st = int8 ? tc_encode_code_map(&p.map_x, p.x, p.depth, p.rows, p.ldx, 1, p.x_rows)
+              : tc_encode_bf16_map(&p.map_x, p.x, p.depth, p.rows, 1, 1, p.ldx, p.rows * p.ldx, p.rows * p.ldx, p.x_rows);
+  if (st != MAO_OK) return st;
+  static const Kernel kernels[10] = {
+      few_kernel<true, false, 0, 1>,          few_kernel<true, false, 0, 2>,
+      few_kernel<false, false, 0, 1>,         few_kernel<false, false, 0, 2>,
+      few_kernel<false, true, MAO_SILU, 1>,   few_kernel<false, true, MAO_SILU, 2>,
+      few_kernel<false, true, MAO_GELU, 1>,   few_kernel<false, true, MAO_GELU, 2>,
+      few_kernel<false, true, MAO_GELU_TANH, 1>, few_kernel<false, true, MAO_GELU_TANH, 2>};
+  static std::atomic<bool> ready[64];
+  st = once_per_device(ready, [&] {
+    cudaError_t err = cudaSuccess;
+    for (int f = 0; f < 10 && err == cudaSuccess; ++f)
+      err = cudaFuncSetAttribute(kernels[f], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 1024 + WARPS * ring_bytes(f >= 4, 1 + f % 2));
+    return err;
+  });
+  if (st != MAO_OK) return st;
+  g_launched.store(true, std::memory_order_release);
+  const int64_t units = p.offsets ? int64_t(num_sms()) : int64_t(p.tiles_i) * ceil_div(p.rows, p.height);
+  return launch_dependent(kernels[(int8 ? 0 : gate ? 4 + 2 * act : 2) + two], unsigned(units < num_sms() ? units : num_sms()),
+                          THREADS, size_t(1024 + WARPS * ring_bytes(gate, 1 + two)), stream, p);
+}
+
+mao_status few_read_and_clear_error(cudaStream_t stream) {
+  return g_launched.load(std::memory_order_acquire) ? read_and_clear_error(stream) : MAO_OK;
+}
+
+}  // namespace mao

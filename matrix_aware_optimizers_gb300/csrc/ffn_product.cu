@@ -29,6 +29,7 @@
 #include "common.cuh"
 #include "ffn.h"
 #include "ffn_act.cuh"
+#include "ffn_few.h"
 #include "ffn_tiles.cuh"
 #include "internal.h"
 #include "ns_plan.h"
@@ -56,7 +57,9 @@ enum Epilogue { PLAIN, GATE, GATE_BACK };
 
 struct FfnParams : TileParams {
   CUtensorMap map_p;
-  CUtensorMap map_q[Q_BOXES];  // boxes of 16, 32, 64, 128 rows (TN: the last only, 64 x 64)
+  // Boxes of 16, 32, 64, 128 rows. The last only for products of one run (half a tile's height) and
+  // TN (64 x 64)
+  CUtensorMap map_q[Q_BOXES];
   void* d;                     // PLAIN: D; GATE, GATE_BACK: H
   __nv_bfloat16* z;            // G and U: GATE writes them (null: not wanted), GATE_BACK reads them
   __nv_bfloat16* dz;           // GATE_BACK: dG and dU
@@ -343,7 +346,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int i = t.i0 + (EPI == GATE ? HALF / 2 : HALF) * int(cta);
       const int j = t.j0 + (t.n >> 1) * int(cta);
       const int z = FORM != TN ? t.g : 0;
-      const int q_rows = t.n >> 1;  // a multiple of 16
+      const bool one_box = !p.offsets;
+      const int q_rows = one_box && !q_mn ? p.height >> 1 : t.n >> 1;  // a multiple of 16
       const int q_chunks = (q_rows + 63) >> 6;
       const uint32_t q_bytes = q_mn ? uint32_t(q_chunks) * CHUNK_BYTES : uint32_t(q_rows) * BK * 2;
       for (int kb = 0; kb < t.nkb; ++kb) {
@@ -370,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (q_mn) {
             for (int c = 0; c < q_chunks; ++c)
               tma_load_4d_pair(dst + OP_BYTES + c * CHUNK_BYTES, &p.map_q[Q_BOXES - 1], fb, j + 64 * c, k, t.half, 0);
-          } else if (q_rows == HALF) {
+          } else if (one_box || q_rows == HALF) {
             tma_load_4d_pair(dst + OP_BYTES, &p.map_q[Q_BOXES - 1], fb, k, j, second, 0);
           } else {
             for (int box = Q_BOXES - 2, at = 0; box >= 0; --box)
@@ -782,6 +786,7 @@ struct Forward {
   Forward(const mao_mat& X, const mao_mat& Up, const mao_mat& Down, int32_t groups, bool grouped)
       : s{X.rows, X.cols, Down.cols, Down.rows / groups}, ldh(round_up(s.N, 8)), x(operand(X)), up(operand(Up)),
         down(operand(Down)), gate{NT, GATE, s.N, s.R, s.K, 1}, out{NT, PLAIN, s.C, s.R, s.N, 1} {
+    if (few_rows(s.R, grouped, false)) return;  // these products are not cut
     gate.choose(grouped);
     out.choose(grouped);
   }
@@ -813,12 +818,13 @@ struct Backward {
   }
 };
 
-// Maps of a K-major Q: boxes of 16, 32, 64, 128 rows.
-mao_status encode_q(FfnParams& p, const void* base, int64_t cols, int64_t rows, int64_t halves, int64_t ld,
-                    int64_t half_stride) {
+// Maps of a K-major Q.
+mao_status encode_q(FfnParams& p, const Plan& plan, bool grouped, const void* base, int64_t cols, int64_t rows,
+                    int64_t halves, int64_t ld, int64_t half_stride) {
   mao_status st = MAO_OK;
-  for (int b = 0; b < Q_BOXES && st == MAO_OK; ++b)
-    st = tc_encode_bf16_map(&p.map_q[b], base, cols, rows, halves, 1, ld, half_stride, rows * ld, 16 << b);
+  for (int b = grouped ? 0 : Q_BOXES - 1; b < Q_BOXES && st == MAO_OK; ++b)
+    st = tc_encode_bf16_map(&p.map_q[b], base, cols, rows, halves, 1, ld, half_stride, rows * ld,
+                            grouped ? 16 << b : plan.split.height / 2);
   return st;
 }
 
@@ -845,9 +851,41 @@ mao_status gated_ffn_launch(const mao_mat& X, const mao_mat& up, const mao_mat& 
   mao_status st = copies.launch(stream);
   if (st != MAO_OK) return st;
 
+  if (few_rows(s.R, runs.offsets != nullptr, runs.counts != nullptr)) {
+    FewParams q = {};
+    q.offsets = runs.offsets;
+    q.counts = runs.counts;
+    q.groups = runs.groups;
+    q.rows = int32_t(s.R);
+    q.I = int32_t(s.N);
+    q.depth = int32_t(s.K);
+    q.w = f.up.data;
+    q.ldw = f.up.ld;
+    q.x = f.x.data;
+    q.ldx = f.x.ld;
+    q.d = h;
+    q.ld = f.ldh;
+    q.dtype = MAO_BF16;
+    if (Z) {
+      q.z = static_cast<__nv_bfloat16*>(Z->data);
+      q.ldz = Z->ld;
+    }
+    st = few_launch(q, false, true, act, stream);
+    if (st != MAO_OK) return st;
+    q.I = int32_t(s.C);
+    q.depth = int32_t(s.N);
+    q.w = f.down.data;
+    q.ldw = f.down.ld;
+    q.x = h;
+    q.ldx = f.ldh;
+    q.d = Y.data;
+    q.ld = Y.ld;
+    q.dtype = Y.dtype;
+    return few_launch(q, false, false, act, stream);
+  }
   FfnParams p = {};
   st = tc_encode_bf16_map(&p.map_p, f.up.data, s.K, s.N, 2, runs.groups, f.up.ld, s.N * f.up.ld, 2 * s.N * f.up.ld, 16);
-  if (st == MAO_OK) st = encode_q(p, f.x.data, s.K, s.R, 1, f.x.ld, s.R * f.x.ld);
+  if (st == MAO_OK) st = encode_q(p, f.gate, runs.offsets != nullptr, f.x.data, s.K, s.R, 1, f.x.ld, s.R * f.x.ld);
   if (st != MAO_OK) return st;
   p.d = h;
   p.ld = f.ldh;
@@ -863,7 +901,7 @@ mao_status gated_ffn_launch(const mao_mat& X, const mao_mat& up, const mao_mat& 
 
   FfnParams q = {};
   st = tc_encode_bf16_map(&q.map_p, f.down.data, s.N, s.C, 1, runs.groups, f.down.ld, s.C * f.down.ld, s.C * f.down.ld, HALF);
-  if (st == MAO_OK) st = encode_q(q, h, s.N, s.R, 1, f.ldh, s.R * f.ldh);
+  if (st == MAO_OK) st = encode_q(q, f.out, runs.offsets != nullptr, h, s.N, s.R, 1, f.ldh, s.R * f.ldh);
   if (st != MAO_OK) return st;
   set_out(q, Y);
   return run(f.out, act, q, runs, s.R, at, stream);
@@ -906,7 +944,7 @@ mao_status gated_ffn_backward_launch(const mao_mat& dY, const mao_mat& X, const 
   {
     FfnParams p = {};
     st = tc_encode_bf16_map(&p.map_p, b.down.data, s.N, s.C, 1, runs.groups, b.down.ld, s.C * b.down.ld, s.C * b.down.ld, BK);
-    if (st == MAO_OK) st = encode_q(p, b.dy.data, s.C, s.R, 1, b.dy.ld, s.R * b.dy.ld);
+    if (st == MAO_OK) st = encode_q(p, b.back, runs.offsets != nullptr, b.dy.data, s.C, s.R, 1, b.dy.ld, s.R * b.dy.ld);
     if (st != MAO_OK) return st;
     p.d = h;
     p.ld = b.ldh;
@@ -924,7 +962,7 @@ mao_status gated_ffn_backward_launch(const mao_mat& dY, const mao_mat& X, const 
   if (dX) {
     FfnParams p = {};
     st = tc_encode_bf16_map(&p.map_p, b.up.data, s.K, s.N, 2, runs.groups, b.up.ld, s.N * b.up.ld, 2 * s.N * b.up.ld, BK);
-    if (st == MAO_OK) st = encode_q(p, dz, s.N, s.R, 2, 2 * b.ldh, b.ldh);
+    if (st == MAO_OK) st = encode_q(p, b.dx, runs.offsets != nullptr, dz, s.N, s.R, 2, 2 * b.ldh, b.ldh);
     if (st != MAO_OK) return st;
     set_out(p, *dX);
     st = run(b.dx, act, p, runs, s.R, at, stream);

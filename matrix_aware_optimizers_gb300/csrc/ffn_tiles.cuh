@@ -261,6 +261,7 @@ inline Cut choose_cut(int64_t tiles_i, int64_t J, int64_t nkb, double block, dou
       }
     }
   }
+  if (J < best.height) best.height = int(round_up(J, 32));
   return best;
 }
 

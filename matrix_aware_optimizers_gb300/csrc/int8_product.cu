@@ -28,6 +28,7 @@
 
 #include "common.cuh"
 #include "ffn.h"
+#include "ffn_few.h"
 #include "ffn_tiles.cuh"
 #include "internal.h"
 #include "ns_plan.h"
@@ -61,7 +62,7 @@ static_assert(B_COL + B_STAGES * B_COLS <= TMEM_COLS, "TMEM budget");
 
 struct Int8Params : TileParams {
   CUtensorMap map_p;
-  CUtensorMap map_q[Q_BOXES];  // boxes of 16, 32, 64, 128 rows
+  CUtensorMap map_q[Q_BOXES];  // boxes of 16, 32, 64, 128 rows; of one run the last, half a tile's height
   const float* sa;             // scales of A's rows, of B's (null: parts of a sum, not scaled)
   const float* sb;
   void* d;
@@ -261,7 +262,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     for (int tile = pair; ok && tile < total; tile += npairs) {
       decode<NT, TILE, BK>(p, lo, cnt, begin, tile, t);
       const int j = t.j0 + (t.n >> 1) * int(cta);
-      const int q_rows = t.n >> 1;  // a multiple of 16
+      const bool one_box = !p.offsets;
+      const int q_rows = one_box ? p.height >> 1 : t.n >> 1;  // a multiple of 16
       for (int kb = 0; kb < t.nkb; ++kb) {
         if (!wait_warp<false>(&aempty_bar[stage], phase ^ 1u, abort_flag, limit)) {
           ok = false;
@@ -270,8 +272,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint32_t fb = full0 + 8 * stage, dst = smem_u32(ast) + stage * A_BYTES;
         const int k = (t.kb0 + kb) * BK;
         if (elected) {
-          if (leader) mbar_expect_tx(smem_u32(&afull_bar[stage]), uint32_t(t.n) * BK * 2);
-          for (int box = Q_BOXES - 1, at = 0; box >= 0; --box)
+          if (leader) mbar_expect_tx(smem_u32(&afull_bar[stage]), 2 * uint32_t(q_rows) * BK * 2);
+          if (one_box) {
+            tma_load_4d_pair(dst, &p.map_q[Q_BOXES - 1], fb, k, j, 0, 0);
+            tma_load_4d_pair(dst + HALF_BYTES, &p.map_q[Q_BOXES - 1], fb, k + HK, j, 0, 0);
+          }
+          for (int box = Q_BOXES - 1, at = 0; box >= 0 && !one_box; --box)
             if (q_rows & (16 << box)) {
               tma_load_4d_pair(dst + at * (HK * 2), &p.map_q[box], fb, k, j + at, 0, 0);
               tma_load_4d_pair(dst + HALF_BYTES + at * (HK * 2), &p.map_q[box], fb, k + HK, j + at, 0, 0);
@@ -589,18 +595,38 @@ size_t half_bytes(const mao_int8& A) { return size_t(round_up(A.rows * half_ld(A
 }  // namespace
 
 size_t int8_product_workspace_size(const mao_int8& A, const mao_int8& B, bool grouped) {
-  if (A.rows == 0) return 0;
+  if (A.rows == 0 || few_rows(A.rows, grouped, false)) return 0;
   const Cut s = grouped ? Cut{TILE, 1, 0} : cut_of(A, B);
   return half_bytes(A) + (s.splits > 1 ? size_t(round_up(int64_t(s.splits) * A.rows * round_up(B.rows, 4) * 4, 256)) : 0);
 }
 mao_status int8_product_launch(const mao_int8& A, const mao_int8& B, const mao_mat& D, const Runs& runs,
                                void* workspace, cudaStream_t stream) {
   if (A.rows == 0) return MAO_OK;
+  if (few_rows(A.rows, runs.offsets != nullptr, runs.counts != nullptr)) {
+    FewParams q = {};
+    q.offsets = runs.offsets;
+    q.counts = runs.counts;
+    q.groups = runs.groups;
+    q.rows = int32_t(A.rows);
+    q.I = int32_t(B.rows);
+    q.depth = int32_t(A.cols);
+    q.w = B.codes;
+    q.ldw = B.ld;
+    q.x = A.codes;
+    q.ldx = A.ld;
+    q.sa = A.scales;
+    q.sb = B.scales;
+    q.d = D.data;
+    q.ld = D.ld;
+    q.dtype = D.dtype;
+    return few_launch(q, true, false, 0, stream);
+  }
   Int8Params p = {};
   mao_status st = tc_encode_code_map(&p.map_p, B.codes, B.cols, B.rows, B.ld, B.count, HALF);
-  for (int b = 0; b < Q_BOXES && st == MAO_OK; ++b)
+  const Cut cut = runs.offsets ? Cut{TILE, 1, 0} : cut_of(A, B);
+  for (int b = runs.offsets ? 0 : Q_BOXES - 1; b < Q_BOXES && st == MAO_OK; ++b)
     st = tc_encode_bf16_map(&p.map_q[b], workspace, A.cols, A.rows, 1, 1, half_ld(A), A.rows * half_ld(A),
-                            A.rows * half_ld(A), 16 << b);
+                            A.rows * half_ld(A), runs.offsets ? 16 << b : cut.height / 2);
   if (st != MAO_OK) return st;
   p.offsets = runs.offsets;
   p.counts = runs.offsets ? runs.counts : nullptr;
@@ -618,7 +644,6 @@ mao_status int8_product_launch(const mao_int8& A, const mao_int8& B, const mao_m
   p.ld = D.ld;
   p.dtype = D.dtype;
   p.paired = D.dtype == MAO_BF16 && D.cols % 2 == 0 && reinterpret_cast<uintptr_t>(D.data) % 4 == 0 && D.ld % 2 == 0;
-  const Cut cut = runs.offsets ? Cut{TILE, 1, 0} : cut_of(A, B);
   void* parts = static_cast<uint8_t*>(workspace) + half_bytes(A);
   p.height = cut.height;
   p.splits = cut.splits;
