@@ -1,15 +1,16 @@
 // The feed-forward products for few rows: Y = X W^T (W's rows are channels), the gated pair of them,
 // and the same of 8-bit integers. Reading W bounds them: each weight is read once, and nothing
 // may hold the reads up. A block per SM works on sixteen channels at a time, whose sums' length its
-// eight warps share, 128 bytes of each row at a time; every warp has a ring of its own in shared
+// eight warps share, 128 bytes of each row at a time (short sums: as many teams of four or two
+// warps, each with channels of its own); every warp has a ring of its own in shared
 // memory that its TMA loads keep full across the ends of sums (24 KB per warp: 192 KB under way
 // per SM), so no warp waits for another but where a sum ends.
 //
 // Up to sixteen rows of X meet the weights in mma.sync m16n8k16 with fp32 sums: with so few rows the
 // tensor cores' rate does not count, and the fragments come straight from the ring. Any order of the
 // products within a sum does, so a lane takes 32 bytes in a row of W's row and the same 32 of X's and
-// hands out four of their entries per product. 8-bit codes become fp16 on the way, exactly. The
-// warps' sums are added in their order.
+// hands out eight of them per product. 8-bit codes are multiplied as whole numbers (m16n8k32): slower
+// products than fp16's, but no conversion. The warps' sums are added in their order.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -42,39 +43,46 @@ struct FewKernelParams : FewParams {
   CUtensorMap map_w;
   CUtensorMap map_x;
   int32_t x_rows;  // rows of an X box
+  int32_t team;    // warps that share a unit: 8, 4 or 2
 };
 
-// A lane's 32 bytes of a row as words of two 16-bit entries.
-template <bool INT8>
+// A lane's 32 bytes of a row.
 struct Entries {
-  static constexpr int WORDS = INT8 ? 16 : 8;
-  uint32_t w[WORDS];
+  uint32_t w[8];
 };
-
-__device__ __forceinline__ void codes_to_half(uint32_t codes, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = codes ^ 0x80808080u;  // code + 128 into the low byte of 1024, less 1152
-  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
-  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
-  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
-  lo = *reinterpret_cast<const uint32_t*>(&x);
-  hi = *reinterpret_cast<const uint32_t*>(&y);
-}
 
 // Bytes 32 (lane % 4) .. + 31 of row r of a box (128-byte rows, swizzled).
-template <bool INT8>
-__device__ __forceinline__ Entries<INT8> entries(const uint8_t* box, int r, int lane) {
-  Entries<INT8> e;
+__device__ __forceinline__ Entries entries(const uint8_t* box, int r, int lane) {
   const int c = 2 * (lane & 3);
   const uint4 a = *reinterpret_cast<const uint4*>(box + r * 128 + 16 * (c ^ (r & 7)));
   const uint4 b = *reinterpret_cast<const uint4*>(box + r * 128 + 16 * ((c + 1) ^ (r & 7)));
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    if (INT8) codes_to_half(w[q], e.w[INT8 ? 2 * q : 0], e.w[INT8 ? 2 * q + 1 : 0]);
-    else e.w[q] = w[q];
-  }
-  return e;
+  return Entries{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+
+// The sums of a lane: fp32, or whole numbers.
+template <bool INT8>
+struct Sums {
+  using T = float;
+};
+template <>
+struct Sums<true> {
+  using T = int;
+};
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ void tma_load(bool codes, uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
@@ -109,7 +117,7 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
   }
 }
 
-// Unit number `unit`: sixteen channels for up to 8 NT rows of a run.
+// Unit number `unit`: sixteen channels for up to 8 NT rows of a run. The whole warp decodes.
 struct Unit {
   int run = 0;  // at or before the unit's (units come in rising order)
   int i0, n;
@@ -122,7 +130,16 @@ __device__ __forceinline__ void decode_unit(const FewParams& p, const int* lo, c
   int64_t first = 0;
   int rows = p.rows;
   if (p.offsets) {
-    while (begin[u.run + 1] * p.tiles_i <= unit) ++u.run;
+    // (by the whole warp: run after run took 7 us of a call with 128 runs)
+    while (true) {
+      const int g = u.run + 1 + (threadIdx.x & 31);
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, g >= p.groups || begin[g] * p.tiles_i > unit);
+      if (past) {
+        u.run += __ffs(past) - 1;
+        break;
+      }
+      u.run += 32;
+    }
     local = unit - begin[u.run] * p.tiles_i;
     count = begin[u.run + 1] - begin[u.run];
     first = lo[u.run];
@@ -137,6 +154,7 @@ __device__ __forceinline__ void decode_unit(const FewParams& p, const int* lo, c
 template <bool INT8, bool GATE, int ACT, int NT>
 __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__ FewKernelParams p) {
   constexpr int MATS = GATE ? 2 : 1;
+  constexpr int CHAINS = MATS * NT == 1 ? 2 : 1;  // sums in turn, so that products do not wait for one another
   constexpr int STAGE = MATS * BOX_BYTES + NT * 1024;  // a multiple of 1024
   constexpr int RING = ring_bytes(GATE, NT), STAGES = RING / STAGE;
   static_assert(RING % 1024 == 0 && STAGE % 1024 == 0, "swizzled boxes");
@@ -171,9 +189,11 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
   const int chunks = (p.depth * (INT8 ? 1 : 2) + 127) / 128;
   const int step = INT8 ? 128 : 64;  // entries of a chunk
 
-  // The warp's items: chunks warp, warp + 8, ... of each of the block's units. The next one to load:
+  // The warp's items: every team-th chunk of each of its team's units. The next one to load:
+  const int team = p.team, member = warp % team;
+  const int unit0 = int(blockIdx.x) * (WARPS / team) + warp / team, unit_step = int(gridDim.x) * (WARPS / team);
   Unit next;
-  int next_unit = blockIdx.x, next_chunk = warp, loaded = 0;
+  int next_unit = unit0, next_chunk = member, loaded = 0;
   if (next_chunk >= chunks) next_unit = units;  // no chunk of any sum is this warp's
   if (next_unit < units) decode_unit<NT>(p, lo, cnt, begin, next_unit, next);
   auto load_next = [&]() {
@@ -188,10 +208,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
       tma_load(INT8, dst + MATS * BOX_BYTES, &p.map_x, bar, k, int(next.j0), 0, 0);
     }
     ++loaded;
-    next_chunk += WARPS;
+    next_chunk += team;
     if (next_chunk >= chunks) {
-      next_chunk = warp;
-      next_unit += gridDim.x;
+      next_chunk = member;
+      next_unit += unit_step;
       if (next_unit < units) decode_unit<NT>(p, lo, cnt, begin, next_unit, next);
     }
   };
@@ -209,26 +229,26 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
   Unit u;
   int used = 0, flip = 0;
   bool ok = true;
-  for (int unit = blockIdx.x; unit < units; unit += gridDim.x, flip ^= 1) {
+  for (int unit = unit0; unit < units; unit += unit_step, flip ^= 1) {
     decode_unit<NT>(p, lo, cnt, begin, unit, u);
-    float acc[MATS][NT][4] = {};
-    for (int c = warp; c < chunks; c += WARPS) {
+    typename Sums<INT8>::T acc[CHAINS][MATS][NT][4] = {};
+    for (int c = member; c < chunks; c += team) {
       const int stage = used % STAGES;
       ok = ok && wait_warp<false>(&bars[warp][stage], uint32_t(used / STAGES) & 1u, abort_flag, p.timeout_ns);
       if (!ok) break;
       const uint8_t* box = ring + stage * STAGE;
       const int r = lane >> 2;
-      Entries<INT8> x[NT];
+      Entries x[NT];
 #pragma unroll
-      for (int q = 0; q < NT; ++q) x[q] = entries<INT8>(box + MATS * BOX_BYTES, r + 8 * q, lane);
+      for (int q = 0; q < NT; ++q) x[q] = entries(box + MATS * BOX_BYTES, r + 8 * q, lane);
 #pragma unroll
       for (int m = 0; m < MATS; ++m) {
-        const Entries<INT8> a = entries<INT8>(box + m * BOX_BYTES, r, lane);
-        const Entries<INT8> b = entries<INT8>(box + m * BOX_BYTES, r + 8, lane);
+        const Entries a = entries(box + m * BOX_BYTES, r, lane);
+        const Entries b = entries(box + m * BOX_BYTES, r + 8, lane);
 #pragma unroll
-        for (int s = 0; s < Entries<INT8>::WORDS; s += 2)
+        for (int s = 0; s < 8; s += 2)
 #pragma unroll
-          for (int q = 0; q < NT; ++q) mma<INT8>(acc[m][q], a.w[s], b.w[s], a.w[s + 1], b.w[s + 1], x[q].w[s], x[q].w[s + 1]);
+          for (int q = 0; q < NT; ++q) mma(acc[(s / 2) % CHAINS][m][q], a.w[s], b.w[s], a.w[s + 1], b.w[s + 1], x[q].w[s], x[q].w[s + 1]);
       }
       ++used;
       __syncwarp();  // every lane has read the stage
@@ -238,19 +258,27 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     for (int m = 0; m < MATS; ++m)
 #pragma unroll
       for (int q = 0; q < NT; ++q)
-        *reinterpret_cast<float4*>(parts[flip][warp][m][q][lane]) =
-            make_float4(acc[m][q][0], acc[m][q][1], acc[m][q][2], acc[m][q][3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          parts[flip][warp][m][q][lane][e] = float(CHAINS == 1 ? acc[0][m][q][e] : acc[0][m][q][e] + acc[CHAINS - 1][m][q][e]);
     // (the other half of `parts` was read before this barrier's last use but one)
-    __syncthreads();
-    // thread: row j0 + r of X, channel i0 + c
-    const int c = threadIdx.x % CHANNELS, r = threadIdx.x / CHANNELS, i = u.i0 + c;
-    if (r < u.n && i < p.I) {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / team), "r"(32 * team) : "memory");
+    // row j0 + r of X, channel i0 + c
+    for (int x = threadIdx.x % (32 * team); x < CHANNELS * u.n; x += 32 * team) {
+      const int c = x % CHANNELS, r = x / CHANNELS, i = u.i0 + c;
+      if (i >= p.I) continue;
       float v[MATS] = {};
       const int from = (c & 7) * 4 + ((r & 7) >> 1), e = (c >> 3) * 2 + (r & 1);
+      float part[WARPS][MATS];  // all on their way before the first is added
 #pragma unroll
-      for (int m = 0; m < MATS; ++m)
+      for (int w = 0; w < WARPS; ++w)
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) v[m] += parts[flip][w][m][NT == 1 ? 0 : r >> 3][from][e];
+        for (int m = 0; m < MATS; ++m)
+          part[w][m] = w < team ? parts[flip][warp - member + w][m][NT == 1 ? 0 : r >> 3][from][e] : 0.0f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w)
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) v[m] += part[w][m];
       const int64_t j = u.j0 + r;
       if (GATE) {
         static_cast<__nv_bfloat16*>(p.d)[j * p.ld + i] = __float2bfloat16_rn(activate<ACT>(v[0]) * v[MATS - 1]);
@@ -284,6 +312,9 @@ mao_status few_launch(const FewParams& params, bool int8, bool gate, int32_t act
   const int two = !p.offsets && p.rows > 8;
   p.height = two ? 16 : 8;
   p.x_rows = p.rows < p.height ? p.rows : p.height;
+  const int64_t chunks = ceil_div(int64_t(p.depth) * (int8 ? 1 : 2), 128);
+  const int64_t least = int8 ? 8 : 4;  // chunks of a warp (14336 x 4096 8-bit, one row: 15.1 us; with four 16.1)
+  p.team = chunks >= 8 * least ? 8 : chunks >= 4 * least ? 4 : 2;
   const int64_t mats = gate ? 2 : 1, w_rows = int64_t(p.I);
   mao_status st = int8 ? tc_encode_code_map(&p.map_w, p.w, p.depth, w_rows, p.ldw, p.groups, CHANNELS)
                        : tc_encode_bf16_map(&p.map_w, p.w, p.depth, w_rows, mats, p.groups, p.ldw, w_rows * p.ldw,
@@ -308,8 +339,9 @@ mao_status few_launch(const FewParams& params, bool int8, bool gate, int32_t act
   });
   if (st != MAO_OK) return st;
   g_launched.store(true, std::memory_order_release);
-  const int64_t units = p.offsets ? int64_t(num_sms()) : int64_t(p.tiles_i) * ceil_div(p.rows, p.height);
-  return launch_dependent(kernels[(int8 ? 0 : gate ? 4 + 2 * act : 2) + two], unsigned(units < num_sms() ? units : num_sms()),
+  const int64_t units = p.offsets ? int64_t(num_sms()) * WARPS : int64_t(p.tiles_i) * ceil_div(p.rows, p.height);
+  const int64_t blocks = ceil_div(units, WARPS / p.team);
+  return launch_dependent(kernels[(int8 ? 0 : gate ? 4 + 2 * act : 2) + two], unsigned(blocks < num_sms() ? blocks : num_sms()),
                           THREADS, size_t(1024 + WARPS * ring_bytes(gate, 1 + two)), stream, p);
 }
 
