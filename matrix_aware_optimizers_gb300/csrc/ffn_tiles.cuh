@@ -238,7 +238,7 @@ struct Cut {
 // 3 TB/s for the sum of the fp32 parts, which stay in L2. tiles_i: tiles of i (of all matrices).
 inline Cut choose_cut(int64_t tiles_i, int64_t J, int64_t nkb, double block, double least_block, double epilogue,
                       int64_t outputs, int64_t least_kb) {
-  const int64_t pairs = num_sms() / 2;
+  const int64_t pairs = num_sms() > 1 ? num_sms() / 2 : 1;  // (sizes are asked for without a GPU, too)
   Cut best{TILE, 1, int(nkb)};
   double least = 1e30;
   for (int h = TILE; h >= 32; h /= 2) {
