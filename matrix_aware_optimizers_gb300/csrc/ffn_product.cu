@@ -43,14 +43,14 @@ using namespace ffn;
 
 constexpr int BK = 64;                // depth per stage: rows of 128 bytes
 constexpr int OP_BYTES = HALF * BK * 2;
-constexpr int STAGE_BYTES = 2 * OP_BYTES;
+constexpr int RING_BYTES = 12 * OP_BYTES;  // six stages; more of them where few rows make Q's part small
 constexpr int CHUNK_BYTES = 64 * BK * 2;  // 64 values of i or j of an MN-major operand
-constexpr int STAGES = 6;
+constexpr int MAX_STAGES = 11;
 constexpr int EPI_WARPS = 16;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 512;
 constexpr int Q_BOXES = 4;            // heights of boxes of a K-major Q: 16 << b rows
-constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + TABLE_BYTES + 512;
+constexpr size_t SMEM = 1024 + RING_BYTES + TABLE_BYTES + 512;
 static_assert(SMEM <= 232448, "shared memory budget of one CTA");
 
 enum Epilogue { PLAIN, GATE, GATE_BACK };
@@ -68,6 +68,7 @@ struct FfnParams : TileParams {
   int32_t dtype;
   int32_t paired, paired_z;  // entries 2 i, 2 i + 1 of a row are one 4-byte word (D; Z)
   int32_t part_half;           // GATE: columns from G's parts to U's
+  int32_t stages, stage_bytes; // of the ring
 };
 
 // Instruction descriptor of kind::f16: bf16 operands, fp32 sums, M = 256.
@@ -270,13 +271,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  int* lo = reinterpret_cast<int*>(ring + STAGES * STAGE_BYTES);
+  int* lo = reinterpret_cast<int*>(ring + RING_BYTES);
   int* cnt = lo + MAX_GROUPS + 2;
   int* begin = cnt + MAX_GROUPS + 2;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + STAGES * STAGE_BYTES + TABLE_BYTES);
-  uint64_t* full_bar = bars;                  // [STAGES]  (used in the even CTA)
-  uint64_t* empty_bar = full_bar + STAGES;    // [STAGES]
-  uint64_t* tfull_bar = empty_bar + STAGES;   // [2]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + RING_BYTES + TABLE_BYTES);
+  uint64_t* full_bar = bars;                  // [stages]  (used in the even CTA)
+  uint64_t* empty_bar = full_bar + MAX_STAGES;  // [stages]
+  uint64_t* tfull_bar = empty_bar + MAX_STAGES; // [2]
   uint64_t* tempty_bar = tfull_bar + 2;       // [2]       (even CTA)
   uint64_t* drain_bar = tempty_bar + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
@@ -289,11 +290,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int pair = blockIdx.x >> 1;
   const int npairs = gridDim.x >> 1;
   const uint64_t limit = p.timeout_ns;
+  const int stages = p.stages, stage_bytes = p.stage_bytes;
   constexpr int p_mn = FORM != NT, q_mn = FORM == TN;
   constexpr int STEP_I = EPI == GATE ? HALF : TILE;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(smem_u32(&full_bar[s]), 1);
       mbar_init(smem_u32(&empty_bar[s]), 1);
     }
@@ -319,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   // launched as a programmatic dependent: the set-up so far may overlap the previous kernel
   wait_for_previous();
-  make_table<THREADS>(p, lo, cnt, begin, reinterpret_cast<int*>(bars + 24));
+  make_table<THREADS>(p, lo, cnt, begin, reinterpret_cast<int*>(bars + 40));
   tc_fence_before();
   __syncthreads();
   const int total = FORM == TN ? (p.J + p.height - 1) / p.height * p.tiles_i * p.groups * p.halves * p.splits
@@ -355,7 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           ok = false;
           break;
         }
-        const uint32_t fb = full0 + 8 * stage, dst = ring0 + stage * STAGE_BYTES;
+        const uint32_t fb = full0 + 8 * stage, dst = ring0 + stage * stage_bytes;
         const int b = t.kb0 + kb;
         const int second = FORM == NN && b >= half_kb;  // half of the depth
         const int k = t.k0 + (second ? b - half_kb : b) * BK;
@@ -386,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         armed |= 1u << stage;
         armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-        if (++stage == STAGES) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -394,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     // after an abort, the loads already issued land before the CTA leaves
     if (*abort_flag && leader && lane == 0) {
-      for (int s = 0; s < STAGES; ++s)
+      for (int s = 0; s < stages; ++s)
         if ((armed >> s) & 1u) mbar_drain(smem_u32(&full_bar[s]), (armed_phase >> s) & 1u, 20000000ull);
     }
     __syncwarp();
@@ -430,8 +432,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             break;
           }
           const uint32_t empty = smem_u32(&empty_bar[stage]);
-          const uint64_t at = uint64_t(stage * (STAGE_BYTES >> 4));
-          if (++stage == STAGES) {
+          const uint64_t at = uint64_t(stage * (stage_bytes >> 4));
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -736,6 +738,9 @@ mao_status run(const Plan& plan, int32_t act, FfnParams& p, const Runs& runs, in
       ffn_sum_kernel<GATE_BACK, MAO_SILU>, ffn_sum_kernel<GATE_BACK, MAO_GELU>, ffn_sum_kernel<GATE_BACK, MAO_GELU_TANH>};
   const int k = plan.epi == GATE ? 3 + act : plan.epi == GATE_BACK ? 6 + act : plan.form;
   const int ks = plan.epi == GATE ? 1 + act : plan.epi == GATE_BACK ? 4 + act : 0;
+  const bool small_q = !runs.offsets && !tn;
+  p.stage_bytes = OP_BYTES + (small_q ? int32_t(round_up(p.height / 2 * BK * 2, 1024)) : OP_BYTES);
+  p.stages = RING_BYTES / p.stage_bytes < MAX_STAGES ? RING_BYTES / p.stage_bytes : MAX_STAGES;
   static std::atomic<bool> ready[64];
   mao_status st = once_per_device(ready, [&] {
     cudaError_t err = cudaSuccess;
