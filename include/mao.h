@@ -585,7 +585,8 @@ mao_status expert_combine_backward(const mao_mat* dY, const mao_mat* Z, const in
  * A gated feed-forward block y = (act(x Wg^T) * (x Wu^T)) Wd^T, trained and served in bf16, or
  * served in 8-bit integers; dense, or as the networks of an expert layer over the runs of rows
  * that expert_plan lays out. As the calls above they take zero rows, read no argument after they
- * return and keep nothing between calls.
+ * return and keep nothing between calls. Outputs and workspaces overlap neither one another nor
+ * the inputs.
  *
  *   Y, Z <- gated_ffn(X, up, down)                   a training step (without Z: serving)
  *   dX, dup, ddown <- gated_ffn_backward(dY, X, up, down, Z)
@@ -613,9 +614,11 @@ enum { MAO_SILU = 0, MAO_GELU = 1, MAO_GELU_TANH = 2 };
  *   X         bf16, R x K (R >= 0).
  *   up        bf16, (groups * 2 N) x K: for each group the N rows of Wg, then those of Wu.
  *   down      bf16, (groups * C) x N.
- *   Z         NULL, or bf16, R x 2 N: G and U, which gated_ffn_backward takes.
+ *   Z         NULL, or f32 or bf16, R x 2 N: G and U, which gated_ffn_backward takes. In f32 the
+ *             gradients are as near as their own rounding and that of the operands let them be; in
+ *             bf16 it takes half the memory, and G and U are rounded once more.
  *   Y         f32 or bf16, R x C.
- * Sums are in fp32; G and U are rounded to bf16 in Z only, H once, to the bf16 operand of the
+ * Sums are in fp32; G and U are rounded in Z only, H once, to the bf16 operand of the
  * second product. An infinite G gives what the formulas give (NaN at -inf).
  * The first kernel computes both projections, the activation and the product; few rows are
  * split over the sums' length, the parts added in a fixed order. Results are the same each time.
@@ -631,7 +634,7 @@ size_t gated_ffn_workspace_bytes(const mao_mat* X, const mao_mat* up, const mao_
                                  int32_t groups, int32_t grouped);
 
 /*
- * Its gradients, from dY (bf16, R x C), the call's X, up, down and the Z that it gave:
+ * Its gradients, from dY (bf16, R x C), the call's X, up, down and the Z (f32 or bf16) that it gave:
  *   dH = dY Wd, dG = dH * U * act'(G), dU = dH * act(G), H = act(G) * U
  *   dX = dG Wg + dU Wu (R x K); dup = [dG^T X; dU^T X] and ddown = dY^T H, shaped as up and down.
  * dG, dU and H are rounded to bf16 once, as operands of the products after them; sums are in

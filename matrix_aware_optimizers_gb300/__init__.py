@@ -881,7 +881,8 @@ def _ws(ws, nbytes, like, stream):
 def gated_ffn(X, up, down, act="silu", offsets=None, counts=None, save=False, out=None,
               out_dtype=torch.bfloat16, Z=None, ws=None, stream=None):
     """Y = (act(X Wg^T) * (X Wu^T)) Wd^T, sums in fp32; with save (or a tensor Z to fill), (Y, Z): Z
-    holds the rows of [X Wg^T, X Wu^T], which gated_ffn_backward takes.
+    holds the rows of [X Wg^T, X Wu^T], which gated_ffn_backward takes, in float32, or with
+    save=torch.bfloat16 in half the memory (the gradients then carry its rounding too).
 
     X: bfloat16 [T, K]. up: bfloat16 [2 N, K], the N rows of Wg, then those of Wu. down:
     bfloat16 [C, N]. act: "silu", "gelu" or "gelu_tanh". offsets: int32 tensor of groups + 1
@@ -905,8 +906,11 @@ def gated_ffn(X, up, down, act="silu", offsets=None, counts=None, save=False, ou
     if Z is not None:
         z = _desc(Z)
     elif save:
-        Z, zp = _out(None, (x.rows, 2 * N), torch.bfloat16, "", X, stream)
-        z = _abi.MaoMat(zp, x.rows, 2 * N, 2 * N, _abi.MAO_BF16, 0)
+        saved = torch.float32 if save is True else save
+        if saved not in _FLOATS:
+            raise ValueError("save must be True, False, float32 or bfloat16")
+        Z, zp = _out(None, (x.rows, 2 * N), saved, "", X, stream)
+        z = _abi.MaoMat(zp, x.rows, 2 * N, 2 * N, _FLOATS[saved], 0)
     refs = ctypes.byref(x), ctypes.byref(u), ctypes.byref(d)
     need = 0 if ws is not None else \
         lib().gated_ffn_workspace_bytes(*refs, groups, off is not None)
@@ -932,8 +936,8 @@ def gated_ffn_backward(dY, X, up, down, Z, act="silu", offsets=None, counts=None
     kind = _act(act)
     off, cnt, groups = _runs(offsets, counts)
     x, u, d, K, N, C = _block(X, up, down, groups)
-    if dY.dtype != torch.bfloat16 or Z.dtype != torch.bfloat16:
-        raise ValueError("dY and Z must be bfloat16")
+    if dY.dtype != torch.bfloat16:
+        raise ValueError("dY must be bfloat16")
     dy, z = _desc(dY), _desc(Z)
     if grad_dtype not in _FLOATS:
         raise ValueError("grad_dtype must be float32 or bfloat16")

@@ -74,7 +74,7 @@ mao_status gated_ffn(const mao_mat* X, const mao_mat* up, const mao_mat* down, i
   mao_status st = check_runs(offsets, counts, groups);
   if (st == MAO_OK) st = check_act(act);
   if (st == MAO_OK) st = check_block(X, up, down, groups);
-  if (st == MAO_OK && Z) st = check_rows(Z, true);
+  if (st == MAO_OK && Z) st = check_rows(Z, false);
   if (st == MAO_OK) st = check_rows(Y, false);
   if (st != MAO_OK) return st;
   if (!shaped(Y, X->rows, down->rows / groups) || (Z && !shaped(Z, X->rows, 2 * down->cols)))
@@ -101,7 +101,7 @@ mao_status gated_ffn_backward(const mao_mat* dY, const mao_mat* X, const mao_mat
   if (st == MAO_OK) st = check_act(act);
   if (st == MAO_OK) st = check_block(X, up, down, groups);
   if (st == MAO_OK) st = check_rows(dY, true);
-  if (st == MAO_OK) st = check_rows(Z, true);
+  if (st == MAO_OK) st = check_rows(Z, false);
   for (const mao_mat* D : {dX, dup, ddown})
     if (st == MAO_OK && D) st = check_rows(D, false);
   if (st != MAO_OK) return st;

@@ -45,4 +45,48 @@ __device__ __forceinline__ void activate(float x, float& a, float& slope) {
   }
 }
 
+// Two values at a time: the packed fp32 instructions halve the arithmetic of an epilogue.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split_pair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// act(x) and its slope, of two values.
+template <int ACT>
+__device__ __forceinline__ void activate2(uint64_t x, uint64_t& a, uint64_t& slope) {
+  float x0, x1;
+  if (ACT == MAO_SILU) {
+    const uint64_t t = mul2(x, pair_of(-1.4426950408889634f, -1.4426950408889634f));
+    float e0, e1, s0, s1;
+    split_pair(t, x0, x1);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(x0));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(x1));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(1.0f + e0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(1.0f + e1));
+    const uint64_t s = pair_of(s0, s1);
+    a = mul2(x, s);
+    slope = fma2(a, fma2(s, pair_of(-1.0f, -1.0f), pair_of(1.0f, 1.0f)), s);
+  } else {
+    float a0, a1, s0, s1;
+    split_pair(x, x0, x1);
+    activate<ACT>(x0, a0, s0);
+    activate<ACT>(x1, a1, s1);
+    a = pair_of(a0, a1);
+    slope = pair_of(s0, s1);
+  }
+}
+
 }  // namespace mao

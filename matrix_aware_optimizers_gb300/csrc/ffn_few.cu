@@ -219,10 +219,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 
   if (p.offsets) {  // rows that hold no tokens, while the first loads are under way
     const int turn = int(blockIdx.x) * WARPS + warp, turns = int(gridDim.x) * WARPS;
-    const int es = p.dtype == MAO_F32 ? 4 : 2;
+    const int es = p.dtype == MAO_F32 ? 4 : 2, ez = p.z_dtype == MAO_F32 ? 4 : 2;
     for_unused_rows(p, lo, cnt, turn, turns, [&](int64_t j0, int64_t j1, int64_t every) {
       if (!GATE) clear_rows(p.d, p.ld * es, int64_t(p.I) * es, j0, j1, every, lane);
-      else if (p.z) clear_rows(p.z, p.ldz * 2, int64_t(p.I) * 4, j0, j1, every, lane);
+      else if (p.z) clear_rows(p.z, p.ldz * ez, int64_t(p.I) * 2 * ez, j0, j1, every, lane);
     });
   }
 
@@ -283,8 +283,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
       if (GATE) {
         static_cast<__nv_bfloat16*>(p.d)[j * p.ld + i] = __float2bfloat16_rn(activate<ACT>(v[0]) * v[MATS - 1]);
         if (p.z) {
-          p.z[j * p.ldz + i] = __float2bfloat16_rn(v[0]);
-          p.z[j * p.ldz + p.I + i] = __float2bfloat16_rn(v[MATS - 1]);
+          store_elem(p.z, j * p.ldz + i, p.z_dtype, v[0]);
+          store_elem(p.z, j * p.ldz + p.I + i, p.z_dtype, v[MATS - 1]);
         }
       } else {
         if (INT8) v[0] = v[0] * __ldg(p.sa + j) * __ldg(p.sb + int64_t(u.run) * p.I + i);

@@ -1,8 +1,6 @@
 // Launcher of the feed-forward products for few rows.
 #pragma once
 
-#include <cuda_bf16.h>
-
 #include "ffn_tiles.cuh"
 
 namespace mao {
@@ -13,9 +11,9 @@ struct FewParams : ffn::TileParams {  // rows, I, depth, offsets, counts, groups
   const float* sa;  // 8-bit integers: scales of X's rows and of W's
   const float* sb;
   void* d;          // H (gated), D
-  __nv_bfloat16* z; // gated: G and U, or null
+  void* z;          // gated: G and U, fp32 or bf16, or null
   int64_t ldw, ldx, ld, ldz;  // in entries
-  int32_t dtype;
+  int32_t dtype, z_dtype;
 };
 mao_status few_launch(const FewParams& params, bool int8, bool gate, int32_t act, cudaStream_t stream);
 

@@ -61,12 +61,13 @@ struct FfnParams : TileParams {
   // TN (64 x 64)
   CUtensorMap map_q[Q_BOXES];
   void* d;                     // PLAIN: D; GATE, GATE_BACK: H
-  __nv_bfloat16* z;            // G and U: GATE writes them (null: not wanted), GATE_BACK reads them
+  void* z;                     // G and U, fp32 or bf16: GATE writes them (null: not wanted), GATE_BACK reads them
   __nv_bfloat16* dz;           // GATE_BACK: dG and dU
   int64_t ld, ldz, lddz;
   int32_t dz_half;             // columns from dG to dU
   int32_t dtype;
-  int32_t paired, paired_z;  // entries 2 i, 2 i + 1 of a row are one 4-byte word (D; Z)
+  int32_t z_dtype;
+  int32_t paired, paired_z;  // entries 2 i, 2 i + 1 of a row are one word (D: of bf16; Z: of its type)
   int32_t part_half;           // GATE: columns from G's parts to U's
   int32_t stages, stage_bytes; // of the ring
 };
@@ -96,6 +97,12 @@ __device__ __forceinline__ void mma_block(uint32_t elected, uint32_t d, uint64_t
 }
 
 // ------------------------------------------------------------------ output
+
+__device__ __forceinline__ uint32_t pack2(uint64_t p) {
+  float a, b;
+  split_pair(p, a, b);
+  return pack(a, b);
+}
 
 // Sixteen rows of D (from row j on, those below j_end) at column i of this lane.
 __device__ __forceinline__ void store16(const FfnParams& p, const Tile& t, int j, int i,
@@ -150,7 +157,7 @@ __device__ __forceinline__ void gate16(const FfnParams& p, const Tile& t, int j,
   const int64_t row = j + 2 * up + odd;
   // H's rows are padded to whole words
   __nv_bfloat16* h = static_cast<__nv_bfloat16*>(p.d) + row * p.ld + col;
-  __nv_bfloat16* z = p.z + row * p.ldz + col;
+  __nv_bfloat16* z = static_cast<__nv_bfloat16*>(p.z) + row * p.ldz + col;
 #pragma unroll
   for (int c = 0; c < 16; c += 4) {
     const float s0 = up ? v[c] : v[c + 2], s1 = up ? v[c + 1] : v[c + 3];
@@ -161,7 +168,18 @@ __device__ __forceinline__ void gate16(const FfnParams& p, const Tile& t, int j,
     const bool ok = in && c < left;
     if (ok) store_word(h, wh);
     h += 4 * p.ld;
-    if (p.z) {
+    if (p.z && p.z_dtype == MAO_F32) {  // this lane's channel of its two rows
+      float* zf = static_cast<float*>(p.z) + int64_t(j + c + 2 * up) * p.ldz + i;
+      const int rows = t.j_end - (j + c + 2 * up);
+      if (i < p.I && rows > 0) {
+        zf[0] = g0;
+        zf[p.I] = u0;
+      }
+      if (i < p.I && rows > 1) {
+        zf[p.ldz] = g1;
+        zf[p.ldz + p.I] = u1;
+      }
+    } else if (p.z) {
       const uint32_t wg = swap_pair(g0, g1, odd), wu = swap_pair(u0, u1, odd);
       if (p.paired_z) {
         if (ok) {
@@ -182,50 +200,70 @@ __device__ __forceinline__ void gate16(const FfnParams& p, const Tile& t, int j,
   }
 }
 
-// GATE_BACK: G and U of the sixteen rows at column i, two columns of every second row if paired
-// (even lanes of rows j, j + 2, ..., odd lanes of the others).
-struct Saved {
+// GATE_BACK: G and U of sixteen rows at column i and its neighbour: even lanes have those of rows j,
+// j + 2, ..., odd lanes of the others.
+template <bool F32>
+struct Saved;
+template <>
+struct Saved<false> {
   uint32_t g[8], u[8];
-};
-__device__ __forceinline__ void load_saved(const FfnParams& p, const Tile& t, int j, int i, int lane,
-                                           Saved& s) {
-  const int odd = lane & 1;
-  if (p.paired_z) {
-    const __nv_bfloat16* z = p.z + int64_t(j + odd) * p.ldz + i - odd;
+  __device__ __forceinline__ void load(const FfnParams& p, const Tile& t, int j, int i, int lane) {
+    const int odd = lane & 1, col = i - odd;
+    const uint16_t* z = static_cast<const uint16_t*>(p.z) + int64_t(j + odd) * p.ldz + col;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const bool ok = i < p.I && j + 2 * c + odd < t.j_end;
-      s.g[c] = ok ? __ldg(reinterpret_cast<const uint32_t*>(z)) : 0u;
-      s.u[c] = ok ? __ldg(reinterpret_cast<const uint32_t*>(z + p.I)) : 0u;
+      const bool a = col < p.I && j + 2 * c + odd < t.j_end, b = a && col + 1 < p.I;
+      if (p.paired_z) {
+        g[c] = a ? __ldg(reinterpret_cast<const uint32_t*>(z)) : 0u;
+        u[c] = a ? __ldg(reinterpret_cast<const uint32_t*>(z + p.I)) : 0u;
+      } else {
+        g[c] = (a ? uint32_t(z[0]) : 0u) | (b ? uint32_t(z[1]) << 16 : 0u);
+        u[c] = (a ? uint32_t(z[p.I]) : 0u) | (b ? uint32_t(z[p.I + 1]) << 16 : 0u);
+      }
       z += 2 * p.ldz;
     }
-    return;
   }
-  // entry by entry: the two columns of this lane's rows
-  const int col = i - odd;
+  static __device__ __forceinline__ uint64_t wide(uint32_t w) { return pair_of(low_half(w), high_half(w)); }
+  __device__ __forceinline__ uint64_t gate(int c) const { return wide(g[c]); }
+  __device__ __forceinline__ uint64_t linear(int c) const { return wide(u[c]); }
+};
+template <>
+struct Saved<true> {
+  uint64_t g[8], u[8];
+  __device__ __forceinline__ void load(const FfnParams& p, const Tile& t, int j, int i, int lane) {
+    const int odd = lane & 1, col = i - odd;
+    const float* z = static_cast<const float*>(p.z) + int64_t(j + odd) * p.ldz + col;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const int row = j + 2 * c + odd;
-    const uint16_t* z = reinterpret_cast<const uint16_t*>(p.z) + int64_t(row) * p.ldz + col;
-    const bool a = col < p.I && row < t.j_end, b = col + 1 < p.I && row < t.j_end;
-    s.g[c] = (a ? uint32_t(z[0]) : 0u) | (b ? uint32_t(z[1]) << 16 : 0u);
-    s.u[c] = (a ? uint32_t(z[p.I]) : 0u) | (b ? uint32_t(z[p.I + 1]) << 16 : 0u);
+    for (int c = 0; c < 8; ++c) {
+      const bool a = col < p.I && j + 2 * c + odd < t.j_end, b = a && col + 1 < p.I;
+      if (p.paired_z) {
+        g[c] = a ? __ldg(reinterpret_cast<const unsigned long long*>(z)) : 0ull;
+        u[c] = a ? __ldg(reinterpret_cast<const unsigned long long*>(z + p.I)) : 0ull;
+      } else {
+        g[c] = pair_of(a ? z[0] : 0.0f, b ? z[1] : 0.0f);
+        u[c] = pair_of(a ? z[p.I] : 0.0f, b ? z[p.I + 1] : 0.0f);
+      }
+      z += 2 * p.ldz;
+    }
   }
-}
+  __device__ __forceinline__ uint64_t gate(int c) const { return g[c]; }
+  __device__ __forceinline__ uint64_t linear(int c) const { return u[c]; }
+};
 
 // Asks L2 for a tile's G and U (this CTA's columns), two threads per row.
 __device__ __forceinline__ void prefetch_saved(const FfnParams& p, const Tile& t, int cta, int thread) {
   const int i = t.i0 + HALF * cta, row = t.j0 + (thread >> 1);
   if (row >= t.j_end) return;
-  const __nv_bfloat16* z = p.z + int64_t(row) * p.ldz + (thread & 1 ? p.I : 0);
-  if (i < p.I) prefetch_l2(z + i);
-  if (i + 64 < p.I) prefetch_l2(z + i + 64);
+  const int es = p.z_dtype == MAO_F32 ? 4 : 2;
+  const uint8_t* z = static_cast<const uint8_t*>(p.z) + (int64_t(row) * p.ldz + (thread & 1 ? p.I : 0) + i) * es;
+  const int bytes = min(HALF, p.I - i) * es;
+  for (int b = 0; b < bytes; b += 128) prefetch_l2(z + b);
 }
 
 // dG, dU and H of sixteen rows of dH. The buffers' rows are padded to whole words.
-template <int ACT>
+template <int ACT, bool F32>
 __device__ __forceinline__ void gate_back16(const FfnParams& p, const Tile& t, int j, int i,
-                                            const float (&v)[16], const Saved& s, int lane) {
+                                            const float (&v)[16], const Saved<F32>& s, int lane) {
   const int odd = lane & 1, col = i - odd;
   const int left = col < p.I ? t.j_end - j - odd : 0;  // rows from this lane's first on
   const int64_t row = j + odd;
@@ -235,15 +273,13 @@ __device__ __forceinline__ void gate_back16(const FfnParams& p, const Tile& t, i
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     const float o = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[2 * c] : v[2 * c + 1], 1);
-    const float d0 = odd ? o : v[2 * c], d1 = odd ? v[2 * c + 1] : o;
-    float a0, a1, s0, s1;
-    activate<ACT>(low_half(s.g[c]), a0, s0);
-    activate<ACT>(high_half(s.g[c]), a1, s1);
-    const float u0 = low_half(s.u[c]), u1 = high_half(s.u[c]);
+    const uint64_t d = odd ? pair_of(o, v[2 * c + 1]) : pair_of(v[2 * c], o), u = s.linear(c);
+    uint64_t a, slope;
+    activate2<ACT>(s.gate(c), a, slope);
     if (2 * c < left) {
-      store_word(dg, pack(d0 * u0 * s0, d1 * u1 * s1));
-      store_word(du, pack(d0 * a0, d1 * a1));
-      store_word(h, pack(a0 * u0, a1 * u1));
+      store_word(dg, pack2(mul2(mul2(d, u), slope)));
+      store_word(du, pack2(mul2(d, a)));
+      store_word(h, pack2(mul2(a, u)));
     }
     dg += 2 * p.lddz;
     du += 2 * p.lddz;
@@ -256,7 +292,8 @@ template <int EPI>
 __device__ __forceinline__ void clear_unused(const FfnParams& p, int64_t j0, int64_t j1, int64_t step, int lane) {
   const int es = p.dtype == MAO_F32 ? 4 : 2;
   if (EPI != GATE) clear_rows(p.d, p.ld * es, int64_t(p.I) * es, j0, j1, step, lane);
-  if (EPI == GATE && p.z) clear_rows(p.z, p.ldz * 2, int64_t(p.I) * 4, j0, j1, step, lane);
+  const int ez = p.z_dtype == MAO_F32 ? 4 : 2;
+  if (EPI == GATE && p.z) clear_rows(p.z, p.ldz * ez, int64_t(p.I) * 2 * ez, j0, j1, step, lane);
   if (EPI == GATE_BACK) {
     clear_rows(p.dz, p.lddz * 2, int64_t(p.I) * 2, j0, j1, step, lane);
     clear_rows(p.dz + p.dz_half, p.lddz * 2, int64_t(p.I) * 2, j0, j1, step, lane);
@@ -265,7 +302,7 @@ __device__ __forceinline__ void clear_unused(const FfnParams& p, int64_t j0, int
 
 // ------------------------------------------------------------------ the kernel
 
-template <int FORM, int EPI, int ACT>
+template <int FORM, int EPI, int ACT, bool ZF32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     ffn_kernel(const __grid_constant__ FfnParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -489,24 +526,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int acc = local & 1;
       const int n = t.j_end - t.j0;
       // this warp's 64 columns in four steps, every fourth sixteen
-      Saved z, next;
-      if (saved) load_saved(p, t, t.j0 + 16 * part, i, lane, z);
       // every lane waits; the warp goes on only if all of them saw the accumulator
       if (!wait_warp<false>(&tfull_bar[acc], uint32_t(local >> 1) & 1u, abort_flag, limit)) break;
       tc_fence_after();
       const uint32_t trow = tmem_base + (uint32_t(32 * quad) << 16) + uint32_t(acc * TILE);
 #pragma unroll 1
       for (int c = 16 * part; c < n; c += 64) {
+        Saved<ZF32> z;
         float v[16];
+        if (saved) z.load(p, t, t.j0 + c, i, lane);
         tmem_ld16(trow + uint32_t(c), v);
-        // the next step's G and U are on their way while this one is worked on
-        if (saved && c + 64 < n) load_saved(p, t, t.j0 + c + 64, i, lane, next);
         tmem_wait(v);
         if (EPI == GATE && p.splits > 1) store16_gate_parts(p, t, t.j0 + c, i, v, lane);
         else if (EPI == GATE) gate16<ACT>(p, t, t.j0 + c, i, v, lane);
-        else if (saved) gate_back16<ACT>(p, t, t.j0 + c, i, v, z, lane);
+        else if (saved) gate_back16<ACT, ZF32>(p, t, t.j0 + c, i, v, z, lane);
         else store16(p, t, t.j0 + c, i, v, lane);
-        if (saved) z = next;
       }
       tc_fence_before();
       __syncwarp();
@@ -588,16 +622,20 @@ __global__ void __launch_bounds__(256) ffn_sum_kernel(const __grid_constant__ Su
       for (int c = 0; c < 4; ++c) h[c] = activate<ACT>(v[c]) * u[c];
       store4(static_cast<__nv_bfloat16*>(q.d) + j * q.ld, i, q.I, q.paired, h);
       if (q.z) {
-        store4(q.z + j * q.ldz, i, q.I, q.paired_z, v);
-        store4(q.z + j * q.ldz + q.I, i, q.I, q.paired_z, u);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (i + c < q.I) {
+            store_elem(q.z, j * q.ldz + i + c, q.z_dtype, v[c]);
+            store_elem(q.z, j * q.ldz + q.I + i + c, q.z_dtype, u[c]);
+          }
       }
     } else {
       float h[4], dg[4], du[4];
-      const __nv_bfloat16* z = q.z + j * q.ldz + i;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const bool in = i + c < q.I;
-        const float g = in ? __bfloat162float(z[c]) : 0.0f, u = in ? __bfloat162float(z[q.I + c]) : 0.0f;
+        const float g = in ? load_elem(q.z, j * q.ldz + i + c, q.z_dtype) : 0.0f;
+        const float u = in ? load_elem(q.z, j * q.ldz + q.I + i + c, q.z_dtype) : 0.0f;
         float a, slope;
         activate<ACT>(g, a, slope);
         h[c] = a * u;
@@ -727,16 +765,21 @@ mao_status run(const Plan& plan, int32_t act, FfnParams& p, const Runs& runs, in
   const int64_t tiles = (tn ? ceil_div(plan.J, p.height) * runs.groups * plan.halves
                             : ceil_div(rows, p.height) + (runs.offsets ? runs.groups : 0)) * plan.tiles_i();
   if (tiles * p.splits > 0x7FFF0000) return MAO_ERR_UNSUPPORTED;
-  // the plain products, then those of each activation
-  static const Kernel kernels[9] = {
-      ffn_kernel<NT, PLAIN, 0>, ffn_kernel<NN, PLAIN, 0>, ffn_kernel<TN, PLAIN, 0>,
-      ffn_kernel<NT, GATE, MAO_SILU>, ffn_kernel<NT, GATE, MAO_GELU>, ffn_kernel<NT, GATE, MAO_GELU_TANH>,
-      ffn_kernel<NN, GATE_BACK, MAO_SILU>, ffn_kernel<NN, GATE_BACK, MAO_GELU>, ffn_kernel<NN, GATE_BACK, MAO_GELU_TANH>};
+  // the plain products, then those of each activation (GATE_BACK: from a bf16, then a fp32 Z)
+  static const Kernel kernels[12] = {
+      ffn_kernel<NT, PLAIN, 0, false>, ffn_kernel<NN, PLAIN, 0, false>, ffn_kernel<TN, PLAIN, 0, false>,
+      ffn_kernel<NT, GATE, MAO_SILU, false>, ffn_kernel<NT, GATE, MAO_GELU, false>,
+      ffn_kernel<NT, GATE, MAO_GELU_TANH, false>,
+      ffn_kernel<NN, GATE_BACK, MAO_SILU, false>, ffn_kernel<NN, GATE_BACK, MAO_SILU, true>,
+      ffn_kernel<NN, GATE_BACK, MAO_GELU, false>, ffn_kernel<NN, GATE_BACK, MAO_GELU, true>,
+      ffn_kernel<NN, GATE_BACK, MAO_GELU_TANH, false>, ffn_kernel<NN, GATE_BACK, MAO_GELU_TANH, true>};
   static const SumKernel sums[7] = {
       ffn_sum_kernel<PLAIN, 0>,
       ffn_sum_kernel<GATE, MAO_SILU>, ffn_sum_kernel<GATE, MAO_GELU>, ffn_sum_kernel<GATE, MAO_GELU_TANH>,
       ffn_sum_kernel<GATE_BACK, MAO_SILU>, ffn_sum_kernel<GATE_BACK, MAO_GELU>, ffn_sum_kernel<GATE_BACK, MAO_GELU_TANH>};
-  const int k = plan.epi == GATE ? 3 + act : plan.epi == GATE_BACK ? 6 + act : plan.form;
+  const int k = plan.epi == GATE        ? 3 + act
+                : plan.epi == GATE_BACK ? 6 + 2 * act + (p.z_dtype == MAO_F32)
+                                        : plan.form;
   const int ks = plan.epi == GATE ? 1 + act : plan.epi == GATE_BACK ? 4 + act : 0;
   const bool small_q = !runs.offsets && !tn;
   p.stage_bytes = OP_BYTES + (small_q ? int32_t(round_up(p.height / 2 * BK * 2, 1024)) : OP_BYTES);
@@ -744,7 +787,7 @@ mao_status run(const Plan& plan, int32_t act, FfnParams& p, const Runs& runs, in
   static std::atomic<bool> ready[64];
   mao_status st = once_per_device(ready, [&] {
     cudaError_t err = cudaSuccess;
-    for (int f = 0; f < 9 && err == cudaSuccess; ++f)
+    for (int f = 0; f < 12 && err == cudaSuccess; ++f)
       err = cudaFuncSetAttribute(kernels[f], cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM));
     return err;
   });
@@ -768,6 +811,12 @@ mao_status run(const Plan& plan, int32_t act, FfnParams& p, const Runs& runs, in
                           stream, sum);
 }
 
+void set_saved(FfnParams& p, const mao_mat& Z) {
+  p.z = Z.data;
+  p.ldz = Z.ld;
+  p.z_dtype = Z.dtype;
+  p.paired_z = reinterpret_cast<uintptr_t>(Z.data) % (2 * elem_size(Z.dtype)) == 0 && Z.ld % 2 == 0 && Z.cols % 4 == 0;
+}
 bool words(const void* data, int64_t ld, int64_t cols) {
   return reinterpret_cast<uintptr_t>(data) % 4 == 0 && ld % 2 == 0 && cols % 2 == 0;
 }
@@ -872,8 +921,9 @@ mao_status gated_ffn_launch(const mao_mat& X, const mao_mat& up, const mao_mat& 
     q.ld = f.ldh;
     q.dtype = MAO_BF16;
     if (Z) {
-      q.z = static_cast<__nv_bfloat16*>(Z->data);
+      q.z = Z->data;
       q.ldz = Z->ld;
+      q.z_dtype = Z->dtype;
     }
     st = few_launch(q, false, true, act, stream);
     if (st != MAO_OK) return st;
@@ -896,11 +946,7 @@ mao_status gated_ffn_launch(const mao_mat& X, const mao_mat& up, const mao_mat& 
   p.ld = f.ldh;
   p.dtype = MAO_BF16;
   p.paired = 1;
-  if (Z) {
-    p.z = static_cast<__nv_bfloat16*>(Z->data);
-    p.ldz = Z->ld;
-    p.paired_z = words(Z->data, Z->ld, s.N);
-  }
+  if (Z) set_saved(p, *Z);
   st = run(f.gate, act, p, runs, s.R, at, stream);
   if (st != MAO_OK) return st;
 
@@ -955,9 +1001,7 @@ mao_status gated_ffn_backward_launch(const mao_mat& dY, const mao_mat& X, const 
     p.ld = b.ldh;
     p.dtype = MAO_BF16;
     p.paired = 1;
-    p.z = static_cast<__nv_bfloat16*>(Z.data);
-    p.ldz = Z.ld;
-    p.paired_z = words(Z.data, Z.ld, s.N);
+    set_saved(p, Z);
     p.dz = reinterpret_cast<__nv_bfloat16*>(dz);
     p.lddz = 2 * b.ldh;
     p.dz_half = int32_t(b.ldh);

@@ -81,6 +81,9 @@ def test_types_and_shapes_of_codes_are_refused(calls):  # noqa: F811
     with pytest.raises(ValueError):
         mao.gated_ffn_backward(Stand((4, 72), BF16), Stand((4, 64), BF16), Stand((96, 64), BF16), Stand((72, 48), BF16),
                                Stand((4, 96), BF16), grad_dtype=torch.float16)
+    for save in (torch.float16, "bf16", 1):
+        with pytest.raises(ValueError):
+            mao.gated_ffn(Stand((4, 64), BF16), Stand((96, 64), BF16), Stand((72, 48), BF16), save=save)
     assert not calls
 
 
@@ -103,7 +106,7 @@ def test_block_arguments_rejected_before_any_launch(lib):
     for kw in (dict(X=None), dict(up=None), dict(down=None), dict(Y=None), dict(act=-1), dict(act=3), dict(groups=0),
                dict(groups=2), dict(counts=off), dict(X=mat(9, 64, F)), dict(up=mat(96, 64, F)), dict(X=mat(9, 64, I)),
                dict(up=mat(97, 64)), dict(up=mat(96, 65)), dict(down=mat(72, 47)), dict(down=mat(0, 48)),
-               dict(Y=mat(9, 71)), dict(Y=mat(8, 72)), dict(Z=mat(9, 95)), dict(Z=mat(9, 96, F)), dict(X=mat(-1, 64)),
+               dict(Y=mat(9, 71)), dict(Y=mat(8, 72)), dict(Z=mat(9, 95)), dict(Z=mat(9, 96, I)), dict(X=mat(-1, 64)),
                dict(X=mat(9, 64, ld=63)), dict(X=mat(9, 64, data=None)), dict(Y=mat(9, 72, reserved=1)),
                dict(groups=2, offsets=off, down=mat(73, 48), up=mat(192, 64))):
         assert fwd(**kw) == bad, kw

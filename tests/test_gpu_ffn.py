@@ -49,7 +49,7 @@ def check_forward(y, z, x, up, down, name, offsets=None, counts=None):
     rs = of.runs(len(X), offsets, counts)
     ez, N = bound_z(X, W, rs), D.shape[2]
     if z is not None:
-        np.testing.assert_array_less(np.abs(np64(z) - wz), ez + U8 * (np.abs(wz) + ez) + 1e-30)
+        np.testing.assert_array_less(np.abs(np64(z) - wz), ez + out_slack(np.abs(wz) + ez, z.dtype) + 1e-30)
     G, U, eg, eu = wz[:, :N], wz[:, N:], ez[:, :N], ez[:, N:]
     a = np.abs(of.act(G, name))
     ea = 1.2 * eg + U19 * (a + 2.0 ** -20)  # slopes are below 1.2
@@ -106,11 +106,13 @@ SHAPES = [(1, 1, 1, 1), (1, 64, 16, 64), (2, 8, 3, 9), (7, 130, 33, 70), (32, 64
           (300, 515, 260, 301), (513, 96, 384, 96)]
 
 
+@pytest.mark.parametrize("save", [True, BF16])
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("shape", SHAPES)
-def test_block(cuda, shape, act):
+def test_block(cuda, shape, act, save):
     x, up, down, dy = make(sum(shape), *shape)
-    y, z = mao.gated_ffn(x, up, down, act, save=True)
+    y, z = mao.gated_ffn(x, up, down, act, save=save)
+    assert z.dtype == (F32 if save is True else BF16)
     mao.sync_status()
     check_forward(y, z, x, up, down, act)
     assert torch.equal(mao.gated_ffn(x, up, down, act), y)  # without Z
@@ -131,11 +133,12 @@ def test_fp32_outputs(cuda, shape):
     check_backward(grads, dy, x, up, down, z, "silu")
 
 
-@pytest.mark.parametrize("T", [1, 3, 16, 17, 48, 127, 128, 129])
-def test_few_rows_long_sums(cuda, T):
-    """Few rows: the sums are split, their parts added by the second kernel."""
+@pytest.mark.parametrize("save", [True, BF16])
+@pytest.mark.parametrize("T", [1, 3, 8, 9, 16, 17, 48, 127, 128, 129])
+def test_few_rows_long_sums(cuda, T, save):
+    """Few rows: a kernel of their own, or sums that are split, their parts added by a second kernel."""
     x, up, down, dy = make(T, T, 2048, 1536, 1024)
-    y, z = mao.gated_ffn(x, up, down, "silu", save=True)
+    y, z = mao.gated_ffn(x, up, down, "silu", save=save)
     check_forward(y, z, x, up, down, "silu")
     check_backward(mao.gated_ffn_backward(dy, x, up, down, z, "silu"), dy, x, up, down, z, "silu")
 
@@ -153,15 +156,16 @@ RUNS = [([0, 128, 128, 384, 512], [100, 0, 256, 1], 512),
         ([0, 256, 512, 1024, 1024], [256, 255, 512, 0], 1024)]
 
 
+@pytest.mark.parametrize("save", [True, BF16])
 @pytest.mark.parametrize("use_counts", [False, True])
 @pytest.mark.parametrize("off,cnt,rows", RUNS)
 @pytest.mark.parametrize("dims", [(64, 48, 80), (200, 136, 520), (77, 33, 41)])
-def test_runs(cuda, off, cnt, rows, use_counts, dims):
+def test_runs(cuda, off, cnt, rows, use_counts, dims, save):
     x, up, down, dy = make(rows + dims[0], rows, *dims, groups=4)
     counts = cnt if use_counts else None
     kw = dict(offsets=torch.tensor(off, dtype=torch.int32, device=cuda),
               counts=torch.tensor(cnt, dtype=torch.int32, device=cuda) if use_counts else None)
-    y, z = mao.gated_ffn(x, up, down, "silu", save=True, **kw)
+    y, z = mao.gated_ffn(x, up, down, "silu", save=save, **kw)
     mao.sync_status()
     check_forward(y, z, x, up, down, "silu", off, counts)
     used = torch.zeros(rows, dtype=torch.bool)
@@ -220,12 +224,12 @@ def test_strides_and_outputs(cuda):
         big[:, left:left + t.shape[1]] = t
         return big[:, left:left + t.shape[1]]
 
-    y0, z0 = mao.gated_ffn(x, up, down, "silu", save=True)
-    g0 = mao.gated_ffn_backward(dy, x, up, down, z0, "silu")
-    for left, right in ((8, 8), (1, 2), (3, 4)):
+    for left, right, save in ((8, 8, BF16), (1, 2, BF16), (3, 4, BF16), (4, 4, F32), (1, 2, F32)):
+        y0, z0 = mao.gated_ffn(x, up, down, "silu", save=save)
+        g0 = mao.gated_ffn_backward(dy, x, up, down, z0, "silu")
         xs, us, ds, dys = (wide(t, left, right) for t in (x, up, down, dy))
         out = wide(torch.zeros(T, C, dtype=BF16, device=cuda), left, right)
-        Z = wide(torch.zeros(T, 2 * N, dtype=BF16, device=cuda), left, right)
+        Z = wide(torch.zeros(T, 2 * N, dtype=save, device=cuda), left, right)
         y, z = mao.gated_ffn(xs, us, ds, "silu", out=out, Z=Z)
         assert y is out and z is Z and torch.equal(y, y0) and torch.equal(z, z0)
         outs = [wide(torch.zeros_like(t), left, right) for t in (x, up, down)]
