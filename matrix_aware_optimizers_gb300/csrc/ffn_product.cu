@@ -200,18 +200,18 @@ __device__ __forceinline__ void gate16(const FfnParams& p, const Tile& t, int j,
   }
 }
 
-// GATE_BACK: G and U of sixteen rows at column i and its neighbour: even lanes have those of rows j,
+// GATE_BACK: G and U of eight rows at column i and its neighbour: even lanes have those of rows j,
 // j + 2, ..., odd lanes of the others.
 template <bool F32>
 struct Saved;
 template <>
 struct Saved<false> {
-  uint32_t g[8], u[8];
+  uint32_t g[4], u[4];
   __device__ __forceinline__ void load(const FfnParams& p, const Tile& t, int j, int i, int lane) {
     const int odd = lane & 1, col = i - odd;
     const uint16_t* z = static_cast<const uint16_t*>(p.z) + int64_t(j + odd) * p.ldz + col;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < 4; ++c) {
       const bool a = col < p.I && j + 2 * c + odd < t.j_end, b = a && col + 1 < p.I;
       if (p.paired_z) {
         g[c] = a ? __ldg(reinterpret_cast<const uint32_t*>(z)) : 0u;
@@ -229,12 +229,12 @@ struct Saved<false> {
 };
 template <>
 struct Saved<true> {
-  uint64_t g[8], u[8];
+  uint64_t g[4], u[4];
   __device__ __forceinline__ void load(const FfnParams& p, const Tile& t, int j, int i, int lane) {
     const int odd = lane & 1, col = i - odd;
     const float* z = static_cast<const float*>(p.z) + int64_t(j + odd) * p.ldz + col;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < 4; ++c) {
       const bool a = col < p.I && j + 2 * c + odd < t.j_end, b = a && col + 1 < p.I;
       if (p.paired_z) {
         g[c] = a ? __ldg(reinterpret_cast<const unsigned long long*>(z)) : 0ull;
@@ -260,9 +260,9 @@ __device__ __forceinline__ void prefetch_saved(const FfnParams& p, const Tile& t
   for (int b = 0; b < bytes; b += 128) prefetch_l2(z + b);
 }
 
-// dG, dU and H of sixteen rows of dH. The buffers' rows are padded to whole words.
-template <int ACT, bool F32>
-__device__ __forceinline__ void gate_back16(const FfnParams& p, const Tile& t, int j, int i,
+// dG, dU and H of eight rows of dH, those from FROM on of the sixteen in v. The buffers' rows are padded to whole words.
+template <int ACT, bool F32, int FROM>
+__device__ __forceinline__ void gate_back8(const FfnParams& p, const Tile& t, int j, int i,
                                             const float (&v)[16], const Saved<F32>& s, int lane) {
   const int odd = lane & 1, col = i - odd;
   const int left = col < p.I ? t.j_end - j - odd : 0;  // rows from this lane's first on
@@ -271,9 +271,9 @@ __device__ __forceinline__ void gate_back16(const FfnParams& p, const Tile& t, i
   __nv_bfloat16* dg = p.dz + row * p.lddz + col;
   __nv_bfloat16* du = dg + p.dz_half;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const float o = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[2 * c] : v[2 * c + 1], 1);
-    const uint64_t d = odd ? pair_of(o, v[2 * c + 1]) : pair_of(v[2 * c], o), u = s.linear(c);
+  for (int c = 0; c < 4; ++c) {
+    const float o = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[FROM + 2 * c] : v[FROM + 2 * c + 1], 1);
+    const uint64_t d = odd ? pair_of(o, v[FROM + 2 * c + 1]) : pair_of(v[FROM + 2 * c], o), u = s.linear(c);
     uint64_t a, slope;
     activate2<ACT>(s.gate(c), a, slope);
     if (2 * c < left) {
@@ -530,17 +530,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!wait_warp<false>(&tfull_bar[acc], uint32_t(local >> 1) & 1u, abort_flag, limit)) break;
       tc_fence_after();
       const uint32_t trow = tmem_base + (uint32_t(32 * quad) << 16) + uint32_t(acc * TILE);
+      // G and U of eight rows are on their way while eight others are worked on
+      Saved<ZF32> za, zb;
+      if (saved && 16 * part < n) za.load(p, t, t.j0 + 16 * part, i, lane);
 #pragma unroll 1
       for (int c = 16 * part; c < n; c += 64) {
-        Saved<ZF32> z;
         float v[16];
-        if (saved) z.load(p, t, t.j0 + c, i, lane);
+        if (saved) zb.load(p, t, t.j0 + c + 8, i, lane);
         tmem_ld16(trow + uint32_t(c), v);
         tmem_wait(v);
-        if (EPI == GATE && p.splits > 1) store16_gate_parts(p, t, t.j0 + c, i, v, lane);
-        else if (EPI == GATE) gate16<ACT>(p, t, t.j0 + c, i, v, lane);
-        else if (saved) gate_back16<ACT, ZF32>(p, t, t.j0 + c, i, v, z, lane);
-        else store16(p, t, t.j0 + c, i, v, lane);
+        if (EPI == GATE && p.splits > 1) {
+          store16_gate_parts(p, t, t.j0 + c, i, v, lane);
+        } else if (EPI == GATE) {
+          gate16<ACT>(p, t, t.j0 + c, i, v, lane);
+        } else if (saved) {
+          gate_back8<ACT, ZF32, 0>(p, t, t.j0 + c, i, v, za, lane);
+          if (c + 64 < n) za.load(p, t, t.j0 + c + 64, i, lane);
+          gate_back8<ACT, ZF32, 8>(p, t, t.j0 + c + 8, i, v, zb, lane);
+        } else {
+          store16(p, t, t.j0 + c, i, v, lane);
+        }
       }
       tc_fence_before();
       __syncwarp();
