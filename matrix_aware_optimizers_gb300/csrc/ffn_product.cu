@@ -849,7 +849,7 @@ struct Forward {
   Forward(const mao_mat& X, const mao_mat& Up, const mao_mat& Down, int32_t groups, bool grouped)
       : s{X.rows, X.cols, Down.cols, Down.rows / groups}, ldh(round_up(s.N, 8)), x(operand(X)), up(operand(Up)),
         down(operand(Down)), gate{NT, GATE, s.N, s.R, s.K, 1}, out{NT, PLAIN, s.C, s.R, s.N, 1} {
-    if (few_rows(s.R, grouped, false)) return;  // these products are not cut
+    if (few_rows(s.R, grouped, false, groups)) return;  // these products are not cut
     gate.choose(grouped);
     out.choose(grouped);
   }
@@ -914,7 +914,7 @@ mao_status gated_ffn_launch(const mao_mat& X, const mao_mat& up, const mao_mat& 
   mao_status st = copies.launch(stream);
   if (st != MAO_OK) return st;
 
-  if (few_rows(s.R, runs.offsets != nullptr, runs.counts != nullptr)) {
+  if (few_rows(s.R, runs.offsets != nullptr, runs.counts != nullptr, runs.groups)) {
     FewParams q = {};
     q.offsets = runs.offsets;
     q.counts = runs.counts;
