@@ -2,7 +2,9 @@
 //
 // One pass: a row's values stay in the registers of the threads that share it (those past
 // 8 CACHED per thread are read again), between the largest magnitude and the codes. Instructions
-// bound it: at 22 per value 8192 x 4096 bf16 took 37 us, now 22 (100 MB: 4.6 TB/s).
+// bound it: at 22 per value 8192 x 4096 bf16 took 37 us, now 22 to 27 (on different cards; 100 MB: up to
+// 4.6 TB/s, 68% of the issue slots). 3001 gated rows of 2053 fp32, gelu_tanh: 20 to 25 us (103
+// instructions per value, most of them tanhf's).
 //
 // code = 127 x / a rounded to nearest even, as if computed exactly: x (127 / a) with a rounded
 // quotient is off by less than 2^-15, so only products that near to a border between two codes
