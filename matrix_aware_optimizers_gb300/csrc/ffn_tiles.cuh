@@ -15,7 +15,7 @@ constexpr int MAX_GROUPS = 1024;
 constexpr int BAND = 8;    // tiles of j that share a pass over i
 constexpr size_t TABLE_BYTES = size_t(3) * (MAX_GROUPS + 2) * 4;
 
-enum Form { NT, NN, TN };
+enum Form { NT, NN, TN, GRADS };  // GRADS: a product NN and two TN in one launch
 
 struct TileParams {
   const int32_t* offsets;
@@ -228,6 +228,9 @@ __device__ __forceinline__ void for_unused_rows(const TileParams& p, const int* 
   }
 }
 
+// Pairs of CTAs that fit the GPU (sizes are asked for without one, too).
+inline int64_t cta_pairs() { return num_sms() > 1 ? num_sms() / 2 : 1; }
+
 // How a product of one run is cut: the height of its tiles, and the parts of its depth with their
 // blocks.
 struct Cut {
@@ -235,10 +238,10 @@ struct Cut {
 };
 // The cut with the least time by a model of the kernels, in us: `block` per block of the depth for a
 // tile of 256, less for a lower one down to `least_block`; `epilogue` for a tile of 256; 2.5 us and
-// 3 TB/s for the sum of the fp32 parts, which stay in L2. tiles_i: tiles of i (of all matrices).
-inline Cut choose_cut(int64_t tiles_i, int64_t J, int64_t nkb, double block, double least_block, double epilogue,
+// 3 TB/s for the sum of the fp32 parts, which stay in L2. tiles_i: tiles of i (of all matrices); pairs:
+// pairs of CTAs at work on it.
+inline Cut choose_cut(int64_t pairs, int64_t tiles_i, int64_t J, int64_t nkb, double block, double least_block, double epilogue,
                       int64_t outputs, int64_t least_kb) {
-  const int64_t pairs = num_sms() > 1 ? num_sms() / 2 : 1;  // (sizes are asked for without a GPU, too)
   Cut best{TILE, 1, int(nkb)};
   double least = 1e30;
   for (int h = TILE; h >= 32; h /= 2) {

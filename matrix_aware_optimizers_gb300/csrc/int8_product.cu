@@ -592,7 +592,7 @@ std::atomic<bool> g_launched{false};
 
 // A block of 128 takes a pair 0.55 us, at least 0.4 (the conversion; with few rows the bytes).
 Cut cut_of(const mao_int8& A, const mao_int8& B) {
-  return choose_cut(ceil_div(B.rows, TILE), A.rows, ceil_div(A.cols, BK), 0.55, 0.4, 1.7, A.rows * B.rows, 2);
+  return choose_cut(cta_pairs(), ceil_div(B.rows, TILE), A.rows, ceil_div(A.cols, BK), 0.55, 0.4, 1.7, A.rows * B.rows, 2);
 }
 
 // The workspace: A in fp16, then the parts of split sums.

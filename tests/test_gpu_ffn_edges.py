@@ -175,6 +175,24 @@ def test_many_tiles(cuda):
     check_backward(grads, dy, x, up, down, z, "gelu_tanh", off.tolist(), cnt.tolist())
 
 
+def test_gradients_of_many_tiles(cuda):
+    """So many that each gradient has a launch of its own; the same with some not wanted."""
+    g = torch.Generator().manual_seed(2)
+    cnt = torch.randint(0, 60, (64,), generator=g)
+    off = torch.arange(65) * 128
+    x, up, down, dy = make(9, 64 * 128, 520, 520, 264, groups=64)
+    kw = dict(offsets=off.to(I32).to(cuda), counts=cnt.to(I32).to(cuda))
+    y, z = mao.gated_ffn(x, up, down, "silu", save=True, **kw)
+    grads = mao.gated_ffn_backward(dy, x, up, down, z, "silu", **kw)
+    mao.sync_status()
+    check_backward(grads, dy, x, up, down, z, "silu", off.tolist(), cnt.tolist())
+    for only in range(3):
+        flags = {k: None if i == only else False for i, k in enumerate(("dX", "dup", "ddown"))}
+        some = mao.gated_ffn_backward(dy, x, up, down, z, "silu", **flags, **kw)
+        assert [t is None for t in some] == [i != only for i in range(3)]
+        assert torch.equal(some[only], grads[only])
+
+
 @pytest.mark.parametrize("most", [1, 8, 20])
 def test_few_rows_in_many_runs(cuda, most):
     """A token's copies in a few of many runs of 128 rows: some runs hold more rows than a pass takes."""
