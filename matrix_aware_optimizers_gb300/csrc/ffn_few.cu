@@ -182,8 +182,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   __syncthreads();
-  // launched as a programmatic dependent: the set-up so far may overlap the previous kernel
-  wait_for_previous();
+  // launched as a programmatic dependent: the set-up so far may overlap the previous kernel, with
+  // `early` the first loads of W too
+  if (!p.early) wait_for_previous();
   int units = p.tiles_i * ((p.rows + 8 * NT - 1) / (8 * NT));
   if (p.offsets) {
     make_table<THREADS>(p, lo, cnt, begin, scratch);
@@ -200,16 +201,21 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
   int next_unit = unit0, next_chunk = member, loaded = 0;
   if (next_chunk >= chunks) next_unit = units;  // no chunk of any sum is this warp's
   if (next_unit < units) decode_unit<NT>(p, lo, cnt, begin, next_unit, next);
-  auto load_next = [&]() {
+  int first_k = 0, first_j = 0;  // lane s: where the first load into stage s has its rows of X
+  auto load_next = [&](bool with_x) {
     if (next_unit >= units) return;
     const int stage = loaded % STAGES;
+    const int k = next_chunk * step;
+    if (lane == stage && !with_x) {
+      first_k = k;
+      first_j = int(next.j0);
+    }
     if (lane == 0) {
       const uint32_t bar = smem_u32(&bars[warp][stage]), dst = smem_u32(ring) + stage * STAGE;
-      const int k = next_chunk * step;
       mbar_expect_tx(bar, MATS * BOX_BYTES + p.x_rows * 128);
 #pragma unroll
       for (int m = 0; m < MATS; ++m) tma_load(INT8, dst + m * BOX_BYTES, &p.map_w, bar, k, next.i0, m, next.run);
-      tma_load(INT8, dst + MATS * BOX_BYTES, &p.map_x, bar, k, int(next.j0), 0, 0);
+      if (with_x) tma_load(INT8, dst + MATS * BOX_BYTES, &p.map_x, bar, k, int(next.j0), 0, 0);
     }
     ++loaded;
     next_chunk += team;
@@ -219,7 +225,14 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
       if (next_unit < units) decode_unit<NT>(p, lo, cnt, begin, next_unit, next);
     }
   };
-  for (int s = 0; s < STAGES; ++s) load_next();
+  for (int s = 0; s < STAGES; ++s) load_next(!p.early);
+  if (p.early) {
+    wait_for_previous();
+    if (lane < loaded)
+      tma_load(INT8, smem_u32(ring) + lane * STAGE + MATS * BOX_BYTES, &p.map_x, smem_u32(&bars[warp][lane]), first_k,
+               first_j, 0, 0);
+    __syncwarp();
+  }
 
   if (p.offsets) {  // rows that hold no tokens, while the first loads are under way
     const int turn = int(blockIdx.x) * WARPS + warp, turns = int(gridDim.x) * WARPS;
@@ -256,7 +269,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
       }
       ++used;
       __syncwarp();  // every lane has read the stage
-      load_next();
+      load_next(true);
     }
 #pragma unroll
     for (int m = 0; m < MATS; ++m)

@@ -14,6 +14,7 @@ struct FewParams : ffn::TileParams {  // rows, I, depth, offsets, counts, groups
   void* z;          // gated: G and U, fp32 or bf16, or null
   int64_t ldw, ldx, ld, ldz;  // in entries
   int32_t dtype, z_dtype;
+  int32_t early;    // all but X is older than the kernel before this one
 };
 mao_status few_launch(const FewParams& params, bool int8, bool gate, int32_t act, cudaStream_t stream);
 

@@ -1049,6 +1049,7 @@ mao_status gated_ffn_launch(const mao_mat& X, const mao_mat& up, const mao_mat& 
     q.d = Y.data;
     q.ld = Y.ld;
     q.dtype = Y.dtype;
+    q.early = 1;  // the kernel before it wrote H and Z only, and began after all others
     return few_launch(q, false, false, act, stream);
   }
   FfnArgs<1> gate = {};
