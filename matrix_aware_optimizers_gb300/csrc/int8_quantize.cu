@@ -60,6 +60,9 @@ __device__ __forceinline__ uint32_t top_of(const float (&v)[8]) {
   return top;
 }
 
+__device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ uint32_t bits(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
+
 // Eight values as they lie in memory.
 template <typename T, bool VEC, int TEAM>
 struct Raw {
@@ -72,10 +75,13 @@ struct Raw {
       if (c + 8 <= cols) {
 #pragma unroll
         for (int q = 0; q < WORDS; ++q) w[q] = reinterpret_cast<const uint4*>(x + c)[q];
-      } else {  // (columns are a multiple of what 16 bytes hold: whole words, or none)
+      } else {  // the last columns of a row
+        uint32_t* to = &w[0].x;
 #pragma unroll
-        for (int q = 0; q < WORDS; ++q)
-          w[q] = c + (q + 1) * 8 / WORDS <= cols ? reinterpret_cast<const uint4*>(x + c)[q] : make_uint4(0u, 0u, 0u, 0u);
+        for (int q = 0; q < 4 * WORDS; ++q) to[q] = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (c + q < cols) to[q * WORDS / 2] |= bits(x[c + q]) << (WORDS == 1 ? 16 * (q & 1) : 0);
       }
     } else {
 #pragma unroll

@@ -104,6 +104,9 @@ def test_quantize_strides_and_stacks(cuda, dtype):
     codes, scales = mao.int8_quantize(many)
     for i in (0, 3, 63, 64, 69):
         check_rows(codes[i], scales[i], many[i])
+    even = spread(4, 50, 704).to(dtype).to(cuda)  # aligned rows, widths that are no multiple of a load
+    for C in (1, 3, 8, 33, 300, 699, 702, 704):
+        check_rows(*mao.int8_quantize(even[:, :C]), even[:, :C])
     wide = torch.full((200, 320), 7, dtype=torch.int8, device=cuda)
     sc = torch.empty(200, device=cuda)
     mao.int8_quantize(big[:, :300], out=(wide[:, :300], sc))
@@ -136,6 +139,38 @@ def test_quantize_gated(cuda, dtype, gate, shape):
     else:
         w = 0.5 * g * (1.0 + torch.tanh((2.0 / np.pi) ** 0.5 * (g + 0.044715 * g * g * g))) * u
     check_rows(codes, scales, w)
+
+
+@pytest.mark.parametrize("gate", ["silu", "gelu", "gelu_tanh"])
+def test_quantize_gated_in_doubt(cuda, gate):
+    """Rows in which many values come near to the largest or to borders, and rows near the ends of fp32's
+    range: the codes are those of the documented arithmetic."""
+    C = 1536
+    g = randn(1, 12, C) * 3
+    u = randn(2, 12, C)
+    g[0], u[0] = 1.25, 0.75                              # one value throughout
+    g[1], u[1] = torch.linspace(1.0, 1.0001, C), 1.0     # all near the largest
+    g[2] = -6.0 - randn(3, C).abs()                          # small gates of large factors
+    g[3] = -30.0 - 25.0 * randn(4, C).abs()                  # next to nothing
+    g[4], u[4] = g[4] * 1e-22, u[4] * 1e-22              # products below fp32's range
+    g[5], u[5] = g[5].abs() * 1e18, u[5] * 1e18          # and near its other end
+    g[6] *= 40.0
+    u[7] = 0.0
+    g[8] = 0.0
+    g[9] = 2.0                                           # whole and half multiples of one value
+    u[9] = torch.randint(-254, 255, (C,), generator=torch.Generator().manual_seed(3)) / 2.0
+    g[10, ::2] = -200.0
+    x = torch.cat([g, u], 1)
+    for dtype in (F32, BF16):
+        xx = x.to(dtype).to(cuda)
+        a, b = xx[:, :C].float(), xx[:, C:].float()
+        if gate == "silu":
+            w = a / (1.0 + torch.exp(-a)) * b
+        elif gate == "gelu":
+            w = 0.5 * a * (1.0 + torch.erf(a * 0.5 ** 0.5)) * b
+        else:
+            w = 0.5 * a * (1.0 + torch.tanh((2.0 / np.pi) ** 0.5 * (a + 0.044715 * a * a * a))) * b
+        check_rows(*mao.int8_quantize(xx, gate=gate), w)
 
 
 def test_quantize_gated_extremes(cuda):
