@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(256) int8_sum_kernel(const SumParams p) {
   }
 }
 
-// A's codes in fp16, sixteen per thread and step, a row per warp. With counts the rows that hold no
+// A's codes in fp16, a row per warp, eight codes per lane and step, up to eight steps under way. With counts the rows that hold no
 // tokens are left out (the offsets rise): 128 runs of 125 rows, padded to
 // twice that, 41 us with all of them.
 struct HalfParams {
@@ -554,35 +554,38 @@ struct HalfParams {
   int64_t rows, ld, dld;
   int32_t cols, groups;
 };
+constexpr int AHEAD = 8;  // loads of a lane under way
 __global__ void __launch_bounds__(128) to_half_kernel(const HalfParams p) {
   wait_for_previous();
-  const int per_row = (p.cols + 15) / 16;
+  const int lane = threadIdx.x % 32;
   for (int64_t r = int64_t(blockIdx.x) * 4 + threadIdx.x / 32; r < p.rows; r += int64_t(gridDim.x) * 4) {
     if (p.counts) {
       int lo = -1;  // the last run that starts at or before the row
 #pragma unroll 4
-      for (int g0 = 0; g0 < p.groups; g0 += 32) {
-        const int g = g0 + int(threadIdx.x) % 32;
-        lo += __popc(__ballot_sync(0xFFFFFFFFu, g < p.groups && (g == 0 || __ldg(p.offsets + g) <= r)));
-      }
+      for (int g0 = 0; g0 < p.groups; g0 += 32)
+        lo += __popc(__ballot_sync(0xFFFFFFFFu, g0 + lane < p.groups &&
+                                                    (g0 + lane == 0 || __ldg(p.offsets + g0 + lane) <= r)));
       const int64_t first = max(__ldg(p.offsets + lo), 0), next = __ldg(p.offsets + lo + 1);
       if (first <= r && r < next && r >= first + max(__ldg(p.counts + lo), 0)) continue;
     }
-    for (int g = threadIdx.x % 32; g < per_row; g += 32) {
-      const int c = 16 * g;
-      const int8_t* s = p.src + r * p.ld + c;
-      uint16_t* d = p.dst + r * p.dld + c;
-      if (c + 16 <= p.cols) {
-        const uint4 v = *reinterpret_cast<const uint4*>(s);
-        uint4 a, b;
-        to_half(v.x, a.x, a.y);
-        to_half(v.y, a.z, a.w);
-        to_half(v.z, b.x, b.y);
-        to_half(v.w, b.z, b.w);
-        reinterpret_cast<uint4*>(d)[0] = a;
-        reinterpret_cast<uint4*>(d)[1] = b;
-      } else {
-        for (int q = 0; c + q < p.cols; ++q) d[q] = __half_as_ushort(__int2half_rn(s[q]));
+    const int8_t* s = p.src + r * p.ld;
+    uint16_t* d = p.dst + r * p.dld;
+    for (int c0 = 8 * lane; c0 < p.cols; c0 += 256 * AHEAD) {
+      uint2 v[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (c0 + 256 * k + 8 <= p.cols) v[k] = *reinterpret_cast<const uint2*>(s + c0 + 256 * k);
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const int c = c0 + 256 * k;
+        if (c + 8 <= p.cols) {
+          uint4 h;
+          to_half(v[k].x, h.x, h.y);
+          to_half(v[k].y, h.z, h.w);
+          *reinterpret_cast<uint4*>(d + c) = h;
+        } else {
+          for (int q = 0; c + q < p.cols; ++q) d[q + c] = __half_as_ushort(__int2half_rn(s[q + c]));
+        }
       }
     }
   }
