@@ -49,11 +49,10 @@ using namespace ffn;
 
 constexpr int BK = 128;                   // depth of a stage: rows of 128 bytes of codes
 constexpr int RAW_BYTES = HALF * BK;
-constexpr int RAW_STAGES = 6;
+constexpr int RAW_STAGES = 4;
 constexpr int HK = 64;                    // half of it: rows of 128 bytes of fp16
-constexpr int HALF_BYTES = HALF * HK * 2;
-constexpr int A_BYTES = 2 * HALF_BYTES;
-constexpr int A_STAGES = 3;
+constexpr int A_BYTES = HALF * HK * 2;    // a slot of A
+constexpr int A_SLOTS = 8;
 constexpr int B_STAGES = 2;
 constexpr int EPI_WARPS = 8;
 constexpr int CONV_WARPS = 8;
@@ -63,7 +62,7 @@ constexpr int ACC1 = 128;                 // first column of the second accumula
 constexpr int B_COL = ACC1 + TILE;        // B's stages
 constexpr int B_COLS = BK / 2;
 constexpr int Q_BOXES = 4;                // heights of boxes of A: 16 << b rows
-constexpr size_t SMEM = 1024 + size_t(RAW_STAGES) * RAW_BYTES + size_t(A_STAGES) * A_BYTES + TABLE_BYTES + 512;
+constexpr size_t SMEM = 1024 + size_t(RAW_STAGES) * RAW_BYTES + size_t(A_SLOTS) * A_BYTES + TABLE_BYTES + 512;
 static_assert(SMEM <= 232448, "shared memory budget of one CTA");
 static_assert(B_COL + B_STAGES * B_COLS <= TMEM_COLS, "TMEM budget");
 
@@ -82,18 +81,24 @@ __device__ __forceinline__ uint32_t instr_desc(int n) {
   return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(TILE >> 4) << 24);
 }
 
-// The eight 16-deep products of a stage: B from TMEM (8 columns each), A from shared memory (32
-// bytes along its rows each).
-__device__ __forceinline__ void mma_stage(uint32_t elected, uint32_t d, uint32_t b, uint64_t a,
-                                          uint32_t idesc, uint32_t accumulate) {
+// Whether the two halves of a stage's A, each 64 deep, have a slot of their own (tiles of more than
+// 128 rows) or share one.
+__device__ __forceinline__ bool two_slots(const Int8Params& p, const Tile& t) {
+  return (p.offsets ? t.n : p.height) > HALF;
+}
+
+// Four 16-deep products: B from TMEM (8 columns each), A from shared memory (32 bytes along its rows
+// each).
+__device__ __forceinline__ void mma_half(uint32_t elected, uint32_t d, uint32_t b, uint64_t a, uint32_t idesc,
+                                         uint32_t accumulate) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < 4; ++k) {
     asm volatile(
         "{\n\t.reg .pred a, e;\n\t"
         "setp.ne.b32 a, %4, 0;\n\t"
         "setp.ne.b32 e, %5, 0;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, a;\n\t}\n" ::"r"(d),
-        "r"(b + 8 * k), "l"(a + uint64_t(k < 4 ? 2 * k : (HALF_BYTES >> 4) + 2 * (k - 4))), "r"(idesc),
+        "r"(b + 8 * k), "l"(a + uint64_t(2 * k)), "r"(idesc),
         "r"(k ? 1u : accumulate), "r"(elected)
         : "memory");
   }
@@ -187,15 +192,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint8_t* raw = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ast = raw + RAW_STAGES * RAW_BYTES;
-  int* lo = reinterpret_cast<int*>(ast + A_STAGES * A_BYTES);
+  int* lo = reinterpret_cast<int*>(ast + A_SLOTS * A_BYTES);
   int* cnt = lo + MAX_GROUPS + 2;
   int* begin = cnt + MAX_GROUPS + 2;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ast + A_STAGES * A_BYTES + TABLE_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ast + A_SLOTS * A_BYTES + TABLE_BYTES);
   uint64_t* rfull_bar = bars;                       // [RAW_STAGES]
   uint64_t* rempty_bar = rfull_bar + RAW_STAGES;    // [RAW_STAGES]
-  uint64_t* afull_bar = rempty_bar + RAW_STAGES;    // [A_STAGES]  (used in the even CTA)
-  uint64_t* aempty_bar = afull_bar + A_STAGES;      // [A_STAGES]
-  uint64_t* bfull_bar = aempty_bar + A_STAGES;      // [B_STAGES]  (used in the even CTA)
+  uint64_t* afull_bar = rempty_bar + RAW_STAGES;    // [A_SLOTS]  (used in the even CTA)
+  uint64_t* aempty_bar = afull_bar + A_SLOTS;      // [A_SLOTS]
+  uint64_t* bfull_bar = aempty_bar + A_SLOTS;      // [B_STAGES]  (used in the even CTA)
   uint64_t* bempty_bar = bfull_bar + B_STAGES;      // [B_STAGES]
   uint64_t* tfull_bar = bempty_bar + B_STAGES;      // [2]
   uint64_t* tempty_bar = tfull_bar + 2;             // [2]  all columns read    (even CTA)
@@ -217,7 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&rfull_bar[s]), 1);
       mbar_init(smem_u32(&rempty_bar[s]), CONV_WARPS);
     }
-    for (int s = 0; s < A_STAGES; ++s) {
+    for (int s = 0; s < A_SLOTS; ++s) {
       mbar_init(smem_u32(&afull_bar[s]), 1);
       mbar_init(smem_u32(&aempty_bar[s]), 1);
     }
@@ -271,29 +276,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int j = t.j0 + (t.n >> 1) * int(cta);
       const bool one_box = !p.offsets;
       const int q_rows = one_box ? p.height >> 1 : t.n >> 1;  // a multiple of 16
-      for (int kb = 0; kb < t.nkb; ++kb) {
+      const bool two = two_slots(p, t);
+      for (int at_k = 0; at_k < t.nkb * BK; at_k += two ? HK : BK) {
         if (!wait_warp<false>(&aempty_bar[stage], phase ^ 1u, abort_flag, limit)) {
           ok = false;
           break;
         }
         const uint32_t fb = full0 + 8 * stage, dst = smem_u32(ast) + stage * A_BYTES;
-        const int k = (t.kb0 + kb) * BK;
+        const int k = t.kb0 * BK + at_k;
         if (elected) {
-          if (leader) mbar_expect_tx(smem_u32(&afull_bar[stage]), 2 * uint32_t(q_rows) * BK * 2);
+          if (leader) mbar_expect_tx(smem_u32(&afull_bar[stage]), 2 * uint32_t(q_rows) * (two ? HK : BK) * 2);
           if (one_box) {
             tma_load_4d_pair(dst, &p.map_q[Q_BOXES - 1], fb, k, j, 0, 0);
-            tma_load_4d_pair(dst + HALF_BYTES, &p.map_q[Q_BOXES - 1], fb, k + HK, j, 0, 0);
+            if (!two) tma_load_4d_pair(dst + A_BYTES / 2, &p.map_q[Q_BOXES - 1], fb, k + HK, j, 0, 0);
           }
           for (int box = Q_BOXES - 1, at = 0; box >= 0 && !one_box; --box)
             if (q_rows & (16 << box)) {
               tma_load_4d_pair(dst + at * (HK * 2), &p.map_q[box], fb, k, j + at, 0, 0);
-              tma_load_4d_pair(dst + HALF_BYTES + at * (HK * 2), &p.map_q[box], fb, k + HK, j + at, 0, 0);
+              if (!two) tma_load_4d_pair(dst + A_BYTES / 2 + at * (HK * 2), &p.map_q[box], fb, k + HK, j + at, 0, 0);
               at += 16 << box;
             }
         }
         armed |= 1u << stage;
         armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-        if (++stage == A_STAGES) {
+        if (++stage == A_SLOTS) {
           stage = 0;
           phase ^= 1u;
         }
@@ -301,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     // after an abort, the loads already issued land before the CTA leaves
     if (*abort_flag && leader && lane == 0) {
-      for (int s = 0; s < A_STAGES; ++s)
+      for (int s = 0; s < A_SLOTS; ++s)
         if ((armed >> s) & 1u) mbar_drain(smem_u32(&afull_bar[s]), (armed_phase >> s) & 1u, 20000000ull);
     }
     __syncwarp();
@@ -363,6 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const uint32_t d = tmem_base + uint32_t(acc * ACC1);
         const uint32_t idesc = instr_desc(t.n);
+        const bool two = two_slots(p, t);
         for (int kb = 0; kb < t.nkb; ++kb) {
           // the stage was looked at while the products before were issued
           if (!__all_sync(0xFFFFFFFFu, ready) &&
@@ -373,11 +380,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           tc_fence_after();
           const uint32_t b = tmem_base + uint32_t(B_COL + sb * B_COLS);
-          const uint64_t a = a_desc + uint64_t(sa * (A_BYTES >> 4));
-          const uint32_t aempty = smem_u32(&aempty_bar[sa]), bempty = smem_u32(&bempty_bar[sb]);
-          if (++sa == A_STAGES) {
-            sa = 0;
-            pa ^= 1u;
+          uint64_t a = a_desc + uint64_t(sa * (A_BYTES >> 4));
+          uint32_t aempty = smem_u32(&aempty_bar[sa]);
+          const uint32_t bempty = smem_u32(&bempty_bar[sb]);
+          auto next_slot = [&]() {
+            if (++sa == A_SLOTS) {
+              sa = 0;
+              pa ^= 1u;
+            }
+          };
+          next_slot();
+          mma_half(elected, d, b, a, idesc, kb != 0 ? 1u : 0u);
+          issued = true;
+          if (two) {
+            commit_both(elected, aempty);
+            if (!wait_warp<false>(&afull_bar[sa], pa, abort_flag, limit)) {
+              ok = false;
+              break;
+            }
+            a = a_desc + uint64_t(sa * (A_BYTES >> 4));
+            aempty = smem_u32(&aempty_bar[sa]);
+            next_slot();
+          } else {
+            a += A_BYTES / 2 >> 4;
           }
           if (++sb == B_STAGES) {
             sb = 0;
@@ -385,8 +410,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           ready = limit != 0 && mbar_test_wait(smem_u32(&afull_bar[sa]), pa) &&
                   mbar_test_wait_cluster(smem_u32(&bfull_bar[sb]), pb);
-          mma_stage(elected, d, b, a, idesc, kb != 0 ? 1u : 0u);
-          issued = true;
+          mma_half(elected, d, b + B_COLS / 2, a, idesc, 1u);
           commit_both(elected, bempty);
           commit_both(elected, aempty);
         }
