@@ -11,15 +11,15 @@
 //
 // Tiles of 256 x 256 by a pair of CTAs (cta_group::2, M = 256 channels i, N up to 256 rows j).
 // Roles per CTA (608 threads):
-//   warp 0        TMA producer of A: 128-deep stages of fp16, ring of three
+//   warp 0        TMA producer of A: fp16, a ring of eight slots: 128 deep in one, or 64 with more than 128 rows
 //   warp 1        TMEM allocation; in the even CTA it issues the products (converged, one lane)
 //   warps 2..9    epilogue: two warps per 32-lane quadrant of TMEM; lane = i
 //   warps 10..17  B's rows, one per lane: 64 codes to 32 words of TMEM; four warps for each half of
 //                 a stage
-//   warp 18       TMA producer of B: 128-deep stages of codes, ring of six
-// TMEM: two accumulators of 256 columns that share 128 (columns 0..255 and 128..383), and two
-// stages of B (64 columns each from 384 on). The shared columns are read first, so the next
-// tile's products wait for that only.
+//   warp 18       TMA producer of B: 128-deep stages of codes, ring of four
+// TMEM: two accumulators in 384 columns, one from the left and one from the right, and two stages of B (64
+// columns each). Two tiles of 256 rows share 128 columns; these are read first, and the next tile's
+// products wait for that only.
 //
 // What bounds it: 8192 x 14336 x 4096 takes 527 us in a graph (1.83 PFLOP/s, 95% of cuBLAS's bf16
 // rate alone), 570 us in a run: the tensor cores, then the power limit. Low tiles do not pay
@@ -58,8 +58,7 @@ constexpr int EPI_WARPS = 8;
 constexpr int CONV_WARPS = 8;
 constexpr int THREADS = 32 * (3 + EPI_WARPS + CONV_WARPS);
 constexpr int TMEM_COLS = 512;
-constexpr int ACC1 = 128;                 // first column of the second accumulator
-constexpr int B_COL = ACC1 + TILE;        // B's stages
+constexpr int B_COL = 384;                // B's stages; two accumulators in the columns before
 constexpr int B_COLS = BK / 2;
 constexpr int Q_BOXES = 4;                // heights of boxes of A: 16 << b rows
 constexpr size_t SMEM = 1024 + size_t(RAW_STAGES) * RAW_BYTES + size_t(A_SLOTS) * A_BYTES + TABLE_BYTES + 512;
@@ -75,6 +74,10 @@ struct Int8Params : TileParams {
   int64_t ld;
   int32_t dtype, paired;
 };
+
+// The first column of accumulator `acc` with n of them: one from the left, one from the right. Those
+// of two tiles meet where their columns together pass B_COL, in columns 128 .. 255 at most.
+__device__ __forceinline__ int acc_col(int acc, int n) { return acc ? B_COL - n : 0; }
 
 // Instruction descriptor of kind::f16: fp16 operands, fp32 sums, M = 256.
 __device__ __forceinline__ uint32_t instr_desc(int n) {
@@ -110,6 +113,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// The same of bytes that need not stay in L2.
+__device__ __forceinline__ void tma_load_3d_once(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                                 int32_t y, int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
       : "memory");
 }
 
@@ -314,6 +326,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp == 2 + EPI_WARPS + CONV_WARPS) {
     // ------------------------------------------------------------ TMA producer of B (both CTAs)
     const uint32_t elected = elect_one();
+    uint64_t policy;  // runs read their weights once: L2 had better keep the rows in fp16 (1 to 5%)
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_phase = 0;
     bool ok = true;
@@ -329,7 +343,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (elected) {
           const uint32_t fb = smem_u32(&rfull_bar[stage]);
           mbar_expect_tx(fb, RAW_BYTES);
-          tma_load_3d(smem_u32(raw) + stage * RAW_BYTES, &p.map_p, fb, (t.kb0 + kb) * BK, i, t.g);
+          const uint32_t dst = smem_u32(raw) + stage * RAW_BYTES;
+          if (p.offsets) tma_load_3d_once(dst, &p.map_p, fb, kb * BK, i, t.g, policy);
+          else tma_load_3d(dst, &p.map_p, fb, (t.kb0 + kb) * BK, i, t.g);
         }
         armed |= 1u << stage;
         armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
@@ -357,8 +373,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         decode<NT, TILE, BK>(p, lo, cnt, begin, tile, t);
         const int acc = local & 1;
         // the accumulator's last tile has been read, and of the tile before this one the
-        // columns that the two share (they do if the first accumulator's tile reaches there)
-        const bool meet = (acc ? before_n : t.n) > ACC1;
+        // columns that the two share
+        const bool meet = before_n + t.n > B_COL;
         before_n = t.n;
         if (!wait_warp<true>(&tempty_bar[acc], (uint32_t(local >> 1) & 1u) ^ 1u, abort_flag, limit) ||
             (meet && !wait_warp<true>(&tshared_bar[acc ^ 1], (uint32_t((local + 1) >> 1) & 1u) ^ 1u,
@@ -367,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem_base + uint32_t(acc * ACC1);
+        const uint32_t d = tmem_base + uint32_t(acc_col(acc, t.n));
         const uint32_t idesc = instr_desc(t.n);
         const bool two = two_slots(p, t);
         for (int kb = 0; kb < t.nkb; ++kb) {
@@ -452,12 +468,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // every lane waits; the warp goes on only if all of them saw the accumulator
       if (!wait_warp<false>(&tfull_bar[acc], uint32_t(local >> 1) & 1u, abort_flag, limit)) break;
       tc_fence_after();
-      const uint32_t trow = tmem_base + (uint32_t(32 * quad) << 16) + uint32_t(acc * ACC1);
-      // the half of the columns that both accumulators use, then the other: of each this warp
-      // has every second sixteen
+      const uint32_t trow = tmem_base + (uint32_t(32 * quad) << 16) + uint32_t(acc_col(acc, t.n));
+      // the half with the columns that both accumulators may use, then the other: of each this
+      // warp has every second sixteen
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        const int c0 = ((acc ^ half) ? 0 : ACC1) + 16 * part;
+        const int c0 = ((acc ^ half) ? 0 : HALF) + 16 * part;
 #pragma unroll 1
         for (int q = 0; q < 4; q += 2) {
           const int c = c0 + 32 * q;
