@@ -280,6 +280,23 @@ def test_product_many_tiles(cuda):
     assert torch.equal(y.cpu(), want_product(a, sa, b, sb, BF16, off, cnt))
 
 
+def test_product_runs_of_all_heights(cuda):
+    """Tiles of up to 128 rows and higher ones follow one another in each pair of SMs; the depth ends in
+    the first half of a stage, or in the second."""
+    g = torch.Generator().manual_seed(2)
+    cnt = torch.randint(0, 400, (90,), generator=g).tolist()
+    off = [0]
+    for n in cnt:
+        off.append(off[-1] + (n + 15) // 16 * 16)
+    for K in (700, 736):
+        a, sa = codes(K, off[-1], K)
+        b, sb = codes(12, 90, 520, K)
+        y = mao.int8_product(a, sa, b, sb, offsets=torch.tensor(off, dtype=I32, device=cuda),
+                             counts=torch.tensor(cnt, dtype=I32, device=cuda))
+        mao.sync_status()
+        assert torch.equal(y.cpu(), want_product(a, sa, b, sb, BF16, off, cnt))
+
+
 def test_product_outputs_and_nan(cuda):
     a, sa = codes(1, 50, 96)
     b, sb = codes(2, 60, 96)
