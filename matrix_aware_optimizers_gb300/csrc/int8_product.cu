@@ -21,12 +21,15 @@
 // columns each). Two tiles of 256 rows share 128 columns; these are read first, and the next tile's
 // products wait for that only.
 //
-// What bounds it: 8192 x 14336 x 4096 takes 527 us in a graph (1.83 PFLOP/s, 95% of cuBLAS's bf16
-// rate alone), 570 us in a run: the tensor cores, then the power limit. Low tiles do not pay
+// What bounds it: 8192 x 14336 x 4096 takes 500 to 508 us in a graph (1.9 PFLOP/s: cuBLAS's bf16 rate
+// alone), more in a long run: the tensor cores, then the power limit. Low tiles do not pay
 // less: a product with its M side in TMEM takes some 90 cycles however few the rows, so a stage
-// takes 0.40 us from 32 rows on, 0.50 at 128, 0.67 at 256. (Twice the converting warps, or four stages
+// takes 0.43 us from 32 rows on, 0.50 at 128, 0.6 at 160. (Twice the converting warps, or four stages
 // of B in TMEM for tiles of up to 128 rows: no difference.) 16,001 rows among 128 x [1536 x 2048]:
-// 168 us, 25 of them the rows' conversion (HBM 4.2 TB/s in the product).
+// 148 us, 21 of them the rows' conversion; 128 rows for each of them: 116 us.
+// What the rings look ahead counts: with A in three 32 KB stages, half empty in tiles of up to 128
+// rows, and six stages of B, these two took 168 and 132 us, the prompt 519. Seven slots and five stages: 158
+// instead of 156 at that point; nine slots, or five stages beside eight: as now.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -263,8 +266,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const CUtensorMap* map = lane ? &p.map_q[Q_BOXES - 1] : &p.map_p;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }
-  // launched as a programmatic dependent: the set-up so far may overlap the previous kernel
-  wait_for_previous();
+  // launched as a programmatic dependent: the set-up may overlap the previous kernel's end (all of it
+  // where no offsets are read)
+  if (p.offsets) wait_for_previous();
   make_table<THREADS>(p, lo, cnt, begin, reinterpret_cast<int*>(bars + 48));
   tc_fence_before();
   __syncthreads();
@@ -272,6 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  if (!p.offsets) wait_for_previous();
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer of A (both CTAs)
