@@ -73,6 +73,7 @@ struct alignas(64) FfnParams : TileParams {
   void* z;                     // G and U, fp32 or bf16: GATE writes them (null: not wanted), GATE_BACK reads them
   __nv_bfloat16* dz;           // GATE_BACK: dG and dU
   int64_t ld, ldz, lddz;
+  int32_t early;               // the offsets are older than the kernel before this one
   int32_t dz_half;             // columns from dG to dU
   int32_t dtype;
   int32_t z_dtype;
@@ -373,9 +374,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const CUtensorMap* map = lane & 1 ? &p.map_q[Q_BOXES - 1] : &p.map_p;
     if (p.tiles_i > 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }
-  // launched as a programmatic dependent: the set-up may overlap the previous kernel's end (all of it
-  // where no offsets are read: 1.5 us)
-  if (p0.offsets) wait_for_previous();
+  // launched as a programmatic dependent: the set-up may overlap the previous kernel's end (1.5 us; all
+  // of it unless it reads offsets that that kernel may have written). First loads of down's P as early
+  // made 48 rows 1.4 us slower.
+  const bool early = !p0.offsets || p0.early;
+  if (!early) wait_for_previous();
   make_table<THREADS>(p0, lo, cnt, begin, reinterpret_cast<int*>(bars + 40));
   tc_fence_before();
   __syncthreads();
@@ -400,7 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  if (!p0.offsets) wait_for_previous();
+  if (early) wait_for_previous();
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
@@ -1073,6 +1076,7 @@ mao_status gated_ffn_launch(const mao_mat& X, const mao_mat& up, const mao_mat& 
   if (st == MAO_OK) st = encode_q(q, f.out, runs.offsets != nullptr, h, s.N, s.R, 1, f.ldh, s.R * f.ldh);
   if (st != MAO_OK) return st;
   set_out(q, Y);
+  q.early = 1;
   return run(f.out, act, out, runs, s.R, at, stream);
 }
 
@@ -1151,6 +1155,7 @@ mao_status gated_ffn_backward_launch(const mao_mat& dY, const mao_mat& X, const 
     if (st != MAO_OK) return st;
     set_out(p, *ddown);
   }
+  for (FfnParams& p : grads.p) p.early = 1;
   return run_grads({&b.dx, &b.dup, &b.ddown}, {dX != nullptr, dup != nullptr, ddown != nullptr}, grads, runs, s.R, at, stream);
 }
 

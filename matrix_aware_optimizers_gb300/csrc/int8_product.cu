@@ -266,9 +266,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const CUtensorMap* map = lane ? &p.map_q[Q_BOXES - 1] : &p.map_p;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }
-  // launched as a programmatic dependent: the set-up may overlap the previous kernel's end (all of it
-  // where no offsets are read)
-  if (p.offsets) wait_for_previous();
+  // launched as a programmatic dependent: the set-up may overlap the rows' conversion (which began
+  // after every kernel before it, so that the offsets are there)
   make_table<THREADS>(p, lo, cnt, begin, reinterpret_cast<int*>(bars + 48));
   tc_fence_before();
   __syncthreads();
@@ -276,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  if (!p.offsets) wait_for_previous();
+  wait_for_previous();
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer of A (both CTAs)
