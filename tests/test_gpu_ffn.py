@@ -243,6 +243,35 @@ def test_strides_and_outputs(cuda):
     assert only[0] is None and only[2] is None and torch.equal(only[1], g0[1])
 
 
+@pytest.mark.parametrize("T", [1, 3, 150])
+def test_odd_widths_of_aligned_rows(cuda, T):
+    """Slices whose rows start at multiples of 16 bytes and whose widths are no multiples of that: what
+    lies beside them takes no part and stays as it is."""
+    K, N, C = 97, 71, 83
+    x, up, down, dy = make(11, T, K, N, C)
+
+    def wide(t):
+        big = torch.full((t.shape[0], (t.shape[1] + 15) // 8 * 8), float("nan"), dtype=t.dtype, device=cuda)
+        big[:, :t.shape[1]] = t
+        return big[:, :t.shape[1]]
+
+    for save in (F32, BF16):
+        y0, z0 = mao.gated_ffn(x, up, down, "gelu", save=save)
+        check_forward(y0, z0, x, up, down, "gelu")
+        g0 = mao.gated_ffn_backward(dy, x, up, down, z0, "gelu")
+        xs, us, ds, dys = (wide(t) for t in (x, up, down, dy))
+        out, Z = wide(torch.zeros_like(y0)), wide(torch.zeros_like(z0))
+        y, z = mao.gated_ffn(xs, us, ds, "gelu", out=out, Z=Z)
+        assert y is out and z is Z and torch.equal(y, y0) and torch.equal(z, z0)
+        outs = [wide(torch.zeros_like(t)) for t in (x, up, down)]
+        got = mao.gated_ffn_backward(dys, xs, us, ds, Z, "gelu", dX=outs[0], dup=outs[1], ddown=outs[2])
+        for a, b in zip(got, g0):
+            assert torch.equal(a, b)
+        for t in [out, Z] + outs:
+            assert t._base[:, t.shape[1]:].isnan().all()
+    mao.sync_status()
+
+
 def test_no_rows(cuda):
     x, up, down, dy = make(8, 0, 40, 24, 32)
     y, z = mao.gated_ffn(x, up, down, "silu", save=True)
