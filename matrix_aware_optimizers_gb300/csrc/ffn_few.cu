@@ -10,7 +10,7 @@
 // tensor cores' rate does not count, and the fragments come straight from the ring. Any order of the
 // products within a sum does, so a lane takes 32 bytes in a row of W's row and the same 32 of X's and
 // hands out eight of them per product. 8-bit codes are multiplied as whole numbers (m16n8k32): slower
-// products than fp16's, but no conversion. The warps' sums are added in their order.
+// products than fp16's, but no conversion; one row or two by dot products instead. The warps' sums are added in their order.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -34,8 +34,13 @@ using namespace ffn;
 
 // What bounds it: HBM, at 6.1 TB/s over both products of one row of the 4096-wide block (gated 37 us,
 // 235 MB; down 24 us, 117 MB); a launch and its first loads (5 us) in the shorter calls: an 8-bit
-// product of 14336 x 4096, 59 MB, 15 us; eight of 128 experts' blocks of 2048 x 768, 75 MB, 24 us.
+// product of 14336 x 4096, 59 MB, 13 us; eight of 128 experts' blocks of 2048 x 768, 75 MB, 24 us.
 // Weights loaded straight to registers instead, two batches in turn: 46 and 33 us.
+// 8-bit rows that are multiplied by dot products of four codes: the whole numbers' tensor products take
+// as long for one row as for eight, and hold up the stream (14336 x 4096, one row and two: 12.9 and 14.0 us
+// against 15.8; three: 15.8 either way). Two or four stages at a time, or X's codes straight to
+// registers: 14.6 to 15.7.
+constexpr int DOT_ROWS = 2;
 constexpr int WARPS = 8;
 constexpr int THREADS = 32 * WARPS;
 constexpr int CHANNELS = 16;           // per unit
@@ -231,12 +236,30 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
   for (int unit = unit0; unit < units; unit += unit_step, flip ^= 1) {
     decode_unit<NT>(p, lo, cnt, begin, unit, u);
     typename Sums<INT8>::T acc[CHAINS][MATS][NT][4] = {};
+    int dots[DOT_ROWS][2] = {};  // of up to DOT_ROWS rows: of row j of X with W's rows r and r + 8
     for (int c = member; c < chunks; c += team) {
       const int stage = used % STAGES;
       ok = ok && wait_warp<false>(&bars[warp][stage], uint32_t(used / STAGES) & 1u, abort_flag, p.timeout_ns);
       if (!ok) break;
       const uint8_t* box = ring + stage * STAGE;
       const int r = lane >> 2;
+      if (INT8 && NT == 1 && u.n <= DOT_ROWS) {
+        const Entries a = entries(box, r, lane), b = entries(box, r + 8, lane);
+#pragma unroll
+        for (int j = 0; j < DOT_ROWS; ++j) {
+          if (j >= u.n) break;
+          const Entries x = entries(box + BOX_BYTES, j, lane);
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            dots[j][0] = __dp4a(int(a.w[s]), int(x.w[s]), dots[j][0]);
+            dots[j][1] = __dp4a(int(b.w[s]), int(x.w[s]), dots[j][1]);
+          }
+        }
+        ++used;
+        __syncwarp();  // every lane has read the stage
+        load_next(true);
+        continue;
+      }
       Entries x[NT];
 #pragma unroll
       for (int q = 0; q < NT; ++q) x[q] = entries(box + MATS * BOX_BYTES, r + 8 * q, lane);
@@ -252,6 +275,18 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
       ++used;
       __syncwarp();  // every lane has read the stage
       load_next(true);
+    }
+    if (INT8 && NT == 1 && u.n <= DOT_ROWS) {
+      // a lane's sums are over a quarter of the columns; lane 4 c + j / 2 hands over row j's, channels c, c + 8
+#pragma unroll
+      for (int j = 0; j < DOT_ROWS; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          int v = dots[j][h];
+          v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+          v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+          if ((lane & 3) == j >> 1) acc[0][0][0][2 * h + (j & 1)] = v;
+        }
     }
 #pragma unroll
     for (int m = 0; m < MATS; ++m)
@@ -312,7 +347,7 @@ mao_status few_launch(const FewParams& params, bool int8, bool gate, int32_t act
   p.height = two ? 16 : 8;
   p.x_rows = p.rows < p.height ? p.rows : p.height;
   const int64_t chunks = ceil_div(int64_t(p.depth) * (int8 ? 1 : 2), 128);
-  const int64_t least = int8 ? 8 : 4;  // chunks of a warp (14336 x 4096 8-bit, one row: 15.1 us; with four 16.1)
+  const int64_t least = int8 ? 8 : 4;  // chunks of a warp (14336 x 4096 8-bit, one row: 12.9 us; four 15.2, sixteen 14.8)
   p.team = chunks >= 8 * least ? 8 : chunks >= 4 * least ? 4 : 2;
   const int64_t mats = gate ? 2 : 1, w_rows = int64_t(p.I);
   mao_status st = int8 ? tc_encode_code_map(&p.map_w, p.w, p.depth, w_rows, p.ldw, p.groups, CHANNELS)

@@ -230,6 +230,19 @@ def test_product_few_rows(cuda, T):
         assert torch.equal(y.cpu(), want_product(a, sa, b, sb, dtype))
 
 
+def test_product_few_rows_in_runs(cuda):
+    """Runs of no, one, two and more rows, side by side; a depth that ends inside a load."""
+    cnt = [0, 1, 2, 3, 1, 8, 9, 2, 0, 17, 1, 2]
+    off = [96 * i for i in range(13)]
+    for N, K in ((300, 700), (40, 16), (528, 2064)):
+        a, sa = codes(13, 96 * 12, K)
+        b, sb = codes(14, 12, N, K)
+        y = mao.int8_product(a, sa, b, sb, offsets=torch.tensor(off, dtype=I32, device=cuda),
+                             counts=torch.tensor(cnt, dtype=I32, device=cuda), out_dtype=F32)
+        mao.sync_status()
+        assert torch.equal(y.cpu(), want_product(a, sa, b, sb, F32, off, cnt))
+
+
 def test_product_exact_at_the_limit(cuda):
     """Sums of the largest codes are exact up to 2^24: 1040 products of 127 * 127 (codes of
     int8_quantize), 1024 of 128 * 128 (any codes)."""
