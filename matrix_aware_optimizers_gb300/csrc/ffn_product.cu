@@ -787,7 +787,7 @@ struct Plan {
     const int64_t outputs = J * matrices() * I * (epi == GATE ? 2 : 1);
     // A block takes a pair 0.27 us (the tensor cores), at least 0.14 (its copies and their waits),
     // or 0.37 where few rows leave the operands' bytes to bound it.
-    split = choose_cut(pairs, tiles_i() * matrices(), J, nkb, 0.27, form != TN && J < 128 ? 0.37 : 0.14,
+    split = choose_cut(pairs, tiles_i() * matrices(), J, nkb, 0.0, 0.27, form != TN && J < 128 ? 0.37 : 0.14,
                        epi == GATE_BACK ? 9.5 : epi == GATE ? 3.5 : 1.7, outputs, 4);
     prows = J * matrices();
     pld = round_up(I, 4) * (epi == GATE ? 2 : 1);
