@@ -343,7 +343,7 @@ mao_status few_launch(const FewParams& params, bool int8, bool gate, int32_t act
   static_cast<FewParams&>(p) = params;
   p.tiles_i = int32_t(ceil_div(p.I, CHANNELS));
   p.timeout_ns = wait_limit_ns();
-  const int two = !p.offsets && p.rows > 8;  // (8-bit rows come up to eight at a time)
+  const int two = !p.offsets && p.rows > 8;
   p.height = two ? 16 : 8;
   p.x_rows = p.rows < p.height ? p.rows : p.height;
   const int64_t chunks = ceil_div(int64_t(p.depth) * (int8 ? 1 : 2), 128);
@@ -357,24 +357,25 @@ mao_status few_launch(const FewParams& params, bool int8, bool gate, int32_t act
     st = int8 ? tc_encode_code_map(&p.map_x, p.x, p.depth, p.rows, p.ldx, 1, p.x_rows)
               : tc_encode_bf16_map(&p.map_x, p.x, p.depth, p.rows, 1, 1, p.ldx, p.rows * p.ldx, p.rows * p.ldx, p.x_rows);
   if (st != MAO_OK) return st;
-  static const Kernel kernels[9] = {
-      few_kernel<true, false, 0, 1>,          few_kernel<false, false, 0, 1>,         few_kernel<false, false, 0, 2>,
+  static const Kernel kernels[10] = {
+      few_kernel<true, false, 0, 1>,          few_kernel<true, false, 0, 2>,
+      few_kernel<false, false, 0, 1>,         few_kernel<false, false, 0, 2>,
       few_kernel<false, true, MAO_SILU, 1>,   few_kernel<false, true, MAO_SILU, 2>,
       few_kernel<false, true, MAO_GELU, 1>,   few_kernel<false, true, MAO_GELU, 2>,
       few_kernel<false, true, MAO_GELU_TANH, 1>, few_kernel<false, true, MAO_GELU_TANH, 2>};
   static std::atomic<bool> ready[64];
   st = once_per_device(ready, [&] {
     cudaError_t err = cudaSuccess;
-    for (int f = 0; f < 9 && err == cudaSuccess; ++f)
+    for (int f = 0; f < 10 && err == cudaSuccess; ++f)
       err = cudaFuncSetAttribute(kernels[f], cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 1024 + WARPS * ring_bytes(f >= 3, f > 0 ? 2 - f % 2 : 1));
+                                 1024 + WARPS * ring_bytes(f >= 4, 1 + f % 2));
     return err;
   });
   if (st != MAO_OK) return st;
   g_launched.store(true, std::memory_order_release);
   const int64_t units = p.offsets ? int64_t(num_sms()) * WARPS : int64_t(p.tiles_i) * ceil_div(p.rows, p.height);
   const int64_t blocks = ceil_div(units, WARPS / p.team);
-  return launch_dependent(kernels[int8 ? 0 : (gate ? 3 + 2 * act : 1) + two], unsigned(blocks < num_sms() ? blocks : num_sms()),
+  return launch_dependent(kernels[(int8 ? 0 : gate ? 4 + 2 * act : 2) + two], unsigned(blocks < num_sms() ? blocks : num_sms()),
                           THREADS, size_t(1024 + WARPS * ring_bytes(gate, 1 + two)), stream, p);
 }
 

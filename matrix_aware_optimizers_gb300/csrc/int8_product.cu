@@ -649,14 +649,14 @@ size_t half_bytes(const mao_int8& A) { return size_t(round_up(A.rows * half_ld(A
 }  // namespace
 
 size_t int8_product_workspace_size(const mao_int8& A, const mao_int8& B, bool grouped) {
-  if (A.rows == 0 || few_rows(A.rows, grouped, false, B.count, true)) return 0;
+  if (A.rows == 0 || few_rows(A.rows, grouped, false, B.count)) return 0;
   const Cut s = grouped ? Cut{TILE, 1, 0} : cut_of(A, B);
   return half_bytes(A) + (s.splits > 1 ? size_t(round_up(int64_t(s.splits) * A.rows * round_up(B.rows, 4) * 4, 256)) : 0);
 }
 mao_status int8_product_launch(const mao_int8& A, const mao_int8& B, const mao_mat& D, const Runs& runs,
                                void* workspace, cudaStream_t stream) {
   if (A.rows == 0) return MAO_OK;
-  if (few_rows(A.rows, runs.offsets != nullptr, runs.counts != nullptr, runs.groups, true)) {
+  if (few_rows(A.rows, runs.offsets != nullptr, runs.counts != nullptr, runs.groups)) {
     FewParams q = {};
     q.offsets = runs.offsets;
     q.counts = runs.counts;
