@@ -220,7 +220,7 @@ def test_product(cuda, dtype, shape):
     assert torch.equal(y.cpu(), want_product(a, sa, b, sb, dtype))
 
 
-@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 40, 100, 128, 200])
+@pytest.mark.parametrize("T", [1, 2, 3, 8, 9, 15, 16, 17, 40, 100, 128, 200])
 def test_product_few_rows(cuda, T):
     """Few rows and long sums, which are split."""
     a, sa = codes(T, T, 4000)
