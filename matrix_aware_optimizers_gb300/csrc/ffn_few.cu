@@ -138,8 +138,8 @@ __device__ __forceinline__ void decode_unit(const FewParams& p, const int* lo, c
   }
   const int it = local / count, jt = local - it * count;
   u.i0 = it * CHANNELS;
-  u.j0 = first + jt * (8 * NT);
-  u.n = min(8 * NT, rows - jt * (8 * NT));
+  u.j0 = first + int64_t(jt) * (8 * NT);
+  u.n = int(min(int64_t(8 * NT), rows - int64_t(jt) * (8 * NT)));
 }
 
 template <bool INT8, bool GATE, int ACT, int NT>

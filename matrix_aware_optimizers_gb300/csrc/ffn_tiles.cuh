@@ -65,7 +65,8 @@ __device__ __forceinline__ void make_table(const TileParams& p, int* lo, int* cn
       for (int g = 0; g < n; ++g) lo[g + 1] = max(lo[g + 1], lo[g]);
     __syncthreads();
   }
-  // thread i (of 256) sums the tiles of groups 4 i .. 4 i + 3
+  // thread i sums the tiles of groups 4 i .. 4 i + 3
+  static_assert(4 * THREADS >= MAX_GROUPS, "a thread for every four groups");
   int c[4], own = 0;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -95,6 +96,7 @@ __device__ __forceinline__ void make_table(const TileParams& p, int* lo, int* cn
     if (g <= n) begin[g] = s;
     s += c[q];
   }
+  if (tid == THREADS - 1 && 4 * THREADS <= n) begin[n] = s;  // no thread's four reach that entry
 }
 
 // A split's share of the depth, and its rows of the partial sums.
