@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(256) int8_sum_kernel(const SumParams p) {
 }
 
 // A's codes in fp16, a row per warp, eight codes per lane and step, up to eight steps under way. With counts the rows that hold no
-// tokens are left out (the offsets rise): 128 runs of 125 rows, padded to
+// tokens are left out: 128 runs of 125 rows, padded to
 // twice that, 41 us with all of them.
 struct HalfParams {
   const int8_t* src;
@@ -604,13 +604,18 @@ __global__ void __launch_bounds__(128) to_half_kernel(const HalfParams p) {
   const int lane = threadIdx.x % 32;
   for (int64_t r = int64_t(blockIdx.x) * 4 + threadIdx.x / 32; r < p.rows; r += int64_t(gridDim.x) * 4) {
     if (p.counts) {
-      int lo = -1;  // the last run that starts at or before the row
+      // offset `end` is the first past the row, and the run before it begins at the largest so far: the
+      // product's table raises offsets that fall
+      int end = p.groups + 1, first = 0;
 #pragma unroll 4
-      for (int g0 = 0; g0 < p.groups; g0 += 32)
-        lo += __popc(__ballot_sync(0xFFFFFFFFu, g0 + lane < p.groups &&
-                                                    (g0 + lane == 0 || __ldg(p.offsets + g0 + lane) <= r)));
-      const int64_t first = max(__ldg(p.offsets + lo), 0), next = __ldg(p.offsets + lo + 1);
-      if (first <= r && r < next && r >= first + max(__ldg(p.counts + lo), 0)) continue;
+      for (int g0 = 0; g0 <= p.groups; g0 += 32) {
+        const int g = g0 + lane, at = g <= p.groups ? __ldg(p.offsets + g) : 0;
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, at > r);
+        if (past) end = min(end, g0 + __ffs(past) - 1);
+        if (g < end) first = max(first, at);
+      }
+      first = __reduce_max_sync(0xFFFFFFFFu, first);
+      if (end > 0 && end <= p.groups && r >= int64_t(first) + max(__ldg(p.counts + end - 1), 0)) continue;
     }
     const int8_t* s = p.src + r * p.ld;
     uint16_t* d = p.dst + r * p.dld;

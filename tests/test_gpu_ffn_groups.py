@@ -106,3 +106,14 @@ def test_gradients(cuda, groups, use_counts):
     mao.sync_status()
     check_backward(grads, dy, x, up, down, z, "gelu", off, counts)
     check_unused(rows, off, counts, grads[0])
+
+
+FALLING = [([0, 300, 100, 400], [200, 50, 100]), ([-9, 128, 500, 90, 90, 700], [3, 128, 300, 90, 1000]),
+           ([60, 50, 40, 3000, 2800, 3100], [7, 7, 2000, 40, 90]), ([0, 40, 20, 200, 150, 300], [9, 1, 150, 60, 100])]
+
+
+@pytest.mark.parametrize("off,cnt", FALLING)
+def test_counted_runs_of_falling_offsets(cuda, off, cnt):
+    """Offsets that fall are raised to the largest before them, by every part of a call: what the
+    workspace held before is in no output. The last case is one of few rows."""
+    check_calls(cuda, len(cnt), off, cnt, max(off) - (20 if len(cnt) == 5 else 0))
