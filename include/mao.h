@@ -686,7 +686,8 @@ mao_status int8_quantize(const mao_mat* X, int32_t batch, int64_t batch_stride, 
  * run g, D f32 or bf16, R x N.
  *   A      R x K, count 1. B: N x K, count = groups.
  * Products of codes are exact and summed in fp32: the sum is exact while its parts stay below
- * 2^24 (for any codes while K <= 1024). It is scaled by sA, then by sB, and rounded to D's type.
+ * 2^24 (for any codes while K <= 1024), beyond that each partial sum is rounded or cut to
+ * fp32. It is scaled by sA, then by sB, and rounded to D's type.
  *   workspace >= int8_product_workspace_bytes(A, B, offsets != NULL) bytes, 256-byte aligned (A in
  *   fp16; parts of few rows' sums, which are split). Clobbered.
  *   Limits: groups <= 1024, R <= 2^31 - 1024, N, K <= 2^20.

@@ -77,6 +77,13 @@ template <>
 struct Sums<true> {
   using T = int;
 };
+// Two parts of a lane's sum, and the sum in fp32. A warp sums up to 2^17 products of codes (an eighth of
+// a depth of 2^20): more than -2^31, and 2^31 itself where all codes are -128, whose word is that of -2^31.
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ int add(int a, int b) { return int(uint32_t(a) + uint32_t(b)); }
+__device__ __forceinline__ float sum_of(float v) { return v; }
+__device__ __forceinline__ float sum_of(int v) { return v == INT32_MIN ? 0x1p31f : float(v); }
+
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
   asm volatile(
@@ -283,8 +290,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           int v = dots[j][h];
-          v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-          v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+          v = add(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+          v = add(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
           if ((lane & 3) == j >> 1) acc[0][0][0][2 * h + (j & 1)] = v;
         }
     }
@@ -294,7 +301,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
       for (int q = 0; q < NT; ++q)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          parts[flip][warp][m][q][lane][e] = float(CHAINS == 1 ? acc[0][m][q][e] : acc[0][m][q][e] + acc[CHAINS - 1][m][q][e]);
+          parts[flip][warp][m][q][lane][e] =
+              sum_of(CHAINS == 1 ? acc[0][m][q][e] : add(acc[0][m][q][e], acc[CHAINS - 1][m][q][e]));
     // (the other half of `parts` was read before this barrier's last use but one)
     asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / team), "r"(32 * team) : "memory");
     // row j0 + r of X, channel i0 + c
