@@ -41,7 +41,8 @@ __device__ __forceinline__ void activate(float x, float& a, float& slope) {
   } else {
     const float s = fast_sigmoid(2.0f * kTanhC * (x + kTanhA * x * x * x));
     a = x * s;
-    slope = s + a * (1.0f - s) * (2.0f * kTanhC + 6.0f * kTanhC * kTanhA * x * x);
+    // (where x^2 passes fp32's range, a or 1 - s is 0: not to be multiplied by an infinity)
+    slope = s + a * (1.0f - s) * (2.0f * kTanhC + 6.0f * kTanhC * kTanhA * fminf(x * x, 1e30f));
   }
 }
 

@@ -5,10 +5,11 @@ import pytest
 import torch
 
 import matrix_aware_optimizers_gb300 as mao
+from oracle import ffn as of
 
 pytestmark = pytest.mark.gpu
 
-F32 = torch.float32
+BF16, F32 = torch.bfloat16, torch.float32
 
 
 @pytest.mark.parametrize("K", [2 ** 20, 2 ** 20 - 16])
@@ -35,3 +36,31 @@ def test_longest_sums_of_codes(cuda, T, K):
     y = mao.int8_product(A, one(T), B, one(N), out_dtype=F32)
     assert ((y.double() - want).abs() <= 8 * 2.0 ** -24 * (1 + 2.0 ** -20) * want).all()
     mao.sync_status()
+
+
+@pytest.mark.parametrize("saved", [F32, BF16])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("C", [8, 4096])
+def test_slopes_of_large_gates(cuda, act, C, saved):
+    """Where G's square passes fp32's range, the slope is 1 or 0, and so is dG (C = 4096: a sum that is
+    split, its epilogue a kernel of its own)."""
+    G = [1e19, -1e19, 1e20, -1e20, 3e38, -3e38, 4.0, -4.0]
+    z = torch.tensor([G + [1.0] * 8], dtype=saved, device=cuda)
+    down = torch.zeros(C, 8, dtype=BF16, device=cuda)
+    down[:8] = torch.eye(8)
+    dy = torch.zeros(1, C, dtype=BF16, device=cuda)
+    dy[:, :8] = 1.0  # dH = 1
+    up = torch.zeros(16, 8, dtype=BF16, device=cuda)
+    up[:8] = torch.eye(8)  # dX = dG
+    x = torch.ones(1, 8, dtype=BF16, device=cuda)
+    dX, dup, ddown = mao.gated_ffn_backward(dy, x, up, down, z, act, grad_dtype=F32)
+    mao.sync_status()
+    want = of.slope(np.array(G), act)
+    assert want[:6].tolist() == [1.0, 0.0, 1.0, 0.0, 1.0, 0.0]
+    # the slope's own arithmetic: 2^-19 of 1 + |g|; its rounding to bf16: 2^-8
+    own = 2.0 ** -19 * 5
+    slack = own + 2.0 ** -8 * (np.abs(want) + own)
+    slack[:6] = 0.0
+    assert (np.abs(dX[0].double().cpu().numpy() - want) <= slack).all()
+    assert torch.equal(dup[:8, 0], dX[0])  # dG^T X
+    assert torch.isfinite(dup).all() and torch.isfinite(ddown).all()
