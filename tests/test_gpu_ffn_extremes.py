@@ -64,3 +64,18 @@ def test_slopes_of_large_gates(cuda, act, C, saved):
     assert (np.abs(dX[0].double().cpu().numpy() - want) <= slack).all()
     assert torch.equal(dup[:8, 0], dX[0])  # dG^T X
     assert torch.isfinite(dup).all() and torch.isfinite(ddown).all()
+
+
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_infinite_gates(cuda, act, T):
+    """G = U = inf: H is infinite, and the sums multiply it by zero weights too: NaN. G = -inf: -inf times 0
+    in the activation."""
+    x = torch.zeros(T, 16, dtype=BF16, device=cuda)
+    x[0, 0], x[1, 0], x[2:, 0] = float("inf"), float("-inf"), 2.0
+    up = torch.zeros(16, 16, dtype=BF16, device=cuda)
+    up[:, 0] = 1.0
+    down = torch.eye(8, dtype=BF16, device=cuda)
+    y = mao.gated_ffn(x, up, down, act, out_dtype=F32)
+    mao.sync_status()
+    assert y[:2].isnan().all() and torch.isfinite(y[2:]).all()
