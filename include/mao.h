@@ -599,9 +599,14 @@ mao_status expert_combine_backward(const mao_mat* dY, const mao_mat* Z, const in
  * Runs of rows (gated_ffn, gated_ffn_backward, int8_product): offsets is NULL (groups must be
  * 1): one run of all R rows. Otherwise a device array of groups + 1 int32, rising within 0 ..
  * R (values outside are cut to that range, those that fall raised to the largest before them): run
- * g is rows offsets[g] .. offsets[g+1] - 1 and is multiplied by matrix g. counts is NULL, or a device array of groups int32: only the first
- * counts[g] rows of run g hold tokens (values outside 0 .. its length are cut), and the time
- * goes by those. Output rows outside the runs, and in a run from its count on, are zero.
+ * g is rows offsets[g] .. offsets[g+1] - 1 and is multiplied by matrix g. counts is NULL, or a
+ * device array of groups int32: only the first counts[g] rows of run g hold tokens (values outside
+ * 0 .. its length are cut), and the time goes by those. Output rows outside the runs, and in a run
+ * from its count on, are zero.
+ * With counts, calls of gated_ffn and int8_product with R <= 2048 and R < 128 groups are taken for
+ * a few tokens each in runs of their own: a run's matrix is then read once for every eight of its
+ * tokens. Where few runs hold many tokens each, the rows that expert_rows gives are faster than
+ * rows cut to those in use.
  */
 
 enum { MAO_SILU = 0, MAO_GELU = 1, MAO_GELU_TANH = 2 };

@@ -930,8 +930,8 @@ def gated_ffn_backward(dY, X, up, down, Z, act="silu", offsets=None, counts=None
 
     dX, dup, ddown: float32 or bfloat16 tensors to fill, by default new ones of grad_dtype,
     shaped as X, up and down; False: not wanted (None is returned in its place). offsets must
-    be multiples of 128 (expert_plan's), but for the last. With counts, rows of X and dY past
-    their run's count must be finite.
+    be multiples of 128 (expert_plan's), but for the last, which may be T. With counts, rows of X
+    and dY past their run's count must be finite.
     """
     kind = _act(act)
     off, cnt, groups = _runs(offsets, counts)

@@ -26,7 +26,8 @@ mao_status few_read_and_clear_error(cudaStream_t stream);
 // a block per run it may be any number up to 128 a run, and only the device knows; a run of more
 // rows than a pass takes reads its weights again). One row of the 4096-wide block: 56 us against
 // 66 by tiles, 16 rows 63 against 68; 8 and 16 tokens of 128 experts of 2048 x 768: 24 and 40 against
-// 30 and 43, but 130 of 8 experts 36 against 24; an 8-bit product of 14336 x 4096, one row, eight and 16: 13,
+// 30 and 43, but 130 of 8 experts 36 against 24, and where 8 of 17 hold 32 tokens each or 125, in rows
+// cut to those in use, 55 and 192 against 23 and 25 (the header says so); an 8-bit product of 14336 x 4096, one row, eight and 16: 13,
 // 16 and 22 against 22, 20 and 20.
 inline bool few_rows(int64_t rows, bool grouped, bool counts, int32_t groups) {
   return grouped ? counts && rows <= 16 * 128 && rows < int64_t(128) * groups : rows <= 16;

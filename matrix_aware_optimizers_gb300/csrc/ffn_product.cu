@@ -1128,7 +1128,7 @@ mao_status gated_ffn_backward_launch(const mao_mat& dY, const mao_mat& X, const 
     p.dz = reinterpret_cast<__nv_bfloat16*>(dz);
     p.lddz = 2 * b.ldh;
     p.dz_half = int32_t(b.ldh);
-      st = run(b.back, act, back, runs, s.R, at, stream);
+    st = run(b.back, act, back, runs, s.R, at, stream);
     if (st != MAO_OK) return st;
   }
   FfnArgs<3> grads = {};

@@ -49,8 +49,9 @@ unsigned long long wait_limit_ns();
 // Launch accounting (every kernel launch of the library calls this once).
 void count_launch();
 
-// Launches a kernel that may start before the previous one in the stream has finished: it
-// begins with griddepcontrol.wait, before which it touches no global memory.
+// Launches a kernel that may start before the previous one in the stream has finished (when all its
+// blocks are past their own wait, and so everything before it is complete): before its
+// griddepcontrol.wait it writes no global memory, and reads only what is older than that kernel.
 // Judged by its own result: an error that other code left pending is not this launch's.
 template <typename P>
 mao_status launch_dependent(void (*kernel)(const P), dim3 grid, dim3 block, size_t smem,
